@@ -1,0 +1,323 @@
+// C entry points of the 4-bit KV cache (include/g4.h, g4_kv4_*): argument checks, the handle
+// with its cache and workspace, and the launches of kv4.cuh and kv4_attend.cuh.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <new>
+#include <set>
+#include <vector>
+
+#include "host.h"
+#include "kv4.cuh"
+#include "kv4_attend.cuh"
+
+using namespace g4;
+
+struct g4_kv4 {
+  g4_kv4_config cfg{};
+  int device = 0, sms = 0;
+  Kv4Cache c{};
+  std::vector<void*> allocs;
+  size_t bytes = 0;
+  float* lse = nullptr;                       // [n_slots][max_q_len][num_q_heads]
+  int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
+  int* n_moves = nullptr;                     // [n_slots][kvh]
+};
+
+namespace {
+
+template <class T>
+g4_status kv4_alloc(g4_kv4* op, T** p, size_t count, cudaStream_t st) {
+  void* q = nullptr;
+  const size_t n = std::max<size_t>(count, 1) * sizeof(T);
+  const cudaError_t e = cudaMalloc(&q, n);
+  if (e != cudaSuccess) {
+    cuda_ok(e, "cudaMalloc");
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? G4_ERR_OOM : G4_ERR_CUDA;
+  }
+  op->allocs.push_back(q);
+  op->bytes += n;
+  *p = static_cast<T*>(q);
+  CK(cudaMemsetAsync(q, 0, n, st));
+  return G4_OK;
+}
+
+int log2i(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// Tensor argument -> kernel form.  [n][rows][heads][d]; false when it is malformed.
+bool kv4_dense(const g4_kv4_tensor* t, long n, long rows, long heads, int d, bool written, Kv4Dense* out) {
+  *out = Kv4Dense{};
+  if (!t) return true;
+  if (!t->data || t->dtype < G4_DT_F32 || t->dtype > G4_DT_F16) return false;
+  const long es = t->dtype == G4_DT_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(t->data) % es) return false;
+  struct { long stride, size; } ax[3] = {{(long)t->seq_stride, n}, {(long)t->row_stride, rows}, {(long)t->head_stride, heads}};
+  const long most = 1L << 46;  // keeps every offset far inside 64 bits
+  for (auto& x : ax)
+    if (x.stride < 0 || x.stride > most / std::max(x.size, 1L)) return false;
+  if (written) {  // no element twice: each stride steps over all that smaller strides reach
+    std::sort(ax, ax + 3, [](auto& x, auto& y) { return x.stride < y.stride; });
+    long extent = d;
+    for (auto& x : ax) {
+      if (x.size <= 1) continue;
+      if (x.stride < extent) return false;
+      extent += x.stride * (x.size - 1);
+    }
+  }
+  out->p = t->data;
+  out->seq = t->seq_stride;
+  out->row = t->row_stride;
+  out->head = t->head_stride;
+  out->dtype = t->dtype;
+  const long oct = 16 / es;
+  out->vec = reinterpret_cast<uintptr_t>(t->data) % 16 == 0 && t->seq_stride % oct == 0 && t->row_stride % oct == 0 &&
+             t->head_stride % oct == 0;
+  return true;
+}
+
+bool kv4_count(const g4_kv4* op, int n_seq) { return n_seq >= 1 && n_seq <= op->cfg.n_slots; }
+
+// A kernel for the handle's head dim.
+#define KV4_DISPATCH(d, ...)                         \
+  switch (d) {                                       \
+    case 64: { constexpr int D = 64; __VA_ARGS__; break; }    \
+    case 128: { constexpr int D = 128; __VA_ARGS__; break; }  \
+    case 256: { constexpr int D = 256; __VA_ARGS__; break; }  \
+    default: { constexpr int D = 512; __VA_ARGS__; break; }   \
+  }
+
+dim3 kv4_row_grid(const g4_kv4* op, int n_seq, int n_rows) {
+  const long threads = (long)n_rows * op->cfg.num_kv_heads * (op->cfg.head_dim / 8);
+  return dim3((unsigned)((threads + kKv4RowThreads - 1) / kKv4RowThreads), n_seq);
+}
+
+g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t st) {
+  const g4_kv4_config& f = op->cfg;
+  Kv4Cache& c = op->c;
+  c.n_slots = f.n_slots;
+  c.capacity = f.capacity;
+  c.kvh = f.num_kv_heads;
+  c.d = f.head_dim;
+  size_t blocks;
+  if (f.page_size) {
+    c.table = d_page_table;
+    c.bpp = f.page_size / kKv4Block;
+    c.log_bpp = log2i(c.bpp);
+    c.max_pages = cdiv(f.capacity, f.page_size);
+    c.n_pages = f.n_pages;
+    blocks = (size_t)f.n_pages * c.kvh * c.bpp;
+  } else {
+    c.bpp = cdiv(f.capacity, kKv4Block);
+    blocks = (size_t)f.n_slots * c.kvh * c.bpp;
+  }
+  TRY(kv4_alloc(op, &c.data, blocks * 18 * f.head_dim, st));
+  TRY(kv4_alloc(op, &c.err, 1, st));
+  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * f.max_q_len * f.num_q_heads, st));
+  if (f.track) {
+    TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
+    TRY(kv4_alloc(op, &c.weight, blocks * kKv4Block, st));
+    // at most half of a slot's rows move: a move takes an evicted row below the budget and a
+    // kept one beyond it
+    TRY(kv4_alloc(op, &op->holes, (size_t)f.n_slots * c.kvh * f.capacity, st));
+    TRY(kv4_alloc(op, &op->movers, (size_t)f.n_slots * c.kvh * f.capacity, st));
+    TRY(kv4_alloc(op, &op->n_moves, (size_t)f.n_slots * c.kvh, st));
+  }
+  return G4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_page_table, g4_kv4** out) {
+  if (!out) return G4_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!cfg) return G4_ERR_INVALID_ARG;
+  const g4_kv4_config f = *cfg;
+  if (f.n_slots < 1 || f.capacity < 1 || f.num_q_heads < 1 || f.num_kv_heads < 1 || f.max_q_len < 1 || f.page_size < 0 ||
+      f.track < 0 || f.track > 1)
+    return G4_ERR_INVALID_ARG;
+  if (f.num_q_heads % f.num_kv_heads) return G4_ERR_INVALID_ARG;
+  if (f.page_size ? (!d_page_table || f.n_pages < 1) : (d_page_table != nullptr)) return G4_ERR_INVALID_ARG;
+  if (f.n_slots > kKv4MaxSlots || f.capacity > (1 << 20) || f.num_kv_heads > 64 || f.max_q_len > 64 ||
+      f.num_q_heads / f.num_kv_heads > 64)
+    return G4_ERR_UNSUPPORTED;
+  if (f.head_dim != 64 && f.head_dim != 128 && f.head_dim != 256 && f.head_dim != 512) return G4_ERR_UNSUPPORTED;
+  if (f.page_size && (f.page_size < kKv4Block || f.page_size > (1 << 20) || (f.page_size & (f.page_size - 1)) || f.n_pages > (1 << 26)))
+    return G4_ERR_UNSUPPORTED;
+  DEVICE_GUARD(device);
+  g4_kv4* op = new (std::nothrow) g4_kv4();
+  if (!op) return G4_ERR_OOM;
+  op->cfg = f;
+  op->device = device;
+  g4_status s = G4_ERR_CUDA;
+  cudaStream_t st = nullptr;
+  if (cuda_ok(cudaDeviceGetAttribute(&op->sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
+      cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
+    s = kv4_create_impl(op, d_page_table, st);
+    if (!cuda_ok(cudaStreamSynchronize(st), "cudaStreamSynchronize") && s == G4_OK) s = G4_ERR_CUDA;
+    cudaStreamDestroy(st);
+  }
+  if (s != G4_OK) {
+    for (void* p : op->allocs) cudaFree(p);
+    delete op;
+    return s;
+  }
+  *out = op;
+  return G4_OK;
+}
+
+g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_start,
+                        const int32_t* d_counts, int32_t n_rows, const g4_kv4_tensor* k, const g4_kv4_tensor* v,
+                        const int32_t* d_positions, const float* d_weights) {
+  if (!op || !d_slots || !d_start || !k || !v || !kv4_count(op, n_seq) || n_rows < 1 || n_rows > op->cfg.capacity)
+    return G4_ERR_INVALID_ARG;
+  Kv4RowArgs a{};
+  if (!kv4_dense(k, n_seq, n_rows, op->c.kvh, op->c.d, false, &a.k) ||
+      !kv4_dense(v, n_seq, n_rows, op->c.kvh, op->c.d, false, &a.v))
+    return G4_ERR_INVALID_ARG;
+  if (!op->cfg.track && (d_positions || d_weights)) return G4_ERR_UNSUPPORTED;
+  DEVICE_GUARD(op->device);
+  a.c = op->c;
+  a.slots = d_slots;
+  a.start = d_start;
+  a.counts = d_counts;
+  a.n_rows = n_rows;
+  a.positions = d_positions;
+  a.weights = d_weights;
+  KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0,
+                               reinterpret_cast<cudaStream_t>(stream), a));
+  CK(cudaGetLastError());
+  return G4_OK;
+}
+
+g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_start,
+                      const int32_t* d_counts, int32_t n_rows, const g4_kv4_tensor* k, const g4_kv4_tensor* v) {
+  if (!op || !d_slots || !d_start || (!k && !v) || !kv4_count(op, n_seq) || n_rows < 1 || n_rows > op->cfg.capacity)
+    return G4_ERR_INVALID_ARG;
+  Kv4RowArgs a{};
+  if (!kv4_dense(k, n_seq, n_rows, op->c.kvh, op->c.d, true, &a.k) ||
+      !kv4_dense(v, n_seq, n_rows, op->c.kvh, op->c.d, true, &a.v))
+    return G4_ERR_INVALID_ARG;
+  DEVICE_GUARD(op->device);
+  a.c = op->c;
+  a.slots = d_slots;
+  a.start = d_start;
+  a.counts = d_counts;
+  a.n_rows = n_rows;
+  KV4_DISPATCH(op->c.d, launch(kv4_read_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0,
+                               reinterpret_cast<cudaStream_t>(stream), a));
+  CK(cudaGetLastError());
+  return G4_OK;
+}
+
+g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_start,
+                         const int32_t* d_counts, int32_t n_rows, int32_t* d_positions, float* d_weights) {
+  if (!op || !d_slots || !d_start || (!d_positions && !d_weights) || !kv4_count(op, n_seq) || n_rows < 1 ||
+      n_rows > op->cfg.capacity)
+    return G4_ERR_INVALID_ARG;
+  if (!op->cfg.track) return G4_ERR_UNSUPPORTED;
+  DEVICE_GUARD(op->device);
+  Kv4RowArgs a{};
+  a.c = op->c;
+  a.slots = d_slots;
+  a.start = d_start;
+  a.counts = d_counts;
+  a.n_rows = n_rows;
+  a.positions_out = d_positions;
+  a.weights_out = d_weights;
+  launch(kv4_account_kernel, dim3(cdiv(n_rows, kKv4RowThreads), n_seq, op->c.kvh), dim3(kKv4RowThreads), 0,
+         reinterpret_cast<cudaStream_t>(stream), a);
+  CK(cudaGetLastError());
+  return G4_OK;
+}
+
+g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_lens,
+                        int32_t q_len, const int32_t* d_q_lens, float scale, int32_t window, int32_t accumulate,
+                        const g4_kv4_tensor* q, const g4_kv4_tensor* out) {
+  if (!op || !d_slots || !d_lens || !q || !out || !kv4_count(op, n_seq) || q_len < 1 || q_len > op->cfg.max_q_len ||
+      window < 0 || !std::isfinite(scale) || q->dtype != out->dtype)
+    return G4_ERR_INVALID_ARG;
+  Kv4AttendArgs a{};
+  if (!kv4_dense(q, n_seq, q_len, op->cfg.num_q_heads, op->c.d, false, &a.q) ||
+      !kv4_dense(out, n_seq, q_len, op->cfg.num_q_heads, op->c.d, true, &a.out))
+    return G4_ERR_INVALID_ARG;
+  if ((accumulate && !op->cfg.track) || (window && op->cfg.track)) return G4_ERR_UNSUPPORTED;
+  DEVICE_GUARD(op->device);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  a.c = op->c;
+  a.slots = d_slots;
+  a.lens = d_lens;
+  a.q_lens = d_q_lens;
+  a.q_len = q_len;
+  a.heads = op->cfg.num_q_heads;
+  a.group = a.heads / op->c.kvh;
+  a.scale = scale != 0.f ? scale : (float)(1.0 / std::sqrt((double)op->c.d));
+  a.window = window;
+  a.accumulate = accumulate != 0;
+  a.lse = op->lse;
+  KV4_DISPATCH(op->c.d, {
+    launch(kv4_attend_kernel<D>, dim3(q_len * a.heads, n_seq), dim3(kKv4AttThreads), 0, st, a);
+    if (a.accumulate)
+      launch(kv4_gain_kernel<D>, dim3(std::min(cdiv(op->cfg.capacity, 4), 1024), n_seq, op->c.kvh), dim3(kKv4AttThreads),
+             0, st, a);
+  });
+  CK(cudaGetLastError());
+  return G4_OK;
+}
+
+g4_status g4_kv4_evict(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_lens,
+                       int32_t budget, int32_t recent, int32_t* d_new_lens) {
+  if (!op || !d_slots || !d_lens || !d_new_lens || d_new_lens == d_lens || !kv4_count(op, n_seq) || budget < 1 ||
+      budget > op->cfg.capacity || recent < 0 || recent > budget)
+    return G4_ERR_INVALID_ARG;
+  if (!op->cfg.track) return G4_ERR_UNSUPPORTED;
+  DEVICE_GUARD(op->device);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Kv4EvictArgs a{};
+  a.c = op->c;
+  a.slots = d_slots;
+  a.lens = d_lens;
+  a.budget = budget;
+  a.recent = recent;
+  a.new_lens = d_new_lens;
+  a.holes = op->holes;
+  a.movers = op->movers;
+  a.n_moves = op->n_moves;
+  launch(kv4_select_kernel, dim3(n_seq, op->c.kvh), dim3(kKv4EvictThreads), 0, st, a);
+  const int per = kKv4RowThreads / (op->c.d / 8);  // moves of a CTA at a time
+  KV4_DISPATCH(op->c.d, launch(kv4_move_kernel<D>, dim3(std::max(1, std::min(cdiv(budget, per), 64)), n_seq, op->c.kvh),
+                               dim3(kKv4RowThreads), 0, st, a));
+  CK(cudaGetLastError());
+  return G4_OK;
+}
+
+g4_status g4_kv4_get_device_error(g4_kv4* op, g4_stream stream, int32_t* word_out) {
+  if (!op) return G4_ERR_INVALID_ARG;
+  DEVICE_GUARD(op->device);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int w = 0;
+  CK(cudaMemcpyAsync(&w, op->c.err, sizeof(int), cudaMemcpyDeviceToHost, st));
+  CK(cudaMemsetAsync(op->c.err, 0, sizeof(int), st));
+  CK(cudaStreamSynchronize(st));
+  if (word_out) *word_out = w;
+  if (w & G4_DEV_TIMEOUT) return G4_ERR_TIMEOUT;
+  return w ? G4_ERR_DEVICE_CHECK : G4_OK;
+}
+
+int64_t g4_kv4_bytes(const g4_kv4* op) { return op ? (int64_t)op->bytes : 0; }
+
+void g4_kv4_free(g4_kv4* op) {
+  if (!op) return;
+  DeviceGuard dg(op->device);
+  cudaDeviceSynchronize();
+  for (void* p : op->allocs) cudaFree(p);
+  delete op;
+}
+
+}  // extern "C"

@@ -27,6 +27,10 @@ G4_DEV_BAD_TOKEN = 1
 G4_DEV_BAD_POSITION = 2
 G4_DEV_TIMEOUT = 4
 G4_DEV_BAD_SLOT = 8
+G4_DEV_BAD_VALUE = 16
+G4_DT_F32 = 0
+G4_DT_BF16 = 1
+G4_DT_F16 = 2
 
 _INT_FIELDS = ("num_layers", "num_kv_shared_layers", "hidden", "num_q_heads", "num_kv_heads",
                "head_dim_sliding", "head_dim_full", "sliding_window", "full_every", "mlp",
@@ -64,6 +68,16 @@ class g4_weights(ctypes.Structure):
 class g4_phase_stat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", c_int32), ("ms_total", ctypes.c_double),
                 ("bytes_total", ctypes.c_double)]
+
+
+class g4_kv4_config(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("n_slots", "capacity", "num_q_heads", "num_kv_heads", "head_dim",
+                                       "max_q_len", "page_size", "n_pages", "track")]
+
+
+class g4_kv4_tensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("dtype", c_int32), ("seq_stride", c_int64), ("row_stride", c_int64),
+                ("head_stride", c_int64)]
 
 
 class G4Error(RuntimeError):
@@ -106,6 +120,17 @@ def _load():
         "g4_linear_free": (None, [P]),
         "g4_argmax_rows": (c_int, [c_int, P, c_int32, c_int32, P, P]),
         "g4_argmax_rows_static": (c_int, [c_int, P, c_int32, c_int32, P, P]),
+        "g4_kv4_create": (c_int, [c_int, POINTER(g4_kv4_config), P, POINTER(P)]),
+        "g4_kv4_append": (c_int, [P, P, c_int32, P, P, P, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor),
+                                  P, P]),
+        "g4_kv4_read": (c_int, [P, P, c_int32, P, P, P, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor)]),
+        "g4_kv4_account": (c_int, [P, P, c_int32, P, P, P, c_int32, P, P]),
+        "g4_kv4_attend": (c_int, [P, P, c_int32, P, P, c_int32, P, c_float, c_int32, c_int32, POINTER(g4_kv4_tensor),
+                                  POINTER(g4_kv4_tensor)]),
+        "g4_kv4_evict": (c_int, [P, P, c_int32, P, P, c_int32, c_int32, P]),
+        "g4_kv4_get_device_error": (c_int, [P, P, POINTER(c_int32)]),
+        "g4_kv4_bytes": (c_int64, [P]),
+        "g4_kv4_free": (None, [P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -57,7 +57,13 @@ enum { G4_BF16 = 0, G4_W4A16 = 1 };
 enum { G4_KV_BF16 = 0, G4_KV_INT8 = 1 };
 
 /* Device error word bits (g4_get_device_error). */
-enum { G4_DEV_BAD_TOKEN = 1, G4_DEV_BAD_POSITION = 2, G4_DEV_TIMEOUT = 4, G4_DEV_BAD_SLOT = 8 };
+enum {
+  G4_DEV_BAD_TOKEN = 1,
+  G4_DEV_BAD_POSITION = 2,
+  G4_DEV_TIMEOUT = 4,
+  G4_DEV_BAD_SLOT = 8,
+  G4_DEV_BAD_VALUE = 16 /* a key or value that is not finite (g4_kv4_append) */
+};
 
 /* Model shape and the numeric constants the pages leave open (every one is a field).
  * Layer l is "full" iff l % full_every == full_every - 1, else "sliding" ("4 sliding, 1 full,
@@ -295,6 +301,128 @@ g4_status g4_argmax_rows(int device, g4_stream stream, int32_t n_rows, int32_t n
  * threads) race on it and must be serialised by the caller. */
 g4_status g4_argmax_rows_static(int device, g4_stream stream, int32_t n_rows, int32_t n_cols,
                                 const float* d_logits, int32_t* d_ids);
+
+/* ----------------------------------------------------------------------------------------
+ * A KV cache held in 4 bits, with the attention that reads it and the eviction of rows.
+ *
+ * One g4_kv4 holds the rows of one layer.  A row of one KV head is a key and a value of
+ * head_dim numbers; each group of 32 numbers is held in the linears' int4 convention, signed
+ * codes under one bf16 scale: s = bf16(max|x| / 7), c = round-half-even(x / s) clipped to +-7,
+ * standing for the value bf16(c * s) (a group of zeros has s = 0).  A row of one KV head takes
+ * 9/8 head_dim bytes, key and value together (head_dim 256: 288, in bf16 1,024).
+ *
+ * Rows live in slots, row 0 .. capacity - 1 each: at fixed places (page_size 0), or in pages of
+ * page_size rows: row r of slot s is row r % page_size of page table[s][r / page_size].  The
+ * caller keeps each slot's number of rows and passes it to the calls (device arrays, so that a
+ * step needs no synchronisation and can be captured into a graph).  Row order is free except
+ * that a sequence's newest q_len rows are its query tokens' own (g4_kv4_attend).
+ *
+ * Errors of one sequence that only the device can see (a slot out of range or named twice where
+ * the call writes; rows outside the capacity; a page that is missing or outside the pool; a
+ * count outside its bound) set the op's device error word and that sequence is skipped: its
+ * rows, account and outputs stay as they were, except that g4_kv4_attend gives zeros.  A missing
+ * page costs only its rows: they are not written, not read, and not seen by the attention.
+ *
+ * The handle holds one workspace: calls on one g4_kv4 (captured graphs that hold such calls
+ * included) must be ordered by the caller, on one stream or by events.  No call after
+ * g4_kv4_create allocates or synchronises, except g4_kv4_get_device_error and g4_kv4_free.
+ * --------------------------------------------------------------------------------------*/
+
+typedef struct g4_kv4 g4_kv4;
+
+enum { G4_DT_F32 = 0, G4_DT_BF16 = 1, G4_DT_F16 = 2 };
+
+typedef struct g4_kv4_config {
+  int32_t n_slots;      /* 1..1024 */
+  int32_t capacity;     /* rows per slot, 1..1048576 */
+  int32_t num_q_heads;  /* a multiple of num_kv_heads, at most 64 per KV head */
+  int32_t num_kv_heads; /* 1..64; query heads h * G .. h * G + G - 1 read KV head h */
+  int32_t head_dim;     /* 64, 128, 256 or 512 */
+  int32_t max_q_len;    /* query tokens per sequence and call, 1..64 */
+  int32_t page_size;    /* 0: fixed places; else a power of two >= 16 */
+  int32_t n_pages;      /* pages of the pool (page_size > 0) */
+  int32_t track;        /* 1: every row carries its position and accumulated attention weight */
+} g4_kv4_config;
+
+/* A dense tensor [sequences][rows][heads][head_dim] on the device; strides in elements, head_dim
+ * contiguous.  Tensors that are written must not overlap themselves. */
+typedef struct g4_kv4_tensor {
+  void* data;
+  int32_t dtype; /* G4_DT_* */
+  int64_t seq_stride, row_stride, head_stride;
+} g4_kv4_tensor;
+
+/* Make an empty cache on `device`.  d_page_table: int32 [n_slots][ceil(capacity / page_size)],
+ * BORROWED (read by every call on its stream; entries outside 0 .. n_pages - 1 mean no page;
+ * pages of a slot that is appended to or evicted from must be its own), NULL with page_size 0.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes outside the bounds above), OOM, CUDA. */
+g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_page_table,
+                        g4_kv4** out);
+
+/* Code rows into the cache: for sequence i, rows t < d_counts[i] (NULL: n_rows) of k and v
+ * [n_seq][n_rows][num_kv_heads][head_dim] become rows d_start[i] + t of slot d_slots[i], in
+ * place of what was there.  A number that is not finite sets G4_DEV_BAD_VALUE and is stored as
+ * 0 (NaN) or as the largest finite number of its sign.  With track, the rows' positions and
+ * accumulated weights become d_positions and d_weights [n_seq][num_kv_heads][n_rows] (NULL: the
+ * row index, and 0); without it both must be NULL.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows outside 1..capacity, NULL or malformed
+ * tensors), UNSUPPORTED (positions or weights without track). */
+g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                        const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
+                        const g4_kv4_tensor* k, const g4_kv4_tensor* v,
+                        const int32_t* d_positions, const float* d_weights);
+
+/* Give rows back as the values they stand for, the inverse addressing of g4_kv4_append (k or v
+ * may be NULL, not both).  Rows at and beyond d_counts[i] are left as they were.
+ * Errors: INVALID_ARG. */
+g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                      const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
+                      const g4_kv4_tensor* k, const g4_kv4_tensor* v);
+
+/* Positions and accumulated weights of rows, [n_seq][num_kv_heads][n_rows] (either may be NULL,
+ * not both).  Errors: INVALID_ARG, UNSUPPORTED (a cache without track). */
+g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                         const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
+                         int32_t* d_positions, float* d_weights);
+
+/* Softmax attention of q_len query tokens per sequence over rows 0 .. d_lens[i] - 1 of its slot,
+ * the sequence's own newest rows included: with m = d_q_lens[i] (NULL: q_len) query tokens,
+ * token t sits at row d_lens[i] - m + t and sees rows up to its own (and with window > 0 only
+ * the newest `window` of those):
+ *   s_j = scale * q . K_j        o = sum_j softmax(s)_j V_j        (scale 0: 1/sqrt(head_dim))
+ * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type.  A token that sees no row gets
+ * zeros; query rows t >= m of `out` are left as they were.  accumulate != 0 (track, window 0):
+ * each row's account grows by the attention weights it received, summed over the sequence's
+ * query tokens and the query heads of its KV head.  The same slot may be named twice only
+ * without accumulate.  The sums run in a fixed order: equal calls give equal bits.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0,
+ * a scale that is not finite, q and out of different types, malformed tensors), UNSUPPORTED
+ * (accumulate without track; a window with a cache that tracks: after an eviction its rows are
+ * no longer in position order). */
+g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                        const int32_t* d_lens, int32_t q_len, const int32_t* d_q_lens, float scale,
+                        int32_t window, int32_t accumulate, const g4_kv4_tensor* q,
+                        const g4_kv4_tensor* out);
+
+/* Cut slots back to `budget` rows per KV head (track): of rows 0 .. d_lens[i] - 1 the ones at the
+ * newest `recent` positions (position > newest - recent) are kept first, then those with the
+ * largest accumulated weight (a NaN ranks last), equal ones by the lowest row.  Kept rows below
+ * the budget stay where they are; the kept rows from beyond it move, in row order, into the
+ * places of the evicted rows below it, in row order, each with its position and account.
+ * d_new_lens[i] = min(d_lens[i], budget); it must not be d_lens.  KV heads choose for themselves.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, budget outside 1..capacity, recent outside
+ * 0..budget, NULL, d_new_lens == d_lens), UNSUPPORTED (a cache without track). */
+g4_status g4_kv4_evict(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                       const int32_t* d_lens, int32_t budget, int32_t recent, int32_t* d_new_lens);
+
+/* Synchronise `stream`, read and clear the op's device error word (as g4_get_device_error). */
+g4_status g4_kv4_get_device_error(g4_kv4* op, g4_stream stream, int32_t* word_out);
+
+/* Bytes of device memory the op owns. */
+int64_t g4_kv4_bytes(const g4_kv4* op);
+
+/* Release everything the op owns (after synchronising its device).  NULL is a no-op. */
+void g4_kv4_free(g4_kv4* op);
 
 #ifdef __cplusplus
 }
