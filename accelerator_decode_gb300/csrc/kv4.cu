@@ -19,7 +19,10 @@ struct g4_kv4 {
   Kv4Cache c{};
   std::vector<void*> allocs;
   size_t bytes = 0;
-  float* lse = nullptr;                       // [n_slots][max_q_len][num_q_heads]
+  float* lse = nullptr;                       // [n_slots][kvh][row tiles * 8]
+  float4* part_o = nullptr;                   // partial sums of the spans (kv4_attend.cuh)
+  float2* part_ml = nullptr;
+  int smem_optin = 0;
   int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
   int* n_moves = nullptr;                     // [n_slots][kvh]
 };
@@ -91,6 +94,60 @@ bool kv4_count(const g4_kv4* op, int n_seq) { return n_seq >= 1 && n_seq <= op->
     default: { constexpr int D = 512; __VA_ARGS__; break; }   \
   }
 
+#define KV4_DISPATCH_TYPE(dt, ...)                                       \
+  switch (dt) {                                                          \
+    case G4_DT_F32: { constexpr int DT = G4_DT_F32; __VA_ARGS__; break; }   \
+    case G4_DT_F16: { constexpr int DT = G4_DT_F16; __VA_ARGS__; break; }   \
+    default: { constexpr int DT = G4_DT_BF16; __VA_ARGS__; break; }         \
+  }
+
+std::mutex g_kv4_mu;
+std::set<int> g_kv4_devices;  // devices whose kernels have their shared-memory limit set
+template <int D, int DT>
+void kv4_attrs(int optin) {
+  set_max_dyn(kv4_attend_kernel<D, DT>, optin);
+  set_max_dyn(kv4_gain_kernel<D, DT>, optin);
+  carve_max(kv4_join_kernel<D, Kv4Att<D, DT>::kKeys>);
+}
+template <int D>
+void kv4_attrs_d(int optin) {
+  kv4_attrs<D, G4_DT_F32>(optin);
+  kv4_attrs<D, G4_DT_BF16>(optin);
+  kv4_attrs<D, G4_DT_F16>(optin);
+  carve_max(kv4_append_kernel<D>);
+  carve_max(kv4_read_kernel<D>);
+  carve_max(kv4_move_kernel<D>);
+}
+void kv4_init(int device, int optin) {
+  std::lock_guard<std::mutex> lk(g_kv4_mu);
+  if (!g_kv4_devices.insert(device).second) return;
+  kv4_attrs_d<64>(optin);
+  kv4_attrs_d<128>(optin);
+  kv4_attrs_d<256>(optin);
+  kv4_attrs_d<512>(optin);
+  carve_max(kv4_account_kernel);
+  carve_max(kv4_select_kernel);
+  cudaGetLastError();
+}
+int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads), 8); }
+
+template <int D, int DT>
+void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
+  using C = Kv4Att<D, DT>;
+  const int ctas = op->sms * C::kMinCtas;
+  // the ring takes what shared memory the CTAs of an SM leave each other (1 KB each is the system's)
+  const int room = (op->smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
+  a.stages = std::max(2, std::min(4, room / C::kTile));
+  a.min_tiles = 1;
+  launch(kv4_attend_kernel<D, DT>, dim3(ctas), dim3(C::kThreads), C::smem(a.stages, a.n_seq), st, a);
+  const int items = a.n_seq * a.c.kvh * a.row_tiles;
+  launch(kv4_join_kernel<D, C::kKeys>, dim3(items, std::max(1, D * 2 / kKv4JoinThreads)), dim3(kKv4JoinThreads),
+         ((size_t)a.n_seq + 1) * 8, st, a, ctas);
+  if (a.accumulate)
+    launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(op->cfg.capacity, 64), 8 * op->sms / a.n_seq)), a.n_seq, a.c.kvh),
+           dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
+}
+
 dim3 kv4_row_grid(const g4_kv4* op, int n_seq, int n_rows) {
   const long threads = (long)n_rows * op->cfg.num_kv_heads * (op->cfg.head_dim / 8);
   return dim3((unsigned)((threads + kKv4RowThreads - 1) / kKv4RowThreads), n_seq);
@@ -117,7 +174,10 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   }
   TRY(kv4_alloc(op, &c.data, blocks * 18 * f.head_dim, st));
   TRY(kv4_alloc(op, &c.err, 1, st));
-  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * f.max_q_len * f.num_q_heads, st));
+  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len) * 8, st));
+  const size_t parts = (size_t)2 * op->sms * 3;  // at most three CTAs per SM, two partial items each
+  TRY(kv4_alloc(op, &op->part_o, parts * (f.head_dim * 2), st));
+  TRY(kv4_alloc(op, &op->part_ml, parts * 8, st));
   if (f.track) {
     TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
     TRY(kv4_alloc(op, &c.weight, blocks * kKv4Block, st));
@@ -158,7 +218,9 @@ g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_p
   g4_status s = G4_ERR_CUDA;
   cudaStream_t st = nullptr;
   if (cuda_ok(cudaDeviceGetAttribute(&op->sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
+      cuda_ok(cudaDeviceGetAttribute(&op->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
+    kv4_init(device, op->smem_optin);
     s = kv4_create_impl(op, d_page_table, st);
     if (!cuda_ok(cudaStreamSynchronize(st), "cudaStreamSynchronize") && s == G4_OK) s = G4_ERR_CUDA;
     cudaStreamDestroy(st);
@@ -254,19 +316,18 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.slots = d_slots;
   a.lens = d_lens;
   a.q_lens = d_q_lens;
+  a.n_seq = n_seq;
   a.q_len = q_len;
   a.heads = op->cfg.num_q_heads;
   a.group = a.heads / op->c.kvh;
-  a.scale = scale != 0.f ? scale : (float)(1.0 / std::sqrt((double)op->c.d));
+  a.row_tiles = kv4_row_tiles(op, q_len);
+  a.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)op->c.d)) * 1.4426950408889634);
   a.window = window;
   a.accumulate = accumulate != 0;
   a.lse = op->lse;
-  KV4_DISPATCH(op->c.d, {
-    launch(kv4_attend_kernel<D>, dim3(q_len * a.heads, n_seq), dim3(kKv4AttThreads), 0, st, a);
-    if (a.accumulate)
-      launch(kv4_gain_kernel<D>, dim3(std::min(cdiv(op->cfg.capacity, 4), 1024), n_seq, op->c.kvh), dim3(kKv4AttThreads),
-             0, st, a);
-  });
+  a.part_o = op->part_o;
+  a.part_ml = op->part_ml;
+  KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op, a, st))));
   CK(cudaGetLastError());
   return G4_OK;
 }

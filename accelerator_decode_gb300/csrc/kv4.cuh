@@ -2,7 +2,9 @@
 //
 // A row of one KV head is a key and a value of D numbers.  Each group of 32 numbers is held as
 // signed 4-bit codes under one bf16 scale, the convention of the W4A16 weights:
-//   s = bf16(max|x| / 7)     c = round-half-even(x / s) clipped to +-7     value = bf16(c * s)
+//   s = bf16(max|x| * (1/7))     c = round-half-even(x / s) clipped to +-7     value = bf16(c * s)
+// (1/7 and its product in fp32: a group whose exact quotient lies within an fp32 rounding of the
+// middle between two bf16 numbers, about one in 100,000, may take the other one as its scale)
 // so a row takes 2 (D/2 + D/16) bytes (D = 256: 288, against 1,024 in bf16 and 520 in int8).
 // Every value is finite by construction (append replaces what is not finite), so a row that a
 // mask hides can be multiplied by a zero weight without turning the sum into a NaN.
@@ -28,22 +30,22 @@ __device__ __forceinline__ void kv4_load8(const Kv4Dense& x, long off, float (&v
   if (x.dtype == G4_DT_F32) {
     const float* p = reinterpret_cast<const float*>(x.p) + off;
     if (x.vec) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
       v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __ldg(p + e);
+      for (int e = 0; e < 8; ++e) v[e] = __ldcg(p + e);
     }
     return;
   }
   uint32_t u[4];
   const uint16_t* p = reinterpret_cast<const uint16_t*>(x.p) + off;
   if (x.vec) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p));
     u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = (uint32_t)__ldg(p + 2 * e) | ((uint32_t)__ldg(p + 2 * e + 1) << 16);
+    for (int e = 0; e < 4; ++e) u[e] = (uint32_t)__ldcg(p + 2 * e) | ((uint32_t)__ldcg(p + 2 * e + 1) << 16);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -94,11 +96,31 @@ __device__ __forceinline__ void kv4_store8(const Kv4Dense& x, long off, const fl
   }
 }
 
+__device__ __forceinline__ void kv4_store4(const Kv4Dense& x, long off, float4 v) {
+  if (x.dtype == G4_DT_F32) {
+    float* p = reinterpret_cast<float*>(x.p) + off;
+    if (x.vec) {
+      *reinterpret_cast<float4*>(p) = v;
+    } else {
+      p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+    }
+    return;
+  }
+  const uint32_t a = kv4_pack2(x.dtype, v.x, v.y), b = kv4_pack2(x.dtype, v.z, v.w);
+  uint16_t* p = reinterpret_cast<uint16_t*>(x.p) + off;
+  if (x.vec) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+  } else {
+    p[0] = (uint16_t)a; p[1] = (uint16_t)(a >> 16); p[2] = (uint16_t)b; p[3] = (uint16_t)(b >> 16);
+  }
+}
+
 // -------------------------------------------------------------------------- one group
-// Scale of a group from its largest magnitude.  The largest scale whose 7-fold is still a
-// finite bf16 bounds it.
+// Scale of a group from its largest magnitude: one fp32 product (an IEEE division costs about
+// ten instructions and buys nothing: any scale this near serves the codes as well).  The
+// largest scale whose 7-fold is still a finite bf16 bounds it.
 __device__ __forceinline__ __nv_bfloat16 kv4_scale(float amax) {
-  return __float2bfloat16_rn(fminf(amax / 7.f, 4.8301e37f));
+  return __float2bfloat16_rn(fminf(__fmul_rn(amax, 1.f / 7.f), 4.8301e37f));
 }
 // Code of x under scale s: round-half-even(x / s) clipped to +-7, exactly.  A quotient in 32
 // bits may round onto a border (c + 1/2) s from either side, so a first guess is corrected
@@ -125,7 +147,7 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t scale2) {
 // Does any earlier entry name the same slot as entry i?  (block-wide; every thread calls it)
 __device__ __forceinline__ bool kv4_repeated(const int* slots, int i, int slot) {
   int hit = 0;
-  for (int j = threadIdx.x; j < i; j += blockDim.x) hit |= __ldg(slots + j) == slot;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) hit |= __ldcg(slots + j) == slot;
   return __syncthreads_or(hit) != 0;
 }
 
@@ -143,9 +165,9 @@ struct Kv4RowArgs {
 // Rows [row0, row0 + count) of sequence i, after its checks; count 0 when it is skipped.
 // writes: a slot that an earlier sequence of the call names is skipped too (block-wide).
 __device__ __forceinline__ bool kv4_rows_of(const Kv4RowArgs& a, int i, bool writes, int* slot, int* row0, int* count) {
-  *slot = __ldg(a.slots + i);
-  *row0 = __ldg(a.start + i);
-  *count = a.counts ? __ldg(a.counts + i) : a.n_rows;
+  *slot = __ldcg(a.slots + i);
+  *row0 = __ldcg(a.start + i);
+  *count = a.counts ? __ldcg(a.counts + i) : a.n_rows;
   int bad = 0;
   if (*slot < 0 || *slot >= a.c.n_slots) bad = G4_DEV_BAD_SLOT;
   else if (*count < 0 || *count > a.n_rows || *row0 < 0 || *row0 > a.c.capacity - *count) bad = G4_DEV_BAD_POSITION;
@@ -221,8 +243,8 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
   if (odd_value) set_err(a.c.err, G4_DEV_BAD_VALUE);
   if (o == 0 && a.c.pos && b >= 0) {
     const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
-    a.c.pos[b * kKv4Block + r] = a.positions ? __ldg(a.positions + at) : row;
-    a.c.weight[b * kKv4Block + r] = a.weights ? __ldg(a.weights + at) : 0.f;
+    a.c.pos[b * kKv4Block + r] = a.positions ? __ldcg(a.positions + at) : row;
+    a.c.weight[b * kKv4Block + r] = a.weights ? __ldcg(a.weights + at) : 0.f;
   }
 }
 
@@ -249,8 +271,8 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_read_kernel(const Kv4RowAr
   const uint8_t* blk = a.c.data + (size_t)b * O::kBlock;
   float v[8];
   if (a.k.p) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(blk + O::k_word(r, o)));
-    const uint32_t s = 0x10001u * __ldg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(r, o >> 2)));
+    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(blk + O::k_word(r, o)));
+    const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(r, o >> 2)));
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const uint32_t x = kv4_pair(w >> (4 * p), s);
@@ -260,10 +282,10 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_read_kernel(const Kv4RowAr
     kv4_store8(a.k, i * a.k.seq + t * a.k.row + h * a.k.head + 8 * o, v);
   }
   if (a.v.p) {
-    const uint32_t s = 0x10001u * __ldg(reinterpret_cast<const uint16_t*>(blk + O::v_scale(r, o >> 2)));
+    const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_scale(r, o >> 2)));
     uint32_t w[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) w[u] = __ldg(reinterpret_cast<const uint16_t*>(blk + O::v_half(r, 2 * o + u)));
+    for (int u = 0; u < 2; ++u) w[u] = __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_half(r, 2 * o + u)));
     const uint32_t x01 = w[0] | (w[1] << 16);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -346,7 +368,7 @@ __global__ void __launch_bounds__(kKv4EvictThreads) kv4_select_kernel(const Kv4E
   const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int slot = __ldg(a.slots + i), len = __ldg(a.lens + i);
+  const int slot = __ldcg(a.slots + i), len = __ldcg(a.lens + i);
   int* n_moves = a.n_moves + (size_t)i * a.c.kvh + h;
   int bad = 0;
   if (slot < 0 || slot >= a.c.n_slots) bad = G4_DEV_BAD_SLOT;
@@ -441,7 +463,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_move_kernel(const Kv4Evict
   const size_t ih = (size_t)i * a.c.kvh + h;
   const int n = __ldcg(a.n_moves + ih), o = threadIdx.x % NO;
   for (int m = (blockIdx.x * kKv4RowThreads + threadIdx.x) / NO; m < n; m += gridDim.x * kKv4RowThreads / NO) {
-    const int slot = __ldg(a.slots + i);
+    const int slot = __ldcg(a.slots + i);
     const int src = __ldcg(a.movers + ih * a.budget + m), dst = __ldcg(a.holes + ih * a.budget + m);
     const long sb = kv4_block(a.c, slot, h, src / kKv4Block), db = kv4_block(a.c, slot, h, dst / kKv4Block);
     const uint8_t* sp = a.c.data + (size_t)sb * O::kBlock;

@@ -2,185 +2,654 @@
 //
 //   s_j = scale q . K_j      o = sum_j softmax(s)_j V_j      account_j += sum over (t, head) softmax(s)_j
 // for the rows j that query token t sees: j <= len - m + t, and j > len - m + t - window.
+//
+// Work: an item is eight query rows (query token x head, all of one KV head) against the rows
+// of their sequence.  All items' key tiles, laid end to end, are cut into equal spans, one per
+// CTA, so a ragged batch or a single long sequence fills the GPU alike; a span's first and last
+// item may be shared with the neighbouring CTAs, which leave partial sums for kv4_join_kernel.
+//
+// Per CTA one producer warp streams key tiles into a shared-memory ring with bulk copies; each
+// consumer warp takes whole blocks of 16 keys through scores, running softmax and output with
+// no synchronisation with the other warps until the item ends.  Both products run on the tensor
+// cores with the cache as the M operand (m16n8k16: 16 keys, or 16 numbers of the value, by 8
+// query rows), so eight query rows waste nothing and 4-bit codes go from a 16-byte load to the
+// operand registers through two ALU operations and two bf16 operations per pair.
 #pragma once
 #include "kv4.cuh"
+#include "mbar.cuh"
 
 namespace g4 {
 
 struct Kv4AttendArgs {
   Kv4Cache c;
   const int *slots, *lens, *q_lens;  // q_lens may be NULL
-  int q_len, heads, group;           // group: query heads per KV head
-  float scale;
+  int n_seq, q_len, heads, group;    // group: query heads per KV head
+  int row_tiles;                     // items of a (sequence, KV head): ceil(q_len * group / 8)
+  float scale;                       // times log2(e)
   int window, accumulate;
+  int min_tiles;                     // a CTA's span is at least this many tiles
+  int stages;
   Kv4Dense q, out;
-  float* lse;                        // [n_seq][q_len][heads], log2 of the softmax's sum
+  float* lse;                        // [n_seq][kvh][row_tiles * 8]: log2 of the softmax's sum
+  float4* part_o;                    // [2 * CTAs][D / 32][2][32]: a span's partial first and last item
+  float2* part_ml;                   // [2 * CTAs][8]: running maximum (log2 units) and sum
 };
 
 // Sequence i's slot, rows and query tokens; false (uniform over the block) when it is skipped.
 __device__ __forceinline__ bool kv4_seq(const Kv4AttendArgs& a, int i, int* slot, int* len, int* m) {
-  *slot = __ldg(a.slots + i);
-  *len = __ldg(a.lens + i);
-  *m = a.q_lens ? __ldg(a.q_lens + i) : a.q_len;
-  int bad = 0;
-  if (*slot < 0 || *slot >= a.c.n_slots) bad = G4_DEV_BAD_SLOT;
-  else if (*len < 0 || *len > a.c.capacity || *m < 0 || *m > a.q_len) bad = G4_DEV_BAD_POSITION;
-  if (a.accumulate && kv4_repeated(a.slots, i, *slot)) bad |= G4_DEV_BAD_SLOT;
-  if (bad && threadIdx.x == 0) set_err(a.c.err, bad);
-  return bad == 0;
+  *slot = __ldcg(a.slots + i);
+  *len = __ldcg(a.lens + i);
+  *m = a.q_lens ? __ldcg(a.q_lens + i) : a.q_len;
+  return *slot >= 0 && *slot < a.c.n_slots && *len >= 0 && *len <= a.c.capacity && *m >= 0 && *m <= a.q_len;
+}
+// Error bits of a skipped sequence.
+__device__ __forceinline__ int kv4_seq_error(const Kv4AttendArgs& a, int slot) {
+  return slot < 0 || slot >= a.c.n_slots ? G4_DEV_BAD_SLOT : G4_DEV_BAD_POSITION;
 }
 
-constexpr int kKv4AttThreads = 128;
-
-// Octet o of a key / value row as fp32.
-template <int D>
-__device__ __forceinline__ void kv4_k8(const uint8_t* blk, int r, int o, float (&v)[8]) {
-  using O = Kv4Off<D>;
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(blk + O::k_word(r, o)));
-  const uint32_t s = 0x10001u * __ldg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(r, o >> 2)));
+__device__ __forceinline__ void named_bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float kv4_exp2(float x) {  // 2^x, relative error 2^-22; 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16)
+__device__ __forceinline__ void kv4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t kv4_transpose(uint32_t x) {  // 8 x 8 matrix of 16-bit numbers
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// x = the bf16 numbers of `parts` registers added up: the first takes x's top 8 bits, each next
+// one 8 of the rest.  bf16 queries need one part, fp16 two (11 bits), fp32 three (24 bits); a
+// softmax weight two (2^-17 of it, against an output rounded at 2^-9 or 2^-12) or, for fp32
+// outputs, three.
+template <int PARTS>
+__device__ __forceinline__ void kv4_split(float x, float y, uint32_t (&p)[PARTS]) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint32_t x = kv4_pair(w >> (4 * p), s);
-    v[2 * p] = bf16_lo(x);
-    v[2 * p + 1] = bf16_hi(x);
+  for (int i = 0; i < PARTS; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    p[i] = as_u32(h);
+    if (i + 1 < PARTS) {
+      x -= bf16_lo(p[i]);
+      y -= bf16_hi(p[i]);
+    }
   }
 }
-template <int D>
-__device__ __forceinline__ void kv4_v8(const uint8_t* blk, int r, int o, float (&v)[8]) {
-  using O = Kv4Off<D>;
-  const uint32_t s = 0x10001u * __ldg(reinterpret_cast<const uint16_t*>(blk + O::v_scale(r, o >> 2)));
-  uint32_t w[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) w[u] = __ldg(reinterpret_cast<const uint16_t*>(blk + O::v_half(r, 2 * o + u)));
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint32_t x = kv4_pair((w[0] | (w[1] << 16)) >> (4 * p), s);
-    v[p] = bf16_lo(x);
-    v[4 + p] = bf16_hi(x);
-  }
-}
 
-// One CTA per (query token and head, sequence); a warp takes every fourth key, its lanes the
-// octets of the row, with a running maximum and sum per warp.
-template <int D>
-__global__ void __launch_bounds__(kKv4AttThreads) kv4_attend_kernel(const Kv4AttendArgs a) {
-  using O = Kv4Off<D>;
-  constexpr int OL = D > 256 ? D / 256 : 1;  // octets per lane
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int i = blockIdx.y, t = blockIdx.x / a.heads, hq = blockIdx.x % a.heads, h = hq / a.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  pdl_trigger();
-  int slot, len, m;
-  const bool ok = kv4_seq(a, i, &slot, &len, &m);
-  if (ok && t >= m) return;
-  const int row = ok ? len - m + t : -1;
-  const int lo = a.window > 0 ? max(0, row - a.window + 1) : 0;
-  float q[OL][8], acc[OL][8], mx = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < OL; ++e) {
-    const int o = lane + 32 * e;
-    if (o < D / 8) kv4_load8(a.q, i * a.q.seq + t * a.q.row + hq * a.q.head + 8 * o, q[e]);
-    else
-#pragma unroll
-      for (int x = 0; x < 8; ++x) q[e][x] = 0.f;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) acc[e][x] = 0.f;
+template <int D, int DT>
+struct Kv4Att {
+  static constexpr int kQP = DT == G4_DT_F32 ? 3 : DT == G4_DT_F16 ? 2 : 1;  // parts of a query
+  static constexpr int kPP = DT == G4_DT_F32 ? 3 : 2;                       // parts of a weight
+  static constexpr int kWarps = D == 512 ? 8 : 4;      // consumer warps
+  static constexpr int kSets = kWarps / 4;             // sets of four warps take tiles in turn
+  static constexpr int kBpw = D >= 256 ? 1 : 256 / D;  // blocks a warp takes of a tile
+  static constexpr int kBlocks = 4 * kBpw;             // blocks of a tile
+  static constexpr int kKeys = kBlocks * kKv4Block;    // keys of a tile: 256, 128, 64, 64
+  static constexpr int kTile = kBlocks * 18 * D;       // bytes of a tile: 18 KB (D = 512: 36 KB)
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;
+  static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
+  static constexpr int kOBytes = 4 * D * 32;           // four warps' sums, [warp][D / 32][2][lane] float4
+  static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
+  static __host__ __device__ size_t smem(int stages, int n_seq) {
+    return (size_t)stages * kTile + kFixed + ((size_t)n_seq + 1) * 8;
   }
-  for (int j = lo + warp; j <= row; j += 4) {
-    const long b = kv4_block(a.c, slot, h, j / kKv4Block);
-    if (b < 0) {
-      if (lane == 0) set_err(a.c.err, G4_DEV_BAD_POSITION);
-      continue;
-    }
-    const uint8_t* blk = a.c.data + (size_t)b * O::kBlock;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < OL; ++e) {
-      const int o = lane + 32 * e;
-      if (o < D / 8) {
-        float k[8];
-        kv4_k8<D>(blk, j % kKv4Block, o, k);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) s += q[e][x] * k[x];
-      }
-    }
-    s = warp_sum(s) * a.scale * 1.4426950408889634f;
-    const float mn = fmaxf(mx, s), al = exp2f(mx - mn), p = exp2f(s - mn);
-    mx = mn;
-    sum = sum * al + p;
-#pragma unroll
-    for (int e = 0; e < OL; ++e) {
-      const int o = lane + 32 * e;
-      if (o < D / 8) {
-        float v[8];
-        kv4_v8<D>(blk, j % kKv4Block, o, v);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) acc[e][x] = acc[e][x] * al + p * v[x];
-      }
-    }
+};
+
+// first[i] = key tiles of all items of sequences before i (n_seq + 1 entries, by the whole block):
+// sequence i has kvh * row_tiles items of the same number of tiles.
+template <int KEYS>
+__device__ __forceinline__ int kv4_tiles(const Kv4AttendArgs& a, int len, int m, int* tile0) {
+  const int lo = a.window > 0 ? max(0, len - m + 1 - a.window) : 0;  // first row that token 0 sees
+  *tile0 = lo / KEYS;
+  return m > 0 && len > 0 ? (len + KEYS - 1) / KEYS - *tile0 : 0;
+}
+template <int KEYS>
+__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* first, bool report) {
+  const int T = blockDim.x, per = (a.n_seq + T - 1) / T, i0 = threadIdx.x * per;
+  for (int i = i0; i < min(a.n_seq, i0 + per); ++i) {
+    int slot, len, m, t0;
+    bool ok = kv4_seq(a, i, &slot, &len, &m);
+    if (!ok && report) set_err(a.c.err, kv4_seq_error(a, slot));
+    if (a.accumulate && ok)  // a slot that an earlier sequence names is skipped
+      for (int j = 0; j < i; ++j) ok = ok && __ldcg(a.slots + j) != slot;
+    first[i + 1] = ok ? (long long)kv4_tiles<KEYS>(a, len, m, &t0) * a.c.kvh * a.row_tiles : -1;
   }
-  if (lane == 0) { sm[warp] = mx; sl[warp] = sum; }
-#pragma unroll
-  for (int e = 0; e < OL; ++e)
-    if (lane + 32 * e < D / 8)
-#pragma unroll
-      for (int x = 0; x < 8; ++x) so[warp][(lane + 32 * e) * 8 + x] = acc[e][x];
   __syncthreads();
-  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float w[4], l = 0.f;
+  if (threadIdx.x < 32) {  // running sum, 32 sequences at a time; skipped ones are marked by -1
+    long long base = 0;
+    if (threadIdx.x == 0) first[0] = 0;
+    for (int i = 0; i < a.n_seq; i += 32) {
+      long long v = i + threadIdx.x < a.n_seq ? first[i + threadIdx.x + 1] : 0;
+      v = max(v, 0LL);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    w[x] = sl[x] > 0.f ? exp2f(sm[x] - mm) : (sl[x] != sl[x] ? sl[x] : 0.f);
-    l += w[x] * sl[x];
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if ((int)threadIdx.x >= o) v += u;
+      }
+      if (i + threadIdx.x < a.n_seq) first[i + threadIdx.x + 1] = base + v;
+      base += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  for (int o = threadIdx.x; o < D / 8; o += kKv4AttThreads) {
-    float v[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      v[x] = (w[0] * so[0][8 * o + x] + w[1] * so[1][8 * o + x] + w[2] * so[2][8 * o + x] + w[3] * so[3][8 * o + x]) * inv;
-    kv4_store8(a.out, i * a.out.seq + t * a.out.row + hq * a.out.head + 8 * o, v);
-  }
-  if (threadIdx.x == 0) a.lse[((size_t)i * a.q_len + t) * a.heads + hq] = l != 0.f ? mm + log2f(l) : INFINITY;
+  __syncthreads();
+}
+// Tiles per CTA.
+__device__ __forceinline__ long long kv4_span(const Kv4AttendArgs& a, long long total, int ctas) {
+  return max((long long)a.min_tiles, (total + ctas - 1) / ctas);
 }
 
-// A warp per row of (sequence, KV head): the weights it received, recomputed from the scores.
-template <int D>
-__global__ void __launch_bounds__(kKv4AttThreads) kv4_gain_kernel(const Kv4AttendArgs a) {
+// A run of tiles of one item: what a CTA does between two item borders.
+struct Kv4Run {
+  int seq, head, row_tile;
+  int slot, len, m;
+  int tile, tiles;     // first tile (absolute) and their number
+  bool first, last;    // the run holds the item's first / last tile
+};
+// The run that starts at global tile g (g < end <= total).
+template <int KEYS>
+__device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long long* first, long long g, long long end) {
+  int lo = 0, hi = a.n_seq - 1;  // the last sequence with first[i] <= g (empty ones in between share it)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (first[mid] <= g) lo = mid; else hi = mid - 1;
+  }
+  Kv4Run r;
+  r.seq = lo;
+  kv4_seq(a, lo, &r.slot, &r.len, &r.m);
+  int t0;
+  const int n = kv4_tiles<KEYS>(a, r.len, r.m, &t0);
+  const long long x = g - first[lo];
+  const int item = (int)(x / n), off = (int)(x % n);
+  r.head = item / a.row_tiles;
+  r.row_tile = item % a.row_tiles;
+  r.tile = t0 + off;
+  r.tiles = (int)min((long long)(n - off), end - g);
+  r.first = off == 0;
+  r.last = off + r.tiles == n;
+  return r;
+}
+
+// ------------------------------------------------------------------------- the kernel
+template <int D, int DT>
+__global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCtas) kv4_attend_kernel(const Kv4AttendArgs a) {
   using O = Kv4Off<D>;
-  constexpr int OL = D > 256 ? D / 256 : 1;
-  const int i = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using C = Kv4Att<D, DT>;
+  constexpr int W = D / 32;  // words of a key (or value pair) per lane
+  extern __shared__ __align__(128) uint8_t kv4_smem[];
+  uint8_t* ring = kv4_smem;
+  uint4* qs = reinterpret_cast<uint4*>(ring + (size_t)a.stages * C::kTile);
+  float4* os = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(qs) + C::kQBytes);
+  float2* mls = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(os) + C::kOBytes);  // [warp][8]
+  uint64_t* full = reinterpret_cast<uint64_t*>(mls + C::kWarps * 8);
+  uint64_t* empty = full + 8;
+  uint32_t* held = reinterpret_cast<uint32_t*>(empty + 8);  // [8]: blocks of a stage that hold rows
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(held + 8);
+  long long* first = reinterpret_cast<long long*>(full + 32);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
   pdl_wait();
   pdl_trigger();
-  int slot, len, m;
-  if (!kv4_seq(a, i, &slot, &len, &m)) return;
-  for (int j = blockIdx.x * 4 + warp; j < len; j += 4 * gridDim.x) {
-    const long b = kv4_block(a.c, slot, h, j / kKv4Block);
-    if (b < 0) continue;
-    const uint8_t* blk = a.c.data + (size_t)b * O::kBlock;
-    float k[OL][8], gain = 0.f;
+  kv4_plan<C::kKeys>(a, first, blockIdx.x == 0);
+  const long long total = first[a.n_seq];
+  const long long span = kv4_span(a, total, gridDim.x);
+  const long long g0 = min(total, (long long)blockIdx.x * span), g1 = min(total, g0 + span);
+
+  if (warp == C::kWarps) {
+    // ------------------------------------------------ producer: tiles into the ring
+    int it = 0;
+    bool stop = false;
+    for (long long at = g0; at < g1 && !stop;) {
+      const Kv4Run r = kv4_run<C::kKeys>(a, first, at, g1);
+      const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
+      for (int x = 0; x < r.tiles; ++x, ++it) {
+        const int s = it % a.stages;
+        if (it >= a.stages && !mbar_wait(&empty[s], (it / a.stages - 1) & 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        // lane b looks block b up; neighbours in the pool travel in one copy
+        const int b = (r.tile + x) * C::kBlocks + lane;
+        const bool want = lane < C::kBlocks && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
+        const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
+        if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
+        const long before = __shfl_up_sync(0xFFFFFFFFu, at_b, 1);
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
+        const uint32_t joins = __ballot_sync(0xFFFFFFFFu, at_b >= 0 && lane > 0 && before >= 0 && before == at_b - 1);
+        if (lane == 0) {
+          held[s] = have;
+          mbar_expect_tx(&full[s], __popc(have) * O::kBlock);
+        }
+        __syncwarp();
+        if (at_b >= 0 && !((joins >> lane) & 1)) {
+          const uint32_t after = joins >> 1 >> lane;  // ones while the next block joins
+          const int n = 1 + __ffs(~after) - 1;
+          bulk_g2s(ring + (size_t)s * C::kTile + lane * O::kBlock, a.c.data + (size_t)at_b * O::kBlock, n * O::kBlock,
+                   &full[s]);
+        }
+      }
+      at += r.tiles;
+    }
+    if (stop) {
+      if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // copies in flight land before the CTA's memory goes, whatever the consumers do
+    for (int k = max(0, it - a.stages); k < it; ++k) mbar_wait_drain(&full[k % a.stages], (k / a.stages) & 1);
+    return;
+  }
+
+  // ---------------------------------------------------- consumers
+  const int set = warp >> 2, wq = warp & 3;
+  int it = 0, piece = 0;
+  for (long long at = g0; at < g1; ++piece) {
+    const Kv4Run r = kv4_run<C::kKeys>(a, first, at, g1);
+    const int n_rows = r.m * a.group, row0 = r.row_tile * 8;
+    // ---- queries of the item's eight rows, as bf16 parts in fragment order
+    named_bar_sync(1, 32 * C::kWarps);
+    for (int e = threadIdx.x; e < W * 32; e += 32 * C::kWarps) {
+      const int w = e >> 5, l = e & 31, row = row0 + (l >> 2);  // lane l: row l / 4, numbers (l % 4) D/4 + 8w ..
+      float v[8];
+      if (row < n_rows) {
+        const int tok = row / a.group, hq = r.head * a.group + row % a.group;
+        kv4_load8(a.q, (long)r.seq * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head + (l & 3) * (D / 4) + 8 * w, v);
+      } else {
 #pragma unroll
-    for (int e = 0; e < OL; ++e)
-      if (lane + 32 * e < D / 8) kv4_k8<D>(blk, j % kKv4Block, lane + 32 * e, k[e]);
-    for (int t = max(0, j - (len - m)); t < m; ++t)
-      for (int g = 0; g < a.group; ++g) {
-        const int hq = h * a.group + g;
-        float s = 0.f;
+        for (int x = 0; x < 8; ++x) v[x] = 0.f;
+      }
+      uint32_t p[4][C::kQP];
 #pragma unroll
-        for (int e = 0; e < OL; ++e) {
-          const int o = lane + 32 * e;
-          if (o < D / 8) {
-            float q[8];
-            kv4_load8(a.q, i * a.q.seq + t * a.q.row + hq * a.q.head + 8 * o, q);
+      for (int x = 0; x < 4; ++x) kv4_split<C::kQP>(v[2 * x], v[2 * x + 1], p[x]);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) s += q[x] * k[e][x];
+      for (int part = 0; part < C::kQP; ++part)
+        qs[(part * W + w) * 32 + l] = make_uint4(p[0][part], p[1][part], p[2][part], p[3][part]);
+    }
+    named_bar_sync(1, 32 * C::kWarps);
+
+    float acc[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // rows that query rows 2t and 2t + 1 see: (low, last]
+    const int ra = min(row0 + 2 * t, n_rows - 1), rb = min(row0 + 2 * t + 1, n_rows - 1);
+    const int last0 = r.len - r.m + ra / a.group, last1 = r.len - r.m + rb / a.group;
+    const int low0 = a.window > 0 ? last0 - a.window : -1, low1 = a.window > 0 ? last1 - a.window : -1;
+    const int last_min = r.len - r.m + min(row0, n_rows - 1) / a.group;
+    const int low_max = a.window > 0 ? r.len - r.m + min(row0 + 7, n_rows - 1) / a.group - a.window : -1;
+
+    for (int x = 0; x < r.tiles; ++x, ++it) {
+      if (C::kSets > 1 && it % C::kSets != set) continue;
+      const int s = it % a.stages;
+      if (!mbar_wait(&full[s], (it / a.stages) & 1, abort_flag)) *abort_flag = 1;
+      const bool dead = *abort_flag;
+      const uint32_t have = dead ? 0u : held[s];
+#pragma unroll 1
+      for (int bb = 0; bb < C::kBpw; ++bb) {
+        const int bi = bb * 4 + wq;
+        if (!((have >> bi) & 1)) continue;
+        const uint8_t* blk = ring + (size_t)s * C::kTile + bi * O::kBlock;
+        const int j0 = ((r.tile + x) * C::kBlocks + bi) * kKv4Block;
+        // scores of 16 keys (rows of the product) by 8 query rows
+        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint4* kc = reinterpret_cast<const uint4*>(blk) + lane;
+        const uint16_t* ks = reinterpret_cast<const uint16_t*>(blk + O::kKs);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const uint4 u = kc[i * 32];  // row g: words 2i, 2i + 1; row g + 8: same
+          const int grp = (t * (D / 4) + 16 * i) / kKv4Group;  // 16 numbers never straddle a group
+          const uint32_t sg = 0x10001u * ks[g * (D / 32) + grp], sh = 0x10001u * ks[(g + 8) * (D / 32) + grp];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t ug = e ? u.y : u.x, uh = e ? u.w : u.z;
+            const uint32_t a0 = kv4_pair(ug, sg), a1 = kv4_pair(uh, sh), a2 = kv4_pair(ug >> 4, sg), a3 = kv4_pair(uh >> 4, sh);
+            const uint32_t b0 = kv4_pair(ug >> 8, sg), b1 = kv4_pair(uh >> 8, sh), b2 = kv4_pair(ug >> 12, sg), b3 = kv4_pair(uh >> 12, sh);
+#pragma unroll
+            for (int part = 0; part < C::kQP; ++part) {
+              const uint4 qv = qs[(part * W + 2 * i + e) * 32 + lane];
+              kv4_mma(c0, a0, a1, a2, a3, qv.x, qv.y);
+              kv4_mma(c1, b0, b1, b2, b3, qv.z, qv.w);
+            }
           }
         }
-        s = warp_sum(s) * a.scale * 1.4426950408889634f;
-        gain += exp2f(s - __ldcg(a.lse + ((size_t)i * a.q_len + t) * a.heads + hq));
+        float s00 = (c0[0] + c1[0]) * a.scale, s01 = (c0[1] + c1[1]) * a.scale;  // key g: rows 2t, 2t + 1
+        float s10 = (c0[2] + c1[2]) * a.scale, s11 = (c0[3] + c1[3]) * a.scale;  // key g + 8
+        if (j0 + kKv4Block - 1 > last_min || j0 <= low_max) {
+          const int ja = j0 + g, jb = ja + 8;
+          if (ja > last0 || ja <= low0) s00 = -INFINITY;
+          if (ja > last1 || ja <= low1) s01 = -INFINITY;
+          if (jb > last0 || jb <= low0) s10 = -INFINITY;
+          if (jb > last1 || jb <= low1) s11 = -INFINITY;
+        }
+        float n0 = fmaxf(s00, s10), n1 = fmaxf(s01, s11);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, o));
+          n1 = fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, o));
+        }
+        if (__any_sync(0xFFFFFFFFu, n0 > mx0 || n1 > mx1)) {
+          n0 = fmaxf(n0, mx0);
+          n1 = fmaxf(n1, mx1);
+          // a row that has seen nothing yet keeps -inf and sums of zero
+          const float f0 = n0 == -INFINITY ? 1.f : kv4_exp2(mx0 - n0), f1 = n1 == -INFINITY ? 1.f : kv4_exp2(mx1 - n1);
+          mx0 = n0;
+          mx1 = n1;
+          l0 *= f0;
+          l1 *= f1;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[i][0] *= f0;
+            acc[i][1] *= f1;
+            acc[i][2] *= f0;
+            acc[i][3] *= f1;
+          }
+        }
+        const float z0 = mx0 == -INFINITY ? 0.f : mx0, z1 = mx1 == -INFINITY ? 0.f : mx1;
+        const float p00 = kv4_exp2(s00 - z0), p01 = kv4_exp2(s01 - z1), p10 = kv4_exp2(s10 - z0), p11 = kv4_exp2(s11 - z1);
+        l0 += p00 + p10;
+        l1 += p01 + p11;
+        uint32_t pa[C::kPP], pb[C::kPP];
+        kv4_split<C::kPP>(p00, p01, pa);
+        kv4_split<C::kPP>(p10, p11, pb);
+#pragma unroll
+        for (int part = 0; part < C::kPP; ++part) {
+          pa[part] = kv4_transpose(pa[part]);
+          pb[part] = kv4_transpose(pb[part]);
+        }
+        // output: 16 numbers of the values (rows of the product) by 8 query rows, over 16 keys
+        const uint4* vc = reinterpret_cast<const uint4*>(blk + O::kV) + lane;
+        const uint32_t* vs = reinterpret_cast<const uint32_t*>(blk + O::kVs);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const uint4 u = vc[i * 32];  // row pair t: words 2i, 2i + 1; pair t + 4: same
+          const int grp = (g * (D / 8) + 8 * i) / kKv4Group;
+          const uint32_t sa = vs[grp * 8 + t], sb = vs[grp * 8 + t + 4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t ua = e ? u.y : u.x, ub = e ? u.w : u.z;
+            const uint32_t a0 = kv4_pair(ua, sa), a1 = kv4_pair(ua >> 4, sa), a2 = kv4_pair(ub, sb), a3 = kv4_pair(ub >> 4, sb);
+            const uint32_t b0 = kv4_pair(ua >> 8, sa), b1 = kv4_pair(ua >> 12, sa), b2 = kv4_pair(ub >> 8, sb), b3 = kv4_pair(ub >> 12, sb);
+#pragma unroll
+            for (int part = 0; part < C::kPP; ++part) {
+              kv4_mma(acc[4 * i + 2 * e], a0, a1, a2, a3, pa[part], pb[part]);
+              kv4_mma(acc[4 * i + 2 * e + 1], b0, b1, b2, b3, pa[part], pb[part]);
+            }
+          }
+        }
       }
-    if (lane == 0) a.c.weight[b * kKv4Block + j % kKv4Block] += gain;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+    at += r.tiles;
+
+    // ---- join the warps' sums
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+    }
+    if (g == 0) {
+      mls[warp * 8 + 2 * t] = make_float2(mx0, l0);
+      mls[warp * 8 + 2 * t + 1] = make_float2(mx1, l1);
+    }
+    named_bar_sync(1, 32 * C::kWarps);
+    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      M0 = fmaxf(M0, mls[w * 8 + 2 * t].x);
+      M1 = fmaxf(M1, mls[w * 8 + 2 * t + 1].x);
+    }
+    const float Z0 = M0 == -INFINITY ? 0.f : M0, Z1 = M1 == -INFINITY ? 0.f : M1;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float2 u = mls[w * 8 + 2 * t], v = mls[w * 8 + 2 * t + 1];
+      L0 += u.y * kv4_exp2(u.x - Z0);
+      L1 += v.y * kv4_exp2(v.x - Z1);
+    }
+    const float f0 = kv4_exp2(mx0 - Z0), f1 = kv4_exp2(mx1 - Z1);
+    auto put = [&](bool add) {
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int sel = 0; sel < 2; ++sel) {
+          const float f = sel ? f1 : f0;
+          float4* p = &os[((wq * W + w) * 2 + sel) * 32 + lane];
+          float4 v = make_float4(acc[2 * w][sel] * f, acc[2 * w][2 + sel] * f, acc[2 * w + 1][sel] * f, acc[2 * w + 1][2 + sel] * f);
+          if (add) {
+            const float4 u = *p;
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+          }
+          *p = v;
+        }
+    };
+    if (C::kSets > 1) {
+      if (set == 1) put(false);
+      named_bar_sync(1, 32 * C::kWarps);
+      if (set == 0) put(true);
+    } else {
+      put(false);
+    }
+    named_bar_sync(1, 32 * C::kWarps);
+    const bool whole = r.first && r.last;
+    const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
+    // thread e: lane l of word w: numbers (l / 4) D/8 + 4w .. of query row 2 (l % 4) + sel
+    for (int e = threadIdx.x; e < W * 64; e += 32 * C::kWarps) {
+      const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6;
+      float4 v = os[e];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        const float4 u = os[k * W * 64 + e];
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      if (!whole) {
+        a.part_o[slot_p * W * 64 + e] = v;
+      } else {
+        const int row = row0 + 2 * (l & 3) + sel;
+        if (row < n_rows) {
+          float L = 0.f, M = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C::kWarps; ++k) M = fmaxf(M, mls[k * 8 + (row & 7)].x);
+          const float Z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+          for (int k = 0; k < C::kWarps; ++k) L += mls[k * 8 + (row & 7)].y * kv4_exp2(mls[k * 8 + (row & 7)].x - Z);
+          const float inv = L != 0.f ? 1.f / L : 0.f;
+          const int tok = row / a.group, hq = r.head * a.group + row % a.group;
+          kv4_store4(a.out, (long)r.seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
+                     make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        }
+      }
+    }
+    if (threadIdx.x < 32 && g == 0) {
+      if (!whole) {
+        a.part_ml[slot_p * 8 + 2 * t] = make_float2(M0, L0);
+        a.part_ml[slot_p * 8 + 2 * t + 1] = make_float2(M1, L1);
+      } else {
+        float* lse = a.lse + (((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile) * 8 + 2 * t;
+        lse[0] = L0 != 0.f ? M0 + log2f(L0) : INFINITY;
+        lse[1] = L1 != 0.f ? M1 + log2f(L1) : INFINITY;
+      }
+    }
+  }
+  if (*abort_flag && threadIdx.x == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------- the join
+// One CTA per item and quarter of its numbers: adds the partial sums that the spans left, in
+// span order.  Items without keys (and skipped sequences) get zeros.  ctas: the grid that ran.
+constexpr int kKv4JoinThreads = 128;
+
+template <int D, int KEYS>
+__global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(const Kv4AttendArgs a, int ctas) {
+  constexpr int W = D / 32;
+  extern __shared__ __align__(16) long long kv4_first[];
+  __shared__ float sM[8], sL[8];
+  const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles;
+  const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
+  pdl_wait();
+  pdl_trigger();
+  kv4_plan<KEYS>(a, kv4_first, false);
+  int slot, len, m;
+  const bool ok = kv4_seq(a, i, &slot, &len, &m);
+  const long long total = kv4_first[a.n_seq], span = kv4_span(a, total, ctas);
+  const long long n = (kv4_first[i + 1] - kv4_first[i]) / per_seq;
+  const long long t0 = kv4_first[i] + n * x, t1 = t0 + n;  // the item's tiles
+  const int n_rows = (ok ? m : a.q_len) * a.group;
+  const long long c0 = n ? t0 / span : 0, c1 = n ? (t1 - 1) / span : 0;
+  if (n && c0 == c1) return;  // one CTA had the whole item
+  // CTA c's partial sums of this item: slot 0 when the item opens its span, else slot 1
+  auto part = [&](long long c) { return c * 2 + (t0 > c * span ? 1 : 0); };
+  if (threadIdx.x < 8) {
+    float M = -INFINITY, L = 0.f;
+    if (n) {
+      for (long long c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[part(c) * 8 + threadIdx.x].x);
+      const float Z = M == -INFINITY ? 0.f : M;
+      for (long long c = c0; c <= c1; ++c) {
+        const float2 u = a.part_ml[part(c) * 8 + threadIdx.x];
+        L += u.y * kv4_exp2(u.x - Z);
+      }
+    }
+    sM[threadIdx.x] = M == -INFINITY ? 0.f : M;
+    sL[threadIdx.x] = L;
+    if (blockIdx.y == 0) a.lse[(long)item * 8 + threadIdx.x] = L != 0.f ? M + log2f(L) : INFINITY;
+  }
+  __syncthreads();
+  for (int e = blockIdx.y * kKv4JoinThreads + threadIdx.x; e < W * 64; e += gridDim.y * kKv4JoinThreads) {
+    const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6, r8 = 2 * (l & 3) + sel, row = rt * 8 + r8;
+    if (row >= n_rows) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n) {
+      const float Z = sM[r8];
+      for (long long c = c0; c <= c1; ++c) {
+        const float f = kv4_exp2(a.part_ml[part(c) * 8 + r8].x - Z);
+        const float4 u = a.part_o[part(c) * W * 64 + e];
+        v.x += f * u.x;
+        v.y += f * u.y;
+        v.z += f * u.z;
+        v.w += f * u.w;
+      }
+    }
+    const float inv = sL[r8] != 0.f ? 1.f / sL[r8] : 0.f;
+    const int tok = row / a.group, hq = head * a.group + row % a.group;
+    kv4_store4(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
+               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  }
+}
+
+// ------------------------------------------------------------------------- the account
+// The weights each row received, recomputed from the scores: p = 2^(s - lse).  A warp holds 16
+// keys of one (sequence, KV head) as tensor-core operands and takes every query row past them,
+// eight at a time, so a row's gain is one warp's sum in a fixed order.
+constexpr int kKv4GainWarps = 4;
+
+template <int D, int DT>
+__global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const Kv4AttendArgs a) {
+  using O = Kv4Off<D>;
+  using C = Kv4Att<D, DT>;
+  constexpr int W = D / 32;
+  extern __shared__ __align__(128) uint8_t kv4_smem[];
+  uint4* qs = reinterpret_cast<uint4*>(kv4_smem);
+  const int i = blockIdx.y, h = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  int slot, len, m;
+  if (!kv4_seq(a, i, &slot, &len, &m) || m == 0) return;
+  if (kv4_repeated(a.slots, i, slot)) {
+    if (threadIdx.x == 0) set_err(a.c.err, G4_DEV_BAD_SLOT);
+    return;
+  }
+  const int n_rows = m * a.group;
+  const int nb = (len + kKv4Block - 1) / kKv4Block;
+  for (int b0 = blockIdx.x * kKv4GainWarps; b0 < nb; b0 += gridDim.x * kKv4GainWarps) {
+    const int b = b0 + warp;
+    const long at = b < nb ? kv4_block(a.c, slot, h, b) : -1;
+    const uint8_t* blk = a.c.data + (size_t)(at < 0 ? 0 : at) * O::kBlock;
+    uint4 u[W / 2];
+    float gain0 = 0.f, gain1 = 0.f;  // keys g and g + 8
+    if (at >= 0)
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) u[k] = __ldcg(reinterpret_cast<const uint4*>(blk) + k * 32 + lane);
+    const uint16_t* ks = reinterpret_cast<const uint16_t*>(blk + O::kKs);
+    // the first row tile that any key of the CTA is seen by
+    const int tok0 = max(0, b0 * kKv4Block - (len - m));
+    for (int rt = tok0 * a.group / 8; rt * 8 < n_rows; ++rt) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < W * 32; e += 32 * kKv4GainWarps) {
+        const int w = e >> 5, l = e & 31, row = rt * 8 + (l >> 2);
+        float v[8];
+        if (row < n_rows) {
+          const int tok = row / a.group, hq = h * a.group + row % a.group;
+          kv4_load8(a.q, (long)i * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head + (l & 3) * (D / 4) + 8 * w, v);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = 0.f;
+        }
+        uint32_t p[4][C::kQP];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) kv4_split<C::kQP>(v[2 * x], v[2 * x + 1], p[x]);
+#pragma unroll
+        for (int part = 0; part < C::kQP; ++part)
+          qs[(part * W + w) * 32 + l] = make_uint4(p[0][part], p[1][part], p[2][part], p[3][part]);
+      }
+      __syncthreads();
+      if (at < 0) continue;
+      float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) {
+        const int grp = (t * (D / 4) + 16 * k) / kKv4Group;
+        const uint32_t sg = 0x10001u * __ldcg(ks + g * (D / 32) + grp), sh = 0x10001u * __ldcg(ks + (g + 8) * (D / 32) + grp);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t ug = e ? u[k].y : u[k].x, uh = e ? u[k].w : u[k].z;
+          const uint32_t a0 = kv4_pair(ug, sg), a1 = kv4_pair(uh, sh), a2 = kv4_pair(ug >> 4, sg), a3 = kv4_pair(uh >> 4, sh);
+          const uint32_t d0 = kv4_pair(ug >> 8, sg), d1 = kv4_pair(uh >> 8, sh), d2 = kv4_pair(ug >> 12, sg), d3 = kv4_pair(uh >> 12, sh);
+#pragma unroll
+          for (int part = 0; part < C::kQP; ++part) {
+            const uint4 qv = qs[(part * W + 2 * k + e) * 32 + lane];
+            kv4_mma(c0, a0, a1, a2, a3, qv.x, qv.y);
+            kv4_mma(c1, d0, d1, d2, d3, qv.z, qv.w);
+          }
+        }
+      }
+      const float* lse = a.lse + (((long)i * a.c.kvh + h) * a.row_tiles + rt) * 8 + 2 * t;
+      const float e0 = __ldcg(lse), e1 = __ldcg(lse + 1);
+      const int ra = rt * 8 + 2 * t, rb = ra + 1, ja = b * kKv4Block + g;
+      const int last0 = ra < n_rows ? len - m + ra / a.group : -1, last1 = rb < n_rows ? len - m + rb / a.group : -1;
+      if (ja <= last0) gain0 += kv4_exp2((c0[0] + c1[0]) * a.scale - e0);
+      if (ja <= last1) gain0 += kv4_exp2((c0[1] + c1[1]) * a.scale - e1);
+      if (ja + 8 <= last0) gain1 += kv4_exp2((c0[2] + c1[2]) * a.scale - e0);
+      if (ja + 8 <= last1) gain1 += kv4_exp2((c0[3] + c1[3]) * a.scale - e1);
+    }
+    if (at < 0) continue;
+    gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 1);
+    gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 1);
+    gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 2);
+    gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 2);
+    if (t < 2) {
+      const int j = b * kKv4Block + g + 8 * t;
+      if (j < len) a.c.weight[at * kKv4Block + g + 8 * t] += t ? gain1 : gain0;
+    }
   }
 }
 

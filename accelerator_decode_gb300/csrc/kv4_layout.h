@@ -47,7 +47,12 @@ struct Kv4Cache {
 // Index of block b (of 16 rows) of (slot, head) in the pool, -1 when it has no page.
 G4_HD long kv4_block(const Kv4Cache& c, int slot, int head, int b) {
   if (!c.table) return ((long)slot * c.kvh + head) * c.bpp + b;
-  const int pg = c.table[(size_t)slot * c.max_pages + (b >> c.log_bpp)];
+  const int* at = c.table + (size_t)slot * c.max_pages + (b >> c.log_bpp);
+#ifdef __CUDA_ARCH__
+  const int pg = __ldcg(at);  // the caller rewrites the table between calls: never from L1
+#else
+  const int pg = *at;
+#endif
   if (pg < 0 || pg >= c.n_pages) return -1;
   return ((long)pg * c.kvh + head) * c.bpp + (b & (c.bpp - 1));
 }

@@ -307,9 +307,10 @@ g4_status g4_argmax_rows_static(int device, g4_stream stream, int32_t n_rows, in
  *
  * One g4_kv4 holds the rows of one layer.  A row of one KV head is a key and a value of
  * head_dim numbers; each group of 32 numbers is held in the linears' int4 convention, signed
- * codes under one bf16 scale: s = bf16(max|x| / 7), c = round-half-even(x / s) clipped to +-7,
- * standing for the value bf16(c * s) (a group of zeros has s = 0).  A row of one KV head takes
- * 9/8 head_dim bytes, key and value together (head_dim 256: 288, in bf16 1,024).
+ * codes under one bf16 scale: s = bf16(max|x| * (1/7)), 1/7 and the product in fp32;
+ * c = round-half-even(x / s) clipped to +-7; standing for the value bf16(c * s) (a group of
+ * zeros has s = 0).  A row of one KV head takes 9/8 head_dim bytes, key and value together
+ * (head_dim 256: 288, in bf16 1,024).
  *
  * Rows live in slots, row 0 .. capacity - 1 each: at fixed places (page_size 0), or in pages of
  * page_size rows: row r of slot s is row r % page_size of page table[s][r / page_size].  The

@@ -22,7 +22,9 @@ def code_rows(x):
     """(codes, scales) of rows x [..., D] (float64 holding the given values)."""
     x = np.nan_to_num(np.asarray(x, np.float64), nan=0.0, posinf=F32_MAX, neginf=-F32_MAX)
     g = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
-    s = np.minimum(bf16_round(np.abs(g).max(-1, keepdims=True) / 7), SCALE_MAX)
+    # the format takes a seventh by an fp32 product
+    seventh = np.abs(g).max(-1, keepdims=True).astype(np.float32) * (np.float32(1) / np.float32(7))
+    s = np.minimum(bf16_round(seventh), SCALE_MAX)
     # quotients of 64 bits: exact at the borders, whose 12 significant bits they hold
     c = np.clip(np.rint(np.divide(g, s, out=np.zeros_like(g), where=s > 0)), -7, 7)
     return c.reshape(x.shape), s[..., 0]
