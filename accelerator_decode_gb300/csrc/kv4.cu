@@ -259,7 +259,8 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
 }
 
 g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_start,
-                      const int32_t* d_counts, int32_t n_rows, const g4_kv4_tensor* k, const g4_kv4_tensor* v) {
+                      const int32_t* d_counts, int32_t n_rows, int32_t zero_rest, const g4_kv4_tensor* k,
+                      const g4_kv4_tensor* v) {
   if (!op || !d_slots || !d_start || (!k && !v) || !kv4_count(op, n_seq) || n_rows < 1 || n_rows > op->cfg.capacity)
     return G4_ERR_INVALID_ARG;
   Kv4RowArgs a{};
@@ -272,6 +273,7 @@ g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t
   a.start = d_start;
   a.counts = d_counts;
   a.n_rows = n_rows;
+  a.zero_rest = zero_rest != 0;
   KV4_DISPATCH(op->c.d, launch(kv4_read_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0,
                                reinterpret_cast<cudaStream_t>(stream), a));
   CK(cudaGetLastError());
@@ -279,7 +281,8 @@ g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t
 }
 
 g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_start,
-                         const int32_t* d_counts, int32_t n_rows, int32_t* d_positions, float* d_weights) {
+                         const int32_t* d_counts, int32_t n_rows, int32_t zero_rest, int32_t* d_positions,
+                         float* d_weights) {
   if (!op || !d_slots || !d_start || (!d_positions && !d_weights) || !kv4_count(op, n_seq) || n_rows < 1 ||
       n_rows > op->cfg.capacity)
     return G4_ERR_INVALID_ARG;
@@ -291,6 +294,7 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
   a.start = d_start;
   a.counts = d_counts;
   a.n_rows = n_rows;
+  a.zero_rest = zero_rest != 0;
   a.positions_out = d_positions;
   a.weights_out = d_weights;
   launch(kv4_account_kernel, dim3(cdiv(n_rows, kKv4RowThreads), n_seq, op->c.kvh), dim3(kKv4RowThreads), 0,
@@ -301,7 +305,7 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
 
 g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_lens,
                         int32_t q_len, const int32_t* d_q_lens, float scale, int32_t window, int32_t accumulate,
-                        const g4_kv4_tensor* q, const g4_kv4_tensor* out) {
+                        int32_t zero_rest, const g4_kv4_tensor* q, const g4_kv4_tensor* out) {
   if (!op || !d_slots || !d_lens || !q || !out || !kv4_count(op, n_seq) || q_len < 1 || q_len > op->cfg.max_q_len ||
       window < 0 || !std::isfinite(scale) || q->dtype != out->dtype)
     return G4_ERR_INVALID_ARG;
@@ -324,6 +328,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)op->c.d)) * 1.4426950408889634);
   a.window = window;
   a.accumulate = accumulate != 0;
+  a.zero_rest = zero_rest != 0;
   a.lse = op->lse;
   a.part_o = op->part_o;
   a.part_ml = op->part_ml;

@@ -160,6 +160,7 @@ struct Kv4RowArgs {
   const float* weights;               // append: same layout, or NULL (0)
   int* positions_out;                 // account
   float* weights_out;
+  int zero_rest;                      // read, account: zeros where there is no row
 };
 
 // Rows [row0, row0 + count) of sequence i, after its checks; count 0 when it is skipped.
@@ -257,41 +258,46 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_read_kernel(const Kv4RowAr
   pdl_wait();
   pdl_trigger();
   int slot, row0, count;
-  if (!kv4_rows_of(a, i, false, &slot, &row0, &count)) return;
+  if (!kv4_rows_of(a, i, false, &slot, &row0, &count)) count = 0;
   const long unit = ((long)blockIdx.x * kKv4RowThreads + threadIdx.x) / NO;
   const int o = threadIdx.x % NO, h = (int)(unit % a.c.kvh);
   const long t_ = unit / a.c.kvh;
-  if (t_ >= count) return;
-  const int t = (int)t_, row = row0 + t, r = row % kKv4Block;
-  const long b = kv4_block(a.c, slot, h, row / kKv4Block);
-  if (b < 0) {
-    if (o == 0) set_err(a.c.err, G4_DEV_BAD_POSITION);
-    return;
+  if (t_ >= (a.zero_rest ? a.n_rows : count)) return;
+  const int t = (int)t_, row = row0 + t, r = row & (kKv4Block - 1);
+  long b = -1;
+  if (t < count) {
+    b = kv4_block(a.c, slot, h, row / kKv4Block);
+    if (b < 0 && o == 0) set_err(a.c.err, G4_DEV_BAD_POSITION);
   }
-  const uint8_t* blk = a.c.data + (size_t)b * O::kBlock;
-  float v[8];
+  if (b < 0 && !a.zero_rest) return;
+  const uint8_t* blk = a.c.data + (size_t)(b < 0 ? 0 : b) * O::kBlock;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (a.k.p) {
-    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(blk + O::k_word(r, o)));
-    const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(r, o >> 2)));
+    if (b >= 0) {
+      const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(blk + O::k_word(r, o)));
+      const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(r, o >> 2)));
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t x = kv4_pair(w >> (4 * p), s);
-      v[2 * p] = bf16_lo(x);
-      v[2 * p + 1] = bf16_hi(x);
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t x = kv4_pair(w >> (4 * p), s);
+        v[2 * p] = bf16_lo(x);
+        v[2 * p + 1] = bf16_hi(x);
+      }
     }
     kv4_store8(a.k, i * a.k.seq + t * a.k.row + h * a.k.head + 8 * o, v);
   }
   if (a.v.p) {
-    const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_scale(r, o >> 2)));
-    uint32_t w[2];
+    if (b >= 0) {
+      const uint32_t s = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_scale(r, o >> 2)));
+      uint32_t w[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) w[u] = __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_half(r, 2 * o + u)));
-    const uint32_t x01 = w[0] | (w[1] << 16);
+      for (int u = 0; u < 2; ++u) w[u] = __ldcg(reinterpret_cast<const uint16_t*>(blk + O::v_half(r, 2 * o + u)));
+      const uint32_t x01 = w[0] | (w[1] << 16);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t x = kv4_pair(x01 >> (4 * p), s);  // number p of both quads
-      v[p] = bf16_lo(x);
-      v[4 + p] = bf16_hi(x);
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t x = kv4_pair(x01 >> (4 * p), s);  // number p of both quads
+        v[p] = bf16_lo(x);
+        v[4 + p] = bf16_hi(x);
+      }
     }
     kv4_store8(a.v, i * a.v.seq + t * a.v.row + h * a.v.head + 8 * o, v);
   }
@@ -303,18 +309,19 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_account_kernel(const Kv4Ro
   pdl_wait();
   pdl_trigger();
   int slot, row0, count;
-  if (!kv4_rows_of(a, i, false, &slot, &row0, &count)) return;
+  if (!kv4_rows_of(a, i, false, &slot, &row0, &count)) count = 0;
   const int t = blockIdx.x * kKv4RowThreads + threadIdx.x;
-  if (t >= count) return;
+  if (t >= (a.zero_rest ? a.n_rows : count)) return;
   const int row = row0 + t;
-  const long b = kv4_block(a.c, slot, h, row / kKv4Block);
-  if (b < 0) {
-    set_err(a.c.err, G4_DEV_BAD_POSITION);
-    return;
+  long b = -1;
+  if (t < count) {
+    b = kv4_block(a.c, slot, h, row / kKv4Block);
+    if (b < 0) set_err(a.c.err, G4_DEV_BAD_POSITION);
   }
+  if (b < 0 && !a.zero_rest) return;
   const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
-  if (a.positions_out) a.positions_out[at] = a.c.pos[b * kKv4Block + row % kKv4Block];
-  if (a.weights_out) a.weights_out[at] = a.c.weight[b * kKv4Block + row % kKv4Block];
+  if (a.positions_out) a.positions_out[at] = b < 0 ? 0 : __ldcg(a.c.pos + b * kKv4Block + row % kKv4Block);
+  if (a.weights_out) a.weights_out[at] = b < 0 ? 0.f : __ldcg(a.c.weight + b * kKv4Block + row % kKv4Block);
 }
 
 // ------------------------------------------------------------------------------- evict

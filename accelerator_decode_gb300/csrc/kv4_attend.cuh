@@ -26,7 +26,7 @@ struct Kv4AttendArgs {
   int n_seq, q_len, heads, group;    // group: query heads per KV head
   int row_tiles;                     // items of a (sequence, KV head): ceil(q_len * group / 8)
   float scale;                       // times log2(e)
-  int window, accumulate;
+  int window, accumulate, zero_rest;
   int min_tiles;                     // a CTA's span is at least this many tiles
   int stages;
   Kv4Dense q, out;
@@ -517,6 +517,16 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(const Kv4Atte
   const long long t0 = kv4_first[i] + n * x, t1 = t0 + n;  // the item's tiles
   const int n_rows = (ok ? m : a.q_len) * a.group;
   const long long c0 = n ? t0 / span : 0, c1 = n ? (t1 - 1) / span : 0;
+  // rows of query tokens beyond the sequence's own
+  if (a.zero_rest && ok && m < a.q_len) {
+    for (int e = blockIdx.y * kKv4JoinThreads + threadIdx.x; e < W * 64; e += gridDim.y * kKv4JoinThreads) {
+      const int l = e & 31, row = rt * 8 + 2 * (l & 3) + ((e >> 5) & 1);
+      if (row < n_rows || row >= a.q_len * a.group) continue;
+      kv4_store4(a.out, (long)i * a.out.seq + (long)(row / a.group) * a.out.row +
+                            (long)(head * a.group + row % a.group) * a.out.head + (l >> 2) * (D / 8) + 4 * (e >> 6),
+                 make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
   if (n && c0 == c1) return;  // one CTA had the whole item
   // CTA c's partial sums of this item: slot 0 when the item opens its span, else slot 1
   auto part = [&](long long c) { return c * 2 + (t0 > c * span ? 1 : 0); };

@@ -123,10 +123,10 @@ def _load():
         "g4_kv4_create": (c_int, [c_int, POINTER(g4_kv4_config), P, POINTER(P)]),
         "g4_kv4_append": (c_int, [P, P, c_int32, P, P, P, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor),
                                   P, P]),
-        "g4_kv4_read": (c_int, [P, P, c_int32, P, P, P, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor)]),
-        "g4_kv4_account": (c_int, [P, P, c_int32, P, P, P, c_int32, P, P]),
-        "g4_kv4_attend": (c_int, [P, P, c_int32, P, P, c_int32, P, c_float, c_int32, c_int32, POINTER(g4_kv4_tensor),
-                                  POINTER(g4_kv4_tensor)]),
+        "g4_kv4_read": (c_int, [P, P, c_int32, P, P, P, c_int32, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor)]),
+        "g4_kv4_account": (c_int, [P, P, c_int32, P, P, P, c_int32, c_int32, P, P]),
+        "g4_kv4_attend": (c_int, [P, P, c_int32, P, P, c_int32, P, c_float, c_int32, c_int32, c_int32,
+                                  POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor)]),
         "g4_kv4_evict": (c_int, [P, P, c_int32, P, P, c_int32, c_int32, P]),
         "g4_kv4_get_device_error": (c_int, [P, P, POINTER(c_int32)]),
         "g4_kv4_bytes": (c_int64, [P]),

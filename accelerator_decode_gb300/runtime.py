@@ -222,36 +222,19 @@ def argmax_rows_static(logits, stream=None):
 _KV4_TYPES = {torch.float32: _g4.G4_DT_F32, torch.bfloat16: _g4.G4_DT_BF16, torch.float16: _g4.G4_DT_F16}
 
 
-def _kv4_tensor(t):
+def _kv4_array(name, t, shape, dtype, index):
+    """Checks a contiguous array on device `index`; its address (None: NULL)."""
     if t is None:
         return None
-    return ctypes.byref(_g4.g4_kv4_tensor(t.data_ptr(), _KV4_TYPES[t.dtype], t.stride(0), t.stride(1), t.stride(2)))
-
-
-def _kv4_dense(name, t, shape, device):
-    """Checks a dense [sequences, rows, heads, head_dim] argument."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype not in _KV4_TYPES:
-        raise TypeError(f"{name} is {t.dtype}: float32, bfloat16 or float16 is wanted")
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: the last dimension has to be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-
-
-def _kv4_array(name, t, shape, dtype, device):
-    """Checks a contiguous per-sequence or per-row array."""
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+    return t.data_ptr()
 
 
 class KV4Cache:
@@ -261,16 +244,17 @@ class KV4Cache:
     page_table: int32 [n_slots, ceil(capacity / page_size)] on the device (kept, and read by every
     call); n_pages defaults to its number of entries.  track: every row carries its position and
     accumulated attention weight, which `evict` goes by.  Calls run on `stream` (default: the
-    current one), where their results are valid; calls on one cache have to be ordered."""
+    current one), where their results are valid; calls on one cache have to be ordered, and come
+    from one host thread at a time."""
 
     def __init__(self, n_slots, capacity, num_q_heads, num_kv_heads, head_dim, max_q_len=64, page_size=0,
                  page_table=None, n_pages=None, track=False, device=None):
-        index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
-        self.device = torch.device("cuda", index)
+        self.index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
+        self.device = torch.device("cuda", self.index)
         if page_size:
             if page_table is None or page_size < 0:
                 raise ValueError("a paged cache needs its page_table")
-            _kv4_array("page_table", page_table, (n_slots, -(-capacity // page_size)), torch.int32, self.device)
+            _kv4_array("page_table", page_table, (n_slots, -(-capacity // page_size)), torch.int32, self.index)
         elif page_table is not None:
             raise ValueError("page_table without page_size")
         self.n_slots, self.capacity, self.track = n_slots, capacity, bool(track)
@@ -279,96 +263,137 @@ class KV4Cache:
         c = _g4.g4_kv4_config(n_slots, capacity, num_q_heads, num_kv_heads, head_dim, max_q_len, page_size,
                               (page_table.numel() if n_pages is None else n_pages) if page_size else 0, int(track))
         h = ctypes.c_void_p()
-        _g4.check(_g4.lib.g4_kv4_create(index, ctypes.byref(c), _ptr(page_table), ctypes.byref(h)), "g4_kv4_create")
+        _g4.check(_g4.lib.g4_kv4_create(self.index, ctypes.byref(c), _ptr(page_table), ctypes.byref(h)),
+                  "g4_kv4_create")
         self.h = h
+        # the two tensor arguments of a call, filled in anew each time
+        self._ta, self._tb = _g4.g4_kv4_tensor(), _g4.g4_kv4_tensor()
+        self._pa, self._pb = ctypes.byref(self._ta), ctypes.byref(self._tb)
 
-    def _call(self, name, stream, used, *args):
-        """One C call on `stream`; the caching allocator learns of the tensors it uses there."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        if s.device != self.device:
-            raise ValueError(f"the stream is on {s.device}, the cache on {self.device}")
-        _g4.check(getattr(_g4.lib, name)(self.h, ctypes.c_void_p(s.cuda_stream), *args), name)
+    # -- arguments ---------------------------------------------------------------------------
+    def _dense(self, name, t, shape, into):
+        """Checks a dense [sequences, rows, heads, head_dim] argument and describes it to C."""
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+        code = _KV4_TYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} is {t.dtype}: float32, bfloat16 or float16 is wanted")
+        s = t.stride()
+        if s[3] != 1:
+            raise ValueError(f"{name}: the last dimension has to be contiguous")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        into.data, into.dtype = t.data_ptr(), code
+        into.seq_stride, into.row_stride, into.head_stride = s[0], s[1], s[2]
+
+    def _fresh(self, t, into):
+        """Describes a contiguous result to C."""
+        into.data, into.dtype = t.data_ptr(), _KV4_TYPES[t.dtype]
+        into.head_stride = t.shape[3]
+        into.row_stride = t.shape[2] * t.shape[3]
+        into.seq_stride = t.shape[1] * into.row_stride
+
+    def _seq(self, name, t, n):
+        return _kv4_array(name, t, (n,), torch.int32, self.index)
+
+    def _stream(self, stream):
+        """The stream's handle."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
+        return stream.cuda_stream
+
+    def _empty(self, shape, dtype, stream):
+        """A result, made on the stream that fills it."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _done(self, status, name, stream, used):
+        """Raises for an error; the caching allocator learns of the tensors used on a given stream."""
+        if status:
+            raise _g4.G4Error(status, name)
         if stream is not None:
             for t in used:
                 if t is not None:
-                    t.record_stream(s)
+                    t.record_stream(stream)
 
-    def _empty(self, shape, dtype, stream, zero=False):
-        """A result, made on the stream that fills it."""
-        make = torch.zeros if zero else torch.empty
-        if stream is None:
-            return make(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(stream):
-            return make(shape, dtype=dtype, device=self.device)
-
-    def _seq(self, **arrays):
-        n = arrays["slots"].numel()
-        for name, t in arrays.items():
-            _kv4_array(name, t, (n,), torch.int32, self.device)
-        return n
-
+    # -- calls -------------------------------------------------------------------------------
     def append(self, k, v, slots, start, counts=None, positions=None, weights=None, stream=None):
         """Code rows k, v [n, rows, num_kv_heads, head_dim] into rows start[i].. of slots[i]."""
-        n = self._seq(slots=slots, start=start, counts=counts)
-        rows = k.shape[1] if k.dim() == 4 else -1
-        for name, t in (("k", k), ("v", v)):
-            _kv4_dense(name, t, (n, rows, self.num_kv_heads, self.head_dim), self.device)
+        n, rows = slots.numel(), k.shape[1] if k.dim() == 4 else -1
+        shape = (n, rows, self.num_kv_heads, self.head_dim)
+        self._dense("k", k, shape, self._ta)
+        self._dense("v", v, shape, self._tb)
         per = (n, self.num_kv_heads, rows)
-        _kv4_array("positions", positions, per, torch.int32, self.device)
-        _kv4_array("weights", weights, per, torch.float32, self.device)
-        self._call("g4_kv4_append", stream, (k, v, slots, start, counts, positions, weights), n, _ptr(slots),
-                   _ptr(start), _ptr(counts), rows, _kv4_tensor(k), _kv4_tensor(v), _ptr(positions), _ptr(weights))
+        status = _g4.lib.g4_kv4_append(
+            self.h, self._stream(stream), n, self._seq("slots", slots, n), self._seq("start", start, n),
+            self._seq("counts", counts, n), rows, self._pa, self._pb,
+            _kv4_array("positions", positions, per, torch.int32, self.index),
+            _kv4_array("weights", weights, per, torch.float32, self.index))
+        self._done(status, "g4_kv4_append", stream, (k, v, slots, start, counts, positions, weights))
 
     def read(self, slots, start, n_rows, counts=None, dtype=torch.bfloat16, stream=None):
-        """(k, v) of rows start[i].. of slots[i], [n, n_rows, num_kv_heads, head_dim]; rows at and
-        beyond counts[i] are zeros."""
-        n = self._seq(slots=slots, start=start, counts=counts)
+        """(k, v) of rows start[i].. of slots[i], [n, n_rows, num_kv_heads, head_dim]; zeros where
+        there is no row (at and beyond counts[i], on a missing page)."""
+        n = slots.numel()
         shape = (n, n_rows, self.num_kv_heads, self.head_dim)
         if dtype not in _KV4_TYPES:
             raise TypeError(f"rows cannot be given as {dtype}")
-        k, v = (self._empty(shape, dtype, stream, counts is not None) for _ in range(2))
-        self._call("g4_kv4_read", stream, (slots, start, counts), n, _ptr(slots), _ptr(start), _ptr(counts), n_rows,
-                   _kv4_tensor(k), _kv4_tensor(v))
+        args = (self._seq("slots", slots, n), self._seq("start", start, n), self._seq("counts", counts, n))
+        k, v = self._empty(shape, dtype, stream), self._empty(shape, dtype, stream)
+        self._fresh(k, self._ta)
+        self._fresh(v, self._tb)
+        status = _g4.lib.g4_kv4_read(self.h, self._stream(stream), n, *args, n_rows, 1, self._pa, self._pb)
+        self._done(status, "g4_kv4_read", stream, (slots, start, counts))
         return k, v
 
     def account(self, slots, start, n_rows, counts=None, stream=None):
-        """(positions, accumulated weights) of rows, [n, num_kv_heads, n_rows]; zeros beyond counts[i]."""
-        n = self._seq(slots=slots, start=start, counts=counts)
+        """(positions, accumulated weights) of rows, [n, num_kv_heads, n_rows]; zeros where there is
+        no row."""
+        n = slots.numel()
         shape = (n, self.num_kv_heads, n_rows)
-        pos = self._empty(shape, torch.int32, stream, counts is not None)
-        weight = self._empty(shape, torch.float32, stream, counts is not None)
-        self._call("g4_kv4_account", stream, (slots, start, counts), n, _ptr(slots), _ptr(start), _ptr(counts), n_rows,
-                   _ptr(pos), _ptr(weight))
+        args = (self._seq("slots", slots, n), self._seq("start", start, n), self._seq("counts", counts, n))
+        pos, weight = self._empty(shape, torch.int32, stream), self._empty(shape, torch.float32, stream)
+        status = _g4.lib.g4_kv4_account(self.h, self._stream(stream), n, *args, n_rows, 1, pos.data_ptr(),
+                                        weight.data_ptr())
+        self._done(status, "g4_kv4_account", stream, (slots, start, counts))
         return pos, weight
 
     def attend(self, q, slots, lens, q_lens=None, scale=0.0, window=0, accumulate=False, out=None, stream=None):
         """Attention of q [n, q_len, num_q_heads, head_dim] over rows 0 .. lens[i] - 1 of slots[i], the
-        query tokens being the newest rows.  Returns out (given, or new and of q's layout)."""
-        n = self._seq(slots=slots, lens=lens, q_lens=q_lens)
-        q_len = q.shape[1] if q.dim() == 4 else -1
+        query tokens being the newest rows.  Returns out: the given tensor, whose rows at and beyond
+        q_lens[i] stay as they were, or a new one, where they are zeros."""
+        n, q_len = slots.numel(), q.shape[1] if q.dim() == 4 else -1
         shape = (n, q_len, self.num_q_heads, self.head_dim)
-        _kv4_dense("q", q, shape, self.device)
-        if out is None:
-            out = self._empty(shape, q.dtype, stream, q_lens is not None)
+        self._dense("q", q, shape, self._ta)
+        args = (self._seq("slots", slots, n), self._seq("lens", lens, n), q_len, self._seq("q_lens", q_lens, n))
+        given = out is not None
+        if given:
+            self._dense("out", out, shape, self._tb)
         else:
-            _kv4_dense("out", out, shape, self.device)
-        self._call("g4_kv4_attend", stream, (q, out, slots, lens, q_lens), n, _ptr(slots), _ptr(lens), q_len,
-                   _ptr(q_lens), float(scale), int(window), int(bool(accumulate)), _kv4_tensor(q), _kv4_tensor(out))
+            out = self._empty(shape, q.dtype, stream)
+            self._fresh(out, self._tb)
+        status = _g4.lib.g4_kv4_attend(self.h, self._stream(stream), n, *args, scale, window, bool(accumulate),
+                                       not given, self._pa, self._pb)
+        self._done(status, "g4_kv4_attend", stream, (q, out, slots, lens, q_lens))
         return out
 
     def evict(self, slots, lens, budget, recent=0, stream=None):
         """Keep `budget` rows of every slot (see g4_kv4_evict); returns the new lens."""
-        n = self._seq(slots=slots, lens=lens)
+        n = slots.numel()
+        args = (self._seq("slots", slots, n), self._seq("lens", lens, n))
         new = self._empty((n,), torch.int32, stream)
-        self._call("g4_kv4_evict", stream, (slots, lens), n, _ptr(slots), _ptr(lens), int(budget), int(recent),
-                   _ptr(new))
+        status = _g4.lib.g4_kv4_evict(self.h, self._stream(stream), n, *args, budget, recent, new.data_ptr())
+        self._done(status, "g4_kv4_evict", stream, (slots, lens))
         return new
 
     def device_error(self, stream=None):
         """(status, word) of the sticky device error word, cleared."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
         w = ctypes.c_int32(0)
-        return _g4.lib.g4_kv4_get_device_error(self.h, ctypes.c_void_p(s.cuda_stream), ctypes.byref(w)), w.value
+        return _g4.lib.g4_kv4_get_device_error(self.h, self._stream(stream), ctypes.byref(w)), w.value
 
     def device_bytes(self):
         return _g4.lib.g4_kv4_bytes(self.h)

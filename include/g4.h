@@ -374,17 +374,19 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
                         const int32_t* d_positions, const float* d_weights);
 
 /* Give rows back as the values they stand for, the inverse addressing of g4_kv4_append (k or v
- * may be NULL, not both).  Rows at and beyond d_counts[i] are left as they were.
+ * may be NULL, not both).  What there is no row for (at and beyond d_counts[i], on a missing
+ * page, of a skipped sequence) is left as it was, or with zero_rest != 0 set to zero.
  * Errors: INVALID_ARG. */
 g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                       const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
-                      const g4_kv4_tensor* k, const g4_kv4_tensor* v);
+                      int32_t zero_rest, const g4_kv4_tensor* k, const g4_kv4_tensor* v);
 
 /* Positions and accumulated weights of rows, [n_seq][num_kv_heads][n_rows] (either may be NULL,
- * not both).  Errors: INVALID_ARG, UNSUPPORTED (a cache without track). */
+ * not both); zero_rest as g4_kv4_read.  Errors: INVALID_ARG, UNSUPPORTED (a cache without
+ * track). */
 g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                          const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
-                         int32_t* d_positions, float* d_weights);
+                         int32_t zero_rest, int32_t* d_positions, float* d_weights);
 
 /* Softmax attention of q_len query tokens per sequence over rows 0 .. d_lens[i] - 1 of its slot,
  * the sequence's own newest rows included: with m = d_q_lens[i] (NULL: q_len) query tokens,
@@ -392,7 +394,7 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * the newest `window` of those):
  *   s_j = scale * q . K_j        o = sum_j softmax(s)_j V_j        (scale 0: 1/sqrt(head_dim))
  * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type.  A token that sees no row gets
- * zeros; query rows t >= m of `out` are left as they were.  accumulate != 0 (track, window 0):
+ * zeros; query rows t >= m of `out` are left as they were, or with zero_rest != 0 set to zero.  accumulate != 0 (track, window 0):
  * each row's account grows by the attention weights it received, summed over the sequence's
  * query tokens and the query heads of its KV head.  The same slot may be named twice only
  * without accumulate.  The sums run in a fixed order: equal calls give equal bits.
@@ -402,8 +404,8 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * no longer in position order). */
 g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                         const int32_t* d_lens, int32_t q_len, const int32_t* d_q_lens, float scale,
-                        int32_t window, int32_t accumulate, const g4_kv4_tensor* q,
-                        const g4_kv4_tensor* out);
+                        int32_t window, int32_t accumulate, int32_t zero_rest,
+                        const g4_kv4_tensor* q, const g4_kv4_tensor* out);
 
 /* Cut slots back to `budget` rows per KV head (track): of rows 0 .. d_lens[i] - 1 the ones at the
  * newest `recent` positions (position > newest - recent) are kept first, then those with the

@@ -135,9 +135,9 @@ def test_null_handles_are_refused(g4):
     assert lib.g4_kv4_create(0, ctypes.byref(g4.g4_kv4_config(**GOOD)), None, None) == bad
     t = g4.g4_kv4_tensor()
     assert lib.g4_kv4_append(None, None, 1, None, None, None, 1, ctypes.byref(t), ctypes.byref(t), None, None) == bad
-    assert lib.g4_kv4_read(None, None, 1, None, None, None, 1, ctypes.byref(t), None) == bad
-    assert lib.g4_kv4_account(None, None, 1, None, None, None, 1, None, None) == bad
-    assert lib.g4_kv4_attend(None, None, 1, None, None, 1, None, 0.0, 0, 0, ctypes.byref(t), ctypes.byref(t)) == bad
+    assert lib.g4_kv4_read(None, None, 1, None, None, None, 1, 0, ctypes.byref(t), None) == bad
+    assert lib.g4_kv4_account(None, None, 1, None, None, None, 1, 0, None, None) == bad
+    assert lib.g4_kv4_attend(None, None, 1, None, None, 1, None, 0.0, 0, 0, 0, ctypes.byref(t), ctypes.byref(t)) == bad
     assert lib.g4_kv4_evict(None, None, 1, None, None, 1, 0, None) == bad
     assert lib.g4_kv4_get_device_error(None, None, None) == bad
     assert lib.g4_kv4_bytes(None) == 0
