@@ -107,7 +107,7 @@ template <int D, int DT>
 void kv4_attrs(int optin) {
   set_max_dyn(kv4_attend_kernel<D, DT>, optin);
   set_max_dyn(kv4_gain_kernel<D, DT>, optin);
-  carve_max(kv4_join_kernel<D, Kv4Att<D, DT>::kKeys>);
+  set_max_dyn(kv4_finish_kernel<D, DT>, optin);
 }
 template <int D>
 void kv4_attrs_d(int optin) {
@@ -140,10 +140,12 @@ void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
   a.stages = std::max(2, std::min(4, room / C::kTile));
   a.min_tiles = 1;
   launch(kv4_attend_kernel<D, DT>, dim3(ctas), dim3(C::kThreads), C::smem(a.stages, a.n_seq), st, a);
-  const int items = a.n_seq * a.c.kvh * a.row_tiles;
-  launch(kv4_join_kernel<D, C::kKeys>, dim3(items, std::max(1, D * 2 / kKv4JoinThreads)), dim3(kKv4JoinThreads),
-         ((size_t)a.n_seq + 1) * 8, st, a, ctas);
-  if (a.accumulate)
+  const int items = a.n_seq * a.c.kvh * a.row_tiles, join_ctas = std::max(1, D * 2 / kKv4FinishThreads);
+  const bool one = a.row_tiles == 1;  // the account of a single row tile rides along with the join
+  const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(op->cfg.capacity, 4 * kKv4Block), cdiv(8 * op->sms, items))) : 0;
+  launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
+         ((size_t)a.n_seq + 3) * 8 + C::kQBytes, st, a, ctas, join_ctas);
+  if (a.accumulate && !one)
     launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(op->cfg.capacity, 64), 8 * op->sms / a.n_seq)), a.n_seq, a.c.kvh),
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
 }
@@ -173,6 +175,7 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
     blocks = (size_t)f.n_slots * c.kvh * c.bpp;
   }
   TRY(kv4_alloc(op, &c.data, blocks * 18 * f.head_dim, st));
+  TRY(kv4_alloc(op, &c.wide, 1, st));
   TRY(kv4_alloc(op, &c.err, 1, st));
   TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len) * 8, st));
   const size_t parts = (size_t)2 * op->sms * 3;  // at most three CTAs per SM, two partial items each

@@ -137,12 +137,46 @@ __device__ __forceinline__ int kv4_code(float x, float s, float up, float inv) {
   return x < 0.f ? -k : k;
 }
 
-// Decoded pair: 128 + n is exact in bf16 for a nibble n under the exponent of 128, subtracting
-// 136 leaves the code exactly, and the product with the scale is the format's only rounding.
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t scale2) {
-  const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
-  return as_u32(__hmul2(__hsub2(as_bf162(x), as_bf162(0x43084308u)), as_bf162(scale2)));
-}
+// Decoding a pair of codes to the bf16 values bf16(c * s).
+//
+// As the low bits of a bf16 number an integer N of up to 8 bits stands for exactly N 2^-133:
+// the subnormals and the first normal binade are one linear scale.  So a nibble n = c + 8 needs
+// no exponent patched in, only a mask, wherever it lies in the low byte, and one fma with the
+// format's single rounding gives the value, scaled by 2^-64 to keep both factors in range:
+//   n 2^-133 * (s 2^69) + (-8 s 2^-64) = (n - 8) s 2^-64          (nibble at bits 0-3)
+//   n 2^-129 * (s 2^65) + (-8 s 2^-64)                            (nibble at bits 4-7)
+// All three scale factors are exact for 2^-60 <= s <= 2^57.  Two ALU and two bf16 operations a
+// pair became 1.25 and 1.  A cache that has ever been given a group outside that range (the
+// flag `wide`, set by append) is decoded the plain way: 128 + n under the exponent of 128, minus
+// 136, times s.
+constexpr float kKv4Up = 18446744073709551616.f;  // 2^64
+template <bool WIDE>
+struct Kv4Scale {
+  uint32_t lo, hi, off;
+  __device__ __forceinline__ explicit Kv4Scale(uint32_t s2) {
+    if constexpr (WIDE) {
+      lo = s2;
+    } else {
+      lo = as_u32(__hmul2(as_bf162(s2), as_bf162(0x62006200u)));   // s 2^69
+      hi = as_u32(__hmul2(as_bf162(s2), as_bf162(0x60006000u)));   // s 2^65
+      off = as_u32(__hmul2(as_bf162(s2), as_bf162(0xA100A100u)));  // -8 s 2^-64
+    }
+  }
+  // nibbles J of both halves of w
+  template <int J>
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+    if constexpr (WIDE) {
+      const uint32_t x = ((w >> (4 * J)) & 0x000F000Fu) | 0x43004300u;
+      return as_u32(__hmul2(__hsub2(as_bf162(x), as_bf162(0x43084308u)), as_bf162(lo)));
+    } else {
+      const uint32_t x = J >= 2 ? w >> 8 : w;
+      return J & 1 ? as_u32(__hfma2(as_bf162(x & 0x00F000F0u), as_bf162(hi), as_bf162(off)))
+                   : as_u32(__hfma2(as_bf162(x & 0x000F000Fu), as_bf162(lo), as_bf162(off)));
+    }
+  }
+};
+constexpr float kKv4Narrow = 0x1p-60f, kKv4Wide = 0x1p57f;
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t scale2) { return Kv4Scale<true>(scale2).pair<0>(w); }
 
 // Does any earlier entry name the same slot as entry i?  (block-wide; every thread calls it)
 __device__ __forceinline__ bool kv4_repeated(const int* slots, int i, int slot) {
@@ -201,7 +235,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
   uint8_t* blk = a.c.data + (size_t)(b < 0 ? 0 : b) * O::kBlock;
   const int r = row % kKv4Block;
   const unsigned quad = 0xFu << ((threadIdx.x & 31) & ~3);
-  bool odd_value = false;
+  bool odd_value = false, wide = false;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     const Kv4Dense& x = kv ? a.v : a.k;
@@ -220,6 +254,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
     m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
     const __nv_bfloat16 sb = kv4_scale(m);
     const float s = bf16f(sb);
+    wide |= s > 0.f && !(s >= kKv4Narrow && s <= kKv4Wide);
     const float up = s < 1e-30f ? 0x1p100f : 1.f;  // keeps the reciprocal of a tiny scale finite
     const float inv = s > 0.f ? 1.f / (s * up) : 0.f;
     uint32_t n[8];
@@ -242,6 +277,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
     }
   }
   if (odd_value) set_err(a.c.err, G4_DEV_BAD_VALUE);
+  if (wide) *a.c.wide = 1;
   if (o == 0 && a.c.pos && b >= 0) {
     const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
     a.c.pos[b * kKv4Block + r] = a.positions ? __ldcg(a.positions + at) : row;

@@ -92,6 +92,7 @@ struct Kv4Att {
   static constexpr int kSets = kWarps / 4;             // sets of four warps take tiles in turn
   static constexpr int kBpw = D >= 256 ? 1 : 256 / D;  // blocks a warp takes of a tile
   static constexpr int kBlocks = 4 * kBpw;             // blocks of a tile
+  static constexpr int kNB = kBpw;                     // blocks a warp takes through the softmax at a time
   static constexpr int kKeys = kBlocks * kKv4Block;    // keys of a tile: 256, 128, 64, 64
   static constexpr int kTile = kBlocks * 18 * D;       // bytes of a tile: 18 KB (D = 512: 36 KB)
   static constexpr int kThreads = 32 * (kWarps + 1);
@@ -119,8 +120,13 @@ __device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* firs
     int slot, len, m, t0;
     bool ok = kv4_seq(a, i, &slot, &len, &m);
     if (!ok && report) set_err(a.c.err, kv4_seq_error(a, slot));
-    if (a.accumulate && ok)  // a slot that an earlier sequence names is skipped
-      for (int j = 0; j < i; ++j) ok = ok && __ldcg(a.slots + j) != slot;
+    if (a.accumulate && ok) {  // a slot that an earlier sequence names is skipped
+      int same = 0;
+#pragma unroll 4
+      for (int j = 0; j < i; ++j) same |= __ldcg(a.slots + j) == slot;
+      ok = !same;
+      if (same && report) set_err(a.c.err, G4_DEV_BAD_SLOT);
+    }
     first[i + 1] = ok ? (long long)kv4_tiles<KEYS>(a, len, m, &t0) * a.c.kvh * a.row_tiles : -1;
   }
   __syncthreads();
@@ -177,108 +183,135 @@ __device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long lon
   return r;
 }
 
-// ------------------------------------------------------------------------- the kernel
+// ------------------------------------------------------------------------- the pieces
+// Queries of rows row0 .. row0 + 7 of (sequence, KV head) as bf16 parts in the order of the mma's
+// B operand: piece (part, w) of lane l is row l / 4, numbers (l % 4) D/4 + 8w .. + 7.
 template <int D, int DT>
-__global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCtas) kv4_attend_kernel(const Kv4AttendArgs a) {
+__device__ __forceinline__ void kv4_stage_q(const Kv4AttendArgs& a, uint4* qs, int seq, int head, int row0, int n_rows,
+                                            int tid, int threads) {
+  constexpr int W = D / 32, QP = Kv4Att<D, DT>::kQP;
+  for (int e = tid; e < W * 32; e += threads) {
+    const int w = e >> 5, l = e & 31, row = row0 + (l >> 2);
+    float v[8];
+    if (row < n_rows) {
+      const int tok = row / a.group, hq = head * a.group + row % a.group;
+      kv4_load8(a.q, (long)seq * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head + (l & 3) * (D / 4) + 8 * w, v);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = 0.f;
+    }
+    uint32_t p[4][QP];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) kv4_split<QP>(v[2 * x], v[2 * x + 1], p[x]);
+#pragma unroll
+    for (int part = 0; part < QP; ++part) qs[(part * W + w) * 32 + l] = make_uint4(p[0][part], p[1][part], p[2][part], p[3][part]);
+  }
+}
+
+// The scales of one key's numbers that lane t holds, [t D/4, (t+1) D/4): one bf16 per 32 of them
+// (D = 64: of half a group).  two(k): the k-th in both halves of a bf16x2.
+template <int D>
+struct Kv4KeyScales {
+  static constexpr int N = D >= 128 ? D / 128 : 1;
+  uint32_t raw[(N + 1) / 2];
+  __device__ __forceinline__ uint32_t two(int k) const { return __byte_perm(raw[k >> 1], 0u, k & 1 ? 0x3232u : 0x1010u); }
+};
+template <int D>
+__device__ __forceinline__ Kv4KeyScales<D> kv4_key_scales(const uint8_t* ks, int key, int t) {
+  Kv4KeyScales<D> r;
+  const uint8_t* p = ks + key * (D / 16) + (D >= 128 ? t * (D / 64) : (t >> 1) * 2);
+  if constexpr (D == 512) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    r.raw[0] = u.x;
+    r.raw[1] = u.y;
+  } else if constexpr (D == 256) {
+    r.raw[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    r.raw[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+  return r;
+}
+
+// Scores of NB blocks of 16 keys by eight query rows, summed over the head dim (before the
+// softmax scale): c[b] in the mma's accumulator order.  codes(b, i): 16-byte piece i of block b;
+// scales(b, half): scales of key g + 8 half.
+template <int D, int QP, int NB, bool WIDE, class Codes, class Scales>
+__device__ __forceinline__ void kv4_scores(const uint4* qs, int lane, Codes codes, Scales scales, float (&c)[NB][4]) {
+  constexpr int W = D / 32, N = Kv4KeyScales<D>::N;
+  float d[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[b][j] = d[b][j] = 0.f;
+#pragma unroll
+  for (int grp = 0; grp < N; ++grp) {  // a lane's numbers of one group: W / 2 / N pieces
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Kv4Scale<WIDE> sg(scales(b, 0).two(grp)), sh(scales(b, 1).two(grp));
+#pragma unroll
+      for (int i = grp * (W / 2 / N); i < (grp + 1) * (W / 2 / N); ++i) {
+        const uint4 u = codes(b, i);  // row g: words 2i, 2i + 1; row g + 8: same
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t ug = e ? u.y : u.x, uh = e ? u.w : u.z;
+          const uint32_t a0 = sg.template pair<0>(ug), a1 = sh.template pair<0>(uh), a2 = sg.template pair<1>(ug), a3 = sh.template pair<1>(uh);
+          const uint32_t b0 = sg.template pair<2>(ug), b1 = sh.template pair<2>(uh), b2 = sg.template pair<3>(ug), b3 = sh.template pair<3>(uh);
+#pragma unroll
+          for (int part = 0; part < QP; ++part) {
+            const uint4 qv = qs[(part * W + 2 * i + e) * 32 + lane];
+            kv4_mma(c[b], a0, a1, a2, a3, qv.x, qv.y);
+            kv4_mma(d[b], b0, b1, b2, b3, qv.z, qv.w);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[b][j] += d[b][j];
+}
+
+// ------------------------------------------------------------------------- the kernel
+// What the warps of a CTA share.
+template <int D, int DT>
+struct Kv4Shared {
+  uint8_t* ring;
+  uint4* qs;
+  float4* os;
+  float2* mls;        // [warp][8]
+  uint64_t *full, *empty;
+  uint32_t* held;     // [8]: blocks of a stage that hold rows
+  volatile int* abort_flag;
+  long long* first;
+  __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages) {
+    using C = Kv4Att<D, DT>;
+    ring = smem;
+    qs = reinterpret_cast<uint4*>(ring + (size_t)stages * C::kTile);
+    os = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(qs) + C::kQBytes);
+    mls = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(os) + C::kOBytes);
+    full = reinterpret_cast<uint64_t*>(mls + C::kWarps * 8);
+    empty = full + 8;
+    held = reinterpret_cast<uint32_t*>(empty + 8);
+    abort_flag = reinterpret_cast<volatile int*>(held + 8);
+    first = reinterpret_cast<long long*>(full + 32);
+  }
+};
+
+template <int D, int DT, bool WIDE>
+__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, long long g0, long long g1) {
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
-  constexpr int W = D / 32;  // words of a key (or value pair) per lane
-  extern __shared__ __align__(128) uint8_t kv4_smem[];
-  uint8_t* ring = kv4_smem;
-  uint4* qs = reinterpret_cast<uint4*>(ring + (size_t)a.stages * C::kTile);
-  float4* os = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(qs) + C::kQBytes);
-  float2* mls = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(os) + C::kOBytes);  // [warp][8]
-  uint64_t* full = reinterpret_cast<uint64_t*>(mls + C::kWarps * 8);
-  uint64_t* empty = full + 8;
-  uint32_t* held = reinterpret_cast<uint32_t*>(empty + 8);  // [8]: blocks of a stage that hold rows
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(held + 8);
-  long long* first = reinterpret_cast<long long*>(full + 32);
-
+  constexpr int W = D / 32, NB = C::kNB;  // words of a key (or value pair) per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
-  pdl_wait();
-  pdl_trigger();
-  kv4_plan<C::kKeys>(a, first, blockIdx.x == 0);
-  const long long total = first[a.n_seq];
-  const long long span = kv4_span(a, total, gridDim.x);
-  const long long g0 = min(total, (long long)blockIdx.x * span), g1 = min(total, g0 + span);
-
-  if (warp == C::kWarps) {
-    // ------------------------------------------------ producer: tiles into the ring
-    int it = 0;
-    bool stop = false;
-    for (long long at = g0; at < g1 && !stop;) {
-      const Kv4Run r = kv4_run<C::kKeys>(a, first, at, g1);
-      const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
-      for (int x = 0; x < r.tiles; ++x, ++it) {
-        const int s = it % a.stages;
-        if (it >= a.stages && !mbar_wait(&empty[s], (it / a.stages - 1) & 1, abort_flag)) {
-          stop = true;
-          break;
-        }
-        // lane b looks block b up; neighbours in the pool travel in one copy
-        const int b = (r.tile + x) * C::kBlocks + lane;
-        const bool want = lane < C::kBlocks && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
-        const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
-        if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
-        const long before = __shfl_up_sync(0xFFFFFFFFu, at_b, 1);
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
-        const uint32_t joins = __ballot_sync(0xFFFFFFFFu, at_b >= 0 && lane > 0 && before >= 0 && before == at_b - 1);
-        if (lane == 0) {
-          held[s] = have;
-          mbar_expect_tx(&full[s], __popc(have) * O::kBlock);
-        }
-        __syncwarp();
-        if (at_b >= 0 && !((joins >> lane) & 1)) {
-          const uint32_t after = joins >> 1 >> lane;  // ones while the next block joins
-          const int n = 1 + __ffs(~after) - 1;
-          bulk_g2s(ring + (size_t)s * C::kTile + lane * O::kBlock, a.c.data + (size_t)at_b * O::kBlock, n * O::kBlock,
-                   &full[s]);
-        }
-      }
-      at += r.tiles;
-    }
-    if (stop) {
-      if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
-      *abort_flag = 1;
-    }
-    // copies in flight land before the CTA's memory goes, whatever the consumers do
-    for (int k = max(0, it - a.stages); k < it; ++k) mbar_wait_drain(&full[k % a.stages], (k / a.stages) & 1);
-    return;
-  }
-
-  // ---------------------------------------------------- consumers
   const int set = warp >> 2, wq = warp & 3;
+  const float score_scale = WIDE ? a.scale : a.scale * kKv4Up;
   int it = 0, piece = 0;
   for (long long at = g0; at < g1; ++piece) {
-    const Kv4Run r = kv4_run<C::kKeys>(a, first, at, g1);
+    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, at, g1);
     const int n_rows = r.m * a.group, row0 = r.row_tile * 8;
-    // ---- queries of the item's eight rows, as bf16 parts in fragment order
     named_bar_sync(1, 32 * C::kWarps);
-    for (int e = threadIdx.x; e < W * 32; e += 32 * C::kWarps) {
-      const int w = e >> 5, l = e & 31, row = row0 + (l >> 2);  // lane l: row l / 4, numbers (l % 4) D/4 + 8w ..
-      float v[8];
-      if (row < n_rows) {
-        const int tok = row / a.group, hq = r.head * a.group + row % a.group;
-        kv4_load8(a.q, (long)r.seq * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head + (l & 3) * (D / 4) + 8 * w, v);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = 0.f;
-      }
-      uint32_t p[4][C::kQP];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) kv4_split<C::kQP>(v[2 * x], v[2 * x + 1], p[x]);
-#pragma unroll
-      for (int part = 0; part < C::kQP; ++part)
-        qs[(part * W + w) * 32 + l] = make_uint4(p[0][part], p[1][part], p[2][part], p[3][part]);
-    }
+    kv4_stage_q<D, DT>(a, sh.qs, r.seq, r.head, row0, n_rows, threadIdx.x, 32 * C::kWarps);
     named_bar_sync(1, 32 * C::kWarps);
 
     float acc[D / 16][4];
@@ -297,47 +330,33 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
     for (int x = 0; x < r.tiles; ++x, ++it) {
       if (C::kSets > 1 && it % C::kSets != set) continue;
       const int s = it % a.stages;
-      if (!mbar_wait(&full[s], (it / a.stages) & 1, abort_flag)) *abort_flag = 1;
-      const bool dead = *abort_flag;
-      const uint32_t have = dead ? 0u : held[s];
-#pragma unroll 1
-      for (int bb = 0; bb < C::kBpw; ++bb) {
-        const int bi = bb * 4 + wq;
-        if (!((have >> bi) & 1)) continue;
-        const uint8_t* blk = ring + (size_t)s * C::kTile + bi * O::kBlock;
-        const int j0 = ((r.tile + x) * C::kBlocks + bi) * kKv4Block;
-        // scores of 16 keys (rows of the product) by 8 query rows
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint4* kc = reinterpret_cast<const uint4*>(blk) + lane;
-        const uint16_t* ks = reinterpret_cast<const uint16_t*>(blk + O::kKs);
+      if (!mbar_wait(&sh.full[s], (it / a.stages) & 1, sh.abort_flag)) *sh.abort_flag = 1;
+      const uint32_t have = *sh.abort_flag ? 0u : sh.held[s] >> (wq * C::kBpw) & ((1u << C::kBpw) - 1u);
+      if (have) {
+        // the warp's blocks of the tile are neighbours: 16 NB consecutive keys
+        const uint8_t* blk = sh.ring + (size_t)s * C::kTile + wq * C::kBpw * O::kBlock;
+        const int j0 = ((r.tile + x) * C::kBlocks + wq * C::kBpw) * kKv4Block;
+        float c[NB][4];
+        kv4_scores<D, C::kQP, NB, WIDE>(
+            sh.qs, lane, [&](int b, int i) { return reinterpret_cast<const uint4*>(blk + b * O::kBlock)[i * 32 + lane]; },
+            [&](int b, int half) { return kv4_key_scales<D>(blk + b * O::kBlock + O::kKs, g + 8 * half, t); }, c);
+        float n0 = -INFINITY, n1 = -INFINITY;
+        const bool edge = have != (1u << C::kBpw) - 1u || j0 + 16 * NB - 1 > last_min || j0 <= low_max;
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          const uint4 u = kc[i * 32];  // row g: words 2i, 2i + 1; row g + 8: same
-          const int grp = (t * (D / 4) + 16 * i) / kKv4Group;  // 16 numbers never straddle a group
-          const uint32_t sg = 0x10001u * ks[g * (D / 32) + grp], sh = 0x10001u * ks[(g + 8) * (D / 32) + grp];
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t ug = e ? u.y : u.x, uh = e ? u.w : u.z;
-            const uint32_t a0 = kv4_pair(ug, sg), a1 = kv4_pair(uh, sh), a2 = kv4_pair(ug >> 4, sg), a3 = kv4_pair(uh >> 4, sh);
-            const uint32_t b0 = kv4_pair(ug >> 8, sg), b1 = kv4_pair(uh >> 8, sh), b2 = kv4_pair(ug >> 12, sg), b3 = kv4_pair(uh >> 12, sh);
-#pragma unroll
-            for (int part = 0; part < C::kQP; ++part) {
-              const uint4 qv = qs[(part * W + 2 * i + e) * 32 + lane];
-              kv4_mma(c0, a0, a1, a2, a3, qv.x, qv.y);
-              kv4_mma(c1, b0, b1, b2, b3, qv.z, qv.w);
-            }
+          for (int j = 0; j < 4; ++j) c[b][j] *= score_scale;  // keys g (0, 1) and g + 8 (2, 3); rows 2t, 2t + 1
+          if (edge) {
+            const int ja = j0 + 16 * b + g, jb = ja + 8;
+            const bool gone = !((have >> b) & 1);  // no page, or wholly outside: whatever the ring holds there
+            if (gone || ja > last0 || ja <= low0) c[b][0] = -INFINITY;
+            if (gone || ja > last1 || ja <= low1) c[b][1] = -INFINITY;
+            if (gone || jb > last0 || jb <= low0) c[b][2] = -INFINITY;
+            if (gone || jb > last1 || jb <= low1) c[b][3] = -INFINITY;
           }
+          n0 = fmaxf(n0, fmaxf(c[b][0], c[b][2]));
+          n1 = fmaxf(n1, fmaxf(c[b][1], c[b][3]));
         }
-        float s00 = (c0[0] + c1[0]) * a.scale, s01 = (c0[1] + c1[1]) * a.scale;  // key g: rows 2t, 2t + 1
-        float s10 = (c0[2] + c1[2]) * a.scale, s11 = (c0[3] + c1[3]) * a.scale;  // key g + 8
-        if (j0 + kKv4Block - 1 > last_min || j0 <= low_max) {
-          const int ja = j0 + g, jb = ja + 8;
-          if (ja > last0 || ja <= low0) s00 = -INFINITY;
-          if (ja > last1 || ja <= low1) s01 = -INFINITY;
-          if (jb > last0 || jb <= low0) s10 = -INFINITY;
-          if (jb > last1 || jb <= low1) s11 = -INFINITY;
-        }
-        float n0 = fmaxf(s00, s10), n1 = fmaxf(s01, s11);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, o));
@@ -361,40 +380,49 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
           }
         }
         const float z0 = mx0 == -INFINITY ? 0.f : mx0, z1 = mx1 == -INFINITY ? 0.f : mx1;
-        const float p00 = kv4_exp2(s00 - z0), p01 = kv4_exp2(s01 - z1), p10 = kv4_exp2(s10 - z0), p11 = kv4_exp2(s11 - z1);
-        l0 += p00 + p10;
-        l1 += p01 + p11;
-        uint32_t pa[C::kPP], pb[C::kPP];
-        kv4_split<C::kPP>(p00, p01, pa);
-        kv4_split<C::kPP>(p10, p11, pb);
 #pragma unroll
-        for (int part = 0; part < C::kPP; ++part) {
-          pa[part] = kv4_transpose(pa[part]);
-          pb[part] = kv4_transpose(pb[part]);
-        }
-        // output: 16 numbers of the values (rows of the product) by 8 query rows, over 16 keys
-        const uint4* vc = reinterpret_cast<const uint4*>(blk + O::kV) + lane;
-        const uint32_t* vs = reinterpret_cast<const uint32_t*>(blk + O::kVs);
+        for (int b = 0; b < NB; ++b) {
+          if (edge && !((have >> b) & 1)) continue;  // its codes may be anything: not even times zero
+          const float p00 = kv4_exp2(c[b][0] - z0), p01 = kv4_exp2(c[b][1] - z1);
+          const float p10 = kv4_exp2(c[b][2] - z0), p11 = kv4_exp2(c[b][3] - z1);
+          l0 += p00 + p10;
+          l1 += p01 + p11;
+          uint32_t pa[C::kPP], pb[C::kPP];
+          kv4_split<C::kPP>(p00, p01, pa);
+          kv4_split<C::kPP>(p10, p11, pb);
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          const uint4 u = vc[i * 32];  // row pair t: words 2i, 2i + 1; pair t + 4: same
-          const int grp = (g * (D / 8) + 8 * i) / kKv4Group;
-          const uint32_t sa = vs[grp * 8 + t], sb = vs[grp * 8 + t + 4];
+          for (int part = 0; part < C::kPP; ++part) {
+            pa[part] = kv4_transpose(pa[part]);
+            pb[part] = kv4_transpose(pb[part]);
+          }
+          // output: 16 numbers of the values (rows of the product) by 8 query rows, over 16 keys
+          const uint4* vc = reinterpret_cast<const uint4*>(blk + b * O::kBlock + O::kV) + lane;
+          const uint32_t* vs = reinterpret_cast<const uint32_t*>(blk + b * O::kBlock + O::kVs);
+          constexpr int G = D > 256 ? D / 256 : 1;  // groups among a lane's D / 8 numbers
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t ua = e ? u.y : u.x, ub = e ? u.w : u.z;
-            const uint32_t a0 = kv4_pair(ua, sa), a1 = kv4_pair(ua >> 4, sa), a2 = kv4_pair(ub, sb), a3 = kv4_pair(ub >> 4, sb);
-            const uint32_t b0 = kv4_pair(ua >> 8, sa), b1 = kv4_pair(ua >> 12, sa), b2 = kv4_pair(ub >> 8, sb), b3 = kv4_pair(ub >> 12, sb);
+          for (int k = 0; k < G; ++k) {
+            const int grp = D >= 256 ? g * G + k : g * D / 256;
+            const Kv4Scale<WIDE> sa(vs[grp * 8 + t]), sb(vs[grp * 8 + t + 4]);
 #pragma unroll
-            for (int part = 0; part < C::kPP; ++part) {
-              kv4_mma(acc[4 * i + 2 * e], a0, a1, a2, a3, pa[part], pb[part]);
-              kv4_mma(acc[4 * i + 2 * e + 1], b0, b1, b2, b3, pa[part], pb[part]);
+            for (int i = k * (W / 2 / G); i < (k + 1) * (W / 2 / G); ++i) {
+              const uint4 u = vc[i * 32];  // row pair t: words 2i, 2i + 1; pair t + 4: same
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t ua = e ? u.y : u.x, ub = e ? u.w : u.z;
+                const uint32_t a0 = sa.template pair<0>(ua), a1 = sa.template pair<1>(ua), a2 = sb.template pair<0>(ub), a3 = sb.template pair<1>(ub);
+                const uint32_t b0 = sa.template pair<2>(ua), b1 = sa.template pair<3>(ua), b2 = sb.template pair<2>(ub), b3 = sb.template pair<3>(ub);
+#pragma unroll
+                for (int part = 0; part < C::kPP; ++part) {
+                  kv4_mma(acc[4 * i + 2 * e], a0, a1, a2, a3, pa[part], pb[part]);
+                  kv4_mma(acc[4 * i + 2 * e + 1], b0, b1, b2, b3, pa[part], pb[part]);
+                }
+              }
             }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
     }
     at += r.tiles;
 
@@ -405,31 +433,35 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
     }
     if (g == 0) {
-      mls[warp * 8 + 2 * t] = make_float2(mx0, l0);
-      mls[warp * 8 + 2 * t + 1] = make_float2(mx1, l1);
+      sh.mls[warp * 8 + 2 * t] = make_float2(mx0, l0);
+      sh.mls[warp * 8 + 2 * t + 1] = make_float2(mx1, l1);
     }
     named_bar_sync(1, 32 * C::kWarps);
     float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      M0 = fmaxf(M0, mls[w * 8 + 2 * t].x);
-      M1 = fmaxf(M1, mls[w * 8 + 2 * t + 1].x);
+      M0 = fmaxf(M0, sh.mls[w * 8 + 2 * t].x);
+      M1 = fmaxf(M1, sh.mls[w * 8 + 2 * t + 1].x);
     }
     const float Z0 = M0 == -INFINITY ? 0.f : M0, Z1 = M1 == -INFINITY ? 0.f : M1;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      const float2 u = mls[w * 8 + 2 * t], v = mls[w * 8 + 2 * t + 1];
+      const float2 u = sh.mls[w * 8 + 2 * t], v = sh.mls[w * 8 + 2 * t + 1];
       L0 += u.y * kv4_exp2(u.x - Z0);
       L1 += v.y * kv4_exp2(v.x - Z1);
     }
-    const float f0 = kv4_exp2(mx0 - Z0), f1 = kv4_exp2(mx1 - Z1);
+    const bool whole = r.first && r.last;
+    // a whole item is divided by its sum here, a partial one when the spans are joined
+    const float up = WIDE ? 1.f : kKv4Up;
+    const float f0 = kv4_exp2(mx0 - Z0) * up * (whole ? (L0 != 0.f ? 1.f / L0 : 0.f) : 1.f);
+    const float f1 = kv4_exp2(mx1 - Z1) * up * (whole ? (L1 != 0.f ? 1.f / L1 : 0.f) : 1.f);
     auto put = [&](bool add) {
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int sel = 0; sel < 2; ++sel) {
           const float f = sel ? f1 : f0;
-          float4* p = &os[((wq * W + w) * 2 + sel) * 32 + lane];
+          float4* p = &sh.os[((wq * W + w) * 2 + sel) * 32 + lane];
           float4 v = make_float4(acc[2 * w][sel] * f, acc[2 * w][2 + sel] * f, acc[2 * w + 1][sel] * f, acc[2 * w + 1][2 + sel] * f);
           if (add) {
             const float4 u = *p;
@@ -449,15 +481,14 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
       put(false);
     }
     named_bar_sync(1, 32 * C::kWarps);
-    const bool whole = r.first && r.last;
     const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
-    // thread e: lane l of word w: numbers (l / 4) D/8 + 4w .. of query row 2 (l % 4) + sel
+    // entry e: lane l of word w: numbers (l / 4) D/8 + 4w .. of query row 2 (l % 4) + sel
     for (int e = threadIdx.x; e < W * 64; e += 32 * C::kWarps) {
       const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6;
-      float4 v = os[e];
+      float4 v = sh.os[e];
 #pragma unroll
       for (int k = 1; k < 4; ++k) {
-        const float4 u = os[k * W * 64 + e];
+        const float4 u = sh.os[k * W * 64 + e];
         v.x += u.x;
         v.y += u.y;
         v.z += u.z;
@@ -468,16 +499,8 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
       } else {
         const int row = row0 + 2 * (l & 3) + sel;
         if (row < n_rows) {
-          float L = 0.f, M = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < C::kWarps; ++k) M = fmaxf(M, mls[k * 8 + (row & 7)].x);
-          const float Z = M == -INFINITY ? 0.f : M;
-#pragma unroll
-          for (int k = 0; k < C::kWarps; ++k) L += mls[k * 8 + (row & 7)].y * kv4_exp2(mls[k * 8 + (row & 7)].x - Z);
-          const float inv = L != 0.f ? 1.f / L : 0.f;
           const int tok = row / a.group, hq = r.head * a.group + row % a.group;
-          kv4_store4(a.out, (long)r.seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
-                     make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+          kv4_store4(a.out, (long)r.seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w, v);
         }
       }
     }
@@ -492,34 +515,156 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
       }
     }
   }
-  if (*abort_flag && threadIdx.x == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+  if (*sh.abort_flag && threadIdx.x == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
 }
 
-// ---------------------------------------------------------------------------- the join
-// One CTA per item and quarter of its numbers: adds the partial sums that the spans left, in
-// span order.  Items without keys (and skipped sequences) get zeros.  ctas: the grid that ran.
-constexpr int kKv4JoinThreads = 128;
-
-template <int D, int KEYS>
-__global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(const Kv4AttendArgs a, int ctas) {
-  constexpr int W = D / 32;
-  extern __shared__ __align__(16) long long kv4_first[];
-  __shared__ float sM[8], sL[8];
-  const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles;
-  const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
+template <int D, int DT>
+__global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCtas) kv4_attend_kernel(const Kv4AttendArgs a) {
+  using O = Kv4Off<D>;
+  using C = Kv4Att<D, DT>;
+  extern __shared__ __align__(128) uint8_t kv4_smem[];
+  const Kv4Shared<D, DT> sh(kv4_smem, a.stages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 4);
+    }
+    *sh.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
   pdl_wait();
   pdl_trigger();
-  kv4_plan<KEYS>(a, kv4_first, false);
+  const int wide = __ldcg(a.c.wide);
+  kv4_plan<C::kKeys>(a, sh.first, blockIdx.x == 0);
+  const long long total = sh.first[a.n_seq];
+  const long long span = kv4_span(a, total, gridDim.x);
+  const long long g0 = min(total, (long long)blockIdx.x * span), g1 = min(total, g0 + span);
+  if (warp < C::kWarps) {
+    if (wide) kv4_consume<D, DT, true>(a, sh, g0, g1);
+    else kv4_consume<D, DT, false>(a, sh, g0, g1);
+    return;
+  }
+  // ---- producer: tiles into the ring
+  int it = 0;
+  bool stop = false;
+  for (long long at = g0; at < g1 && !stop;) {
+    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, at, g1);
+    const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
+    for (int x = 0; x < r.tiles; ++x, ++it) {
+      const int s = it % a.stages;
+      if (it >= a.stages && !mbar_wait(&sh.empty[s], (it / a.stages - 1) & 1, sh.abort_flag)) {
+        stop = true;
+        break;
+      }
+      // lane b looks block b up; neighbours in the pool travel in one copy
+      const int b = (r.tile + x) * C::kBlocks + lane;
+      const bool want = lane < C::kBlocks && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
+      const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
+      if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
+      const long before = __shfl_up_sync(0xFFFFFFFFu, at_b, 1);
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
+      const uint32_t joins = __ballot_sync(0xFFFFFFFFu, at_b >= 0 && lane > 0 && before >= 0 && before == at_b - 1);
+      if (lane == 0) {
+        sh.held[s] = have;
+        mbar_expect_tx(&sh.full[s], __popc(have) * O::kBlock);
+      }
+      __syncwarp();
+      if (at_b >= 0 && !((joins >> lane) & 1)) {
+        const uint32_t after = joins >> 1 >> lane;  // ones while the next block joins
+        const int n = __ffs(~after);
+        bulk_g2s(sh.ring + (size_t)s * C::kTile + lane * O::kBlock, a.c.data + (size_t)at_b * O::kBlock, n * O::kBlock,
+                 &sh.full[s]);
+      }
+    }
+    at += r.tiles;
+  }
+  if (stop) {
+    if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+    *sh.abort_flag = 1;
+  }
+  // copies in flight land before the CTA's memory goes, whatever the consumers do
+  for (int k = max(0, it - a.stages); k < it; ++k) mbar_wait_drain(&sh.full[k % a.stages], (k / a.stages) & 1);
+}
+
+// -------------------------------------------------------------------------- the finish
+// Second launch.  CTAs with blockIdx.y < join_ctas add the partial sums that the spans left of
+// item blockIdx.x, in span order, each a share of its numbers; items without keys (and skipped
+// sequences) get zeros.  With an account and one item per (sequence, KV head), the others each
+// take a run of the item's keys and add the weights those received, p = 2^(s - lse), recomputed
+// from the keys: a score per key and query row kept from the first launch would cost 64 bytes of
+// traffic a key and a buffer of its own, the codes cost 9/16 D and are still in L2 for the most.
+constexpr int kKv4FinishThreads = 128;
+
+// Adds what the keys `key` and key + 8 of a block receive from eight query rows (this lane: rows
+// 2t and 2t + 1), given the log2 of each row's softmax sum.
+template <int D, int DT, bool WIDE>
+__device__ __forceinline__ void kv4_gain_tile(const Kv4AttendArgs& a, const uint4* qs, const uint8_t* blk, int lane,
+                                              const uint4 (&u)[D / 64], const Kv4KeyScales<D>& s0, const Kv4KeyScales<D>& s1,
+                                              int key, const float* lse8, int len, int m, int row0, int n_rows,
+                                              float& gain0, float& gain1) {
+  const int t = lane & 3;
+  float c[1][4];
+  kv4_scores<D, Kv4Att<D, DT>::kQP, 1, WIDE>(qs, lane, [&](int, int i) { return u[i]; },
+                                             [&](int, int half) { return half ? s1 : s0; }, c);
+  const float sc = WIDE ? a.scale : a.scale * kKv4Up, e0 = lse8[2 * t], e1 = lse8[2 * t + 1];
+  const int ra = row0 + 2 * t, rb = ra + 1;
+  const int last0 = ra < n_rows ? len - m + ra / a.group : -1, last1 = rb < n_rows ? len - m + rb / a.group : -1;
+  if (key <= last0) gain0 += kv4_exp2(c[0][0] * sc - e0);
+  if (key <= last1) gain0 += kv4_exp2(c[0][1] * sc - e1);
+  if (key + 8 <= last0) gain1 += kv4_exp2(c[0][2] * sc - e0);
+  if (key + 8 <= last1) gain1 += kv4_exp2(c[0][3] * sc - e1);
+}
+// A block's codes and scales of this lane, from global memory.
+template <int D>
+struct Kv4KeyBlock {
+  uint4 u[D / 64];
+  Kv4KeyScales<D> s0, s1;
+  __device__ __forceinline__ void load(const uint8_t* blk, int lane) {
+    using O = Kv4Off<D>;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) u[k] = __ldcg(reinterpret_cast<const uint4*>(blk) + k * 32 + lane);
+    s0 = kv4_key_scales<D>(blk + O::kKs, lane >> 2, lane & 3);
+    s1 = kv4_key_scales<D>(blk + O::kKs, (lane >> 2) + 8, lane & 3);
+  }
+};
+// Adds the gains of keys g and g + 8 of block b (pool index at) to the account.
+__device__ __forceinline__ void kv4_add_gain(const Kv4AttendArgs& a, long at, int b, int len, int lane, float gain0, float gain1) {
+  gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 1);
+  gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 1);
+  gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 2);
+  gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 2);
+  const int g = lane >> 2, t = lane & 3;
+  if (t < 2 && b * kKv4Block + g + 8 * t < len) a.c.weight[at * kKv4Block + g + 8 * t] += t ? gain1 : gain0;
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4AttendArgs a, int ctas, int join_ctas) {
+  using C = Kv4Att<D, DT>;
+  using O = Kv4Off<D>;
+  constexpr int W = D / 32;
+  extern __shared__ __align__(128) uint8_t kv4_smem[];
+  long long* first = reinterpret_cast<long long*>(kv4_smem);
+  uint4* qs = reinterpret_cast<uint4*>(kv4_smem + ((size_t)(a.n_seq + 1) * 8 + 15) / 16 * 16);
+  __shared__ float2 part_ml[4][8];
+  __shared__ float sM[8], sL[8], sE[8];
+  const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
+  const bool join = (int)blockIdx.y < join_ctas;
+  pdl_wait();
+  pdl_trigger();
+  const int wide = __ldcg(a.c.wide);
+  kv4_plan<C::kKeys>(a, first, false);
   int slot, len, m;
   const bool ok = kv4_seq(a, i, &slot, &len, &m);
-  const long long total = kv4_first[a.n_seq], span = kv4_span(a, total, ctas);
-  const long long n = (kv4_first[i + 1] - kv4_first[i]) / per_seq;
-  const long long t0 = kv4_first[i] + n * x, t1 = t0 + n;  // the item's tiles
+  const long long total = first[a.n_seq], span = kv4_span(a, total, ctas);
+  const long long n = (first[i + 1] - first[i]) / per_seq;
+  const long long t0 = first[i] + n * x, t1 = t0 + n;  // the item's tiles
   const int n_rows = (ok ? m : a.q_len) * a.group;
-  const long long c0 = n ? t0 / span : 0, c1 = n ? (t1 - 1) / span : 0;
-  // rows of query tokens beyond the sequence's own
-  if (a.zero_rest && ok && m < a.q_len) {
-    for (int e = blockIdx.y * kKv4JoinThreads + threadIdx.x; e < W * 64; e += gridDim.y * kKv4JoinThreads) {
+  const int c0 = n ? (int)(t0 / span) : 0, c1 = n ? (int)((t1 - 1) / span) : 0;
+  const bool whole = n && c0 == c1;  // one CTA had the whole item: its rows are done
+  if (join && a.zero_rest && ok && m < a.q_len) {  // rows of query tokens beyond the sequence's own
+    for (int e = blockIdx.y * kKv4FinishThreads + tid; e < W * 64; e += join_ctas * kKv4FinishThreads) {
       const int l = e & 31, row = rt * 8 + 2 * (l & 3) + ((e >> 5) & 1);
       if (row < n_rows || row >= a.q_len * a.group) continue;
       kv4_store4(a.out, (long)i * a.out.seq + (long)(row / a.group) * a.out.row +
@@ -527,139 +672,129 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(const Kv4Atte
                  make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
-  if (n && c0 == c1) return;  // one CTA had the whole item
+  if (join ? whole : n == 0) return;
   // CTA c's partial sums of this item: slot 0 when the item opens its span, else slot 1
-  auto part = [&](long long c) { return c * 2 + (t0 > c * span ? 1 : 0); };
-  if (threadIdx.x < 8) {
+  auto part = [&](int c) { return (long)c * 2 + (t0 > c * span ? 1 : 0); };
+  if (!whole) {  // every thread a row and every 16th span, then over the threads
     float M = -INFINITY, L = 0.f;
     if (n) {
-      for (long long c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[part(c) * 8 + threadIdx.x].x);
-      const float Z = M == -INFINITY ? 0.f : M;
-      for (long long c = c0; c <= c1; ++c) {
-        const float2 u = a.part_ml[part(c) * 8 + threadIdx.x];
-        L += u.y * kv4_exp2(u.x - Z);
+      for (int c = c0 + (tid >> 3); c <= c1; c += kKv4FinishThreads / 8) {
+        const float2 u = __ldcg(&a.part_ml[part(c) * 8 + (tid & 7)]);
+        const float nm = fmaxf(M, u.x), z = nm == -INFINITY ? 0.f : nm;
+        L = L * kv4_exp2(M - z) + u.y * kv4_exp2(u.x - z);
+        M = nm;
       }
     }
-    sM[threadIdx.x] = M == -INFINITY ? 0.f : M;
-    sL[threadIdx.x] = L;
-    if (blockIdx.y == 0) a.lse[(long)item * 8 + threadIdx.x] = L != 0.f ? M + log2f(L) : INFINITY;
+    auto merge = [&](float m2, float l2) {
+      const float nm = fmaxf(M, m2), z = nm == -INFINITY ? 0.f : nm;
+      L = L * kv4_exp2(M - z) + l2 * kv4_exp2(m2 - z);
+      M = nm;
+    };
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
+      merge(m2, l2);
+    }
+    if (lane < 8) part_ml[warp][lane] = make_float2(M, L);
+    __syncthreads();
+    if (tid < 8) {
+      M = part_ml[0][tid].x;
+      L = part_ml[0][tid].y;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) merge(part_ml[w][tid].x, part_ml[w][tid].y);
+      sM[tid] = M == -INFINITY ? 0.f : M;
+      sL[tid] = L;
+      sE[tid] = L != 0.f ? M + log2f(L) : INFINITY;
+      if (blockIdx.y == 0) a.lse[(long)item * 8 + tid] = sE[tid];
+    }
+  } else if (tid < 8) {
+    sE[tid] = __ldcg(a.lse + (long)item * 8 + tid);
   }
   __syncthreads();
-  for (int e = blockIdx.y * kKv4JoinThreads + threadIdx.x; e < W * 64; e += gridDim.y * kKv4JoinThreads) {
-    const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6, r8 = 2 * (l & 3) + sel, row = rt * 8 + r8;
-    if (row >= n_rows) continue;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n) {
-      const float Z = sM[r8];
-      for (long long c = c0; c <= c1; ++c) {
-        const float f = kv4_exp2(a.part_ml[part(c) * 8 + r8].x - Z);
-        const float4 u = a.part_o[part(c) * W * 64 + e];
-        v.x += f * u.x;
-        v.y += f * u.y;
-        v.z += f * u.z;
-        v.w += f * u.w;
+  if (join) {
+    for (int e = blockIdx.y * kKv4FinishThreads + tid; e < W * 64; e += join_ctas * kKv4FinishThreads) {
+      const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6, r8 = 2 * (l & 3) + sel, row = rt * 8 + r8;
+      if (row >= n_rows) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n) {
+        const float Z = sM[r8];
+#pragma unroll 8
+        for (int c = c0; c <= c1; ++c) {
+          const long p = part(c);
+          const float mc = __ldcg(&a.part_ml[p * 8 + r8].x);
+          const float4 u = __ldcg(&a.part_o[p * W * 64 + e]);
+          const float f = kv4_exp2(mc - Z);
+          v.x += f * u.x;
+          v.y += f * u.y;
+          v.z += f * u.z;
+          v.w += f * u.w;
+        }
       }
+      const float inv = sL[r8] != 0.f ? 1.f / sL[r8] : 0.f;
+      const int tok = row / a.group, hq = head * a.group + row % a.group;
+      kv4_store4(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
+                 make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
     }
-    const float inv = sL[r8] != 0.f ? 1.f / sL[r8] : 0.f;
-    const int tok = row / a.group, hq = head * a.group + row % a.group;
-    kv4_store4(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
-               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    return;
+  }
+  // ---- the account of a run of keys (row_tiles == 1)
+  kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
+  __syncthreads();
+  const int nb = (len + kKv4Block - 1) / kKv4Block, step = (gridDim.y - join_ctas) * 4;
+  for (int b = (blockIdx.y - join_ctas) * 4 + warp; b < nb; b += step) {
+    const long at = kv4_block(a.c, slot, head, b);
+    if (at < 0) continue;
+    const uint8_t* blk = a.c.data + (size_t)at * O::kBlock;
+    Kv4KeyBlock<D> kb;
+    kb.load(blk, lane);
+    float gain0 = 0.f, gain1 = 0.f;
+    const int key = b * kKv4Block + (lane >> 2);
+    if (wide) kv4_gain_tile<D, DT, true>(a, qs, blk, lane, kb.u, kb.s0, kb.s1, key, sE, len, m, 0, n_rows, gain0, gain1);
+    else kv4_gain_tile<D, DT, false>(a, qs, blk, lane, kb.u, kb.s0, kb.s1, key, sE, len, m, 0, n_rows, gain0, gain1);
+    kv4_add_gain(a, at, b, len, lane, gain0, gain1);
   }
 }
 
 // ------------------------------------------------------------------------- the account
-// The weights each row received, recomputed from the scores: p = 2^(s - lse).  A warp holds 16
-// keys of one (sequence, KV head) as tensor-core operands and takes every query row past them,
-// eight at a time, so a row's gain is one warp's sum in a fixed order.
+// Blocks of query tokens (more than eight query rows per KV head): a warp holds 16 keys of one
+// (sequence, KV head) in registers and takes every query row past them, eight at a time, so a
+// row's gain is one warp's sum in a fixed order.
 constexpr int kKv4GainWarps = 4;
 
 template <int D, int DT>
 __global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const Kv4AttendArgs a) {
   using O = Kv4Off<D>;
-  using C = Kv4Att<D, DT>;
-  constexpr int W = D / 32;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
   uint4* qs = reinterpret_cast<uint4*>(kv4_smem);
-  const int i = blockIdx.y, h = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  __shared__ float lse8[8];
+  const int i = blockIdx.y, h = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   pdl_wait();
   pdl_trigger();
   int slot, len, m;
   if (!kv4_seq(a, i, &slot, &len, &m) || m == 0) return;
-  if (kv4_repeated(a.slots, i, slot)) {
-    if (threadIdx.x == 0) set_err(a.c.err, G4_DEV_BAD_SLOT);
-    return;
-  }
+  if (kv4_repeated(a.slots, i, slot)) return;
+  const int wide = __ldcg(a.c.wide);
   const int n_rows = m * a.group;
   const int nb = (len + kKv4Block - 1) / kKv4Block;
   for (int b0 = blockIdx.x * kKv4GainWarps; b0 < nb; b0 += gridDim.x * kKv4GainWarps) {
     const int b = b0 + warp;
     const long at = b < nb ? kv4_block(a.c, slot, h, b) : -1;
     const uint8_t* blk = a.c.data + (size_t)(at < 0 ? 0 : at) * O::kBlock;
-    uint4 u[W / 2];
+    Kv4KeyBlock<D> kb;
+    kb.load(blk, lane);
     float gain0 = 0.f, gain1 = 0.f;  // keys g and g + 8
-    if (at >= 0)
-#pragma unroll
-      for (int k = 0; k < W / 2; ++k) u[k] = __ldcg(reinterpret_cast<const uint4*>(blk) + k * 32 + lane);
-    const uint16_t* ks = reinterpret_cast<const uint16_t*>(blk + O::kKs);
     // the first row tile that any key of the CTA is seen by
     const int tok0 = max(0, b0 * kKv4Block - (len - m));
     for (int rt = tok0 * a.group / 8; rt * 8 < n_rows; ++rt) {
       __syncthreads();
-      for (int e = threadIdx.x; e < W * 32; e += 32 * kKv4GainWarps) {
-        const int w = e >> 5, l = e & 31, row = rt * 8 + (l >> 2);
-        float v[8];
-        if (row < n_rows) {
-          const int tok = row / a.group, hq = h * a.group + row % a.group;
-          kv4_load8(a.q, (long)i * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head + (l & 3) * (D / 4) + 8 * w, v);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = 0.f;
-        }
-        uint32_t p[4][C::kQP];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) kv4_split<C::kQP>(v[2 * x], v[2 * x + 1], p[x]);
-#pragma unroll
-        for (int part = 0; part < C::kQP; ++part)
-          qs[(part * W + w) * 32 + l] = make_uint4(p[0][part], p[1][part], p[2][part], p[3][part]);
-      }
+      kv4_stage_q<D, DT>(a, qs, i, h, rt * 8, n_rows, threadIdx.x, 32 * kKv4GainWarps);
+      if (threadIdx.x < 8) lse8[threadIdx.x] = __ldcg(a.lse + (((long)i * a.c.kvh + h) * a.row_tiles + rt) * 8 + threadIdx.x);
       __syncthreads();
       if (at < 0) continue;
-      float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < W / 2; ++k) {
-        const int grp = (t * (D / 4) + 16 * k) / kKv4Group;
-        const uint32_t sg = 0x10001u * __ldcg(ks + g * (D / 32) + grp), sh = 0x10001u * __ldcg(ks + (g + 8) * (D / 32) + grp);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t ug = e ? u[k].y : u[k].x, uh = e ? u[k].w : u[k].z;
-          const uint32_t a0 = kv4_pair(ug, sg), a1 = kv4_pair(uh, sh), a2 = kv4_pair(ug >> 4, sg), a3 = kv4_pair(uh >> 4, sh);
-          const uint32_t d0 = kv4_pair(ug >> 8, sg), d1 = kv4_pair(uh >> 8, sh), d2 = kv4_pair(ug >> 12, sg), d3 = kv4_pair(uh >> 12, sh);
-#pragma unroll
-          for (int part = 0; part < C::kQP; ++part) {
-            const uint4 qv = qs[(part * W + 2 * k + e) * 32 + lane];
-            kv4_mma(c0, a0, a1, a2, a3, qv.x, qv.y);
-            kv4_mma(c1, d0, d1, d2, d3, qv.z, qv.w);
-          }
-        }
-      }
-      const float* lse = a.lse + (((long)i * a.c.kvh + h) * a.row_tiles + rt) * 8 + 2 * t;
-      const float e0 = __ldcg(lse), e1 = __ldcg(lse + 1);
-      const int ra = rt * 8 + 2 * t, rb = ra + 1, ja = b * kKv4Block + g;
-      const int last0 = ra < n_rows ? len - m + ra / a.group : -1, last1 = rb < n_rows ? len - m + rb / a.group : -1;
-      if (ja <= last0) gain0 += kv4_exp2((c0[0] + c1[0]) * a.scale - e0);
-      if (ja <= last1) gain0 += kv4_exp2((c0[1] + c1[1]) * a.scale - e1);
-      if (ja + 8 <= last0) gain1 += kv4_exp2((c0[2] + c1[2]) * a.scale - e0);
-      if (ja + 8 <= last1) gain1 += kv4_exp2((c0[3] + c1[3]) * a.scale - e1);
+      if (wide) kv4_gain_tile<D, DT, true>(a, qs, blk, lane, kb.u, kb.s0, kb.s1, b * kKv4Block + g, lse8, len, m, rt * 8, n_rows, gain0, gain1);
+      else kv4_gain_tile<D, DT, false>(a, qs, blk, lane, kb.u, kb.s0, kb.s1, b * kKv4Block + g, lse8, len, m, rt * 8, n_rows, gain0, gain1);
     }
-    if (at < 0) continue;
-    gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 1);
-    gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 1);
-    gain0 += __shfl_xor_sync(0xFFFFFFFFu, gain0, 2);
-    gain1 += __shfl_xor_sync(0xFFFFFFFFu, gain1, 2);
-    if (t < 2) {
-      const int j = b * kKv4Block + g + 8 * t;
-      if (j < len) a.c.weight[at * kKv4Block + g + 8 * t] += t ? gain1 : gain0;
-    }
+    if (at >= 0) kv4_add_gain(a, at, b, len, lane, gain0, gain1);
   }
 }
 

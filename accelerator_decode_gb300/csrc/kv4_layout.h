@@ -41,6 +41,7 @@ struct Kv4Cache {
   int bpp;            // blocks per page (static: per slot)
   int max_pages, n_pages;
   int n_slots, capacity, kvh, d;
+  int* wide;          // 1: a scale outside [2^-60, 2^57] has been stored
   int* err;
 };
 
