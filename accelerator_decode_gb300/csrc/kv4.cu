@@ -22,6 +22,7 @@ struct g4_kv4 {
   float* lse = nullptr;                       // [n_slots][kvh][row tiles * 8]
   float4* part_o = nullptr;                   // partial sums of the spans (kv4_attend.cuh)
   float2* part_ml = nullptr;
+  unsigned* tickets = nullptr;                // parts done of an item
   int smem_optin = 0;
   int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
   int* n_moves = nullptr;                     // [n_slots][kvh]
@@ -126,9 +127,10 @@ void kv4_init(int device, int optin) {
   kv4_attrs_d<256>(optin);
   kv4_attrs_d<512>(optin);
   carve_max(kv4_account_kernel);
-  carve_max(kv4_select_kernel);
+  set_max_dyn(kv4_select_kernel, optin);
   cudaGetLastError();
 }
+int kv4_most_moves(const g4_kv4* op) { return std::max(1, op->cfg.capacity / 2); }
 int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads), 8); }
 
 template <int D, int DT>
@@ -138,13 +140,18 @@ void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
   // the ring takes what shared memory the CTAs of an SM leave each other (1 KB each is the system's)
   const int room = (op->smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
   a.stages = std::max(2, std::min(4, room / C::kTile));
-  a.min_tiles = 1;
+  const int items = a.n_seq * a.c.kvh * a.row_tiles;
+  // With items enough, or few tiles, no item is shared by many CTAs, and the last one to finish
+  // joins the parts (a launch less); else the parts of a few long items are joined by a second
+  // launch with CTAs enough for them.
+  a.join_inside = (long)items * kKv4Join >= ctas || cdiv(op->cfg.capacity, C::kKeys) <= kKv4Join;
   launch(kv4_attend_kernel<D, DT>, dim3(ctas), dim3(C::kThreads), C::smem(a.stages, a.n_seq), st, a);
-  const int items = a.n_seq * a.c.kvh * a.row_tiles, join_ctas = std::max(1, D * 2 / kKv4FinishThreads);
+  const int join_ctas = a.join_inside ? 0 : std::max(1, D * 2 / kKv4FinishThreads);
   const bool one = a.row_tiles == 1;  // the account of a single row tile rides along with the join
   const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(op->cfg.capacity, 4 * kKv4Block), cdiv(8 * op->sms, items))) : 0;
-  launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
-         ((size_t)a.n_seq + 3) * 8 + C::kQBytes, st, a, ctas, join_ctas);
+  if (join_ctas + gain_ctas)
+    launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
+           (size_t)a.n_seq * 24 + 16 + C::kQBytes, st, a, ctas, join_ctas);
   if (a.accumulate && !one)
     launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(op->cfg.capacity, 64), 8 * op->sms / a.n_seq)), a.n_seq, a.c.kvh),
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
@@ -181,13 +188,14 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   const size_t parts = (size_t)2 * op->sms * 3;  // at most three CTAs per SM, two partial items each
   TRY(kv4_alloc(op, &op->part_o, parts * (f.head_dim * 2), st));
   TRY(kv4_alloc(op, &op->part_ml, parts * 8, st));
+  TRY(kv4_alloc(op, &op->tickets, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len), st));
   if (f.track) {
     TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
     TRY(kv4_alloc(op, &c.weight, blocks * kKv4Block, st));
     // at most half of a slot's rows move: a move takes an evicted row below the budget and a
     // kept one beyond it
-    TRY(kv4_alloc(op, &op->holes, (size_t)f.n_slots * c.kvh * f.capacity, st));
-    TRY(kv4_alloc(op, &op->movers, (size_t)f.n_slots * c.kvh * f.capacity, st));
+    TRY(kv4_alloc(op, &op->holes, (size_t)f.n_slots * c.kvh * kv4_most_moves(op), st));
+    TRY(kv4_alloc(op, &op->movers, (size_t)f.n_slots * c.kvh * kv4_most_moves(op), st));
     TRY(kv4_alloc(op, &op->n_moves, (size_t)f.n_slots * c.kvh, st));
   }
   return G4_OK;
@@ -335,6 +343,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.lse = op->lse;
   a.part_o = op->part_o;
   a.part_ml = op->part_ml;
+  a.tickets = op->tickets;
   KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op, a, st))));
   CK(cudaGetLastError());
   return G4_OK;
@@ -358,10 +367,14 @@ g4_status g4_kv4_evict(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_
   a.holes = op->holes;
   a.movers = op->movers;
   a.n_moves = op->n_moves;
-  launch(kv4_select_kernel, dim3(n_seq, op->c.kvh), dim3(kKv4EvictThreads), 0, st, a);
+  a.most = kv4_most_moves(op);
+  a.smem_rows = std::min(op->cfg.capacity, (op->smem_optin - 4096) / 4);
+  launch(kv4_select_kernel, dim3(n_seq, op->c.kvh), dim3(kKv4EvictThreads), (size_t)a.smem_rows * 4, st, a);
   const int per = kKv4RowThreads / (op->c.d / 8);  // moves of a CTA at a time
-  KV4_DISPATCH(op->c.d, launch(kv4_move_kernel<D>, dim3(std::max(1, std::min(cdiv(budget, per), 64)), n_seq, op->c.kvh),
-                               dim3(kKv4RowThreads), 0, st, a));
+  const int most = std::min(budget, op->cfg.capacity - budget);
+  if (most > 0)
+    KV4_DISPATCH(op->c.d, launch(kv4_move_kernel<D>, dim3(std::min(cdiv(most, per), std::max(1, cdiv(8 * op->sms, n_seq * op->c.kvh))), n_seq, op->c.kvh),
+                                 dim3(kKv4RowThreads), 0, st, a));
   CK(cudaGetLastError());
   return G4_OK;
 }

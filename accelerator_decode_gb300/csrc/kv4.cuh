@@ -361,53 +361,159 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_account_kernel(const Kv4Ro
 }
 
 // ------------------------------------------------------------------------------- evict
-// One CTA per (sequence, KV head).  Rows are ranked by a 33-bit key: safe rows first, then the
-// weight's bits mapped to an unsigned order (NaN lowest, -0 as +0); `budget`-th largest key by
-// counting digits from the top (8 bits a pass), ties broken by the lowest row.
+// One CTA per (sequence, KV head).  A row's rank is 32 bits: all ones when it is safe, else its
+// weight's bits in an unsigned order (NaN lowest, then -inf; -0 as +0), which stays below.  The
+// budget-th largest rank is found by counting digits from the top, 8 bits a pass, with the ranks
+// in shared memory; a pass ends the search when the digit's rows are wanted all.  Ties go to the
+// lowest rows.  Bound by latency: a handful of passes of about a microsecond over a few KB.
+// (One thread walking the 256 counts, and ranks read anew from global memory in each pass, took
+// 35 us at 1,025 rows.)
 struct Kv4EvictArgs {
   Kv4Cache c;
   const int *slots, *lens;
   int budget, recent;
   int* new_lens;
-  int* holes;   // scratch [n_seq][kvh][budget]: rows below the budget that go
-  int* movers;  // and the kept rows from beyond it that take their places
-  int* n_moves; // [n_seq][kvh]
+  int* holes;    // scratch [n_seq][kvh][most]: rows below the budget that go
+  int* movers;   // and the kept rows from beyond it that take their places
+  int most;      // a slot's moves at the most: half its rows
+  int* n_moves;  // [n_seq][kvh]
+  int smem_rows; // ranks that fit in shared memory
 };
 
 __device__ __forceinline__ uint32_t kv4_rank_bits(float w) {
   if (w != w) return 0u;
   if (w == 0.f) w = 0.f;
   const uint32_t u = __float_as_uint(w);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;  // -inf maps to 0x007FFFFF, above NaN's 0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;  // -inf: 0x007FFFFF; +inf: 0xFF800000
 }
 
 constexpr int kKv4EvictThreads = 512;
+constexpr int kKv4EvictWarps = kKv4EvictThreads / 32;
 
-// Exclusive prefix of one int per thread over the block; *total gets the sum.
-__device__ __forceinline__ int kv4_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int x = v;
+// RANKS: all ranks of the slot are in shared memory (else they are read anew in each pass).
+template <bool RANKS>
+__device__ __forceinline__ void kv4_select(const Kv4EvictArgs& a, int i, int h, int slot, int len, uint32_t* ranks) {
+  __shared__ int hist[256];
+  __shared__ int counts[3][kKv4EvictWarps];
+  __shared__ int sh_newest, sh_digit, sh_want, sh_all;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto at = [&](int r) { return kv4_block(a.c, slot, h, r / kKv4Block) * kKv4Block + r % kKv4Block; };
+  // newest position; the positions wait where the ranks will be
+  if (tid == 0) sh_newest = INT_MIN;
+  if (tid < 256) hist[tid] = 0;
+  __syncthreads();
+  int newest = INT_MIN;
+#pragma unroll 4
+  for (int r = tid; r < len; r += kKv4EvictThreads) {
+    const int p = __ldcg(a.c.pos + at(r));
+    if (RANKS) ranks[r] = (uint32_t)p;
+    newest = max(newest, p);
+  }
+  newest = __reduce_max_sync(0xFFFFFFFFu, newest);
+  if (lane == 0) atomicMax(&sh_newest, newest);
+  __syncthreads();
+  const long oldest_safe = (long)sh_newest - a.recent;  // safe: position > this
+  auto make = [&](int p, float w) { return (long)p > oldest_safe ? 0xFFFFFFFFu : kv4_rank_bits(w); };
+  auto rank = [&](int r) { return RANKS ? ranks[r] : make(__ldcg(a.c.pos + at(r)), __ldcg(a.c.weight + at(r))); };
+  // the budget-th largest rank: `prefix` after the passes, of which the first `want` rows stay
+  uint32_t prefix = 0, mask = 0;
+  int want = a.budget;
+  bool all = false;
+  for (int shift = 24; shift >= 0 && !all; shift -= 8) {
+#pragma unroll 4
+    for (int r = tid; r < len; r += kKv4EvictThreads) {
+      uint32_t k;
+      if (RANKS && shift == 24) {  // a thread turns its own positions into ranks
+        k = make((int)ranks[r], __ldcg(a.c.weight + at(r)));
+        ranks[r] = k;
+      } else {
+        k = rank(r);
+      }
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane: digits 8 lane .. 8 lane + 7; rows with a larger digit than the lane's
+      int n[8], sum = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
+      for (int x = 0; x < 8; ++x) {
+        n[x] = hist[8 * lane + x];
+        sum += n[x];
+      }
+      int above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xFFFFFFFFu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      above -= sum;
+#pragma unroll
+      for (int x = 7; x >= 0; --x) {
+        if (above < want && above + n[x] >= want) {
+          sh_digit = 8 * lane + x;
+          sh_want = want - above;
+          sh_all = above + n[x] == want;
+        }
+        above += n[x];
+        hist[8 * lane + x] = 0;
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sh_digit << shift;
+    mask |= 255u << shift;
+    want = sh_want;
+    all = sh_all != 0;
+  }
+  // Rows whose masked rank is larger stay; of the equal ones the first `want`.  A warp owns a run
+  // of neighbouring rows: count the equal ones, then holes and movers, then write both lists.
+  const int per = ((len + kKv4EvictWarps - 1) / kKv4EvictWarps + 31) / 32 * 32, r0 = warp * per, r1 = min(len, r0 + per);
+  int ties = 0;
+  for (int r = r0 + lane; r - lane < r1; r += 32) ties += __popc(__ballot_sync(0xFFFFFFFFu, r < r1 && (rank(min(r, len - 1)) & mask) == prefix));
+  if (lane == 0) counts[0][warp] = ties;
+  __syncthreads();
+  int ties_before = 0;
+  for (int w = 0; w < warp; ++w) ties_before += counts[0][w];
+  const unsigned below = (1u << lane) - 1u;
+  int n_holes = 0, n_movers = 0;
+  auto walk = [&](auto&& visit) {
+    int seen = ties_before;
+    for (int r = r0 + lane; r - lane < r1; r += 32) {
+      const uint32_t k = rank(min(r, len - 1)) & mask;
+      const unsigned tie = __ballot_sync(0xFFFFFFFFu, r < r1 && k == prefix);
+      const bool kept = r < r1 && (k > prefix || (k == prefix && seen + __popc(tie & below) < want));
+      seen += __popc(tie);
+      visit(r, __ballot_sync(0xFFFFFFFFu, r < min(r1, a.budget) && !kept), __ballot_sync(0xFFFFFFFFu, kept && r >= a.budget));
+    }
+  };
+  walk([&](int, unsigned hole, unsigned mover) {
+    n_holes += __popc(hole);
+    n_movers += __popc(mover);
+  });
+  if (lane == 0) {
+    counts[1][warp] = n_holes;
+    counts[2][warp] = n_movers;
   }
   __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int base = 0, sum = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w < warp) base += warp_sums[w];
-    sum += warp_sums[w];
+  int hole0 = 0, mover0 = 0, total = 0;
+  for (int w = 0; w < kKv4EvictWarps; ++w) {
+    if (w < warp) {
+      hole0 += counts[1][w];
+      mover0 += counts[2][w];
+    }
+    total += counts[1][w];
   }
-  *total = sum;
-  return base + x - v;
+  int* holes = a.holes + ((size_t)i * a.c.kvh + h) * a.most;
+  int* movers = a.movers + ((size_t)i * a.c.kvh + h) * a.most;
+  walk([&](int r, unsigned hole, unsigned mover) {
+    if ((hole >> lane) & 1) holes[hole0 + __popc(hole & below)] = r;
+    if ((mover >> lane) & 1) movers[mover0 + __popc(mover & below)] = r;
+    hole0 += __popc(hole);
+    mover0 += __popc(mover);
+  });
+  if (tid == 0) a.n_moves[(size_t)i * a.c.kvh + h] = total;
 }
 
 __global__ void __launch_bounds__(kKv4EvictThreads) kv4_select_kernel(const Kv4EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int sums[32];
-  __shared__ int sh_newest, sh_digit, sh_above;
+  extern __shared__ uint32_t kv4_ranks[];
   const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -417,80 +523,20 @@ __global__ void __launch_bounds__(kKv4EvictThreads) kv4_select_kernel(const Kv4E
   if (slot < 0 || slot >= a.c.n_slots) bad = G4_DEV_BAD_SLOT;
   else if (len < 0 || len > a.c.capacity) bad = G4_DEV_BAD_POSITION;
   if (kv4_repeated(a.slots, i, slot)) bad |= G4_DEV_BAD_SLOT;
-  if (!bad) {  // every page of the rows is there: a row without one cannot be moved
+  if (!bad && a.c.table) {  // every page of the rows is there: a row without one cannot be moved
     int miss = 0;
     const int nb = (len + kKv4Block - 1) / kKv4Block;
-    for (int b = tid; b < nb; b += blockDim.x) miss |= kv4_block(a.c, slot, h, b) < 0;
+    for (int b = tid * a.c.bpp; b < nb; b += kKv4EvictThreads * a.c.bpp) miss |= kv4_block(a.c, slot, h, b) < 0;
     if (__syncthreads_or(miss)) bad = G4_DEV_BAD_POSITION;
   }
-  if (bad) {
-    if (tid == 0) {
-      set_err(a.c.err, bad);
-      *n_moves = 0;
-      if (h == 0) a.new_lens[i] = len;
-    }
-    return;
+  if (tid == 0) {
+    if (bad) set_err(a.c.err, bad);
+    if (h == 0) a.new_lens[i] = bad ? len : min(len, a.budget);
+    if (bad || len <= a.budget) *n_moves = 0;
   }
-  if (tid == 0 && h == 0) a.new_lens[i] = min(len, a.budget);
-  if (len <= a.budget) {
-    if (tid == 0) *n_moves = 0;
-    return;
-  }
-  auto at = [&](int r) { return kv4_block(a.c, slot, h, r / kKv4Block) * kKv4Block + r % kKv4Block; };
-  // newest position
-  if (tid == 0) sh_newest = INT_MIN;
-  __syncthreads();
-  int newest = INT_MIN;
-  for (int r = tid; r < len; r += blockDim.x) newest = max(newest, a.c.pos[at(r)]);
-  atomicMax(&sh_newest, newest);
-  __syncthreads();
-  const long oldest_safe = (long)sh_newest - a.recent;  // safe: position > this
-  auto key = [&](int r) {
-    const long x = at(r);
-    return ((unsigned long long)((long)a.c.pos[x] > oldest_safe) << 32) | kv4_rank_bits(a.c.weight[x]);
-  };
-  // the budget-th largest key
-  unsigned long long prefix = 0;
-  int want = a.budget;  // rows still to take among those that share the prefix
-  for (int shift = 32; shift >= 0; shift -= 8) {
-    for (int b = tid; b < 256; b += blockDim.x) hist[b] = 0;
-    __syncthreads();
-    for (int r = tid; r < len; r += blockDim.x) {
-      const unsigned long long k = key(r);
-      if ((k >> shift >> 8) == (prefix >> shift >> 8)) atomicAdd(&hist[(k >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int above = 0, dgt = 255;
-      for (; dgt > 0 && above + hist[dgt] < want; --dgt) above += hist[dgt];
-      sh_digit = dgt;
-      sh_above = above;
-    }
-    __syncthreads();
-    want -= sh_above;
-    prefix |= (unsigned long long)sh_digit << shift;
-  }
-  // rows above the key stay; of those equal to it the first `want` do
-  int ties = 0, n_holes = 0, n_movers = 0;
-  int* holes = a.holes + ((size_t)i * a.c.kvh + h) * a.budget;
-  int* movers = a.movers + ((size_t)i * a.c.kvh + h) * a.budget;
-  for (int r0 = 0; r0 < len; r0 += blockDim.x) {
-    const int r = r0 + tid;
-    const unsigned long long k = r < len ? key(r) : 0;
-    int total;
-    const bool tie = r < len && k == prefix;
-    const int before = ties + kv4_scan(tie, sums, &total);
-    ties += total;
-    const bool kept = r < len && (k > prefix || (tie && before < want));
-    const bool hole = r < a.budget && !kept, mover = r >= a.budget && kept;
-    const int hi = n_holes + kv4_scan(hole, sums, &total);
-    n_holes += total;
-    const int mi = n_movers + kv4_scan(mover, sums, &total);
-    n_movers += total;
-    if (hole) holes[hi] = r;
-    if (mover) movers[mi] = r;
-  }
-  if (tid == 0) *n_moves = n_holes;
+  if (bad || len <= a.budget) return;
+  if (len <= a.smem_rows) kv4_select<true>(a, i, h, slot, len, kv4_ranks);
+  else kv4_select<false>(a, i, h, slot, len, nullptr);
 }
 
 // Row movers[m] -> row holes[m] of every (sequence, KV head).  Sources lie at or beyond the
@@ -507,7 +553,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_move_kernel(const Kv4Evict
   const int n = __ldcg(a.n_moves + ih), o = threadIdx.x % NO;
   for (int m = (blockIdx.x * kKv4RowThreads + threadIdx.x) / NO; m < n; m += gridDim.x * kKv4RowThreads / NO) {
     const int slot = __ldcg(a.slots + i);
-    const int src = __ldcg(a.movers + ih * a.budget + m), dst = __ldcg(a.holes + ih * a.budget + m);
+    const int src = __ldcg(a.movers + ih * a.most + m), dst = __ldcg(a.holes + ih * a.most + m);
     const long sb = kv4_block(a.c, slot, h, src / kKv4Block), db = kv4_block(a.c, slot, h, dst / kKv4Block);
     const uint8_t* sp = a.c.data + (size_t)sb * O::kBlock;
     uint8_t* dp = a.c.data + (size_t)db * O::kBlock;

@@ -27,12 +27,13 @@ struct Kv4AttendArgs {
   int row_tiles;                     // items of a (sequence, KV head): ceil(q_len * group / 8)
   float scale;                       // times log2(e)
   int window, accumulate, zero_rest;
-  int min_tiles;                     // a CTA's span is at least this many tiles
+  int join_inside;                   // the CTA that finishes a shared item last joins its parts
   int stages;
   Kv4Dense q, out;
   float* lse;                        // [n_seq][kvh][row_tiles * 8]: log2 of the softmax's sum
   float4* part_o;                    // [2 * CTAs][D / 32][2][32]: a span's partial first and last item
   float2* part_ml;                   // [2 * CTAs][8]: running maximum (log2 units) and sum
+  unsigned* tickets;                 // [items]: parts done, zero between calls
 };
 
 // Sequence i's slot, rows and query tokens; false (uniform over the block) when it is skipped.
@@ -101,12 +102,13 @@ struct Kv4Att {
   static constexpr int kOBytes = 4 * D * 32;           // four warps' sums, [warp][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
-    return (size_t)stages * kTile + kFixed + ((size_t)n_seq + 1) * 8;
+    return (size_t)stages * kTile + kFixed + (size_t)n_seq * 24 + 16;
   }
 };
 
-// first[i] = key tiles of all items of sequences before i (n_seq + 1 entries, by the whole block):
-// sequence i has kvh * row_tiles items of the same number of tiles.
+// The cut of all tiles into spans, worked out by every CTA for itself: first[i] = key tiles of all
+// items of sequences before i (sequence i has kvh * row_tiles items of the same number of tiles),
+// first[n_seq + 1] = tiles of the longest item; seqs[i] = (slot, len, m), len 0 when skipped.
 template <int KEYS>
 __device__ __forceinline__ int kv4_tiles(const Kv4AttendArgs& a, int len, int m, int* tile0) {
   const int lo = a.window > 0 ? max(0, len - m + 1 - a.window) : 0;  // first row that token 0 sees
@@ -114,9 +116,8 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttendArgs& a, int len, int m,
   return m > 0 && len > 0 ? (len + KEYS - 1) / KEYS - *tile0 : 0;
 }
 template <int KEYS>
-__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* first, bool report) {
-  const int T = blockDim.x, per = (a.n_seq + T - 1) / T, i0 = threadIdx.x * per;
-  for (int i = i0; i < min(a.n_seq, i0 + per); ++i) {
+__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* first, int4* seqs, bool report) {
+  for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
     int slot, len, m, t0;
     bool ok = kv4_seq(a, i, &slot, &len, &m);
     if (!ok && report) set_err(a.c.err, kv4_seq_error(a, slot));
@@ -124,32 +125,43 @@ __device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* firs
       int same = 0;
 #pragma unroll 4
       for (int j = 0; j < i; ++j) same |= __ldcg(a.slots + j) == slot;
-      ok = !same;
       if (same && report) set_err(a.c.err, G4_DEV_BAD_SLOT);
+      if (same) len = 0;
     }
-    first[i + 1] = ok ? (long long)kv4_tiles<KEYS>(a, len, m, &t0) * a.c.kvh * a.row_tiles : -1;
+    if (!ok) {  // all its query rows get zeros
+      len = 0;
+      m = a.q_len;
+    }
+    seqs[i] = make_int4(slot, len, m, kv4_tiles<KEYS>(a, len, m, &t0));
   }
   __syncthreads();
-  if (threadIdx.x < 32) {  // running sum, 32 sequences at a time; skipped ones are marked by -1
+  if (threadIdx.x < 32) {  // running sum, 32 sequences at a time
+    const int lane = threadIdx.x;
     long long base = 0;
-    if (threadIdx.x == 0) first[0] = 0;
+    int longest = 0;
+    if (lane == 0) first[0] = 0;
     for (int i = 0; i < a.n_seq; i += 32) {
-      long long v = i + threadIdx.x < a.n_seq ? first[i + threadIdx.x + 1] : 0;
-      v = max(v, 0LL);
+      const int n = i + lane < a.n_seq ? seqs[i + lane].w : 0;
+      longest = max(longest, n);
+      long long v = (long long)n * a.c.kvh * a.row_tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if ((int)threadIdx.x >= o) v += u;
+        if (lane >= o) v += u;
       }
-      if (i + threadIdx.x < a.n_seq) first[i + threadIdx.x + 1] = base + v;
+      if (i + lane < a.n_seq) first[i + lane + 1] = base + v;
       base += __shfl_sync(0xFFFFFFFFu, v, 31);
     }
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    if (lane == 0) first[a.n_seq + 1] = longest;
   }
   __syncthreads();
 }
-// Tiles per CTA.
-__device__ __forceinline__ long long kv4_span(const Kv4AttendArgs& a, long long total, int ctas) {
-  return max((long long)a.min_tiles, (total + ctas - 1) / ctas);
+// Tiles per CTA.  An item that is joined inside is shared by kKv4Join + 1 CTAs at the most.
+constexpr int kKv4Join = 24;
+__device__ __forceinline__ long long kv4_span(const Kv4AttendArgs& a, const long long* first, int ctas) {
+  const long long even = (first[a.n_seq] + ctas - 1) / ctas;
+  return max(1LL, a.join_inside ? max(even, (first[a.n_seq + 1] + kKv4Join - 1) / kKv4Join) : even);
 }
 
 // A run of tiles of one item: what a CTA does between two item borders.
@@ -157,11 +169,13 @@ struct Kv4Run {
   int seq, head, row_tile;
   int slot, len, m;
   int tile, tiles;     // first tile (absolute) and their number
-  bool first, last;    // the run holds the item's first / last tile
+  int of;              // tiles of the item
+  long long item_t0;   // the item's first tile in the order of all
+  bool whole;          // the run is the whole item
 };
 // The run that starts at global tile g (g < end <= total).
 template <int KEYS>
-__device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long long* first, long long g, long long end) {
+__device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long long* first, const int4* seqs, long long g, long long end) {
   int lo = 0, hi = a.n_seq - 1;  // the last sequence with first[i] <= g (empty ones in between share it)
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -169,17 +183,21 @@ __device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long lon
   }
   Kv4Run r;
   r.seq = lo;
-  kv4_seq(a, lo, &r.slot, &r.len, &r.m);
+  const int4 q = seqs[lo];
+  r.slot = q.x;
+  r.len = q.y;
+  r.m = q.z;
+  r.of = q.w;
   int t0;
-  const int n = kv4_tiles<KEYS>(a, r.len, r.m, &t0);
+  kv4_tiles<KEYS>(a, r.len, r.m, &t0);
   const long long x = g - first[lo];
-  const int item = (int)(x / n), off = (int)(x % n);
+  const int item = (int)(x / r.of), off = (int)(x % r.of);
+  r.item_t0 = g - off;
   r.head = item / a.row_tiles;
   r.row_tile = item % a.row_tiles;
   r.tile = t0 + off;
-  r.tiles = (int)min((long long)(n - off), end - g);
-  r.first = off == 0;
-  r.last = off + r.tiles == n;
+  r.tiles = (int)min((long long)(r.of - off), end - g);
+  r.whole = r.tiles == r.of;
   return r;
 }
 
@@ -272,6 +290,80 @@ __device__ __forceinline__ void kv4_scores(const uint4* qs, int lane, Codes code
     for (int j = 0; j < 4; ++j) c[b][j] += d[b][j];
 }
 
+// ------------------------------------------------------------------------ joining parts
+// CTA c's part of the item that starts at tile t0: slot 0 when the item opens c's span, else 1.
+__device__ __forceinline__ long kv4_part(int c, long long t0, long long span) { return (long)c * 2 + (t0 > c * span ? 1 : 0); }
+__device__ __forceinline__ float kv4_lse(float2 ml) { return ml.y != 0.f ? ml.x + log2f(ml.y) : INFINITY; }
+__device__ __forceinline__ void kv4_merge_ml(float2& u, float2 v) {
+  const float m = fmaxf(u.x, v.x), z = m == -INFINITY ? 0.f : m;
+  u.y = u.y * kv4_exp2(u.x - z) + v.y * kv4_exp2(v.x - z);
+  u.x = m;
+}
+// Maximum and sum of the item's eight rows over its parts c0 .. c1 into ml[0..8), by `warps` warps
+// that share barrier `bar` (ml: 8 + 8 * warps entries): a thread takes a row and every 4 warps'th part.
+__device__ __forceinline__ void kv4_join_ml(const Kv4AttendArgs& a, long long t0, long long span, int c0, int c1, int tid,
+                                            int warps, float2* ml, int bar) {
+  float2 u = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+  for (int c = c0 + (tid >> 3); c <= c1; c += 4 * warps) kv4_merge_ml(u, __ldcg(&a.part_ml[kv4_part(c, t0, span) * 8 + (tid & 7)]));
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    const float2 v = make_float2(__shfl_xor_sync(0xFFFFFFFFu, u.x, o), __shfl_xor_sync(0xFFFFFFFFu, u.y, o));
+    kv4_merge_ml(u, v);
+  }
+  if ((tid & 31) < 8) ml[8 + (tid >> 5) * 8 + (tid & 7)] = u;
+  named_bar_sync(bar, 32 * warps);
+  if (tid < 8) {
+    u = ml[8 + tid];
+    for (int w = 1; w < warps; ++w) kv4_merge_ml(u, ml[8 + w * 8 + tid]);
+    ml[tid] = u;
+  }
+  named_bar_sync(bar, 32 * warps);
+}
+// The item's output rows from its parts, in span order (c1 < c0: zeros); entries e0, e0 + step, ..
+template <int D>
+__device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, int head, int row0, int n_rows, long long t0,
+                                              long long span, int c0, int c1, const float2* ml, int e0, int step) {
+  constexpr int W = D / 32;
+  for (int e = e0; e < W * 64; e += step) {
+    const int l = e & 31, r8 = 2 * (l & 3) + ((e >> 5) & 1), w = e >> 6, row = row0 + r8;
+    if (row >= n_rows) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float inv = 0.f;
+    if (c0 <= c1) {
+      const float M = ml[r8].x, Z = M == -INFINITY ? 0.f : M, L = ml[r8].y;
+      inv = L != 0.f ? 1.f / L : 0.f;
+#pragma unroll 8
+      for (int c = c0; c <= c1; ++c) {
+        const long p = kv4_part(c, t0, span);
+        const float mc = __ldcg(&a.part_ml[p * 8 + r8].x);
+        const float4 u = __ldcg(&a.part_o[p * W * 64 + e]);
+        const float f = kv4_exp2(mc - Z);
+        v.x += f * u.x;
+        v.y += f * u.y;
+        v.z += f * u.z;
+        v.w += f * u.w;
+      }
+    }
+    const int tok = row / a.group, hq = head * a.group + row % a.group;
+    kv4_store4(a.out, (long)seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
+               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  }
+}
+// Zeros for the query rows that no tile reaches: those of sequences without rows, and with
+// zero_rest the padding.  Sequences i0, i0 + step, ..
+template <int D>
+__device__ __forceinline__ void kv4_zero_rows(const Kv4AttendArgs& a, const long long* first, const int4* seqs, int i0, int step,
+                                              int tid, int threads) {
+  for (int i = i0; i < a.n_seq; i += step) {
+    const int t0 = seqs[i].w > 0 ? seqs[i].z : 0, t1 = a.zero_rest ? a.q_len : seqs[i].z;  // tokens to clear
+    for (int e = t0 * a.heads * (D / 4) + tid; e < t1 * a.heads * (D / 4); e += threads) {
+      const int x = e % (D / 4), hq = e / (D / 4) % a.heads, tok = e / (D / 4) / a.heads;
+      kv4_store4(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + 4 * x, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+}
+
 // ------------------------------------------------------------------------- the kernel
 // What the warps of a CTA share.
 template <int D, int DT>
@@ -283,8 +375,10 @@ struct Kv4Shared {
   uint64_t *full, *empty;
   uint32_t* held;     // [8]: blocks of a stage that hold rows
   volatile int* abort_flag;
+  volatile int* last;  // this CTA joins the item
+  int4* seqs;
   long long* first;
-  __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages) {
+  __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages, int n_seq) {
     using C = Kv4Att<D, DT>;
     ring = smem;
     qs = reinterpret_cast<uint4*>(ring + (size_t)stages * C::kTile);
@@ -294,12 +388,15 @@ struct Kv4Shared {
     empty = full + 8;
     held = reinterpret_cast<uint32_t*>(empty + 8);
     abort_flag = reinterpret_cast<volatile int*>(held + 8);
-    first = reinterpret_cast<long long*>(full + 32);
+    last = abort_flag + 1;
+    seqs = reinterpret_cast<int4*>(full + 32);
+    first = reinterpret_cast<long long*>(seqs + n_seq);
   }
 };
 
 template <int D, int DT, bool WIDE>
-__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, long long g0, long long g1) {
+__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, long long g0, long long g1,
+                                            long long span) {
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
   constexpr int W = D / 32, NB = C::kNB;  // words of a key (or value pair) per lane
@@ -308,7 +405,7 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
   const float score_scale = WIDE ? a.scale : a.scale * kKv4Up;
   int it = 0, piece = 0;
   for (long long at = g0; at < g1; ++piece) {
-    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, at, g1);
+    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
     const int n_rows = r.m * a.group, row0 = r.row_tile * 8;
     named_bar_sync(1, 32 * C::kWarps);
     kv4_stage_q<D, DT>(a, sh.qs, r.seq, r.head, row0, n_rows, threadIdx.x, 32 * C::kWarps);
@@ -450,7 +547,7 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
       L0 += u.y * kv4_exp2(u.x - Z0);
       L1 += v.y * kv4_exp2(v.x - Z1);
     }
-    const bool whole = r.first && r.last;
+    const bool whole = r.whole;
     // a whole item is divided by its sum here, a partial one when the spans are joined
     const float up = WIDE ? 1.f : kKv4Up;
     const float f0 = kv4_exp2(mx0 - Z0) * up * (whole ? (L0 != 0.f ? 1.f / L0 : 0.f) : 1.f);
@@ -514,6 +611,25 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
         lse[1] = L1 != 0.f ? M1 + log2f(L1) : INFINITY;
       }
     }
+    if (a.join_inside && !whole) {
+      __threadfence();
+      named_bar_sync(1, 32 * C::kWarps);
+      const int c0 = (int)(r.item_t0 / span), c1 = (int)((r.item_t0 + r.of - 1) / span);
+      const long item = ((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile;
+      if (threadIdx.x == 0) {
+        const bool is_last = atomicAdd(a.tickets + item, 1u) == (unsigned)(c1 - c0);
+        if (is_last) a.tickets[item] = 0;
+        *sh.last = is_last;
+      }
+      named_bar_sync(1, 32 * C::kWarps);
+      if (*sh.last) {
+        __threadfence();
+        float2* ml = reinterpret_cast<float2*>(sh.os);
+        kv4_join_ml(a, r.item_t0, span, c0, c1, threadIdx.x, C::kWarps, ml, 1);
+        if (threadIdx.x < 8) a.lse[item * 8 + threadIdx.x] = kv4_lse(ml[threadIdx.x]);
+        kv4_join_rows<D>(a, r.seq, r.head, row0, n_rows, r.item_t0, span, c0, c1, ml, threadIdx.x, 32 * C::kWarps);
+      }
+    }
   }
   if (*sh.abort_flag && threadIdx.x == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
 }
@@ -523,7 +639,7 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
-  const Kv4Shared<D, DT> sh(kv4_smem, a.stages);
+  const Kv4Shared<D, DT> sh(kv4_smem, a.stages, a.n_seq);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
@@ -536,20 +652,22 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   pdl_wait();
   pdl_trigger();
   const int wide = __ldcg(a.c.wide);
-  kv4_plan<C::kKeys>(a, sh.first, blockIdx.x == 0);
+  kv4_plan<C::kKeys>(a, sh.first, sh.seqs, blockIdx.x == 0);
   const long long total = sh.first[a.n_seq];
-  const long long span = kv4_span(a, total, gridDim.x);
+  const long long span = kv4_span(a, sh.first, gridDim.x);
   const long long g0 = min(total, (long long)blockIdx.x * span), g1 = min(total, g0 + span);
   if (warp < C::kWarps) {
-    if (wide) kv4_consume<D, DT, true>(a, sh, g0, g1);
-    else kv4_consume<D, DT, false>(a, sh, g0, g1);
+    if (wide) kv4_consume<D, DT, true>(a, sh, g0, g1, span);
+    else kv4_consume<D, DT, false>(a, sh, g0, g1, span);
+    if (a.join_inside)
+      kv4_zero_rows<D>(a, sh.first, sh.seqs, blockIdx.x, gridDim.x, threadIdx.x, 32 * C::kWarps);
     return;
   }
   // ---- producer: tiles into the ring
   int it = 0;
   bool stop = false;
   for (long long at = g0; at < g1 && !stop;) {
-    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, at, g1);
+    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
     const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
     for (int x = 0; x < r.tiles; ++x, ++it) {
       const int s = it % a.stages;
@@ -588,9 +706,9 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
 }
 
 // -------------------------------------------------------------------------- the finish
-// Second launch.  CTAs with blockIdx.y < join_ctas add the partial sums that the spans left of
-// item blockIdx.x, in span order, each a share of its numbers; items without keys (and skipped
-// sequences) get zeros.  With an account and one item per (sequence, KV head), the others each
+// Second launch.  CTAs with blockIdx.y < join_ctas (none when the first launch joins inside) add
+// the partial sums that the spans left of item blockIdx.x, in span order, each a share of its
+// numbers.  With an account and one item per (sequence, KV head), the others each
 // take a run of the item's keys and add the weights those received, p = 2^(s - lse), recomputed
 // from the keys: a score per key and query row kept from the first launch would cost 64 bytes of
 // traffic a key and a buffer of its own, the codes cost 9/16 D and are still in L2 for the most.
@@ -642,69 +760,35 @@ template <int D, int DT>
 __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4AttendArgs a, int ctas, int join_ctas) {
   using C = Kv4Att<D, DT>;
   using O = Kv4Off<D>;
-  constexpr int W = D / 32;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
-  long long* first = reinterpret_cast<long long*>(kv4_smem);
-  uint4* qs = reinterpret_cast<uint4*>(kv4_smem + ((size_t)(a.n_seq + 1) * 8 + 15) / 16 * 16);
-  __shared__ float2 part_ml[4][8];
-  __shared__ float sM[8], sL[8], sE[8];
+  int4* seqs = reinterpret_cast<int4*>(kv4_smem);
+  uint4* qs = reinterpret_cast<uint4*>(seqs + a.n_seq);
+  long long* first = reinterpret_cast<long long*>(qs + C::kQBytes / 16);
+  __shared__ float2 ml[8 + 8 * kKv4FinishThreads / 32];
+  __shared__ float sE[8];
   const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
   const bool join = (int)blockIdx.y < join_ctas;
+  // What the first launch reads as well can be read before it has ended.
+  const int wide = __ldcg(a.c.wide);
+  kv4_plan<C::kKeys>(a, first, seqs, false);
+  const int slot = seqs[i].x, len = seqs[i].y, m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
+  if (!join && n > 0) kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
+  const long long span = kv4_span(a, first, ctas);
+  const long long t0 = first[i] + (long long)n * x;  // the item's first tile
+  const int c0 = (int)(t0 / span), c1 = n ? (int)((t0 + n - 1) / span) : c0 - 1;
   pdl_wait();
   pdl_trigger();
-  const int wide = __ldcg(a.c.wide);
-  kv4_plan<C::kKeys>(a, first, false);
-  int slot, len, m;
-  const bool ok = kv4_seq(a, i, &slot, &len, &m);
-  const long long total = first[a.n_seq], span = kv4_span(a, total, ctas);
-  const long long n = (first[i + 1] - first[i]) / per_seq;
-  const long long t0 = first[i] + n * x, t1 = t0 + n;  // the item's tiles
-  const int n_rows = (ok ? m : a.q_len) * a.group;
-  const int c0 = n ? (int)(t0 / span) : 0, c1 = n ? (int)((t1 - 1) / span) : 0;
-  const bool whole = n && c0 == c1;  // one CTA had the whole item: its rows are done
-  if (join && a.zero_rest && ok && m < a.q_len) {  // rows of query tokens beyond the sequence's own
-    for (int e = blockIdx.y * kKv4FinishThreads + tid; e < W * 64; e += join_ctas * kKv4FinishThreads) {
-      const int l = e & 31, row = rt * 8 + 2 * (l & 3) + ((e >> 5) & 1);
-      if (row < n_rows || row >= a.q_len * a.group) continue;
-      kv4_store4(a.out, (long)i * a.out.seq + (long)(row / a.group) * a.out.row +
-                            (long)(head * a.group + row % a.group) * a.out.head + (l >> 2) * (D / 8) + 4 * (e >> 6),
-                 make_float4(0.f, 0.f, 0.f, 0.f));
-    }
+  if (join) {
+    if (x == 0 && blockIdx.y == 0) kv4_zero_rows<D>(a, first, seqs, i, a.n_seq, tid, kKv4FinishThreads);
+    if (c1 <= c0) return;  // nothing to see, or one CTA had the whole item
+  } else if (n == 0) {
+    return;
   }
-  if (join ? whole : n == 0) return;
-  // CTA c's partial sums of this item: slot 0 when the item opens its span, else slot 1
-  auto part = [&](int c) { return (long)c * 2 + (t0 > c * span ? 1 : 0); };
-  if (!whole) {  // every thread a row and every 16th span, then over the threads
-    float M = -INFINITY, L = 0.f;
-    if (n) {
-      for (int c = c0 + (tid >> 3); c <= c1; c += kKv4FinishThreads / 8) {
-        const float2 u = __ldcg(&a.part_ml[part(c) * 8 + (tid & 7)]);
-        const float nm = fmaxf(M, u.x), z = nm == -INFINITY ? 0.f : nm;
-        L = L * kv4_exp2(M - z) + u.y * kv4_exp2(u.x - z);
-        M = nm;
-      }
-    }
-    auto merge = [&](float m2, float l2) {
-      const float nm = fmaxf(M, m2), z = nm == -INFINITY ? 0.f : nm;
-      L = L * kv4_exp2(M - z) + l2 * kv4_exp2(m2 - z);
-      M = nm;
-    };
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
-      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
-      merge(m2, l2);
-    }
-    if (lane < 8) part_ml[warp][lane] = make_float2(M, L);
-    __syncthreads();
+  if (c0 < c1 && !a.join_inside) {
+    kv4_join_ml(a, t0, span, c0, c1, tid, kKv4FinishThreads / 32, ml, 1);
     if (tid < 8) {
-      M = part_ml[0][tid].x;
-      L = part_ml[0][tid].y;
-#pragma unroll
-      for (int w = 1; w < 4; ++w) merge(part_ml[w][tid].x, part_ml[w][tid].y);
-      sM[tid] = M == -INFINITY ? 0.f : M;
-      sL[tid] = L;
-      sE[tid] = L != 0.f ? M + log2f(L) : INFINITY;
+      sE[tid] = kv4_lse(ml[tid]);
       if (blockIdx.y == 0) a.lse[(long)item * 8 + tid] = sE[tid];
     }
   } else if (tid < 8) {
@@ -712,34 +796,11 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4
   }
   __syncthreads();
   if (join) {
-    for (int e = blockIdx.y * kKv4FinishThreads + tid; e < W * 64; e += join_ctas * kKv4FinishThreads) {
-      const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6, r8 = 2 * (l & 3) + sel, row = rt * 8 + r8;
-      if (row >= n_rows) continue;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (n) {
-        const float Z = sM[r8];
-#pragma unroll 8
-        for (int c = c0; c <= c1; ++c) {
-          const long p = part(c);
-          const float mc = __ldcg(&a.part_ml[p * 8 + r8].x);
-          const float4 u = __ldcg(&a.part_o[p * W * 64 + e]);
-          const float f = kv4_exp2(mc - Z);
-          v.x += f * u.x;
-          v.y += f * u.y;
-          v.z += f * u.z;
-          v.w += f * u.w;
-        }
-      }
-      const float inv = sL[r8] != 0.f ? 1.f / sL[r8] : 0.f;
-      const int tok = row / a.group, hq = head * a.group + row % a.group;
-      kv4_store4(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
-                 make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    }
+    kv4_join_rows<D>(a, i, head, rt * 8, n_rows, t0, span, c0, c1, ml, blockIdx.y * kKv4FinishThreads + tid,
+                     join_ctas * kKv4FinishThreads);
     return;
   }
   // ---- the account of a run of keys (row_tiles == 1)
-  kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
-  __syncthreads();
   const int nb = (len + kKv4Block - 1) / kKv4Block, step = (gridDim.y - join_ctas) * 4;
   for (int b = (blockIdx.y - join_ctas) * 4 + warp; b < nb; b += step) {
     const long at = kv4_block(a.c, slot, head, b);
