@@ -78,9 +78,12 @@ bool kv4_dense(const g4_kv4_tensor* t, long n, long rows, long heads, int d, boo
   out->row = t->row_stride;
   out->head = t->head_stride;
   out->dtype = t->dtype;
-  const long oct = 16 / es;
-  out->vec = reinterpret_cast<uintptr_t>(t->data) % 16 == 0 && t->seq_stride % oct == 0 && t->row_stride % oct == 0 &&
-             t->head_stride % oct == 0;
+  auto aligned = [&](long bytes) {
+    const long n = bytes / es;
+    return reinterpret_cast<uintptr_t>(t->data) % bytes == 0 && t->seq_stride % n == 0 && t->row_stride % n == 0 &&
+           t->head_stride % n == 0;
+  };
+  out->vec = aligned(32) ? 2 : aligned(16) ? 1 : 0;
   return true;
 }
 
@@ -116,6 +119,8 @@ void kv4_attrs_d(int optin) {
   kv4_attrs<D, G4_DT_BF16>(optin);
   kv4_attrs<D, G4_DT_F16>(optin);
   carve_max(kv4_append_kernel<D>);
+  carve_max(kv4_append_blocks_kernel<D>);
+  carve_max(kv4_read_blocks_kernel<D>);
   carve_max(kv4_read_kernel<D>);
   carve_max(kv4_move_kernel<D>);
 }
@@ -151,12 +156,17 @@ void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
   const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(op->cfg.capacity, 4 * kKv4Block), cdiv(8 * op->sms, items))) : 0;
   if (join_ctas + gain_ctas)
     launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
-           (size_t)a.n_seq * 24 + 16 + C::kQBytes, st, a, ctas, join_ctas);
+           (size_t)a.n_seq * 20 + 16 + C::kQBytes, st, a, ctas, join_ctas);
   if (a.accumulate && !one)
     launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(op->cfg.capacity, 64), 8 * op->sms / a.n_seq)), a.n_seq, a.c.kvh),
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
 }
 
+// Whole-block kernels: every block that n_rows rows from any row on can touch.
+dim3 kv4_block_grid(const g4_kv4* op, int n_seq, int n_rows) {
+  const long units = ((long)(n_rows + 2 * kKv4Block - 2) / kKv4Block) * op->cfg.num_kv_heads;
+  return dim3((unsigned)((units + kKv4BlockWarps - 1) / kKv4BlockWarps), n_seq, 2);
+}
 dim3 kv4_row_grid(const g4_kv4* op, int n_seq, int n_rows) {
   const long threads = (long)n_rows * op->cfg.num_kv_heads * (op->cfg.head_dim / 8);
   return dim3((unsigned)((threads + kKv4RowThreads - 1) / kKv4RowThreads), n_seq);
@@ -185,7 +195,7 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   TRY(kv4_alloc(op, &c.wide, 1, st));
   TRY(kv4_alloc(op, &c.err, 1, st));
   TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len) * 8, st));
-  const size_t parts = (size_t)2 * op->sms * 3;  // at most three CTAs per SM, two partial items each
+  const size_t parts = (size_t)2 * op->sms * kKv4MaxCtas;  // two partial items of every CTA
   TRY(kv4_alloc(op, &op->part_o, parts * (f.head_dim * 2), st));
   TRY(kv4_alloc(op, &op->part_ml, parts * 8, st));
   TRY(kv4_alloc(op, &op->tickets, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len), st));
@@ -263,8 +273,12 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.n_rows = n_rows;
   a.positions = d_positions;
   a.weights = d_weights;
-  KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0,
-                               reinterpret_cast<cudaStream_t>(stream), a));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (n_rows >= kKv4Block) {
+    KV4_DISPATCH(op->c.d, launch(kv4_append_blocks_kernel<D>, kv4_block_grid(op, n_seq, n_rows), dim3(32 * kKv4BlockWarps), 0, st, a));
+  } else {
+    KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0, st, a));
+  }
   CK(cudaGetLastError());
   return G4_OK;
 }
@@ -285,8 +299,12 @@ g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t
   a.counts = d_counts;
   a.n_rows = n_rows;
   a.zero_rest = zero_rest != 0;
-  KV4_DISPATCH(op->c.d, launch(kv4_read_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0,
-                               reinterpret_cast<cudaStream_t>(stream), a));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (n_rows >= kKv4Block) {
+    KV4_DISPATCH(op->c.d, launch(kv4_read_blocks_kernel<D>, kv4_block_grid(op, n_seq, n_rows), dim3(32 * kKv4BlockWarps), 0, st, a));
+  } else {
+    KV4_DISPATCH(op->c.d, launch(kv4_read_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0, st, a));
+  }
   CK(cudaGetLastError());
   return G4_OK;
 }
@@ -325,6 +343,8 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
       !kv4_dense(out, n_seq, q_len, op->cfg.num_q_heads, op->c.d, true, &a.out))
     return G4_ERR_INVALID_ARG;
   if ((accumulate && !op->cfg.track) || (window && op->cfg.track)) return G4_ERR_UNSUPPORTED;
+  // the spans count (key tile, eight query rows) pairs in 32 bits
+  if ((double)n_seq * op->c.kvh * kv4_row_tiles(op, q_len) * cdiv(op->cfg.capacity, 64) >= 2147483647.0) return G4_ERR_UNSUPPORTED;
   DEVICE_GUARD(op->device);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   a.c = op->c;

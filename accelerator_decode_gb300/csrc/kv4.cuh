@@ -23,7 +23,7 @@ struct Kv4Dense {
   void* p;
   long seq, row, head;
   int dtype;  // G4_DT_*
-  int vec;    // base and strides allow 16-byte accesses of whole octets
+  int vec;    // base and strides allow 16-byte (1) or 32-byte (2) accesses of whole octets
 };
 
 __device__ __forceinline__ void kv4_load8(const Kv4Dense& x, long off, float (&v)[8]) {
@@ -115,6 +115,64 @@ __device__ __forceinline__ void kv4_store4(const Kv4Dense& x, long off, float4 v
   }
 }
 
+// Sixteen numbers, in 32-byte accesses where the tensor allows them: a lane then reads or writes
+// whole sectors, whatever its neighbours do.
+__device__ __forceinline__ void kv4_load32b(const void* p, uint32_t (&u)[8]) {
+  asm volatile("ld.global.cg.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void kv4_store32b(void* p, const uint32_t (&u)[8]) {
+  asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+               "r"(u[5]), "r"(u[6]), "r"(u[7]), "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void kv4_load16(const Kv4Dense& x, long off, float* v) {
+  uint32_t u[8];
+  if (x.vec < 2) {
+    kv4_load8(x, off, *reinterpret_cast<float(*)[8]>(v));
+    kv4_load8(x, off + 8, *reinterpret_cast<float(*)[8]>(v + 8));
+  } else if (x.dtype == G4_DT_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      kv4_load32b(reinterpret_cast<const float*>(x.p) + off + 8 * h, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * h + e] = __uint_as_float(u[e]);
+    }
+  } else {
+    kv4_load32b(reinterpret_cast<const uint16_t*>(x.p) + off, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (x.dtype == G4_DT_BF16) {
+        v[2 * e] = bf16_lo(u[e]);
+        v[2 * e + 1] = bf16_hi(u[e]);
+      } else {
+        const __half2 h = *reinterpret_cast<__half2*>(&u[e]);
+        v[2 * e] = __low2float(h);
+        v[2 * e + 1] = __high2float(h);
+      }
+    }
+  }
+}
+__device__ __forceinline__ void kv4_store16(const Kv4Dense& x, long off, const float* v) {
+  uint32_t u[8];
+  if (x.vec < 2) {
+    kv4_store8(x, off, *reinterpret_cast<const float(*)[8]>(v));
+    kv4_store8(x, off + 8, *reinterpret_cast<const float(*)[8]>(v + 8));
+  } else if (x.dtype == G4_DT_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(v[8 * h + e]);
+      kv4_store32b(reinterpret_cast<float*>(x.p) + off + 8 * h, u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = kv4_pack2(x.dtype, v[2 * e], v[2 * e + 1]);
+    kv4_store32b(reinterpret_cast<uint16_t*>(x.p) + off, u);
+  }
+}
+
 // -------------------------------------------------------------------------- one group
 // Scale of a group from its largest magnitude: one fp32 product (an IEEE division costs about
 // ten instructions and buys nothing: any scale this near serves the codes as well).  The
@@ -122,20 +180,37 @@ __device__ __forceinline__ void kv4_store4(const Kv4Dense& x, long off, float4 v
 __device__ __forceinline__ __nv_bfloat16 kv4_scale(float amax) {
   return __float2bfloat16_rn(fminf(__fmul_rn(amax, 1.f / 7.f), 4.8301e37f));
 }
-// Code of x under scale s: round-half-even(x / s) clipped to +-7, exactly.  A quotient in 32
-// bits may round onto a border (c + 1/2) s from either side, so a first guess is corrected
-// against the borders themselves: (c + 1/2) has 4 significant bits and s has 8, so their
-// product is exact.
-__device__ __forceinline__ int kv4_code(float x, float s, float up, float inv) {
-  const float a = fabsf(x);
-  float c = fminf(rintf(a * up * inv), 7.f);
-  const float lo = (c - 0.5f) * s, hi = (c + 0.5f) * s;
-  const bool odd = ((int)c) & 1;
-  if (a > hi || (a == hi && odd)) c += 1.f;
-  else if (a < lo || (a == lo && odd)) c -= 1.f;
-  const int k = (int)fminf(fmaxf(c, 0.f), 7.f);
-  return x < 0.f ? -k : k;
-}
+// Codes under scale s: round-half-even(x / s) clipped to +-7, exactly.  x (1 / s) is off by less
+// than 2^-20, so adding 1.5 2^23 rounds it right and leaves the code in the sum's low bits,
+// unless it lies that near a border (c + 1/2) s; there the borders themselves decide: (c + 1/2)
+// has 4 significant bits and s has 8, so their product is exact.  bf16 inputs meet a border
+// exactly about once in 2,000 numbers.
+struct Kv4Coder {
+  float s, inv, up;
+  __device__ __forceinline__ explicit Kv4Coder(__nv_bfloat16 sb) {
+    s = bf16f(sb);
+    up = s < 1e-30f ? 0x1p100f : 1.f;  // keeps the reciprocal of a tiny scale finite
+    inv = s > 0.f ? 1.f / (s * up) : 0.f;
+  }
+  // low four bits: the code in two's complement
+  __device__ __forceinline__ uint32_t operator()(float x) const {
+    const float q = x * up * inv, u = q + 12582912.f, c = u - 12582912.f;
+    // (a quotient of a subnormal or a clamped scale may lie beyond 7.1)
+    if (fabsf(q - c) > 0.4999f || fabsf(q) > 7.1f) return exact(x, c);
+    return __float_as_uint(u);
+  }
+  __device__ __noinline__ uint32_t exact(float x, float guess) const {
+    const float a = fabsf(x);
+    float c = fminf(fabsf(guess), 7.f);
+    const float lo = (c - 0.5f) * s, hi = (c + 0.5f) * s;
+    const bool odd = ((int)c) & 1;
+    if (a > hi || (a == hi && odd)) c += 1.f;
+    else if (a < lo || (a == lo && odd)) c -= 1.f;
+    const int k = (int)fminf(fmaxf(c, 0.f), 7.f);
+    return (uint32_t)(x < 0.f ? -k : k);
+  }
+};
+constexpr uint32_t kKv4Bias = 0x88888888u;  // two's complement nibbles ^ this = code + 8
 
 // Decoding a pair of codes to the bf16 values bf16(c * s).
 //
@@ -212,8 +287,10 @@ __device__ __forceinline__ bool kv4_rows_of(const Kv4RowArgs& a, int i, bool wri
 }
 
 // ------------------------------------------------------------------------------ append
-// A thread codes one octet (eight numbers) of a row's key and value; the four lanes of a group
-// share their largest magnitude.
+// Two kernels.  Below 16 rows (kKv4Block) a thread codes one octet (eight numbers) of a row's key
+// and value, the four lanes of a group sharing their largest magnitude: short chains, small
+// scattered stores.  From 16 rows on a warp codes a whole block of 16 rows in the layout's own
+// order, so that codes leave in 16-byte pieces and most groups lie in one lane.
 constexpr int kKv4RowThreads = 256;
 
 template <int D>
@@ -253,25 +330,23 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
     m = fmaxf(m, __shfl_xor_sync(quad, m, 1));
     m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
     const __nv_bfloat16 sb = kv4_scale(m);
-    const float s = bf16f(sb);
-    wide |= s > 0.f && !(s >= kKv4Narrow && s <= kKv4Wide);
-    const float up = s < 1e-30f ? 0x1p100f : 1.f;  // keeps the reciprocal of a tiny scale finite
-    const float inv = s > 0.f ? 1.f / (s * up) : 0.f;
+    const Kv4Coder code(sb);
+    wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
     uint32_t n[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) n[e] = s > 0.f ? (uint32_t)(kv4_code(v[e], s, up, inv) + 8) : 8u;
+    for (int e = 0; e < 8; ++e) n[e] = code(v[e]) & 15u;
     if (b >= 0) {
       if (kv == 0) {
         uint32_t w = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) w |= n[e] << ((e >> 1) * 4 + (e & 1) * 16);
-        *reinterpret_cast<uint32_t*>(blk + O::k_word(r, o)) = w;
+        *reinterpret_cast<uint32_t*>(blk + O::k_word(r, o)) = w ^ kKv4Bias;
         if ((o & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::k_scale(r, o >> 2)) = sb;
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           *reinterpret_cast<uint16_t*>(blk + O::v_half(r, 2 * o + u)) =
-              (uint16_t)(n[4 * u] | (n[4 * u + 1] << 4) | (n[4 * u + 2] << 8) | (n[4 * u + 3] << 12));
+              (uint16_t)((n[4 * u] | (n[4 * u + 1] << 4) | (n[4 * u + 2] << 8) | (n[4 * u + 3] << 12)) ^ kKv4Bias);
         if ((o & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::v_scale(r, o >> 2)) = sb;
       }
     }
@@ -358,6 +433,276 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_account_kernel(const Kv4Ro
   const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
   if (a.positions_out) a.positions_out[at] = b < 0 ? 0 : __ldcg(a.c.pos + b * kKv4Block + row % kKv4Block);
   if (a.weights_out) a.weights_out[at] = b < 0 ? 0.f : __ldcg(a.c.weight + b * kKv4Block + row % kKv4Block);
+}
+
+// ---------------------------------------------------------------------- whole blocks
+// A warp per (block of 16 rows, KV head), keys (blockIdx.z 0) and values (1) apart: unit u of
+// sequence i is head u % kvh of the block that holds row start + 16 (u / kvh).  live: bit r = row r of the block is the call's and its index in
+// the call is below `count`.
+constexpr int kKv4BlockWarps = 4;
+struct Kv4BlockUnit {
+  int head, row, base;  // first row of the block; the call's index of it (may be negative)
+  long at;              // pool index, -1: no page
+  unsigned live, rest;  // rows with data; rows of the call without (zero_rest)
+};
+__device__ __forceinline__ bool kv4_block_unit(const Kv4RowArgs& a, int i, bool writes, Kv4BlockUnit* x) {
+  int slot, row0, count;
+  if (!kv4_rows_of(a, i, writes, &slot, &row0, &count)) {
+    if (!a.zero_rest) return false;
+    count = row0 = 0;
+  }
+  const int limit = a.zero_rest ? a.n_rows : count;
+  const long u = (long)blockIdx.x * kKv4BlockWarps + (threadIdx.x >> 5);
+  x->head = (int)(u % a.c.kvh);
+  const long b = row0 / kKv4Block + u / a.c.kvh;
+  if (b * kKv4Block - row0 >= limit) return false;
+  x->row = (int)b * kKv4Block;
+  x->base = x->row - row0;
+  const int lo = max(0, -x->base), hi = min(kKv4Block, limit - x->base), mid = max(lo, min(kKv4Block, count - x->base));
+  const unsigned all = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+  x->live = all & ((1u << mid) - 1u);
+  x->at = -1;
+  if (x->live) {
+    x->at = kv4_block(a.c, slot, x->head, (int)b);
+    if (x->at < 0) {
+      if ((threadIdx.x & 31) == 0) set_err(a.c.err, G4_DEV_BAD_POSITION);
+      x->live = 0;
+    }
+  }
+  x->rest = a.zero_rest ? all & ~x->live : 0u;
+  return true;
+}
+
+// NG groups' worth of numbers of one row into codes: 4 NG words of eight numbers each in two's
+// complement (word order: consecutive numbers, pairs at bits 4j and 16 + 4j) and NG scales.
+struct Kv4Odd {
+  bool value = false, wide = false;
+};
+template <int N>
+__device__ __forceinline__ float kv4_amax(float (&v)[N], Kv4Odd& odd) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) m = fmaxf(m, fabsf(v[e]));  // skips NaN
+  bool fine = m <= 3.402823466e38f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) fine = fine && v[e] == v[e];
+  if (!fine) {  // NaN counts as 0, an infinity as the largest finite number
+    odd.value = true;
+    m = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (!(fabsf(v[e]) <= 3.402823466e38f)) v[e] = v[e] != v[e] ? 0.f : copysignf(3.402823466e38f, v[e]);
+      m = fmaxf(m, fabsf(v[e]));
+    }
+  }
+  return m;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kKv4BlockWarps) kv4_append_blocks_kernel(const Kv4RowArgs a) {
+  using O = Kv4Off<D>;
+  const int i = blockIdx.y, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  Kv4BlockUnit x;
+  if (!kv4_block_unit(a, i, true, &x) || !x.live) return;
+  uint8_t* blk = a.c.data + (size_t)x.at * O::kBlock;
+  Kv4Odd odd;
+  if (blockIdx.z == 0) {  // ---- keys: rows g and g + 8, numbers [t D/4, (t+1) D/4), 32 (D = 64: 16) at a time
+    constexpr int N = D >= 128 ? 32 : 16, NP = N / 16;  // numbers and pieces of a step
+    const long from = (long)i * a.k.seq + (long)x.head * a.k.head + t * (D / 4);
+    for (int k = 0; k < D / 4 / N; ++k) {
+      uint32_t w[NP][4] = {};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = g + 8 * half;
+        const bool on = (x.live >> r) & 1;
+        float v[N];
+#pragma unroll
+        for (int o = 0; o < N / 16; ++o) {
+          if (on) kv4_load16(a.k, from + (long)(x.base + r) * a.k.row + k * N + 16 * o, v + 16 * o);
+          else
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[16 * o + e] = 0.f;
+        }
+        float m = kv4_amax(v, odd);
+        if (D == 64) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        const __nv_bfloat16 sb = kv4_scale(m);
+        const Kv4Coder code(sb);
+        odd.wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
+#pragma unroll
+        for (int o = 0; o < N / 8; ++o) {
+          uint32_t u = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u |= (code(v[8 * o + e]) & 15u) << ((e >> 1) * 4 + (e & 1) * 16);
+          w[o >> 1][2 * half + (o & 1)] = u ^ kKv4Bias;
+        }
+        if (on && (D > 64 || !(t & 1))) *reinterpret_cast<__nv_bfloat16*>(blk + O::k_scale(r, (t * (D / 4) + k * N) / kKv4Group)) = sb;
+      }
+      const bool on0 = (x.live >> g) & 1, on1 = (x.live >> (g + 8)) & 1;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        uint32_t* to = reinterpret_cast<uint32_t*>(blk) + ((k * NP + p) * 32 + lane) * 4;
+        if (on0 && on1) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        } else if (on0) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[p][0], w[p][1]);
+        } else if (on1) {
+          *reinterpret_cast<uint2*>(to + 2) = make_uint2(w[p][2], w[p][3]);
+        }
+      }
+    }
+  }
+  if (blockIdx.z == 1) {  // ---- values: rows 2t, 2t + 1, 2t + 8, 2t + 9, numbers [g D/8, (g+1) D/8), N at a time
+    constexpr int N = D >= 256 ? 32 : D / 8, NP = N / 8;
+    const long from = (long)i * a.v.seq + (long)x.head * a.v.head + g * (D / 8);
+    for (int k = 0; k < D / 8 / N; ++k) {
+      uint32_t w[NP][4] = {};  // [piece][words of the pair t, words of the pair t + 4]
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 2 * t + (q & 1) + 8 * (q >> 1);
+        const bool on = (x.live >> r) & 1;
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = 0.f;
+        if (on) {
+          const long at = from + (long)(x.base + r) * a.v.row + k * N;
+          if constexpr (N == 8) kv4_load8(a.v, at, v);
+          else
+#pragma unroll
+            for (int o = 0; o < N / 16; ++o) kv4_load16(a.v, at + 16 * o, v + 16 * o);
+        }
+        float m = kv4_amax(v, odd);
+        if (D <= 128) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+        if (D == 64) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        const __nv_bfloat16 sb = kv4_scale(m);
+        const Kv4Coder code(sb);
+        odd.wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
+#pragma unroll
+        for (int o = 0; o < NP; ++o)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[o][2 * (q >> 1) + (e >> 2)] |= (code(v[8 * o + e]) & 15u) << ((e & 3) * 4 + (q & 1) * 16);
+        const int n0 = g * (D / 8) + k * N;
+        if (on && n0 % kKv4Group == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::v_scale(r, n0 / kKv4Group)) = sb;
+      }
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        uint32_t* to = reinterpret_cast<uint32_t*>(blk + O::kV) + ((k * NP + p) * 32 + lane) * 4;
+        const unsigned mine = (x.live >> (2 * t)) & 0x303u;
+        if (mine == 0x303u) {
+          *reinterpret_cast<uint4*>(to) =
+              make_uint4(w[p][0] ^ kKv4Bias, w[p][1] ^ kKv4Bias, w[p][2] ^ kKv4Bias, w[p][3] ^ kKv4Bias);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((x.live >> (2 * t + (q & 1) + 8 * (q >> 1))) & 1)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                reinterpret_cast<uint16_t*>(to + 2 * (q >> 1) + e)[q & 1] =
+                    (uint16_t)((w[p][2 * (q >> 1) + e] ^ kKv4Bias) >> (16 * (q & 1)));
+        }
+      }
+    }
+  }
+  if (odd.value) set_err(a.c.err, G4_DEV_BAD_VALUE);
+  if (odd.wide) *a.c.wide = 1;
+  if (blockIdx.z == 0 && a.c.pos && lane < kKv4Block && ((x.live >> lane) & 1)) {
+    const size_t at = ((size_t)i * a.c.kvh + x.head) * a.n_rows + x.base + lane;
+    a.c.pos[x.at * kKv4Block + lane] = a.positions ? __ldcg(a.positions + at) : x.row + lane;
+    a.c.weight[x.at * kKv4Block + lane] = a.weights ? __ldcg(a.weights + at) : 0.f;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kKv4BlockWarps) kv4_read_blocks_kernel(const Kv4RowArgs a) {
+  using O = Kv4Off<D>;
+  const int i = blockIdx.y, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  Kv4BlockUnit x;
+  if (!kv4_block_unit(a, i, false, &x)) return;
+  const uint8_t* blk = a.c.data + (size_t)(x.at < 0 ? 0 : x.at) * O::kBlock;
+  const unsigned any = x.live | x.rest;
+  if (blockIdx.z == 0 && a.k.p) {
+    uint4 u[D / 64] = {};
+    uint32_t s[2][(D / 4 + 31) / 32] = {};
+    if (x.live) {
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) u[k] = __ldcg(reinterpret_cast<const uint4*>(blk) + k * 32 + lane);
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int k = 0; k < (D / 4 + 31) / 32; ++k)
+          s[half][k] = 0x10001u * __ldcg(reinterpret_cast<const uint16_t*>(blk + O::k_scale(g + 8 * half, t * (D / 4) / kKv4Group + k)));
+    }
+    const long to = (long)i * a.k.seq + (long)x.head * a.k.head + t * (D / 4);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = g + 8 * half;
+      if (!((any >> r) & 1)) continue;
+      const bool on = (x.live >> r) & 1;
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p) {
+        float v[16];
+        const uint32_t c0 = half ? u[p].z : u[p].x, c1 = half ? u[p].w : u[p].y;
+        const Kv4Scale<true> sc(s[half][p >> 1]);
+        const uint32_t y[8] = {sc.pair<0>(c0), sc.pair<1>(c0), sc.pair<2>(c0), sc.pair<3>(c0),
+                               sc.pair<0>(c1), sc.pair<1>(c1), sc.pair<2>(c1), sc.pair<3>(c1)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[2 * e] = on ? bf16_lo(y[e]) : 0.f;
+          v[2 * e + 1] = on ? bf16_hi(y[e]) : 0.f;
+        }
+        kv4_store16(a.k, to + (long)(x.base + r) * a.k.row + 16 * p, v);
+      }
+    }
+  }
+  if (blockIdx.z == 1 && a.v.p) {
+    uint4 u[D / 64] = {};
+    constexpr int NG = D >= 256 ? D / 256 : 1;
+    uint32_t s[2][NG] = {};
+    if (x.live) {
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) u[k] = __ldcg(reinterpret_cast<const uint4*>(blk + O::kV) + k * 32 + lane);
+#pragma unroll
+      for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+          s[pr][k] = __ldcg(reinterpret_cast<const uint32_t*>(blk + O::v_scale(2 * t + 8 * pr, g * (D / 8) / kKv4Group + k)));
+    }
+    const long to = (long)i * a.v.seq + (long)x.head * a.v.head + g * (D / 8);
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr) {
+      const int r = 2 * t + 8 * pr;
+      constexpr int PS = D >= 128 ? 2 : 1;  // pieces stored at a time: 16 numbers, or D = 64's eight
+#pragma unroll
+      for (int p0 = 0; p0 < D / 64; p0 += PS) {
+        float even[8 * PS], odd[8 * PS];
+#pragma unroll
+        for (int q = 0; q < PS; ++q) {
+          const int p = p0 + q;
+          const Kv4Scale<true> sc(s[pr][NG > 1 ? p / 4 : 0]);
+          const uint32_t c0 = pr ? u[p].z : u[p].x, c1 = pr ? u[p].w : u[p].y;
+          const uint32_t y[8] = {sc.pair<0>(c0), sc.pair<1>(c0), sc.pair<2>(c0), sc.pair<3>(c0),
+                                 sc.pair<0>(c1), sc.pair<1>(c1), sc.pair<2>(c1), sc.pair<3>(c1)};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            even[8 * q + e] = (x.live >> r) & 1 ? bf16_lo(y[e]) : 0.f;
+            odd[8 * q + e] = (x.live >> (r + 1)) & 1 ? bf16_hi(y[e]) : 0.f;
+          }
+        }
+        const long at = to + (long)(x.base + r) * a.v.row + 8 * p0;
+        if constexpr (PS == 2) {
+          if ((any >> r) & 1) kv4_store16(a.v, at, even);
+          if ((any >> (r + 1)) & 1) kv4_store16(a.v, at + a.v.row, odd);
+        } else {
+          if ((any >> r) & 1) kv4_store8(a.v, at, even);
+          if ((any >> (r + 1)) & 1) kv4_store8(a.v, at + a.v.row, odd);
+        }
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------- evict

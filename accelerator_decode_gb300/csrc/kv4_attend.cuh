@@ -85,6 +85,8 @@ __device__ __forceinline__ void kv4_split(float x, float y, uint32_t (&p)[PARTS]
   }
 }
 
+constexpr int kKv4MaxCtas = 3;
+
 template <int D, int DT>
 struct Kv4Att {
   static constexpr int kQP = DT == G4_DT_F32 ? 3 : DT == G4_DT_F16 ? 2 : 1;  // parts of a query
@@ -97,12 +99,13 @@ struct Kv4Att {
   static constexpr int kKeys = kBlocks * kKv4Block;    // keys of a tile: 256, 128, 64, 64
   static constexpr int kTile = kBlocks * 18 * D;       // bytes of a tile: 18 KB (D = 512: 36 KB)
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;
+  static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
+  static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
   static constexpr int kOBytes = 4 * D * 32;           // four warps' sums, [warp][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
-    return (size_t)stages * kTile + kFixed + (size_t)n_seq * 24 + 16;
+    return (size_t)stages * kTile + kFixed + (size_t)n_seq * 20 + 16;
   }
 };
 
@@ -116,7 +119,7 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttendArgs& a, int len, int m,
   return m > 0 && len > 0 ? (len + KEYS - 1) / KEYS - *tile0 : 0;
 }
 template <int KEYS>
-__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* first, int4* seqs, bool report) {
+__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, int* first, int4* seqs, bool report) {
   for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
     int slot, len, m, t0;
     bool ok = kv4_seq(a, i, &slot, &len, &m);
@@ -137,16 +140,16 @@ __device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* firs
   __syncthreads();
   if (threadIdx.x < 32) {  // running sum, 32 sequences at a time
     const int lane = threadIdx.x;
-    long long base = 0;
+    int base = 0;
     int longest = 0;
     if (lane == 0) first[0] = 0;
     for (int i = 0; i < a.n_seq; i += 32) {
       const int n = i + lane < a.n_seq ? seqs[i + lane].w : 0;
       longest = max(longest, n);
-      long long v = (long long)n * a.c.kvh * a.row_tiles;
+      int v = n * a.c.kvh * a.row_tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
         if (lane >= o) v += u;
       }
       if (i + lane < a.n_seq) first[i + lane + 1] = base + v;
@@ -158,10 +161,10 @@ __device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, long long* firs
   __syncthreads();
 }
 // Tiles per CTA.  An item that is joined inside is shared by kKv4Join + 1 CTAs at the most.
-constexpr int kKv4Join = 24;
-__device__ __forceinline__ long long kv4_span(const Kv4AttendArgs& a, const long long* first, int ctas) {
-  const long long even = (first[a.n_seq] + ctas - 1) / ctas;
-  return max(1LL, a.join_inside ? max(even, (first[a.n_seq + 1] + kKv4Join - 1) / kKv4Join) : even);
+constexpr int kKv4Join = 8;
+__device__ __forceinline__ int kv4_span(const Kv4AttendArgs& a, const int* first, int ctas) {
+  const int even = (int)(((unsigned)first[a.n_seq] + ctas - 1) / ctas);
+  return max(1, a.join_inside ? max(even, (first[a.n_seq + 1] + kKv4Join - 1) / kKv4Join) : even);
 }
 
 // A run of tiles of one item: what a CTA does between two item borders.
@@ -170,12 +173,12 @@ struct Kv4Run {
   int slot, len, m;
   int tile, tiles;     // first tile (absolute) and their number
   int of;              // tiles of the item
-  long long item_t0;   // the item's first tile in the order of all
+  int item_t0;   // the item's first tile in the order of all
   bool whole;          // the run is the whole item
 };
 // The run that starts at global tile g (g < end <= total).
 template <int KEYS>
-__device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long long* first, const int4* seqs, long long g, long long end) {
+__device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const int* first, const int4* seqs, int g, int end) {
   int lo = 0, hi = a.n_seq - 1;  // the last sequence with first[i] <= g (empty ones in between share it)
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -190,13 +193,13 @@ __device__ __forceinline__ Kv4Run kv4_run(const Kv4AttendArgs& a, const long lon
   r.of = q.w;
   int t0;
   kv4_tiles<KEYS>(a, r.len, r.m, &t0);
-  const long long x = g - first[lo];
-  const int item = (int)(x / r.of), off = (int)(x % r.of);
+  const int x = g - first[lo];
+  const int item = (unsigned)x / (unsigned)r.of, off = x - item * r.of;
   r.item_t0 = g - off;
   r.head = item / a.row_tiles;
   r.row_tile = item % a.row_tiles;
   r.tile = t0 + off;
-  r.tiles = (int)min((long long)(r.of - off), end - g);
+  r.tiles = min(r.of - off, end - g);
   r.whole = r.tiles == r.of;
   return r;
 }
@@ -292,7 +295,7 @@ __device__ __forceinline__ void kv4_scores(const uint4* qs, int lane, Codes code
 
 // ------------------------------------------------------------------------ joining parts
 // CTA c's part of the item that starts at tile t0: slot 0 when the item opens c's span, else 1.
-__device__ __forceinline__ long kv4_part(int c, long long t0, long long span) { return (long)c * 2 + (t0 > c * span ? 1 : 0); }
+__device__ __forceinline__ long kv4_part(int c, int t0, int span) { return (long)c * 2 + (t0 > c * span ? 1 : 0); }
 __device__ __forceinline__ float kv4_lse(float2 ml) { return ml.y != 0.f ? ml.x + log2f(ml.y) : INFINITY; }
 __device__ __forceinline__ void kv4_merge_ml(float2& u, float2 v) {
   const float m = fmaxf(u.x, v.x), z = m == -INFINITY ? 0.f : m;
@@ -301,7 +304,7 @@ __device__ __forceinline__ void kv4_merge_ml(float2& u, float2 v) {
 }
 // Maximum and sum of the item's eight rows over its parts c0 .. c1 into ml[0..8), by `warps` warps
 // that share barrier `bar` (ml: 8 + 8 * warps entries): a thread takes a row and every 4 warps'th part.
-__device__ __forceinline__ void kv4_join_ml(const Kv4AttendArgs& a, long long t0, long long span, int c0, int c1, int tid,
+__device__ __forceinline__ void kv4_join_ml(const Kv4AttendArgs& a, int t0, int span, int c0, int c1, int tid,
                                             int warps, float2* ml, int bar) {
   float2 u = make_float2(-INFINITY, 0.f);
 #pragma unroll 4
@@ -322,8 +325,8 @@ __device__ __forceinline__ void kv4_join_ml(const Kv4AttendArgs& a, long long t0
 }
 // The item's output rows from its parts, in span order (c1 < c0: zeros); entries e0, e0 + step, ..
 template <int D>
-__device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, int head, int row0, int n_rows, long long t0,
-                                              long long span, int c0, int c1, const float2* ml, int e0, int step) {
+__device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, int head, int row0, int n_rows, int t0,
+                                              int span, int c0, int c1, const float2* ml, int e0, int step) {
   constexpr int W = D / 32;
   for (int e = e0; e < W * 64; e += step) {
     const int l = e & 31, r8 = 2 * (l & 3) + ((e >> 5) & 1), w = e >> 6, row = row0 + r8;
@@ -353,7 +356,7 @@ __device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, i
 // Zeros for the query rows that no tile reaches: those of sequences without rows, and with
 // zero_rest the padding.  Sequences i0, i0 + step, ..
 template <int D>
-__device__ __forceinline__ void kv4_zero_rows(const Kv4AttendArgs& a, const long long* first, const int4* seqs, int i0, int step,
+__device__ __forceinline__ void kv4_zero_rows(const Kv4AttendArgs& a, const int* first, const int4* seqs, int i0, int step,
                                               int tid, int threads) {
   for (int i = i0; i < a.n_seq; i += step) {
     const int t0 = seqs[i].w > 0 ? seqs[i].z : 0, t1 = a.zero_rest ? a.q_len : seqs[i].z;  // tokens to clear
@@ -377,7 +380,7 @@ struct Kv4Shared {
   volatile int* abort_flag;
   volatile int* last;  // this CTA joins the item
   int4* seqs;
-  long long* first;
+  int* first;
   __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages, int n_seq) {
     using C = Kv4Att<D, DT>;
     ring = smem;
@@ -390,13 +393,13 @@ struct Kv4Shared {
     abort_flag = reinterpret_cast<volatile int*>(held + 8);
     last = abort_flag + 1;
     seqs = reinterpret_cast<int4*>(full + 32);
-    first = reinterpret_cast<long long*>(seqs + n_seq);
+    first = reinterpret_cast<int*>(seqs + n_seq);
   }
 };
 
 template <int D, int DT, bool WIDE>
-__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, long long g0, long long g1,
-                                            long long span) {
+__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, int g0, int g1,
+                                            int span) {
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
   constexpr int W = D / 32, NB = C::kNB;  // words of a key (or value pair) per lane
@@ -404,7 +407,7 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
   const int set = warp >> 2, wq = warp & 3;
   const float score_scale = WIDE ? a.scale : a.scale * kKv4Up;
   int it = 0, piece = 0;
-  for (long long at = g0; at < g1; ++piece) {
+  for (int at = g0; at < g1; ++piece) {
     const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
     const int n_rows = r.m * a.group, row0 = r.row_tile * 8;
     named_bar_sync(1, 32 * C::kWarps);
@@ -614,7 +617,7 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
     if (a.join_inside && !whole) {
       __threadfence();
       named_bar_sync(1, 32 * C::kWarps);
-      const int c0 = (int)(r.item_t0 / span), c1 = (int)((r.item_t0 + r.of - 1) / span);
+      const int c0 = (unsigned)r.item_t0 / (unsigned)span, c1 = (unsigned)(r.item_t0 + r.of - 1) / (unsigned)span;
       const long item = ((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile;
       if (threadIdx.x == 0) {
         const bool is_last = atomicAdd(a.tickets + item, 1u) == (unsigned)(c1 - c0);
@@ -653,9 +656,9 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   pdl_trigger();
   const int wide = __ldcg(a.c.wide);
   kv4_plan<C::kKeys>(a, sh.first, sh.seqs, blockIdx.x == 0);
-  const long long total = sh.first[a.n_seq];
-  const long long span = kv4_span(a, sh.first, gridDim.x);
-  const long long g0 = min(total, (long long)blockIdx.x * span), g1 = min(total, g0 + span);
+  const int total = sh.first[a.n_seq];
+  const int span = kv4_span(a, sh.first, gridDim.x);
+  const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
   if (warp < C::kWarps) {
     if (wide) kv4_consume<D, DT, true>(a, sh, g0, g1, span);
     else kv4_consume<D, DT, false>(a, sh, g0, g1, span);
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   // ---- producer: tiles into the ring
   int it = 0;
   bool stop = false;
-  for (long long at = g0; at < g1 && !stop;) {
+  for (int at = g0; at < g1 && !stop;) {
     const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
     const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
     for (int x = 0; x < r.tiles; ++x, ++it) {
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4
   extern __shared__ __align__(128) uint8_t kv4_smem[];
   int4* seqs = reinterpret_cast<int4*>(kv4_smem);
   uint4* qs = reinterpret_cast<uint4*>(seqs + a.n_seq);
-  long long* first = reinterpret_cast<long long*>(qs + C::kQBytes / 16);
+  int* first = reinterpret_cast<int*>(qs + C::kQBytes / 16);
   __shared__ float2 ml[8 + 8 * kKv4FinishThreads / 32];
   __shared__ float sE[8];
   const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -774,9 +777,9 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4
   kv4_plan<C::kKeys>(a, first, seqs, false);
   const int slot = seqs[i].x, len = seqs[i].y, m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
   if (!join && n > 0) kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
-  const long long span = kv4_span(a, first, ctas);
-  const long long t0 = first[i] + (long long)n * x;  // the item's first tile
-  const int c0 = (int)(t0 / span), c1 = n ? (int)((t0 + n - 1) / span) : c0 - 1;
+  const int span = kv4_span(a, first, ctas);
+  const int t0 = first[i] + n * x;  // the item's first tile
+  const int c0 = (unsigned)t0 / (unsigned)span, c1 = n ? (int)((unsigned)(t0 + n - 1) / (unsigned)span) : c0 - 1;
   pdl_wait();
   pdl_trigger();
   if (join) {

@@ -401,7 +401,8 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0,
  * a scale that is not finite, q and out of different types, malformed tensors), UNSUPPORTED
  * (accumulate without track; a window with a cache that tracks: after an eviction its rows are
- * no longer in position order). */
+ * no longer in position order; n_seq * num_kv_heads * ceil(q_len * heads per KV head / 8) *
+ * ceil(capacity / 64) at 2^31 or more). */
 g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                         const int32_t* d_lens, int32_t q_len, const int32_t* d_q_lens, float scale,
                         int32_t window, int32_t accumulate, int32_t zero_rest,
