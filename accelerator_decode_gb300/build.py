@@ -11,7 +11,7 @@ LIB = os.path.join(HERE, "libg4.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("g4.cu", "kv4.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in (
     "common.cuh", "gemv.cuh", "gemv_s.cuh", "attn.cuh", "attn_mqa.cuh", "misc.cuh", "gemm_tc.cuh", "mega.cuh",
-    "host.h", "mbar.cuh", "kv4_layout.h", "kv4.cuh", "kv4_attend.cuh")]
+    "host.h", "mbar.cuh", "kv4_layout.h", "kv4.cuh", "kv4_attend.cuh", "kv4_block.cuh")]
 HEADERS.append(os.path.join(os.path.dirname(HERE), "include", "g4.h"))
 DEPS = SOURCES + HEADERS
 

@@ -10,6 +10,7 @@
 #include "host.h"
 #include "kv4.cuh"
 #include "kv4_attend.cuh"
+#include "kv4_block.cuh"
 
 using namespace g4;
 
@@ -114,6 +115,12 @@ void kv4_attrs(int optin) {
   set_max_dyn(kv4_finish_kernel<D, DT>, optin);
 }
 template <int D>
+void kv4_attrs_block(int optin) {
+  set_max_dyn(kv4_block_kernel<D, false>, optin);
+  set_max_dyn(kv4_block_kernel<D, true>, optin);
+  carve_max(kv4_block_join_kernel<D>);
+}
+template <int D>
 void kv4_attrs_d(int optin) {
   kv4_attrs<D, G4_DT_F32>(optin);
   kv4_attrs<D, G4_DT_BF16>(optin);
@@ -131,12 +138,33 @@ void kv4_init(int device, int optin) {
   kv4_attrs_d<128>(optin);
   kv4_attrs_d<256>(optin);
   kv4_attrs_d<512>(optin);
+  kv4_attrs_block<64>(optin);
+  kv4_attrs_block<128>(optin);
+  kv4_attrs_block<256>(optin);
   carve_max(kv4_account_kernel);
   set_max_dyn(kv4_select_kernel, optin);
   cudaGetLastError();
 }
 int kv4_most_moves(const g4_kv4* op) { return std::max(1, op->cfg.capacity / 2); }
 int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads), 8); }
+
+// Blocks of query tokens on the 5th-generation tensor cores (kv4_block.cuh).
+bool kv4_block_path(const g4_kv4* op, int q_len, int dtype) {
+  return dtype == G4_DT_BF16 && op->cfg.head_dim <= 256 && q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads) > kKv4BlockRows;
+}
+template <int D>
+void kv4_launch_block(g4_kv4* op, Kv4AttendArgs a, cudaStream_t st) {
+  const int rows = a.q_len * a.group;
+  a.row_tiles = cdiv(rows, kKv4M);
+  a.lse_rows = a.row_tiles * kKv4M;
+  a.join_inside = 0;
+  launch(kv4_block_kernel<D, false>, dim3(op->sms), dim3(kKv4BlockThreads), Kv4Blk<D, false>::smem(a.n_seq), st, a);
+  launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, kKv4M / kKv4BlockJoinRows), dim3(128), (size_t)a.n_seq * 20 + 16,
+         st, a, op->sms);
+  if (!a.accumulate) return;
+  a.row_tiles = 1;  // the account cuts the keys alone into spans
+  launch(kv4_block_kernel<D, true>, dim3(op->sms), dim3(kKv4BlockThreads), Kv4Blk<D, true>::smem(a.n_seq), st, a);
+}
 
 template <int D, int DT>
 void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
@@ -194,10 +222,13 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   TRY(kv4_alloc(op, &c.data, blocks * 18 * f.head_dim, st));
   TRY(kv4_alloc(op, &c.wide, 1, st));
   TRY(kv4_alloc(op, &c.err, 1, st));
-  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len) * 8, st));
-  const size_t parts = (size_t)2 * op->sms * kKv4MaxCtas;  // two partial items of every CTA
-  TRY(kv4_alloc(op, &op->part_o, parts * (f.head_dim * 2), st));
-  TRY(kv4_alloc(op, &op->part_ml, parts * 8, st));
+  const bool blocks_too = kv4_block_path(op, f.max_q_len, G4_DT_BF16);
+  const size_t rows = (size_t)kv4_row_tiles(op, f.max_q_len) * 8;
+  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * (blocks_too ? (rows + kKv4M - 1) / kKv4M * kKv4M : rows), st));
+  // two partial items of every CTA, of 8 query rows each (three CTAs per SM at the most), or 128
+  const size_t part_rows = (size_t)2 * op->sms * std::max(8 * kKv4MaxCtas, blocks_too ? kKv4M : 0);
+  TRY(kv4_alloc(op, &op->part_o, part_rows * f.head_dim / 4, st));
+  TRY(kv4_alloc(op, &op->part_ml, part_rows, st));
   TRY(kv4_alloc(op, &op->tickets, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len), st));
   if (f.track) {
     TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
@@ -361,10 +392,19 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.accumulate = accumulate != 0;
   a.zero_rest = zero_rest != 0;
   a.lse = op->lse;
+  a.lse_rows = a.row_tiles * 8;
   a.part_o = op->part_o;
   a.part_ml = op->part_ml;
   a.tickets = op->tickets;
-  KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op, a, st))));
+  if (kv4_block_path(op, q_len, q->dtype)) {
+    switch (op->c.d) {
+      case 64: kv4_launch_block<64>(op, a, st); break;
+      case 128: kv4_launch_block<128>(op, a, st); break;
+      default: kv4_launch_block<256>(op, a, st); break;
+    }
+  } else {
+    KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op, a, st))));
+  }
   CK(cudaGetLastError());
   return G4_OK;
 }

@@ -30,7 +30,8 @@ struct Kv4AttendArgs {
   int join_inside;                   // the CTA that finishes a shared item last joins its parts
   int stages;
   Kv4Dense q, out;
-  float* lse;                        // [n_seq][kvh][row_tiles * 8]: log2 of the softmax's sum
+  float* lse;                        // [n_seq][kvh][lse_rows]: log2 of the softmax's sum
+  int lse_rows;
   float4* part_o;                    // [2 * CTAs][D / 32][2][32]: a span's partial first and last item
   float2* part_ml;                   // [2 * CTAs][8]: running maximum (log2 units) and sum
   unsigned* tickets;                 // [items]: parts done, zero between calls
@@ -609,7 +610,7 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
         a.part_ml[slot_p * 8 + 2 * t] = make_float2(M0, L0);
         a.part_ml[slot_p * 8 + 2 * t + 1] = make_float2(M1, L1);
       } else {
-        float* lse = a.lse + (((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile) * 8 + 2 * t;
+        float* lse = a.lse + ((long)r.seq * a.c.kvh + r.head) * a.lse_rows + r.row_tile * 8 + 2 * t;
         lse[0] = L0 != 0.f ? M0 + log2f(L0) : INFINITY;
         lse[1] = L1 != 0.f ? M1 + log2f(L1) : INFINITY;
       }
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const Kv4A
     for (int rt = tok0 * a.group / 8; rt * 8 < n_rows; ++rt) {
       __syncthreads();
       kv4_stage_q<D, DT>(a, qs, i, h, rt * 8, n_rows, threadIdx.x, 32 * kKv4GainWarps);
-      if (threadIdx.x < 8) lse8[threadIdx.x] = __ldcg(a.lse + (((long)i * a.c.kvh + h) * a.row_tiles + rt) * 8 + threadIdx.x);
+      if (threadIdx.x < 8) lse8[threadIdx.x] = __ldcg(a.lse + ((long)i * a.c.kvh + h) * a.lse_rows + rt * 8 + threadIdx.x);
       __syncthreads();
       if (at < 0) continue;
       if (wide) kv4_gain_tile<D, DT, true>(a, qs, blk, lane, kb.u, kb.s0, kb.s1, b * kKv4Block + g, lse8, len, m, rt * 8, n_rows, gain0, gain1);

@@ -1,0 +1,580 @@
+// Attention of blocks of query tokens over the 4-bit cache on the 5th-generation tensor cores,
+// for bf16 queries with more than kKv4BlockRows query rows (tokens x heads) per KV head and head
+// dims up to 256; and the account of the weights the rows received.
+//
+// An item is 128 query rows of one KV head.  Its queries sit in tensor memory as the A operand;
+// eight warps decode tiles of 64 keys and values once for all 128 rows into 128-byte-swizzled
+// shared memory; per tile
+//   S = Q K^T  (A tensor memory, B shared, 128 x 64, fp32 in tensor memory, two buffers)
+//   P = 2^(scale S - m) on four warps, a row per thread, written back over S as bf16 parts
+//   O += P V   (A tensor memory, B shared with the head dim leading, 128 x D in tensor memory)
+// P goes in two parts (p - bf16(p) as well), so 16 bits of every weight count; the second pass
+// costs matrix time that the decoding and the exponentials leave free.  A row's reference m is
+// raised, and its sums rescaled, only when a score exceeds it by 2^8: weights up to 256 lose
+// nothing in fp32 or in the parts.
+// Tensor memory holds O (D columns), Q (D / 2) and S (2 x 64): all 512 columns at D = 256.
+//
+// The account (ACCOUNT): the same pipeline without values: a CTA owns a run of keys, takes every
+// block of 128 query rows past them, and adds up p = 2^(scale S - lse) over the rows, by a
+// butterfly over the lanes that leaves each lane two columns, in a fixed order.
+#pragma once
+#include "kv4_attend.cuh"
+
+namespace g4 {
+
+constexpr int kKv4BlockRows = 32;   // more query rows than this per KV head take these kernels
+constexpr int kKv4M = 128;          // query rows of an item
+constexpr int kKv4N = 64;           // keys of a tile
+constexpr int kKv4RunTiles = 16;    // account: tiles of a run at the most
+constexpr int kKv4BlockThreads = 512;
+constexpr int kKv4BlockRing = 3;
+
+template <int D, bool ACCOUNT>
+struct Kv4Blk {
+  static constexpr int kTile = 4 * (ACCOUNT ? 9 : 18) * D;  // coded bytes of a tile in the ring
+  static constexpr int kStride = ACCOUNT ? 9 * D : 18 * D;  // of a block
+  static constexpr int kOperand = kKv4N * D * 2;            // decoded keys (or values) of a tile
+  static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
+  static constexpr int kColQ = D, kColS = D + D / 2;
+  static constexpr int kFixed = 512 /* barriers and flags */ + (ACCOUNT ? 4 * kKv4RunTiles * kKv4N * 4 : 0);
+  static __host__ __device__ size_t smem(int n_seq) {
+    return 1024 + (size_t)(ACCOUNT ? 2 : 4) * kOperand + kKv4BlockRing * kTile + kFixed + (size_t)n_seq * 20 + 16;
+  }
+};
+
+struct Kv4BlockBars {
+  uint64_t full[4], empty[4], kfull[2], kempty[2], vfull[2], sfull[2], pfull[2], pvdone[2], qfull, drained;
+  uint32_t held[8];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Kv4BlockBars) <= 512, "barriers");
+
+__device__ __forceinline__ bool kv4_wait(uint64_t* b, uint32_t parity, Kv4BlockBars* s) {
+  if (*reinterpret_cast<volatile int*>(&s->abort)) return false;
+  if (mbar_wait(b, parity, reinterpret_cast<volatile int*>(&s->abort))) return true;
+  *reinterpret_cast<volatile int*>(&s->abort) = 1;
+  return false;
+}
+__device__ __forceinline__ void kv4_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void kv4_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void kv4_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void kv4_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+// 32 columns of the calling thread's lane, no wait.
+__device__ __forceinline__ void kv4_tld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void kv4_tst32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void kv4_tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void kv4_tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle, rows of 128 bytes in groups of eight 1,024
+// bytes apart.  Keys: the head dim runs along the rows (`lead` unused).  Values: the head dim is
+// the operand's leading dimension and `lead` the distance between its 64-wide slabs.
+__device__ __forceinline__ uint64_t kv4_desc(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead ? lead >> 4 : 1) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16: bf16 operands, fp32 result, M 128.
+__device__ __forceinline__ constexpr uint32_t kv4_idesc(int n, bool b_leading) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_leading ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kKv4M >> 4) << 24);
+}
+
+// ------------------------------------------------------------------------- decoding
+// Bank conflicts: eight lanes store 16 bytes at a time, lanes 4 (g & 1) + t of a phase.  A store
+// address is row R = g or 2t + .., chunk c of its 128 bytes at c ^ (R & 7).  Keys: the lane's
+// chunks are taken in an order permuted by its t and g (and its words swapped into that order by
+// selects); values: lanes of odd g store the odd row of a pair first.  Both make the eight
+// addresses of a phase distinct modulo 128 bytes.
+__device__ __forceinline__ void kv4_cswap(bool swap, uint32_t& a, uint32_t& b) {
+  const uint32_t x = swap ? b : a, y = swap ? a : b;
+  a = x;
+  b = y;
+}
+// Keys: rows of one half (8 half + g) of block b into the operand at `to`.  on false: zeros.
+template <int D, bool WIDE>
+__device__ __forceinline__ void kv4_decode_keys(const uint8_t* blk, int b, int half, bool on, uint8_t* to, int lane) {
+  using O = Kv4Off<D>;
+  constexpr int W = D / 32;
+  const int g = lane >> 2, t = lane & 3, R = 16 * b + 8 * half + g;
+  uint32_t w[W];
+  Kv4KeyScales<D> ks = {};
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      const uint2 u = *reinterpret_cast<const uint2*>(blk + (i * 32 + lane) * 16 + half * 8);
+      w[2 * i] = u.x;
+      w[2 * i + 1] = u.y;
+    }
+    ks = kv4_key_scales<D>(blk + O::kKs, g + 8 * half, t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+  }
+  const int x = D == 256 ? t | (g & 1) << 2 : D == 128 ? t >> 1 | (g & 1) << 1 : 0;
+  if constexpr (W >= 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) kv4_cswap(x & 1, w[i], w[i + 1]);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (!(i & 2)) kv4_cswap(x & 2, w[i], w[i + 2]);
+  }
+  uint32_t first = ks.two(0), second = D == 256 ? ks.two(1) : first;
+  if constexpr (W == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kv4_cswap(x & 4, w[i], w[i + 4]);
+    kv4_cswap(x & 4, first, second);
+  }
+  const Kv4Scale<WIDE> s0(first), s1(second);
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const int n0 = t * (D / 4) + 8 * (j ^ x);  // numbers n0 .. n0 + 7
+    const Kv4Scale<WIDE>& s = j < 4 ? s0 : s1;
+    *reinterpret_cast<uint4*>(to + (n0 >> 6) * (kKv4N * 128) + R * 128 + ((((n0 >> 3) & 7) ^ (R & 7)) << 4)) =
+        make_uint4(s.template pair<0>(w[j]), s.template pair<1>(w[j]), s.template pair<2>(w[j]), s.template pair<3>(w[j]));
+  }
+}
+// Values: rows 2t and 2t + 1 (+ 8 half) of block b.
+template <int D, bool WIDE>
+__device__ __forceinline__ void kv4_decode_values(const uint8_t* blk, int b, int half, bool on, uint8_t* to, int lane) {
+  using O = Kv4Off<D>;
+  const int g = lane >> 2, t = lane & 3;
+  const int odd = D == 64 ? 0 : g & 1, Ra = 16 * b + 8 * half + 2 * t + odd, Rb = Ra ^ 1;
+  const uint32_t take_a = odd ? 0x7632u : 0x5410u, take_b = odd ? 0x5410u : 0x7632u;
+  const uint32_t sv = on ? *reinterpret_cast<const uint32_t*>(blk + O::v_scale(2 * t + 8 * half, g * (D / 8) / kKv4Group)) : 0u;
+  const Kv4Scale<WIDE> s(sv);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    uint2 u = make_uint2(0u, 0u);
+    if (on) u = *reinterpret_cast<const uint2*>(blk + O::kV + (i * 32 + lane) * 16 + half * 8);
+    const uint32_t y[8] = {s.template pair<0>(u.x), s.template pair<1>(u.x), s.template pair<2>(u.x), s.template pair<3>(u.x),
+                           s.template pair<0>(u.y), s.template pair<1>(u.y), s.template pair<2>(u.y), s.template pair<3>(u.y)};
+    const int n0 = g * (D / 8) + 8 * i;
+    uint8_t* slab = to + (n0 >> 6) * (kKv4N * 128);
+    const int c = (n0 >> 3) & 7;
+    *reinterpret_cast<uint4*>(slab + Ra * 128 + ((c ^ (Ra & 7)) << 4)) =
+        make_uint4(__byte_perm(y[0], y[1], take_a), __byte_perm(y[2], y[3], take_a), __byte_perm(y[4], y[5], take_a), __byte_perm(y[6], y[7], take_a));
+    *reinterpret_cast<uint4*>(slab + Rb * 128 + ((c ^ (Rb & 7)) << 4)) =
+        make_uint4(__byte_perm(y[0], y[1], take_b), __byte_perm(y[2], y[3], take_b), __byte_perm(y[4], y[5], take_b), __byte_perm(y[6], y[7], take_b));
+  }
+}
+
+// The run of tiles at `at`: for the account, of at most kKv4RunTiles tiles (a.row_tiles 1), with
+// `blocks` blocks of 128 query rows to take past them.
+template <bool ACCOUNT>
+__device__ __forceinline__ Kv4Run kv4_block_run(const Kv4AttendArgs& a, const int* first, const int4* seqs, int at, int g1, int* blocks) {
+  const Kv4Run r = kv4_run<kKv4N>(a, first, seqs, at, ACCOUNT ? min(g1, at + kKv4RunTiles) : g1);
+  *blocks = ACCOUNT ? (r.m * a.group + kKv4M - 1) / kKv4M : 1;
+  return r;
+}
+
+template <int D, bool ACCOUNT>
+__global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv4AttendArgs a) {
+  using C = Kv4Blk<D, ACCOUNT>;
+  using O = Kv4Off<D>;
+  extern __shared__ __align__(16) uint8_t kv4_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv4_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kop = base;                                             // [2] decoded keys
+  uint8_t* vop = base + 2 * C::kOperand;                           // [2] decoded values
+  uint8_t* ring = base + (ACCOUNT ? 2 : 4) * C::kOperand;
+  Kv4BlockBars* s = reinterpret_cast<Kv4BlockBars*>(ring + kKv4BlockRing * C::kTile);
+  float* gacc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(s) + 512);  // account: [4 warps][keys of a run]
+  int4* seqs = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(s) + C::kFixed);
+  int* first = reinterpret_cast<int*>(seqs + a.n_seq);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKv4BlockRing; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s->kfull[i], 8);
+      mbar_init(&s->kempty[i], 1);
+      mbar_init(&s->vfull[i], 8);
+      mbar_init(&s->sfull[i], 1);
+      mbar_init(&s->pfull[i], 128);
+      mbar_init(&s->pvdone[i], 1);
+    }
+    mbar_init(&s->qfull, 128);
+    mbar_init(&s->drained, 1);
+    s->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&s->tmem)), "r"(C::kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  kv4_fence_before();
+  pdl_wait();
+  pdl_trigger();
+  const int wide = __ldcg(a.c.wide);
+  kv4_plan<kKv4N>(a, first, seqs, !ACCOUNT && blockIdx.x == 0);
+  kv4_fence_after();
+  const uint32_t tmem = s->tmem;
+  const int total = first[a.n_seq], span = kv4_span(a, first, gridDim.x);
+  const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer: coded tiles into the ring
+    int n = 0;
+    for (int at = g0; at < g1;) {
+      int blocks;
+      const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+      const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
+      for (int x = 0; x < blocks * r.tiles; ++x, ++n) {
+        const int st = n % kKv4BlockRing;
+        if (n >= kKv4BlockRing) kv4_wait(&s->empty[st], (n / kKv4BlockRing - 1) & 1, s);
+        const int b = (r.tile + x % r.tiles) * 4 + lane;
+        const bool want = lane < 4 && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
+        const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
+        if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
+        if (*reinterpret_cast<volatile int*>(&s->abort)) break;
+        if (lane == 0) {
+          s->held[n & 7] = have;
+          mbar_expect_tx(&s->full[st], __popc(have) * C::kStride);
+        }
+        __syncwarp();
+        if (at_b >= 0)
+          bulk_g2s(ring + (size_t)st * C::kTile + lane * C::kStride, a.c.data + (size_t)at_b * O::kBlock, C::kStride, &s->full[st]);
+      }
+      if (*reinterpret_cast<volatile int*>(&s->abort)) break;
+      at += r.tiles;
+    }
+    for (int k = max(0, n - kKv4BlockRing); k < n; ++k) mbar_wait_drain(&s->full[k % kKv4BlockRing], (k / kKv4BlockRing) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------ matrix instructions
+    if (lane == 0) {
+      int n = 0, runs = 0;
+      for (int at = g0; at < g1;) {
+        int blocks;
+        const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+        for (int rb = 0; rb < blocks; ++rb, ++runs) {
+          kv4_wait(&s->qfull, runs & 1, s);
+          for (int x = 0; x <= r.tiles; ++x) {
+            if (x < r.tiles) {
+              const int y = n + x, b = y & 1;
+              bool ok = kv4_wait(&s->kfull[b], (y >> 1) & 1, s);
+              // the score buffer is free: its weights went into the output (or the account)
+              if (y >= 2) ok = ok && kv4_wait(ACCOUNT ? &s->pfull[b] : &s->pvdone[b], ((y - 2) >> 1) & 1, s);
+              kv4_fence_after();
+              if (ok) {
+                const uint32_t kaddr = su32(kop + b * C::kOperand);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  kv4_mma_ts(tmem + C::kColS + b * kKv4N, tmem + C::kColQ + k * 8,
+                             kv4_desc(kaddr + (k >> 2) * (kKv4N * 128) + (k & 3) * 32, 0), kv4_idesc(kKv4N, false), k > 0);
+              }
+              kv4_commit(&s->sfull[b]);
+              kv4_commit(&s->kempty[b]);
+            }
+            if (!ACCOUNT && x > 0) {
+              const int y = n + x - 1, b = y & 1;
+              bool ok = kv4_wait(&s->pfull[b], (y >> 1) & 1, s);
+              ok = ok && kv4_wait(&s->vfull[b], (y >> 1) & 1, s);
+              kv4_fence_after();
+              if (ok) {
+                const uint32_t vaddr = su32(vop + b * C::kOperand);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int k = 0; k < kKv4N / 16; ++k)
+                    kv4_mma_ts(tmem, tmem + C::kColS + b * kKv4N + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
+                               kv4_idesc(D, true), x > 1 || part > 0 || k > 0);
+              }
+              kv4_commit(&s->pvdone[b]);
+            }
+          }
+          n += r.tiles;
+        }
+        at += r.tiles;
+      }
+      kv4_commit(&s->drained);
+      mbar_wait_drain(&s->drained, 0);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------ decoding: warp d: half (d & 1) of block d / 2
+    const int d = warp - 8, b = d >> 1, half = d & 1;
+    int n = 0;
+    for (int at = g0; at < g1;) {
+      int blocks;
+      const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+      for (int x = 0; x < blocks * r.tiles; ++x, ++n) {
+        const int st = n % kKv4BlockRing, buf = n & 1;
+        kv4_wait(&s->full[st], (n / kKv4BlockRing) & 1, s);
+        const bool on = (s->held[n & 7] >> b) & 1;
+        const uint8_t* blk = ring + (size_t)st * C::kTile + b * C::kStride;
+        if (n >= 2) kv4_wait(&s->kempty[buf], ((n - 2) >> 1) & 1, s);
+        if (wide) kv4_decode_keys<D, true>(blk, b, half, on, kop + buf * C::kOperand, lane);
+        else kv4_decode_keys<D, false>(blk, b, half, on, kop + buf * C::kOperand, lane);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->kfull[buf]);
+        if (!ACCOUNT) {
+          if (n >= 2) kv4_wait(&s->pvdone[buf], ((n - 2) >> 1) & 1, s);
+          if (wide) kv4_decode_values<D, true>(blk, b, half, on, vop + buf * C::kOperand, lane);
+          else kv4_decode_values<D, false>(blk, b, half, on, vop + buf * C::kOperand, lane);
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->vfull[buf]);
+        }
+        if (lane == 0) mbar_arrive(&s->empty[st]);
+      }
+      at += r.tiles;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------ softmax: a query row per thread
+    const int row_in = threadIdx.x - 128, wq = warp - 4;
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    const float sc = wide ? a.scale : a.scale * kKv4Up, up = wide ? 1.f : kKv4Up;
+    int n = 0, piece = 0;
+    for (int at = g0; at < g1; ++piece) {
+      int blocks;
+      const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+      const int n_rows = r.m * a.group;
+      if (ACCOUNT)
+        for (int k = row_in; k < 4 * r.tiles * kKv4N; k += 128) gacc[k] = 0.f;
+      if (ACCOUNT) named_bar_sync(2, 128);
+      for (int rb = 0; rb < blocks; ++rb) {
+        const int row0 = (ACCOUNT ? rb : r.row_tile) * kKv4M, row = row0 + row_in;
+        const int tok = min(row, n_rows - 1) / a.group, hq = r.head * a.group + min(row, n_rows - 1) % a.group;
+        // ---- the row's queries into tensor memory
+        const long q0 = (long)r.seq * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t u[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row < n_rows) {
+              const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + q0 + c * 64 + e * 8;
+              if (a.q.vec) {
+                v = __ldcg(reinterpret_cast<const uint4*>(p));
+              } else {
+                uint32_t* vv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) vv[k] = (uint32_t)__ldcg(p + 2 * k) | ((uint32_t)__ldcg(p + 2 * k + 1) << 16);
+              }
+            }
+            u[4 * e] = v.x;
+            u[4 * e + 1] = v.y;
+            u[4 * e + 2] = v.z;
+            u[4 * e + 3] = v.w;
+          }
+          kv4_tst32(lane_base + C::kColQ + c * 32, u);
+        }
+        kv4_tst_wait();
+        kv4_fence_before();
+        mbar_arrive(&s->qfull);
+        // rows it sees: (low, last]
+        const int last = r.len - r.m + tok, low = a.window > 0 ? last - a.window : -1;
+        const int tok_max = min(row0 + kKv4M, n_rows) - 1;
+        const int last_min = r.len - r.m + row0 / a.group, low_max = a.window > 0 ? r.len - r.m + tok_max / a.group - a.window : -1;
+        const float lse = !ACCOUNT ? 0.f
+                          : row < n_rows ? __ldcg(a.lse + ((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row) : INFINITY;
+        float m = -INFINITY, l = 0.f;
+        for (int x = 0; x < r.tiles; ++x, ++n) {
+          const int b = n & 1;
+          kv4_wait(&s->sfull[b], (n >> 1) & 1, s);
+          kv4_fence_after();
+          const uint32_t cols = lane_base + C::kColS + b * kKv4N;
+          uint32_t v[64];
+          kv4_tld32(cols, v);
+          kv4_tld32(cols + 32, v + 32);
+          kv4_tld_wait();
+          float* f = reinterpret_cast<float*>(v);
+          const int j0 = (r.tile + x) * kKv4N;
+          const uint32_t have = s->held[n & 7];
+#pragma unroll
+          for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(v[k]) * sc;
+          if (have != 15u || j0 + kKv4N - 1 > last_min || j0 <= low_max) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+              if (j0 + k > last || j0 + k <= low || !((have >> (k >> 4)) & 1)) f[k] = -INFINITY;
+          }
+          if constexpr (ACCOUNT) {
+            kv4_fence_before();
+            mbar_arrive(&s->pfull[b]);  // the scores are in registers
+#pragma unroll
+            for (int k = 0; k < 64; ++k) f[k] = kv4_exp2(f[k] - lse);
+            // each step a lane keeps half of its columns and adds its partner's half of them
+#pragma unroll
+            for (int o = 16, w = 32; o > 0; o >>= 1, w >>= 1) {
+              const bool hi = lane & o;
+#pragma unroll
+              for (int k = 0; k < w; ++k) {
+                const float keep = hi ? f[k + w] : f[k], send = hi ? f[k] : f[k + w];
+                f[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+              }
+            }
+            float* to = gacc + (wq * r.tiles + x) * kKv4N + 2 * lane;  // lane's columns: 2 lane, 2 lane + 1
+            to[0] += f[0];
+            to[1] += f[1];
+          } else {
+            float mx = f[0];
+#pragma unroll
+            for (int k = 1; k < 64; ++k) mx = fmaxf(mx, f[k]);
+            const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
+            if (__any_sync(0xFFFFFFFFu, raise)) {  // a row's numbers do not depend on its neighbours'
+              const float nm = raise ? mx : m, fac = raise ? kv4_exp2(m - nm) : 1.f;
+              m = nm;
+              l *= fac;
+              if (x > 0) {  // the output so far follows: the previous tile's product has to be in
+                kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
+                kv4_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t u[32];
+                  kv4_tld32(lane_base + c, u);
+                  kv4_tld_wait();
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * fac);
+                  kv4_tst32(lane_base + c, u);
+                }
+                kv4_tst_wait();
+              }
+            }
+            const float z = m == -INFINITY ? 0.f : m;
+            uint32_t hi[32];
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float p0 = kv4_exp2(f[2 * k] - z), p1 = kv4_exp2(f[2 * k + 1] - z);
+              s0 += p0;
+              s1 += p1;
+              hi[k] = as_u32(__floats2bfloat162_rn(p0, p1));
+              v[k] = as_u32(__floats2bfloat162_rn(p0 - bf16_lo(hi[k]), p1 - bf16_hi(hi[k])));
+            }
+            l += s0 + s1;
+            kv4_tst32(cols, hi);
+            kv4_tst32(cols + 32, v);
+            kv4_tst_wait();
+            kv4_fence_before();
+            mbar_arrive(&s->pfull[b]);
+          }
+        }
+        if constexpr (!ACCOUNT) {
+          // ---- the run's output row
+          kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
+          kv4_fence_after();
+          const bool whole = r.whole;
+          const float inv = (whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f) * up;
+          const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
+          float* part = reinterpret_cast<float*>(a.part_o) + (slot_p * kKv4M + row_in) * D;
+          const long o0 = (long)r.seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t u[32];
+            kv4_tld32(lane_base + c, u);
+            kv4_tld_wait();
+            float* f = reinterpret_cast<float*>(u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(u[k]) * inv;
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) kv4_store32b(part + c + 8 * k, *reinterpret_cast<const uint32_t(*)[8]>(u + 8 * k));
+            } else if (row < n_rows) {
+              kv4_store16(a.out, o0 + c, f);
+              kv4_store16(a.out, o0 + c + 16, f + 16);
+            }
+          }
+          if (!whole) a.part_ml[slot_p * kKv4M + row_in] = make_float2(m, l);
+          else a.lse[((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row] = kv4_lse(make_float2(m, l));
+          kv4_fence_before();
+        }
+      }
+      if constexpr (ACCOUNT) {
+        named_bar_sync(2, 128);
+        const int keys = r.tiles * kKv4N;
+        for (int k = row_in; k < keys; k += 128) {
+          const int j = r.tile * kKv4N + k;
+          if (j >= r.len) continue;
+          const long at_b = kv4_block(a.c, r.slot, r.head, j / kKv4Block);
+          if (at_b >= 0)
+            a.c.weight[at_b * kKv4Block + j % kKv4Block] += (gacc[k] + gacc[keys + k]) + (gacc[2 * keys + k] + gacc[3 * keys + k]);
+        }
+        named_bar_sync(2, 128);
+      }
+      at += r.tiles;
+    }
+  }
+  kv4_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && s->abort) set_err(a.c.err, G4_DEV_TIMEOUT);
+  if (warp == 1) {
+    kv4_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols) : "memory");
+  }
+}
+
+// Joins the parts of shared items, in span order: 16 rows of item blockIdx.x per CTA.  Also the
+// zeros of rows that no tile reaches.
+constexpr int kKv4BlockJoinRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(128) kv4_block_join_kernel(const Kv4AttendArgs a, int ctas) {
+  extern __shared__ __align__(16) uint8_t kv4_raw[];
+  int4* seqs = reinterpret_cast<int4*>(kv4_raw);
+  int* first = reinterpret_cast<int*>(seqs + a.n_seq);
+  const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles, tid = threadIdx.x;
+  const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
+  kv4_plan<kKv4N>(a, first, seqs, false);  // inputs of the first launch too: read before it ends
+  const int m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
+  const int span = kv4_span(a, first, ctas), t0 = first[i] + n * x;
+  const int c0 = (unsigned)t0 / (unsigned)span, c1 = n ? (int)((unsigned)(t0 + n - 1) / (unsigned)span) : c0 - 1;
+  pdl_wait();
+  pdl_trigger();
+  if (x == 0 && blockIdx.y == 0) kv4_zero_rows<D>(a, first, seqs, i, a.n_seq, tid, 128);
+  if (c1 <= c0) return;
+  constexpr int T = D / 8;  // threads of a row, eight numbers each
+  const float* part_o = reinterpret_cast<const float*>(a.part_o);
+  for (int k = tid / T; k < kKv4BlockJoinRows; k += 128 / T) {
+    const int rl = blockIdx.y * kKv4BlockJoinRows + k, row = rt * kKv4M + rl, e = tid % T * 8;
+    if (row >= n_rows) break;
+    float2 ml = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) kv4_merge_ml(ml, __ldcg(&a.part_ml[kv4_part(c, t0, span) * kKv4M + rl]));
+    const float Z = ml.x == -INFINITY ? 0.f : ml.x, inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const long p = kv4_part(c, t0, span) * kKv4M + rl;
+      const float f = kv4_exp2(__ldcg(&a.part_ml[p].x) - Z);
+      uint32_t u[8];
+      kv4_load32b(part_o + p * D + e, u);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += f * __uint_as_float(u[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] *= inv;
+    const int tok = row / a.group, hq = head * a.group + row % a.group;
+    kv4_store8(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + e, v);
+    if (tid % T == 0) a.lse[((long)i * a.c.kvh + head) * a.lse_rows + row] = kv4_lse(ml);
+  }
+}
+
+}  // namespace g4

@@ -232,6 +232,22 @@ def test_account(rt, q_len, group, kvh, dtype, d, page):
     check_attend(rt, d, kvh, group, [0, q_len, 64, 65, 700], q_len, dtype, page, track=True, seed=q_len + group)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len,group,kvh,page", [(5, 7, 1, 0), (33, 1, 2, 16), (64, 8, 1, 64), (17, 16, 3, 128)])
+@pytest.mark.parametrize("track", [False, True])
+def test_token_blocks(rt, d, q_len, group, kvh, page, track):
+    """More than 32 query rows per KV head: ragged tokens, prompts shorter than a tile, rows that no
+    tile reaches, items shared by many CTAs."""
+    lens = [q_len, 0, 64, 65, 700, 1, 2051]
+    q_lens = [q_len, q_len, max(1, q_len - 3), 1, q_len, q_len, q_len // 2]
+    check_attend(rt, d, kvh, group, lens, q_len, "bf16", page, q_lens=q_lens, track=track, seed=d + q_len)
+
+
+@pytest.mark.parametrize("window", [1, 63, 64, 300])
+def test_token_block_window(rt, window):
+    check_attend(rt, 128, 2, 8, [9, 64, 65, 900, 40], 9, "bf16", 32, window=window, seed=window)
+
+
 def test_long_context(rt):
     check_attend(rt, 256, 1, 8, [30011, 5], 1, "bf16", 128, track=True, seed=3)
     check_attend(rt, 64, 1, 2, [40007, 39000, 1], 1, "f32", 0, scale=0.03, seed=4)
@@ -257,16 +273,17 @@ def test_strided_query_and_output(rt):
     fine(c)
 
 
-def test_not_finite_query_stays_in_its_row(rt):
+@pytest.mark.parametrize("m,dtype", [(2, "f32"), (2, "bf16"), (6, "bf16")])
+def test_not_finite_query_stays_in_its_row(rt, m, dtype):
     d, t = 128, 100
     c = make(rt, 1, 128, 8, 1, d)
     c.append(rows((1, t, 1, d), "f32", 1), rows((1, t, 1, d), "f32", 2), i32([0]), i32([0]))
-    q = rows((1, 2, 8, d), "f32", 3)
+    q = rows((1, m, 8, d), dtype, 3)
     clean = c.attend(q, i32([0]), i32([t]))
     q[0, 1, 3, 5] = float("nan")
     q[0, 0, 6, 0] = float("inf")
     out = c.attend(q, i32([0]), i32([t]))
-    bad = torch.zeros(2, 8, dtype=torch.bool)
+    bad = torch.zeros(m, 8, dtype=torch.bool)
     bad[1, 3] = bad[0, 6] = True
     assert out[0][bad.cuda()].isnan().all()
     assert torch.equal(out[0][~bad.cuda()], clean[0][~bad.cuda()])
@@ -445,23 +462,28 @@ def test_device_errors_skip_the_sequence(rt):
     assert c.device_error()[1] == g4.G4_DEV_BAD_SLOT | g4.G4_DEV_BAD_POSITION
 
 
-def test_missing_pages(rt):
+@pytest.mark.parametrize("m,group", [(1, 2), (5, 8)])
+def test_missing_pages(rt, m, group):
     """Rows on missing pages are not written, read or seen; the others are."""
     from accelerator_decode_gb300 import g4
     d, t = 64, 64
+    heads, dtype = group, "f32" if m == 1 else "bf16"
     table = torch.tensor([[1, -1, 4, 0], [2, 3, 99, 5]], dtype=torch.int32, device="cuda")
-    c = make(rt, 2, t, 2, 1, d, 16, page_table=table, n_pages=6, track=True)
+    c = make(rt, 2, t, heads, 1, d, 16, page_table=table, n_pages=6, track=True)
     k, v = rows((2, t, 1, d), "f32", 1), rows((2, t, 1, d), "f32", 2)
     c.append(k, v, i32([0, 1]), i32([0, 0]))
     assert c.device_error()[1] == g4.G4_DEV_BAD_POSITION
-    q = rows((2, 1, 2, d), "f32", 3)
+    q = rows((2, m, heads, d), dtype, 3)
     out = c.attend(q, i32([0, 1]), i32([t, t]), accumulate=True)
     assert c.device_error()[1] == g4.G4_DEV_BAD_POSITION
     for i, gone in enumerate([(16, 32), (32, 48)]):
         keep = np.r_[0:gone[0], gone[1]:t]
         kk, vv = ref.values(host(k[i]))[keep], ref.values(host(v[i]))[keep]
-        want, _ = ref.attend(host(q[i]), kk, vv, 2, 1 / np.sqrt(d))
-        assert (np.abs(host(out[i]) - want) <= attend_bound(host(q[i]), kk, vv, 1 / np.sqrt(d), "f32", want)).all()
+        want, gain = ref.attend(host(q[i]), kk, vv, group, 1 / np.sqrt(d))
+        assert (np.abs(host(out[i]) - want) <= attend_bound(host(q[i]), kk, vv, 1 / np.sqrt(d), dtype, want)).all()
+        _, w = c.account(i32([i]), i32([0]), t)
+        assert np.abs(host(w[0, 0])[keep] - gain[0]).max() < 1e-4 * m * group and not host(w[0, 0])[gone[0]:gone[1]].any()
+    c.device_error()
     rk, _ = c.read(i32([0, 1]), i32([0, 0]), t, i32([t, t]), dtype=torch.float32)
     assert c.device_error()[1] == g4.G4_DEV_BAD_POSITION
     np.testing.assert_array_equal(host(rk[0, :16]), ref.values(host(k[0, :16])))
