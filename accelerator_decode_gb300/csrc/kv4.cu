@@ -367,7 +367,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
                         int32_t q_len, const int32_t* d_q_lens, float scale, int32_t window, int32_t accumulate,
                         int32_t zero_rest, const g4_kv4_tensor* q, const g4_kv4_tensor* out) {
   if (!op || !d_slots || !d_lens || !q || !out || !kv4_count(op, n_seq) || q_len < 1 || q_len > op->cfg.max_q_len ||
-      window < 0 || !std::isfinite(scale) || q->dtype != out->dtype)
+      window < 0 || !(scale >= 0.f) || !std::isfinite(scale) || q->dtype != out->dtype)
     return G4_ERR_INVALID_ARG;
   Kv4AttendArgs a{};
   if (!kv4_dense(q, n_seq, q_len, op->cfg.num_q_heads, op->c.d, false, &a.q) ||

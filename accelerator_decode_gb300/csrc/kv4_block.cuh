@@ -5,18 +5,22 @@
 // An item is 128 query rows of one KV head.  Its queries sit in tensor memory as the A operand;
 // eight warps decode tiles of 64 keys and values once for all 128 rows into 128-byte-swizzled
 // shared memory; per tile
-//   S = Q K^T  (A tensor memory, B shared, 128 x 64, fp32 in tensor memory, two buffers)
-//   P = 2^(scale S - m) on four warps, a row per thread, written back over S as bf16 parts
+//   S = Q K^T  (A tensor memory, B shared, 128 x 64, fp32 in tensor memory)
+//   P = 2^(scale S - m) on four warps, a row per thread, to tensor memory as bf16 parts
 //   O += P V   (A tensor memory, B shared with the head dim leading, 128 x D in tensor memory)
+// S is free again as soon as the four warps hold it in registers, so the next tile's S is made
+// while they take exponentials, and O while they take the next tile's.  (With P written over S
+// in two buffers, the next product waited for the output's: 3,300 cycles a tile.)
 // P goes in two parts (p - bf16(p) as well), so 16 bits of every weight count; the second pass
 // costs matrix time that the decoding and the exponentials leave free.  A row's reference m is
 // raised, and its sums rescaled, only when a score exceeds it by 2^8: weights up to 256 lose
 // nothing in fp32 or in the parts.
-// Tensor memory holds O (D columns), Q (D / 2) and S (2 x 64): all 512 columns at D = 256.
+// Tensor memory holds O (D columns), Q (D / 2), S and P (64 each): all 512 columns at D = 256.
 //
 // The account (ACCOUNT): the same pipeline without values: a CTA owns a run of keys, takes every
 // block of 128 query rows past them, and adds up p = 2^(scale S - lse) over the rows, by a
-// butterfly over the lanes that leaves each lane two columns, in a fixed order.
+// butterfly over the lanes that leaves each lane two columns, in a fixed order.  There S has two
+// buffers and Q two, filled ahead by four warps of their own.
 #pragma once
 #include "kv4_attend.cuh"
 
@@ -35,7 +39,9 @@ struct Kv4Blk {
   static constexpr int kStride = ACCOUNT ? 9 * D : 18 * D;  // of a block
   static constexpr int kOperand = kKv4N * D * 2;            // decoded keys (or values) of a tile
   static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
-  static constexpr int kColQ = D, kColS = D + D / 2;
+  // attention: O, Q, S, P; account: Q twice, S twice
+  static constexpr int kColQ = ACCOUNT ? 0 : D, kColS = ACCOUNT ? D : D + D / 2, kColP = kColS + kKv4N;
+  static constexpr int kDecoders = ACCOUNT ? 4 : 8;         // decoding warps: a block each, or half a block
   static constexpr int kFixed = 512 /* barriers and flags */ + (ACCOUNT ? 4 * kKv4RunTiles * kKv4N * 4 : 0);
   static __host__ __device__ size_t smem(int n_seq) {
     return 1024 + (size_t)(ACCOUNT ? 2 : 4) * kOperand + kKv4BlockRing * kTile + kFixed + (size_t)n_seq * 20 + 16;
@@ -43,7 +49,7 @@ struct Kv4Blk {
 };
 
 struct Kv4BlockBars {
-  uint64_t full[4], empty[4], kfull[2], kempty[2], vfull[2], sfull[2], pfull[2], pvdone[2], qfull, drained;
+  uint64_t full[4], empty[4], kfull[2], kempty[2], vfull[2], sfull[2], sread[2], qfull[2], qdone[2], pfull, pvdone[2], drained;
   uint32_t held[8];
   uint32_t tmem;
   int abort;
@@ -51,6 +57,7 @@ struct Kv4BlockBars {
 static_assert(sizeof(Kv4BlockBars) <= 512, "barriers");
 
 __device__ __forceinline__ bool kv4_wait(uint64_t* b, uint32_t parity, Kv4BlockBars* s) {
+  if (mbar_try(b, parity)) return true;
   if (*reinterpret_cast<volatile int*>(&s->abort)) return false;
   if (mbar_wait(b, parity, reinterpret_cast<volatile int*>(&s->abort))) return true;
   *reinterpret_cast<volatile int*>(&s->abort) = 1;
@@ -182,6 +189,36 @@ __device__ __forceinline__ void kv4_decode_values(const uint8_t* blk, int b, int
   }
 }
 
+// The queries of a row (zeros when it is none) into its lane of tensor memory, bf16 pairs.
+template <int D>
+__device__ __forceinline__ void kv4_load_queries(const Kv4AttendArgs& a, const Kv4Run& r, int row, uint32_t addr) {
+  const bool on = row < r.m * a.group;
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p);
+  if (on) p += (long)r.seq * a.q.seq + (long)(row / a.group) * a.q.row + (long)(r.head * a.group + row % a.group) * a.q.head;
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += 128) {  // up to 256 bytes in flight
+    constexpr int N = D < 128 ? 64 : 128;
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 16; ++e) {
+      uint32_t(&w)[8] = *reinterpret_cast<uint32_t(*)[8]>(u + 8 * e);
+      const uint16_t* q = p + c0 + 16 * e;
+      if (!on) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = 0u;
+      } else if (a.q.vec == 2) {
+        kv4_load32b(q, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = (uint32_t)__ldcg(q + 2 * k) | ((uint32_t)__ldcg(q + 2 * k + 1) << 16);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < N / 64; ++c) kv4_tst32(addr + c0 / 2 + c * 32, u + 32 * c);
+  }
+  kv4_tst_wait();
+}
+
 // The run of tiles at `at`: for the account, of at most kKv4RunTiles tiles (a.row_tiles 1), with
 // `blocks` blocks of 128 query rows to take past them.
 template <bool ACCOUNT>
@@ -209,17 +246,19 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKv4BlockRing; ++i) {
       mbar_init(&s->full[i], 1);
-      mbar_init(&s->empty[i], 8);
+      mbar_init(&s->empty[i], C::kDecoders);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s->kfull[i], 8);
+      mbar_init(&s->kfull[i], C::kDecoders);
       mbar_init(&s->kempty[i], 1);
-      mbar_init(&s->vfull[i], 8);
+      mbar_init(&s->vfull[i], C::kDecoders);
       mbar_init(&s->sfull[i], 1);
-      mbar_init(&s->pfull[i], 128);
+      mbar_init(&s->sread[i], 128);
+      mbar_init(&s->qfull[i], 128);
+      mbar_init(&s->qdone[i], 1);
       mbar_init(&s->pvdone[i], 1);
     }
-    mbar_init(&s->qfull, 128);
+    mbar_init(&s->pfull, 128);
     mbar_init(&s->drained, 1);
     s->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -268,34 +307,37 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
     for (int k = max(0, n - kKv4BlockRing); k < n; ++k) mbar_wait_drain(&s->full[k % kKv4BlockRing], (k / kKv4BlockRing) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------ matrix instructions
+    // Scores: attention one buffer, account two; the buffer is free once it has been read.
+    constexpr int NS = ACCOUNT ? 2 : 1;
     if (lane == 0) {
       int n = 0, runs = 0;
       for (int at = g0; at < g1;) {
         int blocks;
         const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
         for (int rb = 0; rb < blocks; ++rb, ++runs) {
-          kv4_wait(&s->qfull, runs & 1, s);
+          const int qb = ACCOUNT ? runs & 1 : 0;
+          bool ok = kv4_wait(&s->qfull[qb], (ACCOUNT ? runs >> 1 : runs) & 1, s);
           for (int x = 0; x <= r.tiles; ++x) {
             if (x < r.tiles) {
-              const int y = n + x, b = y & 1;
-              bool ok = kv4_wait(&s->kfull[b], (y >> 1) & 1, s);
-              // the score buffer is free: its weights went into the output (or the account)
-              if (y >= 2) ok = ok && kv4_wait(ACCOUNT ? &s->pfull[b] : &s->pvdone[b], ((y - 2) >> 1) & 1, s);
+              const int y = n + x, b = y & 1, sb = y % NS;
+              ok = kv4_wait(&s->kfull[b], (y >> 1) & 1, s) && ok;
+              if (y >= NS) ok = kv4_wait(&s->sread[sb], (y / NS - 1) & 1, s) && ok;
               kv4_fence_after();
               if (ok) {
                 const uint32_t kaddr = su32(kop + b * C::kOperand);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                  kv4_mma_ts(tmem + C::kColS + b * kKv4N, tmem + C::kColQ + k * 8,
+                  kv4_mma_ts(tmem + C::kColS + sb * kKv4N, tmem + C::kColQ + qb * (D / 2) + k * 8,
                              kv4_desc(kaddr + (k >> 2) * (kKv4N * 128) + (k & 3) * 32, 0), kv4_idesc(kKv4N, false), k > 0);
               }
-              kv4_commit(&s->sfull[b]);
+              kv4_commit(&s->sfull[sb]);
               kv4_commit(&s->kempty[b]);
+              if (ACCOUNT && x + 1 == r.tiles) kv4_commit(&s->qdone[qb]);
             }
             if (!ACCOUNT && x > 0) {
               const int y = n + x - 1, b = y & 1;
-              bool ok = kv4_wait(&s->pfull[b], (y >> 1) & 1, s);
-              ok = ok && kv4_wait(&s->vfull[b], (y >> 1) & 1, s);
+              ok = kv4_wait(&s->vfull[b], (y >> 1) & 1, s) && ok;
+              ok = kv4_wait(&s->pfull, y & 1, s) && ok;
               kv4_fence_after();
               if (ok) {
                 const uint32_t vaddr = su32(vop + b * C::kOperand);
@@ -303,7 +345,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                   for (int k = 0; k < kKv4N / 16; ++k)
-                    kv4_mma_ts(tmem, tmem + C::kColS + b * kKv4N + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
+                    kv4_mma_ts(tmem, tmem + C::kColP + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
                                kv4_idesc(D, true), x > 1 || part > 0 || k > 0);
               }
               kv4_commit(&s->pvdone[b]);
@@ -316,28 +358,49 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
       kv4_commit(&s->drained);
       mbar_wait_drain(&s->drained, 0);
     }
+  } else if (ACCOUNT && warp >= 12) {
+    // ------------------------------------------------ account: queries, a block of rows ahead
+    int runs = 0;
+    for (int at = g0; at < g1;) {
+      int blocks;
+      const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+      for (int rb = 0; rb < blocks; ++rb, ++runs) {
+        const int qb = runs & 1;
+        if (runs >= 2) kv4_wait(&s->qdone[qb], ((runs - 2) >> 1) & 1, s);
+        kv4_fence_after();
+        kv4_load_queries<D>(a, r, rb * kKv4M + (int)threadIdx.x - 384,
+                            tmem + ((uint32_t)((warp - 12) * 32) << 16) + C::kColQ + qb * (D / 2));
+        kv4_fence_before();
+        mbar_arrive(&s->qfull[qb]);
+      }
+      at += r.tiles;
+    }
   } else if (warp >= 8) {
-    // ------------------------------------------------ decoding: warp d: half (d & 1) of block d / 2
-    const int d = warp - 8, b = d >> 1, half = d & 1;
+    // ------------------------------------------------ decoding: warp d: half (d & 1) of block d / 2,
+    // or (account) both halves of block d
+    const int d = warp - 8;
     int n = 0;
     for (int at = g0; at < g1;) {
       int blocks;
       const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
       for (int x = 0; x < blocks * r.tiles; ++x, ++n) {
-        const int st = n % kKv4BlockRing, buf = n & 1;
+        const int st = n % kKv4BlockRing, buf = n & 1, b = ACCOUNT ? d : d >> 1;
         kv4_wait(&s->full[st], (n / kKv4BlockRing) & 1, s);
         const bool on = (s->held[n & 7] >> b) & 1;
         const uint8_t* blk = ring + (size_t)st * C::kTile + b * C::kStride;
         if (n >= 2) kv4_wait(&s->kempty[buf], ((n - 2) >> 1) & 1, s);
-        if (wide) kv4_decode_keys<D, true>(blk, b, half, on, kop + buf * C::kOperand, lane);
-        else kv4_decode_keys<D, false>(blk, b, half, on, kop + buf * C::kOperand, lane);
+#pragma unroll 1
+        for (int half = ACCOUNT ? 0 : d & 1; half < (ACCOUNT ? 2 : (d & 1) + 1); ++half) {
+          if (wide) kv4_decode_keys<D, true>(blk, b, half, on, kop + buf * C::kOperand, lane);
+          else kv4_decode_keys<D, false>(blk, b, half, on, kop + buf * C::kOperand, lane);
+        }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->kfull[buf]);
         if (!ACCOUNT) {
           if (n >= 2) kv4_wait(&s->pvdone[buf], ((n - 2) >> 1) & 1, s);
-          if (wide) kv4_decode_values<D, true>(blk, b, half, on, vop + buf * C::kOperand, lane);
-          else kv4_decode_values<D, false>(blk, b, half, on, vop + buf * C::kOperand, lane);
+          if (wide) kv4_decode_values<D, true>(blk, b, d & 1, on, vop + buf * C::kOperand, lane);
+          else kv4_decode_values<D, false>(blk, b, d & 1, on, vop + buf * C::kOperand, lane);
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->vfull[buf]);
@@ -362,34 +425,11 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
       for (int rb = 0; rb < blocks; ++rb) {
         const int row0 = (ACCOUNT ? rb : r.row_tile) * kKv4M, row = row0 + row_in;
         const int tok = min(row, n_rows - 1) / a.group, hq = r.head * a.group + min(row, n_rows - 1) % a.group;
-        // ---- the row's queries into tensor memory
-        const long q0 = (long)r.seq * a.q.seq + (long)tok * a.q.row + (long)hq * a.q.head;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t u[32];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < n_rows) {
-              const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + q0 + c * 64 + e * 8;
-              if (a.q.vec) {
-                v = __ldcg(reinterpret_cast<const uint4*>(p));
-              } else {
-                uint32_t* vv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) vv[k] = (uint32_t)__ldcg(p + 2 * k) | ((uint32_t)__ldcg(p + 2 * k + 1) << 16);
-              }
-            }
-            u[4 * e] = v.x;
-            u[4 * e + 1] = v.y;
-            u[4 * e + 2] = v.z;
-            u[4 * e + 3] = v.w;
-          }
-          kv4_tst32(lane_base + C::kColQ + c * 32, u);
+        if (!ACCOUNT) {
+          kv4_load_queries<D>(a, r, row, lane_base + C::kColQ);
+          kv4_fence_before();
+          mbar_arrive(&s->qfull[0]);
         }
-        kv4_tst_wait();
-        kv4_fence_before();
-        mbar_arrive(&s->qfull);
         // rows it sees: (low, last]
         const int last = r.len - r.m + tok, low = a.window > 0 ? last - a.window : -1;
         const int tok_max = min(row0 + kKv4M, n_rows) - 1;
@@ -398,29 +438,28 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
                           : row < n_rows ? __ldcg(a.lse + ((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row) : INFINITY;
         float m = -INFINITY, l = 0.f;
         for (int x = 0; x < r.tiles; ++x, ++n) {
-          const int b = n & 1;
-          kv4_wait(&s->sfull[b], (n >> 1) & 1, s);
+          const int sb = ACCOUNT ? n & 1 : 0;
+          kv4_wait(&s->sfull[sb], (ACCOUNT ? n >> 1 : n) & 1, s);
           kv4_fence_after();
-          const uint32_t cols = lane_base + C::kColS + b * kKv4N;
           uint32_t v[64];
-          kv4_tld32(cols, v);
-          kv4_tld32(cols + 32, v + 32);
+          kv4_tld32(lane_base + C::kColS + sb * kKv4N, v);
+          kv4_tld32(lane_base + C::kColS + sb * kKv4N + 32, v + 32);
           kv4_tld_wait();
-          float* f = reinterpret_cast<float*>(v);
           const int j0 = (r.tile + x) * kKv4N;
           const uint32_t have = s->held[n & 7];
+          kv4_fence_before();
+          mbar_arrive(&s->sread[sb]);  // the scores are in registers
+          float f[64];
 #pragma unroll
-          for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(v[k]) * sc;
+          for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(v[k]);
           if (have != 15u || j0 + kKv4N - 1 > last_min || j0 <= low_max) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
               if (j0 + k > last || j0 + k <= low || !((have >> (k >> 4)) & 1)) f[k] = -INFINITY;
           }
           if constexpr (ACCOUNT) {
-            kv4_fence_before();
-            mbar_arrive(&s->pfull[b]);  // the scores are in registers
 #pragma unroll
-            for (int k = 0; k < 64; ++k) f[k] = kv4_exp2(f[k] - lse);
+            for (int k = 0; k < 64; ++k) f[k] = kv4_exp2(fmaf(f[k], sc, -lse));
             // each step a lane keeps half of its columns and adds its partner's half of them
 #pragma unroll
             for (int o = 16, w = 32; o > 0; o >>= 1, w >>= 1) {
@@ -438,6 +477,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
             float mx = f[0];
 #pragma unroll
             for (int k = 1; k < 64; ++k) mx = fmaxf(mx, f[k]);
+            mx *= sc;
             const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
             if (__any_sync(0xFFFFFFFFu, raise)) {  // a row's numbers do not depend on its neighbours'
               const float nm = raise ? mx : m, fac = raise ? kv4_exp2(m - nm) : 1.f;
@@ -459,22 +499,25 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
               }
             }
             const float z = m == -INFINITY ? 0.f : m;
-            uint32_t hi[32];
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float p0 = kv4_exp2(f[2 * k] - z), p1 = kv4_exp2(f[2 * k + 1] - z);
+              const float p0 = kv4_exp2(fmaf(f[2 * k], sc, -z)), p1 = kv4_exp2(fmaf(f[2 * k + 1], sc, -z));
               s0 += p0;
               s1 += p1;
-              hi[k] = as_u32(__floats2bfloat162_rn(p0, p1));
-              v[k] = as_u32(__floats2bfloat162_rn(p0 - bf16_lo(hi[k]), p1 - bf16_hi(hi[k])));
+              v[k] = as_u32(__floats2bfloat162_rn(p0, p1));
+              v[32 + k] = as_u32(__floats2bfloat162_rn(p0 - bf16_lo(v[k]), p1 - bf16_hi(v[k])));
             }
             l += s0 + s1;
-            kv4_tst32(cols, hi);
-            kv4_tst32(cols + 32, v);
+            if (x > 0) {  // the previous tile's weights have been used
+              kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
+              kv4_fence_after();
+            }
+            kv4_tst32(lane_base + C::kColP, v);
+            kv4_tst32(lane_base + C::kColP + 32, v + 32);
             kv4_tst_wait();
             kv4_fence_before();
-            mbar_arrive(&s->pfull[b]);
+            mbar_arrive(&s->pfull);
           }
         }
         if constexpr (!ACCOUNT) {

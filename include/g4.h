@@ -399,7 +399,7 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * query tokens and the query heads of its KV head.  The same slot may be named twice only
  * without accumulate.  The sums run in a fixed order: equal calls give equal bits.
  * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0,
- * a scale that is not finite, q and out of different types, malformed tensors), UNSUPPORTED
+ * a scale that is negative or not finite, q and out of different types, malformed tensors), UNSUPPORTED
  * (accumulate without track; a window with a cache that tracks: after an eviction its rows are
  * no longer in position order; n_seq * num_kv_heads * ceil(q_len * heads per KV head / 8) *
  * ceil(capacity / 64) at 2^31 or more). */

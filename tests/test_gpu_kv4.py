@@ -405,7 +405,8 @@ def test_refusals(rt):
     refused(uns, c.attend, q, s, l, accumulate=True)
     refused(uns, t.attend, q, s, l, window=4)
     refused(bad, c.attend, q, s, l, window=-1)
-    refused(bad, c.attend, q, s, l, scale=float("inf"))
+    for scale in (float("inf"), float("nan"), -0.5):
+        refused(bad, c.attend, q, s, l, scale=scale)
     refused(bad, c.attend, q, s, l, out=torch.empty(2, 2, 4, d, dtype=torch.bfloat16, device="cuda"))
     refused(bad, c.attend, q, s, l, out=torch.empty(2, 2, 1, d, device="cuda").expand(2, 2, 4, d))
     refused(bad, c.attend, rows((2, 5, 4, d), "f32", 2), s, l)
