@@ -396,7 +396,8 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.part_o = op->part_o;
   a.part_ml = op->part_ml;
   a.tickets = op->tickets;
-  if (kv4_block_path(op, q_len, q->dtype)) {
+  // (a few hundred sequences' spans no longer fit beside the operands of a 256-wide head)
+  if (kv4_block_path(op, q_len, q->dtype) && (int)Kv4Blk<256, false>::smem(n_seq) <= op->smem_optin) {
     switch (op->c.d) {
       case 64: kv4_launch_block<64>(op, a, st); break;
       case 128: kv4_launch_block<128>(op, a, st); break;

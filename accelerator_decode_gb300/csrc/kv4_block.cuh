@@ -2,25 +2,26 @@
 // for bf16 queries with more than kKv4BlockRows query rows (tokens x heads) per KV head and head
 // dims up to 256; and the account of the weights the rows received.
 //
-// An item is 128 query rows of one KV head.  Its queries sit in tensor memory as the A operand;
-// eight warps decode tiles of 64 keys and values once for all 128 rows into 128-byte-swizzled
-// shared memory; per tile
-//   S = Q K^T  (A tensor memory, B shared, 128 x 64, fp32 in tensor memory)
+// An item is 128 query rows of one KV head.  Four warps decode tiles of 64 keys, and four of values,
+// once for all 128 rows into 128-byte-swizzled shared memory; per pair of tiles
+//   S = Q K^T  (both operands shared, 128 x 128, fp32 in tensor memory)
+// and per tile
 //   P = 2^(scale S - m) on four warps, a row per thread, to tensor memory as bf16 parts
 //   O += P V   (A tensor memory, B shared with the head dim leading, 128 x D in tensor memory)
-// S is free again as soon as the four warps hold it in registers, so the next tile's S is made
-// while they take exponentials, and O while they take the next tile's.  (With P written over S
-// in two buffers, the next product waited for the output's: 3,300 cycles a tile.)
+// S is free again as soon as the four warps hold its second half in registers, so the next
+// pair's S is made while they take exponentials.  A product whose A operand lies in tensor
+// memory takes about 125 cycles per 16 numbers of depth however narrow it is: with Q there and
+// 64 keys at a time the scores alone took 2,000 of 3,400 cycles a tile.
 // P goes in two parts (p - bf16(p) as well), so 16 bits of every weight count; the second pass
-// costs matrix time that the decoding and the exponentials leave free.  A row's reference m is
-// raised, and its sums rescaled, only when a score exceeds it by 2^8: weights up to 256 lose
-// nothing in fp32 or in the parts.
-// Tensor memory holds O (D columns), Q (D / 2), S and P (64 each): all 512 columns at D = 256.
+// costs 150 cycles a tile.  A row's reference m is raised, and its sums rescaled, only when a
+// score exceeds it by 2^8: weights up to 256 lose nothing in fp32 or in the parts.
+// Tensor memory holds O (D columns), S (128) and P (2 x 64): all 512 columns at D = 256.
 //
 // The account (ACCOUNT): the same pipeline without values: a CTA owns a run of keys, takes every
 // block of 128 query rows past them, and adds up p = 2^(scale S - lse) over the rows, by a
-// butterfly over the lanes that leaves each lane two columns, in a fixed order.  There S has two
-// buffers and Q two, filled ahead by four warps of their own.
+// butterfly over the lanes that leaves each lane two columns, in a fixed order.  There the
+// queries lie in tensor memory, twice, filled ahead by four warps of their own, S has two
+// buffers, and so have the decoded keys.
 #pragma once
 #include "kv4_attend.cuh"
 
@@ -31,26 +32,28 @@ constexpr int kKv4M = 128;          // query rows of an item
 constexpr int kKv4N = 64;           // keys of a tile
 constexpr int kKv4RunTiles = 16;    // account: tiles of a run at the most
 constexpr int kKv4BlockThreads = 512;
-constexpr int kKv4BlockRing = 3;
 
 template <int D, bool ACCOUNT>
 struct Kv4Blk {
-  static constexpr int kTile = 4 * (ACCOUNT ? 9 : 18) * D;  // coded bytes of a tile in the ring
-  static constexpr int kStride = ACCOUNT ? 9 * D : 18 * D;  // of a block
-  static constexpr int kOperand = kKv4N * D * 2;            // decoded keys (or values) of a tile
-  static constexpr int kCols = D == 256 ? 512 : D == 128 ? 512 : 256;
-  // attention: O, Q, S, P; account: Q twice, S twice
-  static constexpr int kColQ = ACCOUNT ? 0 : D, kColS = ACCOUNT ? D : D + D / 2, kColP = kColS + kKv4N;
-  static constexpr int kDecoders = ACCOUNT ? 4 : 8;         // decoding warps: a block each, or half a block
+  static constexpr int kHalf = 9 * D;                       // coded keys (or values) of a block
+  static constexpr int kTile = 4 * kHalf;                   // and of a tile: a ring stage
+  static constexpr int kKRing = ACCOUNT ? 3 : 2, kVRing = ACCOUNT ? 0 : 1;  // stages: what fits beside the operands
+  static constexpr int kOperand = kKv4N * D * 2;            // decoded keys or values of a tile
+  static constexpr int kKBufs = ACCOUNT ? 2 : 1;            // pairs of decoded key tiles
+  static constexpr int kSBufs = kKBufs;
+  static constexpr int kCols = 512;
+  static constexpr int kColQ = 0, kColS = D, kColP = D + 128;  // attention: O at 0; account: Q twice
   static constexpr int kFixed = 512 /* barriers and flags */ + (ACCOUNT ? 4 * kKv4RunTiles * kKv4N * 4 : 0);
+  static constexpr int kOps = (ACCOUNT ? 4 : 6) * kOperand; // keys 2 x 2; or queries 2, keys 2, values 2
   static __host__ __device__ size_t smem(int n_seq) {
-    return 1024 + (size_t)(ACCOUNT ? 2 : 4) * kOperand + kKv4BlockRing * kTile + kFixed + (size_t)n_seq * 20 + 16;
+    return 1024 + (size_t)kOps + (kKRing + kVRing) * kTile + kFixed + (size_t)n_seq * 20 + 16;
   }
 };
 
 struct Kv4BlockBars {
-  uint64_t full[4], empty[4], kfull[2], kempty[2], vfull[2], sfull[2], sread[2], qfull[2], qdone[2], pfull, pvdone[2], drained;
-  uint32_t held[8];
+  uint64_t full[4], empty[4], kfull[2], kempty[2], vfull[2], sfull[2], sread[2], qfull[2], qdone[2], pfull[2], pvdone[2], drained;
+  uint32_t held[2][16];  // blocks of a tile that hold rows, as its keys and values come; a producer is at
+                         // most ten tiles ahead of a reader
   uint32_t tmem;
   int abort;
 };
@@ -70,6 +73,12 @@ __device__ __forceinline__ void kv4_mma_ts(uint32_t d, uint32_t a, uint64_t b, u
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void kv4_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
 __device__ __forceinline__ void kv4_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
@@ -121,73 +130,104 @@ __device__ __forceinline__ void kv4_cswap(bool swap, uint32_t& a, uint32_t& b) {
   a = x;
   b = y;
 }
-// Keys: rows of one half (8 half + g) of block b into the operand at `to`.  on false: zeros.
-template <int D, bool WIDE>
-__device__ __forceinline__ void kv4_decode_keys(const uint8_t* blk, int b, int half, bool on, uint8_t* to, int lane) {
-  using O = Kv4Off<D>;
-  constexpr int W = D / 32;
-  const int g = lane >> 2, t = lane & 3, R = 16 * b + 8 * half + g;
-  uint32_t w[W];
-  Kv4KeyScales<D> ks = {};
-  if (on) {
+// The codes and scales of a block go to registers first, so the ring's stage is free while they
+// are decoded.
+template <int D>
+struct Kv4BlockKeys {
+  static constexpr int W = D / 32;
+  uint32_t w[2][W];  // rows g and g + 8
+  Kv4KeyScales<D> ks[2];
+  __device__ __forceinline__ void load(const uint8_t* blk, bool on, int lane) {
+    using O = Kv4Off<D>;
+    if (!on) {  // zeros
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[0][i] = w[1][i] = 0u;
+      ks[0] = ks[1] = {};
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) {
-      const uint2 u = *reinterpret_cast<const uint2*>(blk + (i * 32 + lane) * 16 + half * 8);
-      w[2 * i] = u.x;
-      w[2 * i + 1] = u.y;
+      const uint4 u = reinterpret_cast<const uint4*>(blk)[i * 32 + lane];
+      w[0][2 * i] = u.x;
+      w[0][2 * i + 1] = u.y;
+      w[1][2 * i] = u.z;
+      w[1][2 * i + 1] = u.w;
     }
-    ks = kv4_key_scales<D>(blk + O::kKs, g + 8 * half, t);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = 0;
+    ks[0] = kv4_key_scales<D>(blk + O::kKs, lane >> 2, lane & 3);
+    ks[1] = kv4_key_scales<D>(blk + O::kKs, (lane >> 2) + 8, lane & 3);
   }
-  const int x = D == 256 ? t | (g & 1) << 2 : D == 128 ? t >> 1 | (g & 1) << 1 : 0;
-  if constexpr (W >= 4) {
+  // As block b (0-7) of a pair of tiles into the operand at `to`.
+  template <bool WIDE>
+  __device__ __forceinline__ void store(int b, uint8_t* to, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int x = D == 256 ? t | (g & 1) << 2 : D == 128 ? t >> 1 | (g & 1) << 1 : 0;
 #pragma unroll
-    for (int i = 0; i < W; i += 2) kv4_cswap(x & 1, w[i], w[i + 1]);
+    for (int half = 0; half < 2; ++half) {
+      const int R = 16 * b + 8 * half + g;
+      uint32_t(&v)[W] = w[half];
+      if constexpr (W >= 4) {
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (!(i & 2)) kv4_cswap(x & 2, w[i], w[i + 2]);
+        for (int i = 0; i < W; i += 2) kv4_cswap(x & 1, v[i], v[i + 1]);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (!(i & 2)) kv4_cswap(x & 2, v[i], v[i + 2]);
+      }
+      uint32_t first = ks[half].two(0), second = D == 256 ? ks[half].two(1) : first;
+      if constexpr (W == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kv4_cswap(x & 4, v[i], v[i + 4]);
+        kv4_cswap(x & 4, first, second);
+      }
+      const Kv4Scale<WIDE> s0(first), s1(second);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const int n0 = t * (D / 4) + 8 * (j ^ x);  // numbers n0 .. n0 + 7
+        const Kv4Scale<WIDE>& s = j < 4 ? s0 : s1;
+        *reinterpret_cast<uint4*>(to + (n0 >> 6) * (2 * kKv4N * 128) + R * 128 + ((((n0 >> 3) & 7) ^ (R & 7)) << 4)) =
+            make_uint4(s.template pair<0>(v[j]), s.template pair<1>(v[j]), s.template pair<2>(v[j]), s.template pair<3>(v[j]));
+      }
+    }
   }
-  uint32_t first = ks.two(0), second = D == 256 ? ks.two(1) : first;
-  if constexpr (W == 8) {
+};
+template <int D>
+struct Kv4BlockValues {
+  uint4 u[D / 64];  // row pair t: x, y; pair t + 4: z, w
+  uint32_t sv[2];
+  __device__ __forceinline__ void load(const uint8_t* blk, bool on, int lane) {  // blk: the coded values
+    using O = Kv4Off<D>;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kv4_cswap(x & 4, w[i], w[i + 4]);
-    kv4_cswap(x & 4, first, second);
-  }
-  const Kv4Scale<WIDE> s0(first), s1(second);
+    for (int i = 0; i < D / 64; ++i) u[i] = on ? reinterpret_cast<const uint4*>(blk)[i * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    const int n0 = t * (D / 4) + 8 * (j ^ x);  // numbers n0 .. n0 + 7
-    const Kv4Scale<WIDE>& s = j < 4 ? s0 : s1;
-    *reinterpret_cast<uint4*>(to + (n0 >> 6) * (kKv4N * 128) + R * 128 + ((((n0 >> 3) & 7) ^ (R & 7)) << 4)) =
-        make_uint4(s.template pair<0>(w[j]), s.template pair<1>(w[j]), s.template pair<2>(w[j]), s.template pair<3>(w[j]));
+    for (int half = 0; half < 2; ++half)
+      sv[half] = on ? *reinterpret_cast<const uint32_t*>(blk - O::kV + O::v_scale(2 * t + 8 * half, g * (D / 8) / kKv4Group)) : 0u;
   }
-}
-// Values: rows 2t and 2t + 1 (+ 8 half) of block b.
-template <int D, bool WIDE>
-__device__ __forceinline__ void kv4_decode_values(const uint8_t* blk, int b, int half, bool on, uint8_t* to, int lane) {
-  using O = Kv4Off<D>;
-  const int g = lane >> 2, t = lane & 3;
-  const int odd = D == 64 ? 0 : g & 1, Ra = 16 * b + 8 * half + 2 * t + odd, Rb = Ra ^ 1;
-  const uint32_t take_a = odd ? 0x7632u : 0x5410u, take_b = odd ? 0x5410u : 0x7632u;
-  const uint32_t sv = on ? *reinterpret_cast<const uint32_t*>(blk + O::v_scale(2 * t + 8 * half, g * (D / 8) / kKv4Group)) : 0u;
-  const Kv4Scale<WIDE> s(sv);
+  // As block b (0-3) of a tile into the operand at `to`.
+  template <bool WIDE>
+  __device__ __forceinline__ void store(int b, uint8_t* to, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int odd = D == 64 ? 0 : g & 1;
+    const uint32_t take_a = odd ? 0x7632u : 0x5410u, take_b = odd ? 0x5410u : 0x7632u;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    uint2 u = make_uint2(0u, 0u);
-    if (on) u = *reinterpret_cast<const uint2*>(blk + O::kV + (i * 32 + lane) * 16 + half * 8);
-    const uint32_t y[8] = {s.template pair<0>(u.x), s.template pair<1>(u.x), s.template pair<2>(u.x), s.template pair<3>(u.x),
-                           s.template pair<0>(u.y), s.template pair<1>(u.y), s.template pair<2>(u.y), s.template pair<3>(u.y)};
-    const int n0 = g * (D / 8) + 8 * i;
-    uint8_t* slab = to + (n0 >> 6) * (kKv4N * 128);
-    const int c = (n0 >> 3) & 7;
-    *reinterpret_cast<uint4*>(slab + Ra * 128 + ((c ^ (Ra & 7)) << 4)) =
-        make_uint4(__byte_perm(y[0], y[1], take_a), __byte_perm(y[2], y[3], take_a), __byte_perm(y[4], y[5], take_a), __byte_perm(y[6], y[7], take_a));
-    *reinterpret_cast<uint4*>(slab + Rb * 128 + ((c ^ (Rb & 7)) << 4)) =
-        make_uint4(__byte_perm(y[0], y[1], take_b), __byte_perm(y[2], y[3], take_b), __byte_perm(y[4], y[5], take_b), __byte_perm(y[6], y[7], take_b));
+    for (int half = 0; half < 2; ++half) {
+      const int Ra = 16 * b + 8 * half + 2 * t + odd, Rb = Ra ^ 1;
+      const Kv4Scale<WIDE> s(sv[half]);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t p = half ? u[i].z : u[i].x, q = half ? u[i].w : u[i].y;
+        const uint32_t y[8] = {s.template pair<0>(p), s.template pair<1>(p), s.template pair<2>(p), s.template pair<3>(p),
+                               s.template pair<0>(q), s.template pair<1>(q), s.template pair<2>(q), s.template pair<3>(q)};
+        const int n0 = g * (D / 8) + 8 * i;
+        uint8_t* slab = to + (n0 >> 6) * (kKv4N * 128);
+        const int c = (n0 >> 3) & 7;
+        *reinterpret_cast<uint4*>(slab + Ra * 128 + ((c ^ (Ra & 7)) << 4)) =
+            make_uint4(__byte_perm(y[0], y[1], take_a), __byte_perm(y[2], y[3], take_a), __byte_perm(y[4], y[5], take_a), __byte_perm(y[6], y[7], take_a));
+        *reinterpret_cast<uint4*>(slab + Rb * 128 + ((c ^ (Rb & 7)) << 4)) =
+            make_uint4(__byte_perm(y[0], y[1], take_b), __byte_perm(y[2], y[3], take_b), __byte_perm(y[4], y[5], take_b), __byte_perm(y[6], y[7], take_b));
+      }
+    }
   }
-}
+};
 
 // The queries of a row (zeros when it is none) into its lane of tensor memory, bf16 pairs.
 template <int D>
@@ -219,6 +259,31 @@ __device__ __forceinline__ void kv4_load_queries(const Kv4AttendArgs& a, const K
   kv4_tst_wait();
 }
 
+// The queries of an item's 128 rows into a swizzled operand, by four warps: a warp copies whole
+// rows, so its loads are contiguous.
+template <int D>
+__device__ __forceinline__ void kv4_share_queries(const Kv4AttendArgs& a, const Kv4Run& r, int row0, uint8_t* to, int tid) {
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p);
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+#pragma unroll 8
+  for (int e = tid; e < kKv4M * CH; e += 128) {
+    const int R = e / CH, c = e % CH, row = row0 + R;
+    uint8_t* dst = to + (c >> 3) * (kKv4M * 128) + R * 128 + (((c & 7) ^ (R & 7)) << 4);
+    const bool on = row < r.m * a.group;
+    const uint16_t* src = p + (on ? (long)r.seq * a.q.seq + (long)(row / a.group) * a.q.row + (long)(r.head * a.group + row % a.group) * a.q.head + 8 * c : 0);
+    if (a.q.vec) {
+      cp_async16(dst, src, on);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = on ? (uint32_t)__ldcg(src + 2 * k) | ((uint32_t)__ldcg(src + 2 * k + 1) << 16) : 0u;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  cp_async_wait_all();
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
 // The run of tiles at `at`: for the account, of at most kKv4RunTiles tiles (a.row_tiles 1), with
 // `blocks` blocks of 128 query rows to take past them.
 template <bool ACCOUNT>
@@ -234,31 +299,32 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
   using O = Kv4Off<D>;
   extern __shared__ __align__(16) uint8_t kv4_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv4_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* kop = base;                                             // [2] decoded keys
-  uint8_t* vop = base + 2 * C::kOperand;                           // [2] decoded values
-  uint8_t* ring = base + (ACCOUNT ? 2 : 4) * C::kOperand;
-  Kv4BlockBars* s = reinterpret_cast<Kv4BlockBars*>(ring + kKv4BlockRing * C::kTile);
+  uint8_t* kop = base;                                             // [kKBufs] decoded keys of a pair of tiles
+  uint8_t* qop = base + 2 * C::kOperand;                           // attention: queries
+  uint8_t* vop = base + 4 * C::kOperand;                           // attention: [2] decoded values of a tile
+  uint8_t* ring = base + C::kOps;
+  Kv4BlockBars* s = reinterpret_cast<Kv4BlockBars*>(ring + (C::kKRing + C::kVRing) * C::kTile);
   float* gacc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(s) + 512);  // account: [4 warps][keys of a run]
   int4* seqs = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(s) + C::kFixed);
   int* first = reinterpret_cast<int*>(seqs + a.n_seq);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKv4BlockRing; ++i) {
+    for (int i = 0; i < C::kKRing + C::kVRing; ++i) {  // keys' stages, then values'
       mbar_init(&s->full[i], 1);
-      mbar_init(&s->empty[i], C::kDecoders);
+      mbar_init(&s->empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s->kfull[i], C::kDecoders);
+      mbar_init(&s->kfull[i], 8);  // two tiles of four warps
       mbar_init(&s->kempty[i], 1);
-      mbar_init(&s->vfull[i], C::kDecoders);
+      mbar_init(&s->vfull[i], 4);
       mbar_init(&s->sfull[i], 1);
       mbar_init(&s->sread[i], 128);
       mbar_init(&s->qfull[i], 128);
       mbar_init(&s->qdone[i], 1);
+      mbar_init(&s->pfull[i], 128);
       mbar_init(&s->pvdone[i], 1);
     }
-    mbar_init(&s->pfull, 128);
     mbar_init(&s->drained, 1);
     s->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -277,81 +343,88 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
   const int total = first[a.n_seq], span = kv4_span(a, first, gridDim.x);
   const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
 
-  if (warp == 0) {
-    // ------------------------------------------------ producer: coded tiles into the ring
+  if (warp == 0 || (!ACCOUNT && warp == 2)) {
+    // ------------------------------------------------ producers: coded keys (warp 0), values (warp 2)
+    const int part = warp >> 1, ring0 = part * C::kKRing, stages = part ? 1 : C::kKRing;
     int n = 0;
-    for (int at = g0; at < g1;) {
+    bool stop = false;
+    for (int at = g0; at < g1 && !stop;) {
       int blocks;
       const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
       const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
       for (int x = 0; x < blocks * r.tiles; ++x, ++n) {
-        const int st = n % kKv4BlockRing;
-        if (n >= kKv4BlockRing) kv4_wait(&s->empty[st], (n / kKv4BlockRing - 1) & 1, s);
-        const int b = (r.tile + x % r.tiles) * 4 + lane;
+        const int b = (r.tile + x % r.tiles) * 4 + lane, st = ring0 + n % stages;
         const bool want = lane < 4 && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
         const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
         if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
         const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
-        if (*reinterpret_cast<volatile int*>(&s->abort)) break;
+        if (n >= stages) kv4_wait(&s->empty[st], (n / stages - 1) & 1, s);
+        stop = __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&s->abort));
+        if (stop) break;
         if (lane == 0) {
-          s->held[n & 7] = have;
-          mbar_expect_tx(&s->full[st], __popc(have) * C::kStride);
+          s->held[part][n & 15] = have;
+          mbar_expect_tx(&s->full[st], __popc(have) * C::kHalf);
         }
         __syncwarp();
         if (at_b >= 0)
-          bulk_g2s(ring + (size_t)st * C::kTile + lane * C::kStride, a.c.data + (size_t)at_b * O::kBlock, C::kStride, &s->full[st]);
+          bulk_g2s(ring + (size_t)st * C::kTile + lane * C::kHalf, a.c.data + (size_t)at_b * O::kBlock + part * C::kHalf, C::kHalf,
+                   &s->full[st]);
       }
-      if (*reinterpret_cast<volatile int*>(&s->abort)) break;
       at += r.tiles;
     }
-    for (int k = max(0, n - kKv4BlockRing); k < n; ++k) mbar_wait_drain(&s->full[k % kKv4BlockRing], (k / kKv4BlockRing) & 1);
+    for (int k = max(0, n - stages); k < n; ++k) mbar_wait_drain(&s->full[ring0 + k % stages], (k / stages) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------ matrix instructions
-    // Scores: attention one buffer, account two; the buffer is free once it has been read.
-    constexpr int NS = ACCOUNT ? 2 : 1;
     if (lane == 0) {
-      int n = 0, runs = 0;
+      int n = 0, pairs = 0, runs = 0;  // tiles, pairs of tiles and blocks of rows so far
       for (int at = g0; at < g1;) {
         int blocks;
         const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+        const int np = (r.tiles + 1) / 2;
         for (int rb = 0; rb < blocks; ++rb, ++runs) {
           const int qb = ACCOUNT ? runs & 1 : 0;
           bool ok = kv4_wait(&s->qfull[qb], (ACCOUNT ? runs >> 1 : runs) & 1, s);
-          for (int x = 0; x <= r.tiles; ++x) {
-            if (x < r.tiles) {
-              const int y = n + x, b = y & 1, sb = y % NS;
-              ok = kv4_wait(&s->kfull[b], (y >> 1) & 1, s) && ok;
-              if (y >= NS) ok = kv4_wait(&s->sread[sb], (y / NS - 1) & 1, s) && ok;
+          for (int q = 0; q <= np; ++q) {
+            if (q < np) {  // scores of pair q
+              const int y = pairs + q, kb = y % C::kKBufs, sb = y % C::kSBufs;
+              ok = kv4_wait(&s->kfull[kb], (y / C::kKBufs) & 1, s) && ok;
+              if (y >= C::kSBufs) ok = kv4_wait(&s->sread[sb], (y / C::kSBufs - 1) & 1, s) && ok;
               kv4_fence_after();
               if (ok) {
-                const uint32_t kaddr = su32(kop + b * C::kOperand);
+                const uint32_t kaddr = su32(kop + kb * 2 * C::kOperand), qaddr = su32(qop);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  kv4_mma_ts(tmem + C::kColS + sb * kKv4N, tmem + C::kColQ + qb * (D / 2) + k * 8,
-                             kv4_desc(kaddr + (k >> 2) * (kKv4N * 128) + (k & 3) * 32, 0), kv4_idesc(kKv4N, false), k > 0);
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t off = (k >> 2) * (kKv4M * 128) + (k & 3) * 32;
+                  const uint64_t kd = kv4_desc(kaddr + off, 0);
+                  if (ACCOUNT) kv4_mma_ts(tmem + C::kColS + sb * 128, tmem + C::kColQ + qb * (D / 2) + k * 8, kd, kv4_idesc(128, false), k > 0);
+                  else kv4_mma_ss(tmem + C::kColS, kv4_desc(qaddr + off, 0), kd, kv4_idesc(128, false), k > 0);
+                }
               }
               kv4_commit(&s->sfull[sb]);
-              kv4_commit(&s->kempty[b]);
-              if (ACCOUNT && x + 1 == r.tiles) kv4_commit(&s->qdone[qb]);
+              kv4_commit(&s->kempty[kb]);
+              if (ACCOUNT && q + 1 == np) kv4_commit(&s->qdone[qb]);
             }
-            if (!ACCOUNT && x > 0) {
-              const int y = n + x - 1, b = y & 1;
-              ok = kv4_wait(&s->vfull[b], (y >> 1) & 1, s) && ok;
-              ok = kv4_wait(&s->pfull, y & 1, s) && ok;
-              kv4_fence_after();
-              if (ok) {
-                const uint32_t vaddr = su32(vop + b * C::kOperand);
+            if (!ACCOUNT && q > 0) {  // outputs of pair q - 1
+              for (int x = 2 * q - 2; x < min(2 * q, r.tiles); ++x) {
+                const int y = n + x, b = y & 1;
+                ok = kv4_wait(&s->vfull[b], (y >> 1) & 1, s) && ok;
+                ok = kv4_wait(&s->pfull[b], (y >> 1) & 1, s) && ok;
+                kv4_fence_after();
+                if (ok) {
+                  const uint32_t vaddr = su32(vop + b * C::kOperand);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                  for (int part = 0; part < 2; ++part)
 #pragma unroll
-                  for (int k = 0; k < kKv4N / 16; ++k)
-                    kv4_mma_ts(tmem, tmem + C::kColP + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
-                               kv4_idesc(D, true), x > 1 || part > 0 || k > 0);
+                    for (int k = 0; k < kKv4N / 16; ++k)
+                      kv4_mma_ts(tmem, tmem + C::kColP + b * 64 + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
+                                 kv4_idesc(D, true), x > 0 || part > 0 || k > 0);
+                }
+                kv4_commit(&s->pvdone[b]);
               }
-              kv4_commit(&s->pvdone[b]);
             }
           }
           n += r.tiles;
+          pairs += np;
         }
         at += r.tiles;
       }
@@ -375,37 +448,55 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
       }
       at += r.tiles;
     }
-  } else if (warp >= 8) {
-    // ------------------------------------------------ decoding: warp d: half (d & 1) of block d / 2,
-    // or (account) both halves of block d
-    const int d = warp - 8;
+  } else if (warp >= 12) {
+    // ------------------------------------------------ values: warp 12 + b decodes block b
+    const int b = warp - 12, st = C::kKRing;
     int n = 0;
     for (int at = g0; at < g1;) {
       int blocks;
       const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
-      for (int x = 0; x < blocks * r.tiles; ++x, ++n) {
-        const int st = n % kKv4BlockRing, buf = n & 1, b = ACCOUNT ? d : d >> 1;
-        kv4_wait(&s->full[st], (n / kKv4BlockRing) & 1, s);
-        const bool on = (s->held[n & 7] >> b) & 1;
-        const uint8_t* blk = ring + (size_t)st * C::kTile + b * C::kStride;
-        if (n >= 2) kv4_wait(&s->kempty[buf], ((n - 2) >> 1) & 1, s);
-#pragma unroll 1
-        for (int half = ACCOUNT ? 0 : d & 1; half < (ACCOUNT ? 2 : (d & 1) + 1); ++half) {
-          if (wide) kv4_decode_keys<D, true>(blk, b, half, on, kop + buf * C::kOperand, lane);
-          else kv4_decode_keys<D, false>(blk, b, half, on, kop + buf * C::kOperand, lane);
-        }
+      for (int x = 0; x < r.tiles; ++x, ++n) {
+        const int buf = n & 1;
+        kv4_wait(&s->full[st], n & 1, s);
+        Kv4BlockValues<D> v;
+        v.load(ring + (size_t)st * C::kTile + b * C::kHalf, (s->held[1][n & 15] >> b) & 1, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->empty[st]);
+        if (n >= 2) kv4_wait(&s->pvdone[buf], ((n - 2) >> 1) & 1, s);
+        if (wide) v.template store<true>(b, vop + buf * C::kOperand, lane);
+        else v.template store<false>(b, vop + buf * C::kOperand, lane);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s->kfull[buf]);
-        if (!ACCOUNT) {
-          if (n >= 2) kv4_wait(&s->pvdone[buf], ((n - 2) >> 1) & 1, s);
-          if (wide) kv4_decode_values<D, true>(blk, b, d & 1, on, vop + buf * C::kOperand, lane);
-          else kv4_decode_values<D, false>(blk, b, d & 1, on, vop + buf * C::kOperand, lane);
+        if (lane == 0) mbar_arrive(&s->vfull[buf]);
+      }
+      at += r.tiles;
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------ keys: warp 8 + b decodes block b
+    const int b = warp - 8;
+    int n = 0, pairs = 0;
+    for (int at = g0; at < g1;) {
+      int blocks;
+      const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
+      for (int rb = 0; rb < blocks; ++rb) {
+        for (int x = 0; x < r.tiles; ++x, ++n) {
+          const int y = pairs + (x >> 1), kb = y % C::kKBufs, st = n % C::kKRing;
+          kv4_wait(&s->full[st], (n / C::kKRing) & 1, s);
+          Kv4BlockKeys<D> k;
+          k.load(ring + (size_t)st * C::kTile + b * C::kHalf, (s->held[0][n & 15] >> b) & 1, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->empty[st]);
+          if (y >= C::kKBufs) kv4_wait(&s->kempty[kb], (y / C::kKBufs - 1) & 1, s);
+          if (wide) k.template store<true>((x & 1) * 4 + b, kop + kb * 2 * C::kOperand, lane);
+          else k.template store<false>((x & 1) * 4 + b, kop + kb * 2 * C::kOperand, lane);
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s->vfull[buf]);
+          if (lane == 0) {
+            mbar_arrive(&s->kfull[kb]);
+            if (x + 1 == r.tiles && !(x & 1)) mbar_arrive(&s->kfull[kb]);  // a last pair of one tile
+          }
         }
-        if (lane == 0) mbar_arrive(&s->empty[st]);
+        pairs += (r.tiles + 1) / 2;
       }
       at += r.tiles;
     }
@@ -414,7 +505,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
     const int row_in = threadIdx.x - 128, wq = warp - 4;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
     const float sc = wide ? a.scale : a.scale * kKv4Up, up = wide ? 1.f : kKv4Up;
-    int n = 0, piece = 0;
+    int n = 0, pairs = 0, piece = 0;
     for (int at = g0; at < g1; ++piece) {
       int blocks;
       const Kv4Run r = kv4_block_run<ACCOUNT>(a, first, seqs, at, g1, &blocks);
@@ -426,8 +517,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
         const int row0 = (ACCOUNT ? rb : r.row_tile) * kKv4M, row = row0 + row_in;
         const int tok = min(row, n_rows - 1) / a.group, hq = r.head * a.group + min(row, n_rows - 1) % a.group;
         if (!ACCOUNT) {
-          kv4_load_queries<D>(a, r, row, lane_base + C::kColQ);
-          kv4_fence_before();
+          kv4_share_queries<D>(a, r, row0, qop, row_in);
           mbar_arrive(&s->qfull[0]);
         }
         // rows it sees: (low, last]
@@ -438,17 +528,18 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
                           : row < n_rows ? __ldcg(a.lse + ((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row) : INFINITY;
         float m = -INFINITY, l = 0.f;
         for (int x = 0; x < r.tiles; ++x, ++n) {
-          const int sb = ACCOUNT ? n & 1 : 0;
-          kv4_wait(&s->sfull[sb], (ACCOUNT ? n >> 1 : n) & 1, s);
+          const int y = pairs + (x >> 1), sb = y % C::kSBufs;
+          kv4_wait(&s->sfull[sb], (y / C::kSBufs) & 1, s);
           kv4_fence_after();
           uint32_t v[64];
-          kv4_tld32(lane_base + C::kColS + sb * kKv4N, v);
-          kv4_tld32(lane_base + C::kColS + sb * kKv4N + 32, v + 32);
+          const uint32_t cols = lane_base + C::kColS + sb * 128 + (x & 1) * kKv4N;
+          kv4_tld32(cols, v);
+          kv4_tld32(cols + 32, v + 32);
           kv4_tld_wait();
           const int j0 = (r.tile + x) * kKv4N;
-          const uint32_t have = s->held[n & 7];
+          const uint32_t have = s->held[0][n & 15];
           kv4_fence_before();
-          mbar_arrive(&s->sread[sb]);  // the scores are in registers
+          if ((x & 1) || x + 1 == r.tiles) mbar_arrive(&s->sread[sb]);  // the pair's scores are in registers
           float f[64];
 #pragma unroll
           for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(v[k]);
@@ -509,17 +600,19 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
               v[32 + k] = as_u32(__floats2bfloat162_rn(p0 - bf16_lo(v[k]), p1 - bf16_hi(v[k])));
             }
             l += s0 + s1;
-            if (x > 0) {  // the previous tile's weights have been used
-              kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
+            const int pb = n & 1;
+            if (n >= 2) {  // the weights before the previous tile's have been used
+              kv4_wait(&s->pvdone[pb], ((n - 2) >> 1) & 1, s);
               kv4_fence_after();
             }
-            kv4_tst32(lane_base + C::kColP, v);
-            kv4_tst32(lane_base + C::kColP + 32, v + 32);
+            kv4_tst32(lane_base + C::kColP + pb * 64, v);
+            kv4_tst32(lane_base + C::kColP + pb * 64 + 32, v + 32);
             kv4_tst_wait();
             kv4_fence_before();
-            mbar_arrive(&s->pfull);
+            mbar_arrive(&s->pfull[pb]);
           }
         }
+        pairs += (r.tiles + 1) / 2;
         if constexpr (!ACCOUNT) {
           // ---- the run's output row
           kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
@@ -574,9 +667,9 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
   }
 }
 
-// Joins the parts of shared items, in span order: 16 rows of item blockIdx.x per CTA.  Also the
+// Joins the parts of shared items, in span order: four rows of item blockIdx.x per CTA.  Also the
 // zeros of rows that no tile reaches.
-constexpr int kKv4BlockJoinRows = 16;
+constexpr int kKv4BlockJoinRows = 4;
 
 template <int D>
 __global__ void __launch_bounds__(128) kv4_block_join_kernel(const Kv4AttendArgs a, int ctas) {

@@ -243,6 +243,36 @@ def test_token_blocks(rt, d, q_len, group, kvh, page, track):
     check_attend(rt, d, kvh, group, lens, q_len, "bf16", page, q_lens=q_lens, track=track, seed=d + q_len)
 
 
+@pytest.mark.parametrize("d,kvh", [(256, 2), (128, 4), (64, 2)])
+@pytest.mark.parametrize("track", [False, True])
+def test_token_blocks_many_tiles(rt, d, kvh, track):
+    """A batch whose CTAs each take many tiles in a row, several items and odd numbers of them."""
+    n, q_len, group, cap = 40, 36, 4, 1500
+    lens = [36 + (i * 977) % 1465 for i in range(n)]
+    c = make(rt, n, cap, kvh * group, kvh, d, 64, track=track)
+    k, v = rows((n, cap, kvh, d), "bf16", 1), rows((n, cap, kvh, d), "bf16", 2)
+    slots = list(range(n))
+    c.append(k, v, i32(slots), i32([0] * n), i32(lens))
+    q = rows((n, q_len, kvh * group, d), "bf16", 3)
+    out = c.attend(q, i32(slots), i32(lens), accumulate=track)
+    fine(c)
+    for i in range(n):
+        kk, vv = (torch.from_numpy(ref.values(host(x[i, :lens[i]]))).cuda() for x in (k, v))
+        qq = q[i].double().reshape(q_len, kvh, group, d)
+        s = torch.einsum("mkgd,tkd->kgmt", qq, kk) / np.sqrt(d)
+        j, last = torch.arange(lens[i], device="cuda"), lens[i] - q_len + torch.arange(q_len, device="cuda")
+        p = torch.softmax(s.masked_fill(j > last[:, None], -np.inf), -1)
+        want = torch.einsum("kgmt,tkd->mkgd", p, vv).reshape(q_len, kvh * group, d)
+        bound = attend_bound(host(q[i]), host(kk), host(vv), 1 / np.sqrt(d), "bf16", host(want))
+        assert (np.abs(host(out[i]) - host(want)) <= bound).all()
+        # far inside that worst case: an rms error is the output's rounding (2^-9 / sqrt 3 of the value) and little else
+        assert (out[i].double() - want).norm() <= 2.0 ** -8 * want.norm()
+        if track:
+            _, w = c.account(i32([i]), i32([0]), lens[i])
+            gain = p.sum((1, 2))
+            assert (w[0].double() - gain).norm() <= 2e-5 * gain.norm()
+
+
 @pytest.mark.parametrize("window", [1, 63, 64, 300])
 def test_token_block_window(rt, window):
     check_attend(rt, 128, 2, 8, [9, 64, 65, 900, 40], 9, "bf16", 32, window=window, seed=window)
