@@ -159,7 +159,7 @@ void kv4_launch_block(g4_kv4* op, Kv4AttendArgs a, cudaStream_t st) {
   a.lse_rows = a.row_tiles * kKv4M;
   a.join_inside = 0;
   launch(kv4_block_kernel<D, false>, dim3(op->sms), dim3(kKv4BlockThreads), Kv4Blk<D, false>::smem(a.n_seq), st, a);
-  launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, kKv4M / kKv4BlockJoinRows), dim3(128), (size_t)a.n_seq * 20 + 16,
+  launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, D / 16), dim3(kKv4M), (size_t)a.n_seq * 20 + 16,
          st, a, op->sms);
   if (!a.accumulate) return;
   a.row_tiles = 1;  // the account cuts the keys alone into spans

@@ -259,24 +259,29 @@ __device__ __forceinline__ void kv4_load_queries(const Kv4AttendArgs& a, const K
   kv4_tst_wait();
 }
 
-// The queries of an item's 128 rows into a swizzled operand, by four warps: a warp copies whole
-// rows, so its loads are contiguous.
+// The queries of an item's 128 rows into a swizzled operand, by four warps of 32 rows each: a
+// warp copies whole rows, so its loads are contiguous; its lanes work the rows' addresses out
+// beforehand, one each.
 template <int D>
 __device__ __forceinline__ void kv4_share_queries(const Kv4AttendArgs& a, const Kv4Run& r, int row0, uint8_t* to, int tid) {
+  constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks of a row, rows a warp copies at a time
+  const int lane = tid & 31, mine = row0 + tid, sub = lane / CH, c = lane % CH;
   const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p);
-  constexpr int CH = D / 8;  // 16-byte chunks of a row
-#pragma unroll 8
-  for (int e = tid; e < kKv4M * CH; e += 128) {
-    const int R = e / CH, c = e % CH, row = row0 + R;
+  const bool mine_on = mine < r.m * a.group;
+  if (mine_on) p += (long)r.seq * a.q.seq + (long)(mine / a.group) * a.q.row + (long)(r.head * a.group + mine % a.group) * a.q.head;
+  const unsigned on_mask = __ballot_sync(0xFFFFFFFFu, mine_on);
+#pragma unroll 4
+  for (int k = 0; k < 32; k += RP) {
+    const int from = k + sub, R = (tid & ~31) + from;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)p, from)) + 8 * c;
+    const bool on = (on_mask >> from) & 1;
     uint8_t* dst = to + (c >> 3) * (kKv4M * 128) + R * 128 + (((c & 7) ^ (R & 7)) << 4);
-    const bool on = row < r.m * a.group;
-    const uint16_t* src = p + (on ? (long)r.seq * a.q.seq + (long)(row / a.group) * a.q.row + (long)(r.head * a.group + row % a.group) * a.q.head + 8 * c : 0);
     if (a.q.vec) {
       cp_async16(dst, src, on);
     } else {
       uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = on ? (uint32_t)__ldcg(src + 2 * k) | ((uint32_t)__ldcg(src + 2 * k + 1) << 16) : 0u;
+      for (int e = 0; e < 4; ++e) w[e] = on ? (uint32_t)__ldcg(src + 2 * e) | ((uint32_t)__ldcg(src + 2 * e + 1) << 16) : 0u;
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -620,22 +625,23 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
           const bool whole = r.whole;
           const float inv = (whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f) * up;
           const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
-          float* part = reinterpret_cast<float*>(a.part_o) + (slot_p * kKv4M + row_in) * D;
+          float4* part = a.part_o + slot_p * (D / 4) * kKv4M + row_in;  // [D / 4][128 rows]
           const long o0 = (long)r.seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t u[32];
+          for (int c = 0; c < D; c += 64) {
+            uint32_t u[64];
             kv4_tld32(lane_base + c, u);
+            kv4_tld32(lane_base + c + 32, u + 32);
             kv4_tld_wait();
-            float* f = reinterpret_cast<float*>(u);
+            float f[64];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(u[k]) * inv;
+            for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(u[k]) * inv;
             if (!whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) kv4_store32b(part + c + 8 * k, *reinterpret_cast<const uint32_t(*)[8]>(u + 8 * k));
+              for (int k = 0; k < 16; ++k) part[(c / 4 + k) * kKv4M] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
             } else if (row < n_rows) {
-              kv4_store16(a.out, o0 + c, f);
-              kv4_store16(a.out, o0 + c + 16, f + 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) kv4_store16(a.out, o0 + c + 16 * k, f + 16 * k);
             }
           }
           if (!whole) a.part_ml[slot_p * kKv4M + row_in] = make_float2(m, l);
@@ -667,10 +673,8 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
   }
 }
 
-// Joins the parts of shared items, in span order: four rows of item blockIdx.x per CTA.  Also the
-// zeros of rows that no tile reaches.
-constexpr int kKv4BlockJoinRows = 4;
-
+// Joins the parts of shared items, in span order: a thread per row of item blockIdx.x and 16
+// numbers of it, blockIdx.y counting those.  Also the zeros of rows that no tile reaches.
 template <int D>
 __global__ void __launch_bounds__(128) kv4_block_join_kernel(const Kv4AttendArgs a, int ctas) {
   extern __shared__ __align__(16) uint8_t kv4_raw[];
@@ -686,31 +690,34 @@ __global__ void __launch_bounds__(128) kv4_block_join_kernel(const Kv4AttendArgs
   pdl_trigger();
   if (x == 0 && blockIdx.y == 0) kv4_zero_rows<D>(a, first, seqs, i, a.n_seq, tid, 128);
   if (c1 <= c0) return;
-  constexpr int T = D / 8;  // threads of a row, eight numbers each
-  const float* part_o = reinterpret_cast<const float*>(a.part_o);
-  for (int k = tid / T; k < kKv4BlockJoinRows; k += 128 / T) {
-    const int rl = blockIdx.y * kKv4BlockJoinRows + k, row = rt * kKv4M + rl, e = tid % T * 8;
-    if (row >= n_rows) break;
-    float2 ml = make_float2(-INFINITY, 0.f);
+  const int row = rt * kKv4M + tid, e = blockIdx.y * 16;
+  if (row >= n_rows) return;
+  float2 ml = make_float2(-INFINITY, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) kv4_merge_ml(ml, __ldcg(&a.part_ml[kv4_part(c, t0, span) * kKv4M + rl]));
-    const float Z = ml.x == -INFINITY ? 0.f : ml.x, inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const long p = kv4_part(c, t0, span) * kKv4M + rl;
-      const float f = kv4_exp2(__ldcg(&a.part_ml[p].x) - Z);
-      uint32_t u[8];
-      kv4_load32b(part_o + p * D + e, u);
+  for (int c = c0; c <= c1; ++c) kv4_merge_ml(ml, __ldcg(&a.part_ml[kv4_part(c, t0, span) * kKv4M + tid]));
+  const float Z = ml.x == -INFINITY ? 0.f : ml.x, inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
+  float v[16];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] += f * __uint_as_float(u[q]);
+  for (int q = 0; q < 16; ++q) v[q] = 0.f;
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const long p = kv4_part(c, t0, span);
+    const float f = kv4_exp2(__ldcg(&a.part_ml[p * kKv4M + tid].x) - Z);
+    const float4* o = a.part_o + (p * (D / 4) + e / 4) * kKv4M + tid;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 u = __ldcg(o + q * kKv4M);
+      v[4 * q] += f * u.x;
+      v[4 * q + 1] += f * u.y;
+      v[4 * q + 2] += f * u.z;
+      v[4 * q + 3] += f * u.w;
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] *= inv;
-    const int tok = row / a.group, hq = head * a.group + row % a.group;
-    kv4_store8(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + e, v);
-    if (tid % T == 0) a.lse[((long)i * a.c.kvh + head) * a.lse_rows + row] = kv4_lse(ml);
   }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) v[q] *= inv;
+  const int tok = row / a.group, hq = head * a.group + row % a.group;
+  kv4_store16(a.out, (long)i * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + e, v);
+  if (blockIdx.y == 0) a.lse[((long)i * a.c.kvh + head) * a.lse_rows + row] = kv4_lse(ml);
 }
 
 }  // namespace g4
