@@ -37,6 +37,7 @@
 #include "gemv.cuh"
 #include "gemv_s.cuh"
 #include "host.h"
+#include "kv4_host.h"
 #include "mega.cuh"
 #include "misc.cuh"
 
@@ -109,6 +110,13 @@ struct g4_handle {
   std::vector<void*> kc, vc;
   std::vector<float*> ksc, vsc;
   bool kv8 = false;
+  // 4-bit rows (kv_format G4_KV_INT4): per owning layer a cache in kv4.cuh's layout (its blocks
+  // are kc's allocation), one workspace for all layers, the step's normed queries and lengths
+  bool kv4 = false;
+  std::vector<Kv4Cache> kv4c;
+  Kv4Work kv4_work;
+  float* kv4_q = nullptr;
+  int* kv4_lens = nullptr;
   int* page_table = nullptr;
   int page_shift = 0, max_pages = 0, n_pages = 0;
   std::vector<int> pt_host, slot_pages, free_pages;
@@ -978,9 +986,23 @@ void kv_args(const g4_handle* h, const Layer& Src, AttnArgs& a) {
   a.page_shift = h->page_shift;
   a.max_pages = h->max_pages;
 }
+// Attention of a layer over 4-bit rows: the rows' queries (and an owning layer's new keys and
+// values, all of a prefill block's before any is read), then one token per row.
+void launch_layer_kv4(g4_handle* h, const Layer& Y, const float* qkv, int qkv_stride, int n, const int* d_slots,
+                      const int* d_pos, cudaStream_t st) {
+  const g4_config& c = h->cfg;
+  Kv4Cache cache = h->kv4c[h->layers[Y.src].kv];
+  cache.err = h->err;
+  const Kv4Step a{qkv, qkv_stride, c.num_q_heads, Y.own, Y.q_norm, Y.k_norm, c.rms_eps, h->cos_t[Y.full], h->sin_t[Y.full],
+                  d_slots, d_pos, h->kv4_q, h->kv4_lens};
+  kv4_step_rows(cache, a, n, st);
+  kv4_step_attend(cache, h->kv4_work, n, d_slots, h->kv4_lens, c.num_q_heads, Y.scale, Y.full ? 0 : c.sliding_window,
+                  h->kv4_q, h->attn, c.num_q_heads * Y.d, st);
+}
 // Attention launch of layer l (shared by both step paths).
 void launch_layer_attn(g4_handle* h, const Layer& Y, const float* qkv, int qkv_stride, int n, const int* d_slots,
                        const int* d_pos, bool own, cudaStream_t st) {
+  if (h->kv4) return launch_layer_kv4(h, Y, qkv, qkv_stride, n, d_slots, d_pos, st);
   const g4_config& c = h->cfg;
   const Layer& Src = h->layers[Y.src];
   AttnArgs a{};
@@ -1331,8 +1353,12 @@ g4_status run_step(g4_handle* h, cudaStream_t st, int n, const int* d_slots, con
       a.counters = h->attn_cnt;
       a.err = h->err;
       ProfScope ps(prof, Y.full ? "attn.full" : "attn.sliding", 0.0);
-      if (kv_first && Y.own) launch_kv_write_any(a, Y.d, n, h->kv8, st);
-      launch_attn_any(a, Y.d, hpc, n, h->kv8, mqa_on(c.num_q_heads, n), st);
+      if (h->kv4) {
+        launch_layer_kv4(h, Y, h->qkv, Y.qkv.n_valid, n, d_slots, d_pos, st);
+      } else {
+        if (kv_first && Y.own) launch_kv_write_any(a, Y.d, n, h->kv8, st);
+        launch_attn_any(a, Y.d, hpc, n, h->kv8, mqa_on(c.num_q_heads, n), st);
+      }
       if (h->trace)
         for (int i = 0; i < n; ++i)
           cudaMemcpyAsync(h->trace + ((size_t)(l * 2) * c.max_batch + i) * ts, h->attn + (size_t)i * nqd,
@@ -1481,7 +1507,7 @@ g4_status build_mega(g4_handle* h, cudaStream_t st) {
   const g4_config& c = h->cfg;
   const int H = c.hidden, L = c.num_layers, P = c.ple_dim, nq = c.num_q_heads;
   const int G = h->sms, NB = 2;
-  if (H % 8 || h->kv8 || h->t4) return G4_OK;  // the persistent step: bf16 cache rows and tables only
+  if (H % 8 || h->kv8 || h->kv4 || h->t4) return G4_OK;  // the persistent step: bf16 cache rows and tables only
   std::vector<MegaPhase> prog;
   size_t smem_f = 64;  // floats
   auto wred_f = [&]() { return (size_t)2 * kMegaWarps * 2 * NB * 32; };  // double-buffered warp partials
@@ -1844,7 +1870,8 @@ g4_status validate(const g4_config* c) {
   if (!is_pow2_dim(c->head_dim_sliding) || !is_pow2_dim(c->head_dim_full)) return G4_ERR_UNSUPPORTED;
   if (c->hidden % 32 || c->mlp % 32 || c->mlp_shared % 32 || c->ple_dim % 32) return G4_ERR_UNSUPPORTED;
   if (c->max_batch > 64 || c->ple_dim > 1024 || c->hidden > 8192) return G4_ERR_UNSUPPORTED;
-  if (c->kv_format != G4_KV_BF16 && c->kv_format != G4_KV_INT8) return G4_ERR_INVALID_ARG;
+  if (c->kv_format < G4_KV_BF16 || c->kv_format > G4_KV_INT4) return G4_ERR_INVALID_ARG;
+  if (c->kv_format == G4_KV_INT4 && (c->num_q_heads > 64 || c->max_context > (1 << 20))) return G4_ERR_UNSUPPORTED;
   if (c->kv_page_size < 0 || c->kv_pages < 0) return G4_ERR_INVALID_ARG;
   if (c->kv_page_size > 0 && (c->kv_page_size < 16 || (c->kv_page_size & (c->kv_page_size - 1))))
     return G4_ERR_UNSUPPORTED;  // pages of a power of two >= 16 positions
@@ -1934,6 +1961,7 @@ g4_status create_impl(g4_handle* h, const g4_config* cfg, const g4_weights* w, c
   // KV cache: owning layers only.  Static: [max_batch][max_context] rows of d values for K
   // and for V.  Paged: a pool of n_pages pages of page_size rows, and one page table.
   h->kv8 = c.kv_format == G4_KV_INT8;
+  h->kv4 = c.kv_format == G4_KV_INT4;
   size_t kv_rows = (size_t)c.max_batch * c.max_context;
   if (c.kv_page_size > 0) {
     while ((1 << h->page_shift) < c.kv_page_size) ++h->page_shift;
@@ -1948,12 +1976,33 @@ g4_status create_impl(g4_handle* h, const g4_config* cfg, const g4_weights* w, c
     CK(cudaStreamSynchronize(st));
   }
   h->kc.resize(n_own);
+  h->kv4c.resize(n_own);
   h->vc.resize(n_own);
   h->ksc.assign(n_own, nullptr);
   h->vsc.assign(n_own, nullptr);
   for (int l = 0; l < L; ++l) {
     const Layer& Y = h->layers[l];
     if (!Y.own) continue;
+    if (h->kv4) {
+      Kv4Cache k{};
+      k.table = h->page_table;
+      k.bpp = h->page_table ? c.kv_page_size / kKv4Block : cdiv(c.max_context, kKv4Block);
+      while ((1 << k.log_bpp) < k.bpp) ++k.log_bpp;
+      k.max_pages = h->max_pages;
+      k.n_pages = h->n_pages;
+      k.n_slots = c.max_batch;
+      k.capacity = c.max_context;
+      k.kvh = 1;
+      k.d = Y.d;
+      const size_t nb = kv4_cache_bytes((size_t)k.bpp * (h->page_table ? h->n_pages : c.max_batch), 1, Y.d);
+      TRY(dalloc(h, &k.data, nb));
+      TRY(dalloc(h, &k.wide, 1));
+      CK(cudaMemsetAsync(k.data, 0, nb, st));
+      CK(cudaMemsetAsync(k.wide, 0, sizeof(int), st));
+      h->kc[Y.kv] = k.data;
+      h->kv4c[Y.kv] = k;
+      continue;
+    }
     const size_t nb = kv_rows * Y.d * (h->kv8 ? 1 : 2);
     uint8_t *kb = nullptr, *vb = nullptr;
     TRY(dalloc(h, &kb, nb));
@@ -2008,6 +2057,20 @@ g4_status create_impl(g4_handle* h, const g4_config* cfg, const g4_weights* w, c
   TRY(dalloc(h, &h->r_mlp, (size_t)B * H));
   TRY(dalloc(h, &h->pg, (size_t)B * P));
   TRY(dalloc(h, &h->r_ple, (size_t)B * H));
+  if (h->kv4) {
+    kv4_init(h->device, h->smem_optin);
+    Kv4Work& k = h->kv4_work;
+    k.sms = h->sms;
+    k.smem_optin = h->smem_optin;
+    const size_t parts = kv4_work_part_rows(h->sms), items = kv4_work_tickets(B, 1, nq, 1);
+    TRY(dalloc(h, &k.lse, kv4_work_lse(B, 1, nq, 1)));
+    TRY(dalloc(h, &k.part_o, parts * dmax / 4));
+    TRY(dalloc(h, &k.part_ml, parts));
+    TRY(dalloc(h, &k.tickets, items));
+    CK(cudaMemsetAsync(k.tickets, 0, items * sizeof(unsigned), st));
+    TRY(dalloc(h, &h->kv4_q, (size_t)B * nq * dmax));
+    TRY(dalloc(h, &h->kv4_lens, B));
+  }
   {  // staged decode step buffers: kSgMaxParts parts of kMaxNB rows
     h->sq_qkv_w = (nq + 2) * dmax;
     h->sq_gu_w = 2 * Fmax;

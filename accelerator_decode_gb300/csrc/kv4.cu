@@ -11,20 +11,17 @@
 #include "kv4.cuh"
 #include "kv4_attend.cuh"
 #include "kv4_block.cuh"
+#include "kv4_host.h"
 
 using namespace g4;
 
 struct g4_kv4 {
   g4_kv4_config cfg{};
-  int device = 0, sms = 0;
+  int device = 0;
   Kv4Cache c{};
   std::vector<void*> allocs;
   size_t bytes = 0;
-  float* lse = nullptr;                       // [n_slots][kvh][row tiles * 8]
-  float4* part_o = nullptr;                   // partial sums of the spans (kv4_attend.cuh)
-  float2* part_ml = nullptr;
-  unsigned* tickets = nullptr;                // parts done of an item
-  int smem_optin = 0;
+  Kv4Work work;
   int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
   int* n_moves = nullptr;                     // [n_slots][kvh]
 };
@@ -127,23 +124,10 @@ void kv4_attrs_d(int optin) {
   kv4_attrs<D, G4_DT_F16>(optin);
   carve_max(kv4_append_kernel<D>);
   carve_max(kv4_append_blocks_kernel<D>);
+  carve_max(kv4_step_kernel<D>);
   carve_max(kv4_read_blocks_kernel<D>);
   carve_max(kv4_read_kernel<D>);
   carve_max(kv4_move_kernel<D>);
-}
-void kv4_init(int device, int optin) {
-  std::lock_guard<std::mutex> lk(g_kv4_mu);
-  if (!g_kv4_devices.insert(device).second) return;
-  kv4_attrs_d<64>(optin);
-  kv4_attrs_d<128>(optin);
-  kv4_attrs_d<256>(optin);
-  kv4_attrs_d<512>(optin);
-  kv4_attrs_block<64>(optin);
-  kv4_attrs_block<128>(optin);
-  kv4_attrs_block<256>(optin);
-  carve_max(kv4_account_kernel);
-  set_max_dyn(kv4_select_kernel, optin);
-  cudaGetLastError();
 }
 int kv4_most_moves(const g4_kv4* op) { return std::max(1, op->cfg.capacity / 2); }
 int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads), 8); }
@@ -153,40 +137,48 @@ bool kv4_block_path(const g4_kv4* op, int q_len, int dtype) {
   return dtype == G4_DT_BF16 && op->cfg.head_dim <= 256 && q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads) > kKv4BlockRows;
 }
 template <int D>
-void kv4_launch_block(g4_kv4* op, Kv4AttendArgs a, cudaStream_t st) {
+void kv4_launch_block(const Kv4Work& op, Kv4AttendArgs a, cudaStream_t st) {
   const int rows = a.q_len * a.group;
   a.row_tiles = cdiv(rows, kKv4M);
   a.lse_rows = a.row_tiles * kKv4M;
   a.join_inside = 0;
-  launch(kv4_block_kernel<D, false>, dim3(op->sms), dim3(kKv4BlockThreads), Kv4Blk<D, false>::smem(a.n_seq), st, a);
+  launch(kv4_block_kernel<D, false>, dim3(op.sms), dim3(kKv4BlockThreads), Kv4Blk<D, false>::smem(a.n_seq), st, a);
   launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, D / 16), dim3(kKv4M), (size_t)a.n_seq * 20 + 16,
-         st, a, op->sms);
+         st, a, op.sms);
   if (!a.accumulate) return;
   a.row_tiles = 1;  // the account cuts the keys alone into spans
-  launch(kv4_block_kernel<D, true>, dim3(op->sms), dim3(kKv4BlockThreads), Kv4Blk<D, true>::smem(a.n_seq), st, a);
+  launch(kv4_block_kernel<D, true>, dim3(op.sms), dim3(kKv4BlockThreads), Kv4Blk<D, true>::smem(a.n_seq), st, a);
+}
+
+void kv4_use(const Kv4Work& w, Kv4AttendArgs& a) {
+  a.lse = w.lse;
+  a.lse_rows = a.row_tiles * 8;
+  a.part_o = w.part_o;
+  a.part_ml = w.part_ml;
+  a.tickets = w.tickets;
 }
 
 template <int D, int DT>
-void kv4_launch_attend(g4_kv4* op, Kv4AttendArgs& a, cudaStream_t st) {
+void kv4_launch_attend(const Kv4Work& op, Kv4AttendArgs& a, cudaStream_t st) {
   using C = Kv4Att<D, DT>;
-  const int ctas = op->sms * C::kMinCtas;
+  const int ctas = op.sms * C::kMinCtas;
   // the ring takes what shared memory the CTAs of an SM leave each other (1 KB each is the system's)
-  const int room = (op->smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
+  const int room = (op.smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
   a.stages = std::max(2, std::min(4, room / C::kTile));
   const int items = a.n_seq * a.c.kvh * a.row_tiles;
   // With items enough, or few tiles, no item is shared by many CTAs, and the last one to finish
   // joins the parts (a launch less); else the parts of a few long items are joined by a second
   // launch with CTAs enough for them.
-  a.join_inside = (long)items * kKv4Join >= ctas || cdiv(op->cfg.capacity, C::kKeys) <= kKv4Join;
+  a.join_inside = (long)items * kKv4Join >= ctas || cdiv(a.c.capacity, C::kKeys) <= kKv4Join;
   launch(kv4_attend_kernel<D, DT>, dim3(ctas), dim3(C::kThreads), C::smem(a.stages, a.n_seq), st, a);
   const int join_ctas = a.join_inside ? 0 : std::max(1, D * 2 / kKv4FinishThreads);
   const bool one = a.row_tiles == 1;  // the account of a single row tile rides along with the join
-  const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(op->cfg.capacity, 4 * kKv4Block), cdiv(8 * op->sms, items))) : 0;
+  const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(a.c.capacity, 4 * kKv4Block), cdiv(8 * op.sms, items))) : 0;
   if (join_ctas + gain_ctas)
     launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
            (size_t)a.n_seq * 20 + 16 + C::kQBytes, st, a, ctas, join_ctas);
   if (a.accumulate && !one)
-    launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(op->cfg.capacity, 64), 8 * op->sms / a.n_seq)), a.n_seq, a.c.kvh),
+    launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(a.c.capacity, 64), 8 * op.sms / a.n_seq)), a.n_seq, a.c.kvh),
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
 }
 
@@ -223,13 +215,14 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   TRY(kv4_alloc(op, &c.wide, 1, st));
   TRY(kv4_alloc(op, &c.err, 1, st));
   const bool blocks_too = kv4_block_path(op, f.max_q_len, G4_DT_BF16);
-  const size_t rows = (size_t)kv4_row_tiles(op, f.max_q_len) * 8;
-  TRY(kv4_alloc(op, &op->lse, (size_t)f.n_slots * c.kvh * (blocks_too ? (rows + kKv4M - 1) / kKv4M * kKv4M : rows), st));
-  // two partial items of every CTA, of 8 query rows each (three CTAs per SM at the most), or 128
-  const size_t part_rows = (size_t)2 * op->sms * std::max(8 * kKv4MaxCtas, blocks_too ? kKv4M : 0);
-  TRY(kv4_alloc(op, &op->part_o, part_rows * f.head_dim / 4, st));
-  TRY(kv4_alloc(op, &op->part_ml, part_rows, st));
-  TRY(kv4_alloc(op, &op->tickets, (size_t)f.n_slots * c.kvh * kv4_row_tiles(op, f.max_q_len), st));
+  const int group = f.num_q_heads / f.num_kv_heads;
+  const size_t lse = kv4_work_lse(f.n_slots, c.kvh, group, f.max_q_len), lse_blocks = (size_t)f.n_slots * c.kvh * cdiv(f.max_q_len * group, kKv4M) * kKv4M;
+  TRY(kv4_alloc(op, &op->work.lse, blocks_too ? std::max(lse, lse_blocks) : lse, st));
+  // two partial items of every CTA, of 8 query rows each, or 128
+  const size_t part_rows = std::max(kv4_work_part_rows(op->work.sms), blocks_too ? (size_t)2 * op->work.sms * kKv4M : 0);
+  TRY(kv4_alloc(op, &op->work.part_o, part_rows * f.head_dim / 4, st));
+  TRY(kv4_alloc(op, &op->work.part_ml, part_rows, st));
+  TRY(kv4_alloc(op, &op->work.tickets, kv4_work_tickets(f.n_slots, c.kvh, group, f.max_q_len), st));
   if (f.track) {
     TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
     TRY(kv4_alloc(op, &c.weight, blocks * kKv4Block, st));
@@ -243,6 +236,53 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
 }
 
 }  // namespace
+
+// ------------------------------------------------------------------ for the decode step
+namespace g4 {
+
+void kv4_init(int device, int smem_optin) {
+  std::lock_guard<std::mutex> lk(g_kv4_mu);
+  if (!g_kv4_devices.insert(device).second) return;
+  kv4_attrs_d<64>(smem_optin);
+  kv4_attrs_d<128>(smem_optin);
+  kv4_attrs_d<256>(smem_optin);
+  kv4_attrs_d<512>(smem_optin);
+  kv4_attrs_block<64>(smem_optin);
+  kv4_attrs_block<128>(smem_optin);
+  kv4_attrs_block<256>(smem_optin);
+  carve_max(kv4_account_kernel);
+  set_max_dyn(kv4_select_kernel, smem_optin);
+  cudaGetLastError();
+}
+
+size_t kv4_work_lse(int n_seq, int kvh, int group, int q_len) { return (size_t)n_seq * kvh * cdiv(q_len * group, 8) * 8; }
+size_t kv4_work_part_rows(int sms) { return (size_t)2 * sms * 8 * kKv4MaxCtas; }
+size_t kv4_work_tickets(int n_seq, int kvh, int group, int q_len) { return (size_t)n_seq * kvh * cdiv(q_len * group, 8); }
+size_t kv4_cache_bytes(size_t blocks, int kvh, int head_dim) { return blocks * kvh * 18 * head_dim; }
+
+void kv4_step_rows(const Kv4Cache& c, const Kv4Step& a, int n, cudaStream_t st) {
+  KV4_DISPATCH(c.d, launch(kv4_step_kernel<D>, dim3(a.nq + (a.own ? 1 : 0), n), dim3(32), 0, st, c, a));
+}
+
+void kv4_step_attend(const Kv4Cache& c, const Kv4Work& w, int n, const int* slots, const int* lens, int nq, float scale,
+                     int window, float* q, float* out, int out_stride, cudaStream_t st) {
+  Kv4AttendArgs a{};
+  a.c = c;
+  a.slots = slots;
+  a.lens = lens;
+  a.n_seq = n;
+  a.q_len = 1;
+  a.heads = a.group = nq;
+  a.row_tiles = cdiv(nq, 8);
+  a.scale = (float)((double)scale * 1.4426950408889634);
+  a.window = window;
+  a.q = Kv4Dense{q, (long)nq * c.d, (long)nq * c.d, c.d, G4_DT_F32, 2};
+  a.out = Kv4Dense{out, out_stride, out_stride, c.d, G4_DT_F32, out_stride % 8 == 0 ? 2 : 0};
+  kv4_use(w, a);
+  KV4_DISPATCH(c.d, (kv4_launch_attend<D, G4_DT_F32>(w, a, st)));
+}
+
+}  // namespace g4
 
 extern "C" {
 
@@ -269,10 +309,10 @@ g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_p
   op->device = device;
   g4_status s = G4_ERR_CUDA;
   cudaStream_t st = nullptr;
-  if (cuda_ok(cudaDeviceGetAttribute(&op->sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
-      cuda_ok(cudaDeviceGetAttribute(&op->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "cudaDeviceGetAttribute") &&
+  if (cuda_ok(cudaDeviceGetAttribute(&op->work.sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
+      cuda_ok(cudaDeviceGetAttribute(&op->work.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
-    kv4_init(device, op->smem_optin);
+    kv4_init(device, op->work.smem_optin);
     s = kv4_create_impl(op, d_page_table, st);
     if (!cuda_ok(cudaStreamSynchronize(st), "cudaStreamSynchronize") && s == G4_OK) s = G4_ERR_CUDA;
     cudaStreamDestroy(st);
@@ -391,20 +431,16 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.window = window;
   a.accumulate = accumulate != 0;
   a.zero_rest = zero_rest != 0;
-  a.lse = op->lse;
-  a.lse_rows = a.row_tiles * 8;
-  a.part_o = op->part_o;
-  a.part_ml = op->part_ml;
-  a.tickets = op->tickets;
+  kv4_use(op->work, a);
   // (a few hundred sequences' spans no longer fit beside the operands of a 256-wide head)
-  if (kv4_block_path(op, q_len, q->dtype) && (int)Kv4Blk<256, false>::smem(n_seq) <= op->smem_optin) {
+  if (kv4_block_path(op, q_len, q->dtype) && (int)Kv4Blk<256, false>::smem(n_seq) <= op->work.smem_optin) {
     switch (op->c.d) {
-      case 64: kv4_launch_block<64>(op, a, st); break;
-      case 128: kv4_launch_block<128>(op, a, st); break;
-      default: kv4_launch_block<256>(op, a, st); break;
+      case 64: kv4_launch_block<64>(op->work, a, st); break;
+      case 128: kv4_launch_block<128>(op->work, a, st); break;
+      default: kv4_launch_block<256>(op->work, a, st); break;
     }
   } else {
-    KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op, a, st))));
+    KV4_DISPATCH(op->c.d, KV4_DISPATCH_TYPE(q->dtype, (kv4_launch_attend<D, DT>(op->work, a, st))));
   }
   CK(cudaGetLastError());
   return G4_OK;
@@ -429,12 +465,12 @@ g4_status g4_kv4_evict(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_
   a.movers = op->movers;
   a.n_moves = op->n_moves;
   a.most = kv4_most_moves(op);
-  a.smem_rows = std::min(op->cfg.capacity, (op->smem_optin - 4096) / 4);
+  a.smem_rows = std::min(op->cfg.capacity, (op->work.smem_optin - 4096) / 4);
   launch(kv4_select_kernel, dim3(n_seq, op->c.kvh), dim3(kKv4EvictThreads), (size_t)a.smem_rows * 4, st, a);
   const int per = kKv4RowThreads / (op->c.d / 8);  // moves of a CTA at a time
   const int most = std::min(budget, op->cfg.capacity - budget);
   if (most > 0)
-    KV4_DISPATCH(op->c.d, launch(kv4_move_kernel<D>, dim3(std::min(cdiv(most, per), std::max(1, cdiv(8 * op->sms, n_seq * op->c.kvh))), n_seq, op->c.kvh),
+    KV4_DISPATCH(op->c.d, launch(kv4_move_kernel<D>, dim3(std::min(cdiv(most, per), std::max(1, cdiv(8 * op->work.sms, n_seq * op->c.kvh))), n_seq, op->c.kvh),
                                  dim3(kKv4RowThreads), 0, st, a));
   CK(cudaGetLastError());
   return G4_OK;

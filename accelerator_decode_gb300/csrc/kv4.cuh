@@ -13,6 +13,7 @@
 #include <limits.h>
 
 #include "common.cuh"
+#include "kv4_host.h"
 #include "kv4_layout.h"
 
 namespace g4 {
@@ -433,6 +434,95 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_account_kernel(const Kv4Ro
   const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
   if (a.positions_out) a.positions_out[at] = b < 0 ? 0 : __ldcg(a.c.pos + b * kKv4Block + row % kKv4Block);
   if (a.weights_out) a.weights_out[at] = b < 0 ? 0.f : __ldcg(a.c.weight + b * kKv4Block + row % kKv4Block);
+}
+
+// ------------------------------------------------------------------ the step's rows
+// A warp per query head, and one more for the new key and value: norm and RoPE as the decode
+// step's other caches apply them (number lane + 32 e of a row in register e, so a group of 32 is
+// one register across the warp).
+template <int D>
+__global__ void __launch_bounds__(32) kv4_step_kernel(const Kv4Cache c, const Kv4Step a) {
+  using O = Kv4Off<D>;
+  __shared__ uint8_t code_s[2][D];
+  const int unit = blockIdx.x, i = blockIdx.y, lane = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int p = __ldcg(a.positions + i), slot = __ldcg(a.slots + i);
+  const bool ok = p >= 0 && p < c.capacity && slot >= 0 && slot < c.n_slots;
+  if (unit == 0 && lane == 0) {
+    if (p < 0 || p >= c.capacity) set_err(c.err, G4_DEV_BAD_POSITION);
+    if (slot < 0 || slot >= c.n_slots) set_err(c.err, G4_DEV_BAD_SLOT);
+    a.lens[i] = ok ? p + 1 : 0;
+  }
+  if (!ok) return;
+  const float* raw = a.qkv + (size_t)i * a.qkv_stride + (size_t)unit * D;  // unit nq: the key, the value behind it
+  const bool key = unit == a.nq;
+  float x[D / 32], v[D / 32], cs[D / 64], sn[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) {
+    x[e] = __ldcg(raw + lane + 32 * e);
+    if (key) v[e] = __ldcg(raw + D + lane + 32 * e);
+  }
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    cs[e] = __ldg(a.rope_cos + (size_t)p * (D / 2) + lane + 32 * e);
+    sn[e] = __ldg(a.rope_sin + (size_t)p * (D / 2) + lane + 32 * e);
+  }
+  const __nv_bfloat16* gain = key ? a.g_k : a.g_q;
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) ss += x[e] * x[e];
+  const float den = rms_denom(warp_sum(ss), D, a.eps);
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) x[e] = (x[e] / den) * bf16f(gain[lane + 32 * e]);
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {  // RoPE pairs number i with i + D/2
+    const float u = x[e], w = x[e + D / 64];
+    x[e] = u * cs[e] - w * sn[e];
+    x[e + D / 64] = w * cs[e] + u * sn[e];
+  }
+  if (!key) {
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) a.q[((size_t)i * a.nq + unit) * D + lane + 32 * e] = x[e];
+    return;
+  }
+  const long b = kv4_block(c, slot, 0, p / kKv4Block);
+  if (b < 0) {
+    if (lane == 0) set_err(c.err, G4_DEV_BAD_POSITION);
+    return;
+  }
+  uint8_t* blk = c.data + (size_t)b * O::kBlock;
+  const int r = p % kKv4Block;
+  bool odd_value = false, wide = false;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      float y = kv ? v[e] : x[e];
+      if (!(fabsf(y) <= 3.402823466e38f)) {
+        odd_value = true;
+        y = y != y ? 0.f : copysignf(3.402823466e38f, y);
+      }
+      const __nv_bfloat16 sb = kv4_scale(warp_max(fabsf(y)));
+      const Kv4Coder code(sb);
+      wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
+      code_s[kv][lane + 32 * e] = (uint8_t)((code(y) ^ 8u) & 15u);
+      if (lane == 0) *reinterpret_cast<__nv_bfloat16*>(blk + (kv ? O::v_scale(r, e) : O::k_scale(r, e))) = sb;
+    }
+  }
+  __syncwarp();
+  for (int o = lane; o < D / 8; o += 32) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= (uint32_t)code_s[0][8 * o + e] << ((e >> 1) * 4 + (e & 1) * 16);
+    *reinterpret_cast<uint32_t*>(blk + O::k_word(r, o)) = w;
+  }
+  for (int u = lane; u < D / 4; u += 32) {
+    const uint8_t* n = code_s[1] + 4 * u;
+    *reinterpret_cast<uint16_t*>(blk + O::v_half(r, u)) = (uint16_t)(n[0] | (n[1] << 4) | (n[2] << 8) | (n[3] << 12));
+  }
+  if (odd_value) set_err(c.err, G4_DEV_BAD_VALUE);
+  if (wide) *c.wide = 1;
 }
 
 // ---------------------------------------------------------------------- whole blocks

@@ -23,6 +23,7 @@ G4_BF16 = 0
 G4_W4A16 = 1
 G4_KV_BF16 = 0
 G4_KV_INT8 = 1
+G4_KV_INT4 = 2
 G4_DEV_BAD_TOKEN = 1
 G4_DEV_BAD_POSITION = 2
 G4_DEV_TIMEOUT = 4
@@ -158,7 +159,7 @@ def check(status, where):
 def make_config(cfg, weight_format, max_batch, max_context, kv_format="bf16", kv_page_size=0, kv_pages=0,
                 table_format="bf16"):
     c = g4_config()
-    c.kv_format = G4_KV_INT8 if kv_format == "int8" else G4_KV_BF16
+    c.kv_format = {"int8": G4_KV_INT8, "int4": G4_KV_INT4}.get(kv_format, G4_KV_BF16)
     c.kv_page_size = int(kv_page_size)
     c.kv_pages = int(kv_pages)
     c.table_format = G4_W4A16 if table_format == "w4a16" else G4_BF16

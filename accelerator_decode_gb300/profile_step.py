@@ -28,7 +28,7 @@ def main(argv=None):
     ap.add_argument("--config", default="e2b-v8k", choices=sorted(synth.CONFIGS))
     ap.add_argument("--fmt", default="w4a16", choices=["bf16", "w4a16"])
     ap.add_argument("--tables", default="bf16", choices=["bf16", "int4"])
-    ap.add_argument("--kv", default="bf16", choices=["bf16", "int8"])
+    ap.add_argument("--kv", default="bf16", choices=["bf16", "int8", "int4"])
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--position", type=int, default=128)
     ap.add_argument("--steps", type=int, default=3)

@@ -29,7 +29,7 @@ def stream_handle(stream=None):
 
 class Decoder:
     """One libg4 handle.  `weights` is a host weight dict in the canonical format (synth).
-    kv_format "bf16" or "int8" (cache rows); kv_page_size 0 (static rows) or a power of two
+    kv_format "bf16", "int8" or "int4" (cache rows); kv_page_size 0 (static rows) or a power of two
     (paged cache of kv_pages pages, 0 = as many as static rows would take).  Vocabulary
     tables given as int4 dicts (packed, scales) select the int4 table format."""
 

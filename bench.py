@@ -95,7 +95,7 @@ def algorithmic_bytes(cfg, fmt, batch, positions, count_aliased=False, tables="b
     per_w = 0.5 + 2.0 / 32 if fmt == "w4a16" else 2.0
     t4 = tables == "int4"
     wbytes = n_lin * per_w + (V * H * (0.5 + 2.0 / 32) if t4 else V * H * 2)
-    row = (lambda d: d + 4) if kv == "int8" else (lambda d: 2 * d)   # bytes of one cache row
+    row = {"int8": lambda d: d + 4, "int4": lambda d: d // 2 + d // 16}.get(kv, lambda d: 2 * d)  # bytes of a cache row
     kv = []
     for p in positions:
         T = p + 1
@@ -612,7 +612,7 @@ def main(argv=None):
                     help="skip the companion figures (batch 64, bf16, int4 tables + int8 cache)")
     ap.add_argument("--no-companions", dest="companions", action="store_false",
                     help="keep the batch-64 figure, skip the bf16 and int4-table / int8-cache ones")
-    ap.add_argument("--kv", default="bf16", choices=["bf16", "int8"], help="KV cache rows (default bf16)")
+    ap.add_argument("--kv", default="bf16", choices=["bf16", "int8", "int4"], help="KV cache rows (default bf16)")
     ap.add_argument("--impl-check-only", action="store_true", help=argparse.SUPPRESS)
     args = ap.parse_args(argv)
     if args.warmup < 3:

@@ -52,9 +52,10 @@ typedef enum g4_status {
 } g4_status;
 
 enum { G4_BF16 = 0, G4_W4A16 = 1 };
-/* KV cache row formats: bf16 values, or int8 codes with one fp32 scale per row ("One TPU
- * chip, eight agents", Measured: the raw JAX decode kernel, int8 KV cache). */
-enum { G4_KV_BF16 = 0, G4_KV_INT8 = 1 };
+/* KV cache row formats: bf16 values, int8 codes with one fp32 scale per row ("One TPU
+ * chip, eight agents", Measured: the raw JAX decode kernel, int8 KV cache), or int4 codes with
+ * one bf16 scale per 32 values (the linears' convention; see g4_kv4 below). */
+enum { G4_KV_BF16 = 0, G4_KV_INT8 = 1, G4_KV_INT4 = 2 };
 
 /* Device error word bits (g4_get_device_error). */
 enum {
@@ -82,8 +83,10 @@ typedef struct g4_config {
   int32_t group_size;    /* 32 */
   float rms_eps, rope_theta_sliding, rope_theta_full;
   float attn_scale_sliding, attn_scale_full; /* 0 => 1/sqrt(head_dim) */
-  /* KV cache.  kv_format: G4_KV_BF16 or G4_KV_INT8 (row r of d values -> a = max|r|,
-   * s = a / 127, c = round-half-even(r / s) clipped to +-127, stored value c * s).
+  /* KV cache.  kv_format: G4_KV_BF16, G4_KV_INT8 (row r of d values -> a = max|r|,
+   * s = a / 127, c = round-half-even(r / s) clipped to +-127, stored value c * s) or G4_KV_INT4
+   * (each 32 values as in g4_kv4: stored value bf16(c * s); at most 64 query heads; decode steps
+   * and prefill blocks read it with the attention of g4_kv4_attend).
    * kv_page_size: 0 = static rows (slot, position); else paged ("Six serving engines on one
    * Cloud TPU v5e chip", Step 3: page size 128), a power of two >= 16: a slot's positions
    * [k * page, (k+1) * page) live in the pool page its page table names (g4_kv_reserve).

@@ -143,6 +143,17 @@ def kv_int8_dequantize(codes, s, dtype=np.float32):
     return (codes.astype(np.float32) * s.astype(np.float32)).astype(dtype)
 
 
+def kv_int4_values(v, dtype=np.float32):
+    """The values that 4-bit K or V rows (last axis, groups of 32) hold: s = bf16(a * (1/7)) of a
+    group's largest magnitude a (1/7 and the product in fp32), c = round_half_even(v / s) clipped
+    to [-7, 7], value bf16(c * s) -- the W4A16 weights' convention.  A zero group has s = 0."""
+    v = np.asarray(v).astype(np.float32)
+    g = v.reshape(*v.shape[:-1], v.shape[-1] // 32, 32)
+    s = bf16_round(np.max(np.abs(g), axis=-1, keepdims=True) * (np.float32(1) / np.float32(7))).astype(np.float64)
+    c = np.clip(np.rint(g / np.where(s > 0, s, 1.0)), -7, 7)
+    return bf16_round(c * s).reshape(v.shape).astype(dtype)
+
+
 # ----------------------------------------------------------------------------------------
 # Elementwise pieces
 # ----------------------------------------------------------------------------------------
@@ -278,11 +289,13 @@ def param_counts(cfg):
 
 def kv_bytes_per_token(cfg, copy_to_every_layer=False, kv_dtype="bf16"):
     """K+V bytes per token: one KV head per layer that keeps a cache; bf16 values, or int8
-    codes plus one fp32 scale per row."""
+    codes plus one fp32 scale per row, or int4 codes plus one bf16 scale per 32 values."""
     own = owns_kv(cfg)
     layers = range(cfg["num_layers"]) if copy_to_every_layer else [l for l in range(cfg["num_layers"]) if own[l]]
     if kv_dtype == "int8":
         return sum(2 * cfg["num_kv_heads"] * (head_dim(cfg, l) + 4) for l in layers)
+    if kv_dtype == "int4":
+        return sum(2 * cfg["num_kv_heads"] * (head_dim(cfg, l) // 2 + head_dim(cfg, l) // 16) for l in layers)
     assert kv_dtype == "bf16"
     return sum(2 * 2 * cfg["num_kv_heads"] * head_dim(cfg, l) for l in layers)
 
@@ -298,13 +311,13 @@ def int4_table_bytes(n_rows, n_cols, group):
 
 
 class Oracle:
-    """Greedy decoder over a per-sequence static KV cache (bf16 or int8 K/V, one KV head).
+    """Greedy decoder over a per-sequence static KV cache (bf16, int8 or int4 K/V, one KV head).
 
     Per token id t at position p [P3, Steps 3-5; P5, The engine]:
       x = E[t] * sqrt(H)
       tok = T_ple[t] * sqrt(P); pr = RMSNorm((W_pmp x) * H^-1/2 per P-chunk); ple = (pr + tok) / sqrt 2
       per layer l: h = RMSNorm(x); q = RoPE(RMSNorm_head(W_q h)); K/V-owning layers store
-        RoPE(RMSNorm_head(W_k h)) and W_v h at slot p, as bf16 or as int8 rows (kv_dtype);
+        RoPE(RMSNorm_head(W_k h)) and W_v h at slot p, as bf16, int8 or int4 rows (kv_dtype);
         E and T_ple are bf16 tables or int4 tables dequantised on use; attention over the visible
         keys of the source layer's cache; x += RMSNorm(W_o o);
         m = RMSNorm(x); x += RMSNorm(W_d (gelu(W_g m) * (W_u m)));
@@ -314,7 +327,7 @@ class Oracle:
 
     def __init__(self, cfg, weights, max_batch=1, max_context=None, dtype=np.float32,
                  workers=None, kv_dtype="bf16"):
-        assert kv_dtype in ("bf16", "int8")
+        assert kv_dtype in ("bf16", "int8", "int4")
         self.kv_dtype = kv_dtype
         self.cfg = cfg
         self.dtype = dt = np.dtype(dtype)
@@ -412,7 +425,9 @@ class Oracle:
         return q, self._stored(k), self._stored(v)
 
     def _stored(self, r):
-        """The value a cache row holds: bf16(r), or its int8 code times its scale."""
+        """The value a cache row holds: bf16(r), or its int8 or int4 code times its scale."""
+        if self.kv_dtype == "int4":
+            return kv_int4_values(r, self.dtype)
         if self.kv_dtype == "int8":
             return kv_int8_dequantize(*kv_int8_quantize(r), dtype=self.dtype)
         return bf16_round(r)
