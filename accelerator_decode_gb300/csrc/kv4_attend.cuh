@@ -99,7 +99,10 @@ struct Kv4Att {
   static constexpr int kNB = kBpw;                     // blocks a warp takes through the softmax at a time
   static constexpr int kKeys = kBlocks * kKv4Block;    // keys of a tile: 256, 128, 64, 64
   static constexpr int kTile = kBlocks * 18 * D;       // bytes of a tile: 18 KB (D = 512: 36 KB)
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  // D = 512: the first consumer warp fills the ring as well.  A ninth warp would put three on one
+  // scheduler and so leave 168 registers a thread, and the 128 of the output would spill.
+  static constexpr bool kOwnProducer = D != 512;
+  static constexpr int kThreads = 32 * (kWarps + (kOwnProducer ? 1 : 0));
   static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
   static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
@@ -324,34 +327,44 @@ __device__ __forceinline__ void kv4_join_ml(const Kv4AttendArgs& a, int t0, int 
   }
   named_bar_sync(bar, 32 * warps);
 }
-// The item's output rows from its parts, in span order (c1 < c0: zeros); entries e0, e0 + step, ..
+// The item's output rows from its parts, in span order; entries e0, e0 + step, ..  Eight parts'
+// loads are in flight at a time (one after the other they cost a round trip each: 12,000 cycles
+// for four parts of a 256-wide item).
 template <int D>
 __device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, int head, int row0, int n_rows, int t0,
                                               int span, int c0, int c1, const float2* ml, int e0, int step) {
   constexpr int W = D / 32;
   for (int e = e0; e < W * 64; e += step) {
     const int l = e & 31, r8 = 2 * (l & 3) + ((e >> 5) & 1), w = e >> 6, row = row0 + r8;
-    if (row >= n_rows) continue;
+    const float M = ml[r8].x, Z = M == -INFINITY ? 0.f : M, L = ml[r8].y, inv = L != 0.f ? 1.f / L : 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float inv = 0.f;
-    if (c0 <= c1) {
-      const float M = ml[r8].x, Z = M == -INFINITY ? 0.f : M, L = ml[r8].y;
-      inv = L != 0.f ? 1.f / L : 0.f;
-#pragma unroll 8
-      for (int c = c0; c <= c1; ++c) {
-        const long p = kv4_part(c, t0, span);
-        const float mc = __ldcg(&a.part_ml[p * 8 + r8].x);
-        const float4 u = __ldcg(&a.part_o[p * W * 64 + e]);
-        const float f = kv4_exp2(mc - Z);
-        v.x += f * u.x;
-        v.y += f * u.y;
-        v.z += f * u.z;
-        v.w += f * u.w;
+    for (int cb = c0; cb <= c1; cb += 8) {
+      float4 u[8];
+      float f[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (cb + q <= c1) {
+          const long p = kv4_part(cb + q, t0, span);
+          f[q] = __ldcg(&a.part_ml[p * 8 + r8].x);
+          u[q] = __ldcg(&a.part_o[p * W * 64 + e]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (cb + q <= c1) {
+          const float x = kv4_exp2(f[q] - Z);
+          v.x += x * u[q].x;
+          v.y += x * u[q].y;
+          v.z += x * u[q].z;
+          v.w += x * u[q].w;
+        }
       }
     }
-    const int tok = row / a.group, hq = head * a.group + row % a.group;
-    kv4_store4(a.out, (long)seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
-               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (row < n_rows) {
+      const int tok = row / a.group, hq = head * a.group + row % a.group;
+      kv4_store4(a.out, (long)seq * a.out.seq + (long)tok * a.out.row + (long)hq * a.out.head + (l >> 2) * (D / 8) + 4 * w,
+                 make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    }
   }
 }
 // Zeros for the query rows that no tile reaches: those of sequences without rows, and with
@@ -398,16 +411,72 @@ struct Kv4Shared {
   }
 };
 
+// The ring's filling, one tile at a time; called by a whole warp.
+template <int D, int DT>
+struct Kv4Producer {
+  using O = Kv4Off<D>;
+  using C = Kv4Att<D, DT>;
+  Kv4Run r;
+  int at, x, it, lo;
+  __device__ __forceinline__ void start(int g0) {
+    at = g0;
+    x = it = 0;
+    r.tiles = 0;
+  }
+  __device__ __forceinline__ bool more(int g1) const { return at + x < g1; }
+  // The next tile into its stage, which is free.
+  __device__ __forceinline__ void put(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, int g1) {
+    const int lane = threadIdx.x & 31;
+    if (x == r.tiles) {
+      at += x;
+      x = 0;
+      r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
+      lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
+    }
+    const int s = it % a.stages;
+    // lane b looks block b up; neighbours in the pool travel in one copy
+    const int b = (r.tile + x) * C::kBlocks + lane;
+    const bool want = lane < C::kBlocks && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
+    const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
+    if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
+    const long before = __shfl_up_sync(0xFFFFFFFFu, at_b, 1);
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
+    const uint32_t joins = __ballot_sync(0xFFFFFFFFu, at_b >= 0 && lane > 0 && before >= 0 && before == at_b - 1);
+    if (lane == 0) {
+      sh.held[s] = have;
+      mbar_expect_tx(&sh.full[s], __popc(have) * O::kBlock);
+    }
+    __syncwarp();
+    if (at_b >= 0 && !((joins >> lane) & 1)) {
+      const uint32_t after = joins >> 1 >> lane;  // ones while the next block joins
+      const int n = __ffs(~after);
+      bulk_g2s(sh.ring + (size_t)s * C::kTile + lane * O::kBlock, a.c.data + (size_t)at_b * O::kBlock, n * O::kBlock, &sh.full[s]);
+    }
+    ++x;
+    ++it;
+  }
+  // Copies in flight land before the CTA's memory goes, whatever the consumers do.
+  __device__ __forceinline__ void drain(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh) const {
+    for (int k = max(0, it - a.stages); k < it; ++k) mbar_wait_drain(&sh.full[k % a.stages], (k / a.stages) & 1);
+  }
+};
+
+// Returns the first tile of the last run.
 template <int D, int DT, bool WIDE>
-__device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, int g0, int g1,
-                                            int span) {
+__device__ __forceinline__ int kv4_consume(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, int g0, int g1) {
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
   constexpr int W = D / 32, NB = C::kNB;  // words of a key (or value pair) per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int set = warp >> 2, wq = warp & 3;
   const float score_scale = WIDE ? a.scale : a.scale * kKv4Up;
-  int it = 0, piece = 0;
+  Kv4Producer<D, DT> fill;
+  if (!C::kOwnProducer) {
+    fill.start(g0);
+    if (warp == 0)
+      while (fill.it < a.stages && fill.more(g1)) fill.put(a, sh, g1);
+  }
+  int it = 0, piece = 0, last_at = g0;
   for (int at = g0; at < g1; ++piece) {
     const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
     const int n_rows = r.m * a.group, row0 = r.row_tile * 8;
@@ -429,6 +498,24 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
     const int low_max = a.window > 0 ? r.len - r.m + min(row0 + 7, n_rows - 1) / a.group - a.window : -1;
 
     for (int x = 0; x < r.tiles; ++x, ++it) {
+      if (!C::kOwnProducer && warp == 0) {
+        // stages that their warps have left are filled again; only the tile at hand is waited for
+        while (fill.more(g1) && !*sh.abort_flag) {
+          if (fill.it >= a.stages) {
+            uint64_t* e = &sh.empty[fill.it % a.stages];
+            const uint32_t parity = (fill.it / a.stages - 1) & 1;
+            bool free_now = __any_sync(0xFFFFFFFFu, mbar_try(e, parity));
+            if (!free_now && fill.it <= it) {
+              free_now = mbar_wait(e, parity, sh.abort_flag);
+              if (!__all_sync(0xFFFFFFFFu, free_now)) *sh.abort_flag = 1;
+              __syncwarp();
+              free_now = !*sh.abort_flag;
+            }
+            if (!__all_sync(0xFFFFFFFFu, free_now)) break;
+          }
+          fill.put(a, sh, g1);
+        }
+      }
       if (C::kSets > 1 && it % C::kSets != set) continue;
       const int s = it % a.stages;
       if (!mbar_wait(&sh.full[s], (it / a.stages) & 1, sh.abort_flag)) *sh.abort_flag = 1;
@@ -615,31 +702,45 @@ __device__ __forceinline__ void kv4_consume(const Kv4AttendArgs& a, const Kv4Sha
         lse[1] = L1 != 0.f ? M1 + log2f(L1) : INFINITY;
       }
     }
-    if (a.join_inside && !whole) {
-      __threadfence();
-      named_bar_sync(1, 32 * C::kWarps);
-      const int c0 = (unsigned)r.item_t0 / (unsigned)span, c1 = (unsigned)(r.item_t0 + r.of - 1) / (unsigned)span;
-      const long item = ((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile;
-      if (threadIdx.x == 0) {
-        const bool is_last = atomicAdd(a.tickets + item, 1u) == (unsigned)(c1 - c0);
-        if (is_last) a.tickets[item] = 0;
-        *sh.last = is_last;
-      }
-      named_bar_sync(1, 32 * C::kWarps);
-      if (*sh.last) {
-        __threadfence();
-        float2* ml = reinterpret_cast<float2*>(sh.os);
-        kv4_join_ml(a, r.item_t0, span, c0, c1, threadIdx.x, C::kWarps, ml, 1);
-        if (threadIdx.x < 8) a.lse[item * 8 + threadIdx.x] = kv4_lse(ml[threadIdx.x]);
-        kv4_join_rows<D>(a, r.seq, r.head, row0, n_rows, r.item_t0, span, c0, c1, ml, threadIdx.x, 32 * C::kWarps);
-      }
-    }
+    last_at = at - r.tiles;
   }
+  if (!C::kOwnProducer && warp == 0) fill.drain(a, sh);
   if (*sh.abort_flag && threadIdx.x == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+  return last_at;
+}
+
+// The shared items that a CTA's span begins and ends with: the CTA that finishes its part of an
+// item last joins all of them.  After the span, so that nothing of it weighs on the loop's
+// registers.
+template <int D, int DT>
+__device__ __forceinline__ void kv4_join_span(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, int g0, int g1, int last_at, int span) {
+  using C = Kv4Att<D, DT>;
+  if (g0 >= g1) return;
+  __threadfence();
+#pragma unroll 1
+  for (int k = 0; k < (last_at > g0 ? 2 : 1); ++k) {
+    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, k ? last_at : g0, g1);
+    if (r.whole) continue;
+    const int c0 = (unsigned)r.item_t0 / (unsigned)span, c1 = (unsigned)(r.item_t0 + r.of - 1) / (unsigned)span;
+    const long item = ((long)r.seq * a.c.kvh + r.head) * a.row_tiles + r.row_tile;
+    named_bar_sync(1, 32 * C::kWarps);  // every thread's sums are out
+    if (threadIdx.x == 0) {
+      const bool is_last = atomicAdd(a.tickets + item, 1u) == (unsigned)(c1 - c0);
+      if (is_last) a.tickets[item] = 0;
+      *sh.last = is_last;
+    }
+    named_bar_sync(1, 32 * C::kWarps);
+    if (!*sh.last) continue;
+    __threadfence();
+    float2* ml = reinterpret_cast<float2*>(sh.os);
+    kv4_join_ml(a, r.item_t0, span, c0, c1, threadIdx.x, C::kWarps, ml, 1);
+    if (threadIdx.x < 8) a.lse[item * 8 + threadIdx.x] = kv4_lse(ml[threadIdx.x]);
+    kv4_join_rows<D>(a, r.seq, r.head, r.row_tile * 8, r.m * a.group, r.item_t0, span, c0, c1, ml, threadIdx.x, 32 * C::kWarps);
+  }
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCtas) kv4_attend_kernel(const Kv4AttendArgs a) {
+__global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCtas) kv4_attend_kernel(const __grid_constant__ Kv4AttendArgs a) {
   using O = Kv4Off<D>;
   using C = Kv4Att<D, DT>;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
@@ -661,52 +762,27 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   const int span = kv4_span(a, sh.first, gridDim.x);
   const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
   if (warp < C::kWarps) {
-    if (wide) kv4_consume<D, DT, true>(a, sh, g0, g1, span);
-    else kv4_consume<D, DT, false>(a, sh, g0, g1, span);
-    if (a.join_inside)
+    const int last_at = wide ? kv4_consume<D, DT, true>(a, sh, g0, g1) : kv4_consume<D, DT, false>(a, sh, g0, g1);
+    if (a.join_inside) {
+      kv4_join_span<D, DT>(a, sh, g0, g1, last_at, span);
       kv4_zero_rows<D>(a, sh.first, sh.seqs, blockIdx.x, gridDim.x, threadIdx.x, 32 * C::kWarps);
+    }
     return;
   }
   // ---- producer: tiles into the ring
-  int it = 0;
-  bool stop = false;
-  for (int at = g0; at < g1 && !stop;) {
-    const Kv4Run r = kv4_run<C::kKeys>(a, sh.first, sh.seqs, at, g1);
-    const int lo = a.window > 0 ? max(0, r.len - r.m + 1 - a.window) : 0;
-    for (int x = 0; x < r.tiles; ++x, ++it) {
-      const int s = it % a.stages;
-      if (it >= a.stages && !mbar_wait(&sh.empty[s], (it / a.stages - 1) & 1, sh.abort_flag)) {
-        stop = true;
-        break;
-      }
-      // lane b looks block b up; neighbours in the pool travel in one copy
-      const int b = (r.tile + x) * C::kBlocks + lane;
-      const bool want = lane < C::kBlocks && b * kKv4Block < r.len && b * kKv4Block + kKv4Block > lo;
-      const long at_b = want ? kv4_block(a.c, r.slot, r.head, b) : -2;
-      if (at_b == -1) set_err(a.c.err, G4_DEV_BAD_POSITION);
-      const long before = __shfl_up_sync(0xFFFFFFFFu, at_b, 1);
-      const uint32_t have = __ballot_sync(0xFFFFFFFFu, at_b >= 0);
-      const uint32_t joins = __ballot_sync(0xFFFFFFFFu, at_b >= 0 && lane > 0 && before >= 0 && before == at_b - 1);
-      if (lane == 0) {
-        sh.held[s] = have;
-        mbar_expect_tx(&sh.full[s], __popc(have) * O::kBlock);
-      }
-      __syncwarp();
-      if (at_b >= 0 && !((joins >> lane) & 1)) {
-        const uint32_t after = joins >> 1 >> lane;  // ones while the next block joins
-        const int n = __ffs(~after);
-        bulk_g2s(sh.ring + (size_t)s * C::kTile + lane * O::kBlock, a.c.data + (size_t)at_b * O::kBlock, n * O::kBlock,
-                 &sh.full[s]);
-      }
+  Kv4Producer<D, DT> fill;
+  fill.start(g0);
+  while (fill.more(g1)) {
+    const int s = fill.it % a.stages;
+    if (fill.it >= a.stages && !mbar_wait(&sh.empty[s], (fill.it / a.stages - 1) & 1, sh.abort_flag)) {
+      if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
+      *sh.abort_flag = 1;
+      break;
     }
-    at += r.tiles;
+    __syncwarp();
+    fill.put(a, sh, g1);
   }
-  if (stop) {
-    if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
-    *sh.abort_flag = 1;
-  }
-  // copies in flight land before the CTA's memory goes, whatever the consumers do
-  for (int k = max(0, it - a.stages); k < it; ++k) mbar_wait_drain(&sh.full[k % a.stages], (k / a.stages) & 1);
+  fill.drain(a, sh);
 }
 
 // -------------------------------------------------------------------------- the finish
@@ -761,7 +837,7 @@ __device__ __forceinline__ void kv4_add_gain(const Kv4AttendArgs& a, long at, in
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4AttendArgs a, int ctas, int join_ctas) {
+__global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const __grid_constant__ Kv4AttendArgs a, int ctas, int join_ctas) {
   using C = Kv4Att<D, DT>;
   using O = Kv4Off<D>;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
@@ -827,7 +903,7 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const Kv4
 constexpr int kKv4GainWarps = 4;
 
 template <int D, int DT>
-__global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const Kv4AttendArgs a) {
+__global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const __grid_constant__ Kv4AttendArgs a) {
   using O = Kv4Off<D>;
   extern __shared__ __align__(128) uint8_t kv4_smem[];
   uint4* qs = reinterpret_cast<uint4*>(kv4_smem);

@@ -299,7 +299,7 @@ __device__ __forceinline__ Kv4Run kv4_block_run(const Kv4AttendArgs& a, const in
 }
 
 template <int D, bool ACCOUNT>
-__global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv4AttendArgs a) {
+__global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __grid_constant__ Kv4AttendArgs a) {
   using C = Kv4Blk<D, ACCOUNT>;
   using O = Kv4Off<D>;
   extern __shared__ __align__(16) uint8_t kv4_raw[];
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const Kv
 // Joins the parts of shared items, in span order: a thread per row of item blockIdx.x and 16
 // numbers of it, blockIdx.y counting those.  Also the zeros of rows that no tile reaches.
 template <int D>
-__global__ void __launch_bounds__(128) kv4_block_join_kernel(const Kv4AttendArgs a, int ctas) {
+__global__ void __launch_bounds__(128) kv4_block_join_kernel(const __grid_constant__ Kv4AttendArgs a, int ctas) {
   extern __shared__ __align__(16) uint8_t kv4_raw[];
   int4* seqs = reinterpret_cast<int4*>(kv4_raw);
   int* first = reinterpret_cast<int*>(seqs + a.n_seq);
