@@ -106,7 +106,8 @@ struct Kv4Att {
   static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
   static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
-  static constexpr int kOBytes = 4 * D * 32;           // four warps' sums, [warp][D / 32][2][lane] float4
+  static constexpr int kRegions = D >= 256 ? 4 : 2;    // warps whose sums fit in shared memory at a time
+  static constexpr int kOBytes = kRegions * D * 32;    // [region][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
     return (size_t)stages * kTile + kFixed + (size_t)n_seq * 20 + 16;
@@ -297,6 +298,35 @@ __device__ __forceinline__ void kv4_scores(const uint4* qs, int lane, Codes code
     for (int j = 0; j < 4; ++j) c[b][j] += d[b][j];
 }
 
+// What the warps of a CTA share.
+template <int D, int DT>
+struct Kv4Shared {
+  uint8_t* ring;
+  uint4* qs;
+  float4* os;
+  float2* mls;        // [warp][8]
+  uint64_t *full, *empty;
+  uint32_t* held;     // [8]: blocks of a stage that hold rows
+  volatile int* abort_flag;
+  volatile int* last;  // this CTA joins the item
+  int4* seqs;
+  int* first;
+  __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages, int n_seq) {
+    using C = Kv4Att<D, DT>;
+    ring = smem;
+    qs = reinterpret_cast<uint4*>(ring + (size_t)stages * C::kTile);
+    os = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(qs) + C::kQBytes);
+    mls = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(os) + C::kOBytes);
+    full = reinterpret_cast<uint64_t*>(mls + C::kWarps * 8);
+    empty = full + 8;
+    held = reinterpret_cast<uint32_t*>(empty + 8);
+    abort_flag = reinterpret_cast<volatile int*>(held + 8);
+    last = abort_flag + 1;
+    seqs = reinterpret_cast<int4*>(full + 32);
+    first = reinterpret_cast<int*>(seqs + n_seq);
+  }
+};
+
 // ------------------------------------------------------------------------ joining parts
 // CTA c's part of the item that starts at tile t0: slot 0 when the item opens c's span, else 1.
 __device__ __forceinline__ long kv4_part(int c, int t0, int span) { return (long)c * 2 + (t0 > c * span ? 1 : 0); }
@@ -367,6 +397,63 @@ __device__ __forceinline__ void kv4_join_rows(const Kv4AttendArgs& a, int seq, i
     }
   }
 }
+// The same by a CTA's consumer warps once their ring is idle: the parts come through it, all in
+// flight together, and the rolled loops keep the code short.  (Code that runs once a launch costs
+// its fetching: a join unrolled over the parts was slower than one round trip after the other.)
+// Also writes the rows' lse.
+template <int D, int DT>
+__device__ __forceinline__ void kv4_join_ring(const Kv4AttendArgs& a, const Kv4Shared<D, DT>& sh, const Kv4Run& r, int span, int c0, int c1, float* lse) {
+  using C = Kv4Att<D, DT>;
+  constexpr int E = D * 2, T = 32 * C::kWarps, N = E / T;  // 16-byte entries of a part, and of a thread
+  float2* ml = reinterpret_cast<float2*>(sh.os);           // [part][8]
+  float4* buf = reinterpret_cast<float4*>(sh.ring);
+  const int tid = threadIdx.x, n = c1 - c0 + 1, cap = a.stages * C::kTile / (E * 16);
+  const int l = tid & 31, r8 = 2 * (l & 3) + ((tid >> 5) & 1);  // the same row in all of a thread's entries
+  float4 v[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, L = 0.f;
+  for (int p0 = 0; p0 < n; p0 += cap) {
+    const int np = min(cap, n - p0);
+    if (p0) named_bar_sync(1, T);
+    for (int c = 0; c < np; ++c) {
+      const float4* from = a.part_o + kv4_part(c0 + p0 + c, r.item_t0, span) * E + tid;
+#pragma unroll
+      for (int k = 0; k < N; ++k) cp_async16(buf + c * E + tid + k * T, from + k * T, true);
+    }
+    if (p0 == 0)
+      for (int c = tid >> 3; c < n; c += T / 8) ml[c * 8 + (tid & 7)] = __ldcg(&a.part_ml[kv4_part(c0 + c, r.item_t0, span) * 8 + (tid & 7)]);
+    cp_async_wait_all();
+    named_bar_sync(1, T);
+    if (p0 == 0) {
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) M = fmaxf(M, ml[c * 8 + r8].x);
+    }
+    const float Z = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+    for (int c = 0; c < np; ++c) {
+      const float2 m = ml[(p0 + c) * 8 + r8];
+      const float x = kv4_exp2(m.x - Z);
+      L += m.y * x;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float4 u = buf[c * E + tid + k * T];
+        v[k].x += x * u.x;
+        v[k].y += x * u.y;
+        v[k].z += x * u.z;
+        v[k].w += x * u.w;
+      }
+    }
+  }
+  if (tid < 64 && l < 4) lse[r8] = kv4_lse(make_float2(M, L));
+  const int row = r.row_tile * 8 + r8;
+  if (row >= r.m * a.group) return;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  const long to = (long)r.seq * a.out.seq + (long)(row / a.group) * a.out.row + (long)(r.head * a.group + row % a.group) * a.out.head;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    kv4_store4(a.out, to + (l >> 2) * (D / 8) + 4 * ((tid + k * T) >> 6), make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv));
+}
 // Zeros for the query rows that no tile reaches: those of sequences without rows, and with
 // zero_rest the padding.  Sequences i0, i0 + step, ..
 template <int D>
@@ -382,35 +469,6 @@ __device__ __forceinline__ void kv4_zero_rows(const Kv4AttendArgs& a, const int*
 }
 
 // ------------------------------------------------------------------------- the kernel
-// What the warps of a CTA share.
-template <int D, int DT>
-struct Kv4Shared {
-  uint8_t* ring;
-  uint4* qs;
-  float4* os;
-  float2* mls;        // [warp][8]
-  uint64_t *full, *empty;
-  uint32_t* held;     // [8]: blocks of a stage that hold rows
-  volatile int* abort_flag;
-  volatile int* last;  // this CTA joins the item
-  int4* seqs;
-  int* first;
-  __device__ __forceinline__ Kv4Shared(uint8_t* smem, int stages, int n_seq) {
-    using C = Kv4Att<D, DT>;
-    ring = smem;
-    qs = reinterpret_cast<uint4*>(ring + (size_t)stages * C::kTile);
-    os = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(qs) + C::kQBytes);
-    mls = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(os) + C::kOBytes);
-    full = reinterpret_cast<uint64_t*>(mls + C::kWarps * 8);
-    empty = full + 8;
-    held = reinterpret_cast<uint32_t*>(empty + 8);
-    abort_flag = reinterpret_cast<volatile int*>(held + 8);
-    last = abort_flag + 1;
-    seqs = reinterpret_cast<int4*>(full + 32);
-    first = reinterpret_cast<int*>(seqs + n_seq);
-  }
-};
-
 // The ring's filling, one tile at a time; called by a whole warp.
 template <int D, int DT>
 struct Kv4Producer {
@@ -649,7 +707,7 @@ __device__ __forceinline__ int kv4_consume(const Kv4AttendArgs& a, const Kv4Shar
 #pragma unroll
         for (int sel = 0; sel < 2; ++sel) {
           const float f = sel ? f1 : f0;
-          float4* p = &sh.os[((wq * W + w) * 2 + sel) * 32 + lane];
+          float4* p = &sh.os[(((warp % C::kRegions) * W + w) * 2 + sel) * 32 + lane];
           float4 v = make_float4(acc[2 * w][sel] * f, acc[2 * w][2 + sel] * f, acc[2 * w + 1][sel] * f, acc[2 * w + 1][2 + sel] * f);
           if (add) {
             const float4 u = *p;
@@ -661,21 +719,18 @@ __device__ __forceinline__ int kv4_consume(const Kv4AttendArgs& a, const Kv4Shar
           *p = v;
         }
     };
-    if (C::kSets > 1) {
-      if (set == 1) put(false);
+#pragma unroll
+    for (int round = C::kWarps / C::kRegions - 1; round >= 0; --round) {
+      if (warp / C::kRegions == round) put(round + 1 < C::kWarps / C::kRegions);
       named_bar_sync(1, 32 * C::kWarps);
-      if (set == 0) put(true);
-    } else {
-      put(false);
     }
-    named_bar_sync(1, 32 * C::kWarps);
     const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
     // entry e: lane l of word w: numbers (l / 4) D/8 + 4w .. of query row 2 (l % 4) + sel
     for (int e = threadIdx.x; e < W * 64; e += 32 * C::kWarps) {
       const int l = e & 31, sel = (e >> 5) & 1, w = e >> 6;
       float4 v = sh.os[e];
 #pragma unroll
-      for (int k = 1; k < 4; ++k) {
+      for (int k = 1; k < C::kRegions; ++k) {
         const float4 u = sh.os[k * W * 64 + e];
         v.x += u.x;
         v.y += u.y;
@@ -732,10 +787,7 @@ __device__ __forceinline__ void kv4_join_span(const Kv4AttendArgs& a, const Kv4S
     named_bar_sync(1, 32 * C::kWarps);
     if (!*sh.last) continue;
     __threadfence();
-    float2* ml = reinterpret_cast<float2*>(sh.os);
-    kv4_join_ml(a, r.item_t0, span, c0, c1, threadIdx.x, C::kWarps, ml, 1);
-    if (threadIdx.x < 8) a.lse[item * 8 + threadIdx.x] = kv4_lse(ml[threadIdx.x]);
-    kv4_join_rows<D>(a, r.seq, r.head, r.row_tile * 8, r.m * a.group, r.item_t0, span, c0, c1, ml, threadIdx.x, 32 * C::kWarps);
+    kv4_join_ring<D, DT>(a, sh, r, span, c0, c1, a.lse + item * 8);
   }
 }
 
