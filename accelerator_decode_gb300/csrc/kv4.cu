@@ -407,7 +407,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
                         int32_t q_len, const int32_t* d_q_lens, float scale, int32_t window, int32_t accumulate,
                         int32_t zero_rest, const g4_kv4_tensor* q, const g4_kv4_tensor* out) {
   if (!op || !d_slots || !d_lens || !q || !out || !kv4_count(op, n_seq) || q_len < 1 || q_len > op->cfg.max_q_len ||
-      window < 0 || !(scale >= 0.f) || !std::isfinite(scale) || q->dtype != out->dtype)
+      window < 0 || !(scale >= 0.f) || !std::isfinite(scale) || q->dtype != out->dtype || q->data == out->data)
     return G4_ERR_INVALID_ARG;
   Kv4AttendArgs a{};
   if (!kv4_dense(q, n_seq, q_len, op->cfg.num_q_heads, op->c.d, false, &a.q) ||
@@ -428,7 +428,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.group = a.heads / op->c.kvh;
   a.row_tiles = kv4_row_tiles(op, q_len);
   a.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)op->c.d)) * 1.4426950408889634);
-  a.window = window;
+  a.window = window < op->cfg.capacity ? window : 0;  // one that reaches every row is none
   a.accumulate = accumulate != 0;
   a.zero_rest = zero_rest != 0;
   kv4_use(op->work, a);

@@ -286,12 +286,11 @@ class KV4Cache:
         into.data, into.dtype = t.data_ptr(), code
         into.seq_stride, into.row_stride, into.head_stride = s[0], s[1], s[2]
 
-    def _fresh(self, t, into):
+    def _fresh(self, t, code, rows, heads, into):
         """Describes a contiguous result to C."""
-        into.data, into.dtype = t.data_ptr(), _KV4_TYPES[t.dtype]
-        into.head_stride = t.shape[3]
-        into.row_stride = t.shape[2] * t.shape[3]
-        into.seq_stride = t.shape[1] * into.row_stride
+        d = self.head_dim
+        into.data, into.dtype = t.data_ptr(), code
+        into.seq_stride, into.row_stride, into.head_stride = rows * heads * d, heads * d, d
 
     def _seq(self, name, t, n):
         return _kv4_array(name, t, (n,), torch.int32, self.index)
@@ -344,8 +343,8 @@ class KV4Cache:
             raise TypeError(f"rows cannot be given as {dtype}")
         args = (self._seq("slots", slots, n), self._seq("start", start, n), self._seq("counts", counts, n))
         k, v = self._empty(shape, dtype, stream), self._empty(shape, dtype, stream)
-        self._fresh(k, self._ta)
-        self._fresh(v, self._tb)
+        self._fresh(k, _KV4_TYPES[dtype], n_rows, self.num_kv_heads, self._ta)
+        self._fresh(v, _KV4_TYPES[dtype], n_rows, self.num_kv_heads, self._tb)
         status = _g4.lib.g4_kv4_read(self.h, self._stream(stream), n, *args, n_rows, 1, self._pa, self._pb)
         self._done(status, "g4_kv4_read", stream, (slots, start, counts))
         return k, v
@@ -375,7 +374,7 @@ class KV4Cache:
             self._dense("out", out, shape, self._tb)
         else:
             out = self._empty(shape, q.dtype, stream)
-            self._fresh(out, self._tb)
+            self._fresh(out, self._ta.dtype, q_len, self.num_q_heads, self._tb)
         status = _g4.lib.g4_kv4_attend(self.h, self._stream(stream), n, *args, scale, window, bool(accumulate),
                                        not given, self._pa, self._pb)
         self._done(status, "g4_kv4_attend", stream, (q, out, slots, lens, q_lens))

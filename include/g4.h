@@ -358,7 +358,8 @@ typedef struct g4_kv4_tensor {
 
 /* Make an empty cache on `device`.  d_page_table: int32 [n_slots][ceil(capacity / page_size)],
  * BORROWED (read by every call on its stream; entries outside 0 .. n_pages - 1 mean no page;
- * pages of a slot that is appended to or evicted from must be its own), NULL with page_size 0.
+ * pages of a slot that is appended to, evicted from or accumulated for must be its own), NULL
+ * with page_size 0.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes outside the bounds above), OOM, CUDA. */
 g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_page_table,
                         g4_kv4** out);
@@ -396,13 +397,13 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * token t sits at row d_lens[i] - m + t and sees rows up to its own (and with window > 0 only
  * the newest `window` of those):
  *   s_j = scale * q . K_j        o = sum_j softmax(s)_j V_j        (scale 0: 1/sqrt(head_dim))
- * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type.  A token that sees no row gets
+ * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type, sharing no element.  A token that sees no row gets
  * zeros; query rows t >= m of `out` are left as they were, or with zero_rest != 0 set to zero.  accumulate != 0 (track, window 0):
  * each row's account grows by the attention weights it received, summed over the sequence's
  * query tokens and the query heads of its KV head.  The same slot may be named twice only
  * without accumulate.  The sums run in a fixed order: equal calls give equal bits.
  * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0,
- * a scale that is negative or not finite, q and out of different types, malformed tensors), UNSUPPORTED
+ * a scale that is negative or not finite, q and out of different types or at one address, malformed tensors), UNSUPPORTED
  * (accumulate without track; a window with a cache that tracks: after an eviction its rows are
  * no longer in position order; n_seq * num_kv_heads * ceil(q_len * heads per KV head / 8) *
  * ceil(capacity / 64) at 2^31 or more). */

@@ -303,6 +303,39 @@ def test_strided_query_and_output(rt):
     fine(c)
 
 
+def test_packed_projection_and_extreme_arguments(rt):
+    """Queries, keys, values and the output as slices of one packed tensor; a window past every row;
+    scales at both ends; one sequence more than the spans of a block kernel hold."""
+    n, kvh, group, d, t = 2, 2, 3, 128, 70
+    heads = kvh * group
+    pack = rows((n, t, heads + 2 * kvh + heads, d), "bf16", 1)
+    q, k, v, out = pack[:, :, :heads], pack[:, :, heads:heads + kvh], pack[:, :, heads + kvh:heads + 2 * kvh], pack[:, :, heads + 2 * kvh:]
+    c = make(rt, n, 128, heads, kvh, d, 16)
+    c.append(k, v, i32([0, 1]), i32([0, 0]))
+    lens, slots, m = i32([t, t]), i32([0, 1]), 9
+    want = c.attend(q[:, -m:].contiguous(), slots, lens)
+    before = pack[:, :, :heads + 2 * kvh].clone()
+    c.attend(q[:, -m:], slots, lens, out=out[:, -m:])
+    assert torch.equal(out[:, -m:], want) and torch.equal(pack[:, :, :heads + 2 * kvh], before)
+    for w in (128, 1000, (1 << 31) - 1):
+        assert torch.equal(c.attend(q[:, -m:], slots, lens, window=w), want)
+    assert torch.equal(c.attend(q[:, -m:], slots, lens, window=127), want)
+    for scale in (1e-38, 1e30):
+        assert c.attend(q[:, -m:], slots, lens, scale=scale).isfinite().all() or scale > 1
+    one = c.attend(q[:, -m:], slots, lens, scale=1e-38)              # equal weights: the mean of the seen rows
+    vals = torch.from_numpy(ref.values(host(v[0])))
+    np.testing.assert_allclose(host(one[0, -1, 0]), vals[:, 0].mean(0), rtol=2.0 ** -7, atol=2.0 ** -8)
+    many = make(rt, 400, 20, 40, 1, 64)
+    kk, qq = rows((400, 3, 1, 64), "bf16", 2), rows((400, 1, 40, 64), "bf16", 3)
+    order = i32(list(range(400)))
+    many.append(kk, kk, order, i32([0] * 400))
+    whole = many.attend(qq, order, i32([3] * 400))
+    part = many.attend(qq[:100], order[:100], i32([3] * 100))
+    assert (whole[:100].float() - part.float()).abs().max() <= 2.0 ** -7 * part.float().abs().max()
+    fine(c)
+    fine(many)
+
+
 @pytest.mark.parametrize("m,dtype", [(2, "f32"), (2, "bf16"), (6, "bf16")])
 def test_not_finite_query_stays_in_its_row(rt, m, dtype):
     d, t = 128, 100
@@ -360,6 +393,12 @@ def evict_check(rt, lens, budget, recent, kvh=2, d=64, page=16, ties=False, spec
 @pytest.mark.parametrize("ties,special", [(False, False), (True, False), (False, True)])
 def test_evict(rt, lens, budget, recent, ties, special):
     evict_check(rt, lens, budget, recent, ties=ties, special=special, seed=budget)
+
+
+def test_evict_more_rows_than_shared_memory_holds(rt):
+    """60,000 rows of one head: the ranks are read anew in each pass."""
+    evict_check(rt, [60000, 58000], 30001, 700, kvh=1, d=64, page=128, seed=1)
+    evict_check(rt, [60000], 100, 3, kvh=1, d=64, page=0, ties=True, seed=2)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256, 512])
@@ -440,6 +479,7 @@ def test_refusals(rt):
     refused(bad, c.attend, q, s, l, out=torch.empty(2, 2, 4, d, dtype=torch.bfloat16, device="cuda"))
     refused(bad, c.attend, q, s, l, out=torch.empty(2, 2, 1, d, device="cuda").expand(2, 2, 4, d))
     refused(bad, c.attend, rows((2, 5, 4, d), "f32", 2), s, l)
+    refused(bad, c.attend, q, s, l, out=q)
     refused(bad, c.read, s, z, 33)
     refused(bad, c.read, s, z, 0)
     refused(bad, t.evict, s, l, 0)
