@@ -182,6 +182,14 @@ void kv4_launch_attend(const Kv4Work& op, Kv4AttendArgs& a, cudaStream_t st) {
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);
 }
 
+// Whether rows go by whole blocks (a warp each) or by octets (a thread each): by blocks from
+// per_sm blocks per SM on, where the octets' scattered accesses cost more than the blocks' longer
+// chains.  Measured (D = 256, fp32; microseconds by blocks / by octets): append of 104 blocks 9.3 /
+// 5.2, 320: 10.0 / 9.3, 416: 10.3 / 10.4, 1,280: 16.8 / 23.2, 4,096: 36 / 66; read of 32: 3.6 / 3.1,
+// 104: 3.6 / 3.6, 320: 4.2 / 5.7, 4,096: 15 / 32.
+bool kv4_by_blocks(const g4_kv4* op, int n_seq, int n_rows, int per_sm) {
+  return n_rows >= kKv4Block && (long)n_seq * op->cfg.num_kv_heads * cdiv(n_rows, kKv4Block) >= (long)per_sm * op->work.sms;
+}
 // Whole-block kernels: every block that n_rows rows from any row on can touch.
 dim3 kv4_block_grid(const g4_kv4* op, int n_seq, int n_rows) {
   const long units = ((long)(n_rows + 2 * kKv4Block - 2) / kKv4Block) * op->cfg.num_kv_heads;
@@ -345,7 +353,7 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.positions = d_positions;
   a.weights = d_weights;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (n_rows >= kKv4Block) {
+  if (kv4_by_blocks(op, n_seq, n_rows, 3)) {
     KV4_DISPATCH(op->c.d, launch(kv4_append_blocks_kernel<D>, kv4_block_grid(op, n_seq, n_rows), dim3(32 * kKv4BlockWarps), 0, st, a));
   } else {
     KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0, st, a));
@@ -371,7 +379,7 @@ g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t
   a.n_rows = n_rows;
   a.zero_rest = zero_rest != 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (n_rows >= kKv4Block) {
+  if (kv4_by_blocks(op, n_seq, n_rows, 1)) {
     KV4_DISPATCH(op->c.d, launch(kv4_read_blocks_kernel<D>, kv4_block_grid(op, n_seq, n_rows), dim3(32 * kKv4BlockWarps), 0, st, a));
   } else {
     KV4_DISPATCH(op->c.d, launch(kv4_read_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0, st, a));

@@ -182,36 +182,58 @@ __device__ __forceinline__ __nv_bfloat16 kv4_scale(float amax) {
   return __float2bfloat16_rn(fminf(__fmul_rn(amax, 1.f / 7.f), 4.8301e37f));
 }
 // Codes under scale s: round-half-even(x / s) clipped to +-7, exactly.  x (1 / s) is off by less
-// than 2^-20, so adding 1.5 2^23 rounds it right and leaves the code in the sum's low bits,
-// unless it lies that near a border (c + 1/2) s; there the borders themselves decide: (c + 1/2)
-// has 4 significant bits and s has 8, so their product is exact.  bf16 inputs meet a border
-// exactly about once in 2,000 numbers.
+// than 2^-20, so adding 1.5 2^23 rounds it right unless it lies that near a border (c + 1/2) s.
+// There the remainder x - c s decides: c s has 11 significant bits and the remainder at most 24,
+// so one fma gives it exactly, and s / 2 is exact.  (bf16 inputs meet a border exactly about once
+// in 2,000 numbers.)  A scale that is subnormal or that was bounded goes the long way round.
 struct Kv4Coder {
-  float s, inv, up;
+  float s, inv;
+  bool odd;
   __device__ __forceinline__ explicit Kv4Coder(__nv_bfloat16 sb) {
     s = bf16f(sb);
-    up = s < 1e-30f ? 0x1p100f : 1.f;  // keeps the reciprocal of a tiny scale finite
-    inv = s > 0.f ? 1.f / (s * up) : 0.f;
+    odd = s > 0.f && !(s >= 0x1p-120f && s < 4.8e37f);
+    inv = s > 0.f && !odd ? 1.f / s : 0.f;
   }
-  // low four bits: the code in two's complement
-  __device__ __forceinline__ uint32_t operator()(float x) const {
-    const float q = x * up * inv, u = q + 12582912.f, c = u - 12582912.f;
-    // (a quotient of a subnormal or a clamped scale may lie beyond 7.1)
-    if (fabsf(q - c) > 0.4999f || fabsf(q) > 7.1f) return exact(x, c);
-    return __float_as_uint(u);
+  // Four numbers -> their codes + 8 as nibbles, the first in bits 0-3: the sum of 16^j (c_j + 8)
+  // is formed in fp32, where it is exact, and read off the mantissa.
+  __device__ __forceinline__ uint32_t four(const float* x) const {
+    float c[4], q[4], far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[e] = x[e] * inv;
+      c[e] = (q[e] + 12582912.f) - 12582912.f;
+      far = fmaxf(far, fabsf(q[e] - c[e]));
+    }
+    if (far > 0.4999f || odd) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = border(x[e], c[e]);
+    }
+    return __float_as_uint(fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0]))) + (8388608.f + 34952.f)) & 0xFFFFu;
   }
-  __device__ __noinline__ uint32_t exact(float x, float guess) const {
-    const float a = fabsf(x);
-    float c = fminf(fabsf(guess), 7.f);
-    const float lo = (c - 0.5f) * s, hi = (c + 0.5f) * s;
-    const bool odd = ((int)c) & 1;
-    if (a > hi || (a == hi && odd)) c += 1.f;
-    else if (a < lo || (a == lo && odd)) c -= 1.f;
-    const int k = (int)fminf(fmaxf(c, 0.f), 7.f);
-    return (uint32_t)(x < 0.f ? -k : k);
+  __device__ __noinline__ float border(float x, float c) const {  // by value: no array goes to memory for it
+    if (odd) {
+      const float a = fabsf(x);
+      float k = fminf(rintf(a / s), 7.f);  // at most one off
+      const float lo = (k - 0.5f) * s, hi = (k + 0.5f) * s;
+      const bool one = ((int)k) & 1;
+      if (a > hi || (a == hi && one)) k += 1.f;
+      else if (a < lo || (a == lo && one)) k -= 1.f;
+      return copysignf(fminf(fmaxf(k, 0.f), 7.f), x);
+    }
+    const float r = fmaf(-c, s, x), h = 0.5f * s;
+    return fabsf(r) > h || (fabsf(r) == h && (((int)c) & 1)) ? c + copysignf(1.f, r) : c;
+  }
+  // One number: its code + 8.
+  __device__ __forceinline__ uint32_t one(float x) const {
+    const float v[4] = {x, 0.f, 0.f, 0.f};
+    return four(v) & 15u;
   }
 };
-constexpr uint32_t kKv4Bias = 0x88888888u;  // two's complement nibbles ^ this = code + 8
+// A key's word: numbers 2j and 2j + 1 at bits 4j and 16 + 4j.
+__device__ __forceinline__ uint32_t kv4_key_word(const Kv4Coder& code, const float* v) {
+  const float even[4] = {v[0], v[2], v[4], v[6]}, odd[4] = {v[1], v[3], v[5], v[7]};
+  return code.four(even) | code.four(odd) << 16;
+}
 
 // Decoding a pair of codes to the bf16 values bf16(c * s).
 //
@@ -288,10 +310,10 @@ __device__ __forceinline__ bool kv4_rows_of(const Kv4RowArgs& a, int i, bool wri
 }
 
 // ------------------------------------------------------------------------------ append
-// Two kernels.  Below 16 rows (kKv4Block) a thread codes one octet (eight numbers) of a row's key
-// and value, the four lanes of a group sharing their largest magnitude: short chains, small
-// scattered stores.  From 16 rows on a warp codes a whole block of 16 rows in the layout's own
-// order, so that codes leave in 16-byte pieces and most groups lie in one lane.
+// Two kernels.  In small calls a thread codes one octet (eight numbers) of a row's key and value,
+// the four lanes of a group sharing their largest magnitude: short chains, small scattered
+// stores.  In large ones a warp codes a whole block of 16 rows in the layout's own order, so that
+// codes leave in 8-byte pieces and most groups lie in one lane (kv4_by_blocks has the rule).
 constexpr int kKv4RowThreads = 256;
 
 template <int D>
@@ -333,21 +355,13 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
     const __nv_bfloat16 sb = kv4_scale(m);
     const Kv4Coder code(sb);
     wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
-    uint32_t n[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) n[e] = code(v[e]) & 15u;
     if (b >= 0) {
       if (kv == 0) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w |= n[e] << ((e >> 1) * 4 + (e & 1) * 16);
-        *reinterpret_cast<uint32_t*>(blk + O::k_word(r, o)) = w ^ kKv4Bias;
+        *reinterpret_cast<uint32_t*>(blk + O::k_word(r, o)) = kv4_key_word(code, v);
         if ((o & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::k_scale(r, o >> 2)) = sb;
       } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          *reinterpret_cast<uint16_t*>(blk + O::v_half(r, 2 * o + u)) =
-              (uint16_t)((n[4 * u] | (n[4 * u + 1] << 4) | (n[4 * u + 2] << 8) | (n[4 * u + 3] << 12)) ^ kKv4Bias);
+        for (int u = 0; u < 2; ++u) *reinterpret_cast<uint16_t*>(blk + O::v_half(r, 2 * o + u)) = (uint16_t)code.four(v + 4 * u);
         if ((o & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::v_scale(r, o >> 2)) = sb;
       }
     }
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(32) kv4_step_kernel(const Kv4Cache c, const Kv
       const __nv_bfloat16 sb = kv4_scale(warp_max(fabsf(y)));
       const Kv4Coder code(sb);
       wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
-      code_s[kv][lane + 32 * e] = (uint8_t)((code(y) ^ 8u) & 15u);
+      code_s[kv][lane + 32 * e] = (uint8_t)code.one(y);
       if (lane == 0) *reinterpret_cast<__nv_bfloat16*>(blk + (kv ? O::v_scale(r, e) : O::k_scale(r, e))) = sb;
     }
   }
@@ -527,8 +541,8 @@ __global__ void __launch_bounds__(32) kv4_step_kernel(const Kv4Cache c, const Kv
 
 // ---------------------------------------------------------------------- whole blocks
 // A warp per (block of 16 rows, KV head), keys (blockIdx.z 0) and values (1) apart: unit u of
-// sequence i is head u % kvh of the block that holds row start + 16 (u / kvh).  live: bit r = row r of the block is the call's and its index in
-// the call is below `count`.
+// sequence i is head u % kvh of the block that holds row start + 16 (u / kvh).  live: bit r = row
+// r of the block is the call's and its index in the call is below `count`.
 constexpr int kKv4BlockWarps = 4;
 struct Kv4BlockUnit {
   int head, row, base;  // first row of the block; the call's index of it (may be negative)
@@ -563,8 +577,7 @@ __device__ __forceinline__ bool kv4_block_unit(const Kv4RowArgs& a, int i, bool 
   return true;
 }
 
-// NG groups' worth of numbers of one row into codes: 4 NG words of eight numbers each in two's
-// complement (word order: consecutive numbers, pairs at bits 4j and 16 + 4j) and NG scales.
+// What a warp's numbers were like: any not finite; any scale outside the narrow range.
 struct Kv4Odd {
   bool value = false, wide = false;
 };
@@ -572,10 +585,8 @@ template <int N>
 __device__ __forceinline__ float kv4_amax(float (&v)[N], Kv4Odd& odd) {
   float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) m = fmaxf(m, fabsf(v[e]));  // skips NaN
-  bool fine = m <= 3.402823466e38f;
-#pragma unroll
-  for (int e = 0; e < N; ++e) fine = fine && v[e] == v[e];
+  for (int e = 0; e < N; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[e])));  // a NaN stays
+  const bool fine = m <= 3.402823466e38f;
   if (!fine) {  // NaN counts as 0, an infinity as the largest finite number
     odd.value = true;
     m = 0.f;
@@ -601,56 +612,41 @@ __global__ void __launch_bounds__(32 * kKv4BlockWarps) kv4_append_blocks_kernel(
   if (blockIdx.z == 0) {  // ---- keys: rows g and g + 8, numbers [t D/4, (t+1) D/4), 32 (D = 64: 16) at a time
     constexpr int N = D >= 128 ? 32 : 16, NP = N / 16;  // numbers and pieces of a step
     const long from = (long)i * a.k.seq + (long)x.head * a.k.head + t * (D / 4);
-    for (int k = 0; k < D / 4 / N; ++k) {
-      uint32_t w[NP][4] = {};
+#pragma unroll 1
+    for (int step = 0; step < 2 * (D / 4 / N); ++step) {  // rolled: the code is fetched anew in every launch
+      const int k = step >> 1, half = step & 1, r = g + 8 * half;
+      const bool on = (x.live >> r) & 1;
+      float v[N];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
-        const bool on = (x.live >> r) & 1;
-        float v[N];
+      for (int o = 0; o < N / 16; ++o) {
+        if (on) kv4_load16(a.k, from + (long)(x.base + r) * a.k.row + k * N + 16 * o, v + 16 * o);
+        else
 #pragma unroll
-        for (int o = 0; o < N / 16; ++o) {
-          if (on) kv4_load16(a.k, from + (long)(x.base + r) * a.k.row + k * N + 16 * o, v + 16 * o);
-          else
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[16 * o + e] = 0.f;
-        }
-        float m = kv4_amax(v, odd);
-        if (D == 64) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        const __nv_bfloat16 sb = kv4_scale(m);
-        const Kv4Coder code(sb);
-        odd.wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
-#pragma unroll
-        for (int o = 0; o < N / 8; ++o) {
-          uint32_t u = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u |= (code(v[8 * o + e]) & 15u) << ((e >> 1) * 4 + (e & 1) * 16);
-          w[o >> 1][2 * half + (o & 1)] = u ^ kKv4Bias;
-        }
-        if (on && (D > 64 || !(t & 1))) *reinterpret_cast<__nv_bfloat16*>(blk + O::k_scale(r, (t * (D / 4) + k * N) / kKv4Group)) = sb;
+          for (int e = 0; e < 16; ++e) v[16 * o + e] = 0.f;
       }
-      const bool on0 = (x.live >> g) & 1, on1 = (x.live >> (g + 8)) & 1;
+      float m = kv4_amax(v, odd);
+      if (D == 64) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      const __nv_bfloat16 sb = kv4_scale(m);
+      const Kv4Coder code(sb);
+      odd.wide |= code.s > 0.f && !(code.s >= kKv4Narrow && code.s <= kKv4Wide);
+      if (on && (D > 64 || !(t & 1))) *reinterpret_cast<__nv_bfloat16*>(blk + O::k_scale(r, (t * (D / 4) + k * N) / kKv4Group)) = sb;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        uint32_t* to = reinterpret_cast<uint32_t*>(blk) + ((k * NP + p) * 32 + lane) * 4;
-        if (on0 && on1) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
-        } else if (on0) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(w[p][0], w[p][1]);
-        } else if (on1) {
-          *reinterpret_cast<uint2*>(to + 2) = make_uint2(w[p][2], w[p][3]);
-        }
+        const uint2 w = make_uint2(kv4_key_word(code, v + 16 * p), kv4_key_word(code, v + 16 * p + 8));
+        if (on) *reinterpret_cast<uint2*>(blk + ((k * NP + p) * 32 + lane) * 16 + half * 8) = w;
       }
     }
   }
   if (blockIdx.z == 1) {  // ---- values: rows 2t, 2t + 1, 2t + 8, 2t + 9, numbers [g D/8, (g+1) D/8), N at a time
     constexpr int N = D >= 256 ? 32 : D / 8, NP = N / 8;
     const long from = (long)i * a.v.seq + (long)x.head * a.v.head + g * (D / 8);
-    for (int k = 0; k < D / 8 / N; ++k) {
-      uint32_t w[NP][4] = {};  // [piece][words of the pair t, words of the pair t + 4]
+#pragma unroll 1
+    for (int step = 0; step < 2 * (D / 8 / N); ++step) {
+      const int k = step >> 1, pr = step & 1;  // the row pair t or t + 4
+      uint32_t w[NP][2] = {};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = 2 * t + (q & 1) + 8 * (q >> 1);
+      for (int q = 0; q < 2; ++q) {
+        const int r = 2 * t + q + 8 * pr;
         const bool on = (x.live >> r) & 1;
         float v[N];
 #pragma unroll
@@ -671,26 +667,20 @@ __global__ void __launch_bounds__(32 * kKv4BlockWarps) kv4_append_blocks_kernel(
 #pragma unroll
         for (int o = 0; o < NP; ++o)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[o][2 * (q >> 1) + (e >> 2)] |= (code(v[8 * o + e]) & 15u) << ((e & 3) * 4 + (q & 1) * 16);
+          for (int e = 0; e < 2; ++e) w[o][e] |= code.four(v + 8 * o + 4 * e) << (16 * q);
         const int n0 = g * (D / 8) + k * N;
         if (on && n0 % kKv4Group == 0) *reinterpret_cast<__nv_bfloat16*>(blk + O::v_scale(r, n0 / kKv4Group)) = sb;
       }
+      const unsigned both = (x.live >> (2 * t + 8 * pr)) & 3u;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        uint32_t* to = reinterpret_cast<uint32_t*>(blk + O::kV) + ((k * NP + p) * 32 + lane) * 4;
-        const unsigned mine = (x.live >> (2 * t)) & 0x303u;
-        if (mine == 0x303u) {
-          *reinterpret_cast<uint4*>(to) =
-              make_uint4(w[p][0] ^ kKv4Bias, w[p][1] ^ kKv4Bias, w[p][2] ^ kKv4Bias, w[p][3] ^ kKv4Bias);
-        } else {
+        uint32_t* to = reinterpret_cast<uint32_t*>(blk + O::kV) + ((k * NP + p) * 32 + lane) * 4 + 2 * pr;
+        if (both == 3u) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[p][0], w[p][1]);
+        } else if (both) {
+          const int q = both >> 1;  // the one row of the pair that is the call's
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if ((x.live >> (2 * t + (q & 1) + 8 * (q >> 1))) & 1)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                reinterpret_cast<uint16_t*>(to + 2 * (q >> 1) + e)[q & 1] =
-                    (uint16_t)((w[p][2 * (q >> 1) + e] ^ kKv4Bias) >> (16 * (q & 1)));
+          for (int e = 0; e < 2; ++e) reinterpret_cast<uint16_t*>(to + e)[q] = (uint16_t)(w[p][e] >> (16 * q));
         }
       }
     }

@@ -89,6 +89,61 @@ def test_append_strided_unaligned(rt, dtype):
     fine(c)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("page,pad", [(0, 0), (16, 3), (64, 8)])
+def test_append_read_many(rt, d, dtype, page, pad):
+    """Calls large enough to go by whole blocks of rows: ragged starts and counts, blocks filled by
+    two calls, ties (multiples of half a step), NaN and infinities, a missing page, rows kept."""
+    n, kvh, m, cap = 44, 3, 61, 131                   # 44 sequences x 3 heads x 4 blocks
+    g = np.random.default_rng(d + page)
+    c = make(rt, n + 1, cap, 3, kvh, d, page)
+    a, b = (rows((n, m, kvh, d + pad), dtype, s)[..., pad // 2:pad // 2 + d] for s in (1, 2))
+    a[::3, :, :, :32] = torch.randint(-14, 15, (15, m, kvh, 32), generator=torch.Generator().manual_seed(3)).to(a) * 0.5
+    a[::3, :, :, 5] = 7
+    b[1::3, :, :, 32:64] = a[::3, :, :, :32]
+    slots = g.permutation(n + 1)[:n]
+    start = g.integers(0, 40, n)
+    first, count = g.integers(0, 31, n), g.integers(31, m + 1, n)
+    first[:3], count[:3] = (0, 1, 30), (m, 31, 0)
+    late = np.maximum(count - first, 0)
+    # rows first.. in one call, rows 0..first in another: blocks shared by two calls keep both
+    ka, vb = a.clone(), b.clone()
+    for i in range(n):
+        ka[i, :late[i]], vb[i, :late[i]] = a[i, first[i]:first[i] + late[i]], b[i, first[i]:first[i] + late[i]]
+    c.append(ka, vb, i32(slots.tolist()), i32((start + first).tolist()), i32(late.tolist()))
+    c.append(a, b, i32(slots.tolist()), i32(start.tolist()), i32(np.minimum(first, count).tolist()))
+    fine(c)
+    for typ in TYPES.values():
+        rk, rv = c.read(i32(slots.tolist()), i32(start.tolist()), m, i32(count.tolist()), dtype=typ)
+        for got, x in ((rk, a), (rv, b)):
+            want, got = ref.values(host(x)), host(got)
+            for i in range(n):
+                np.testing.assert_array_equal(got[i, :count[i]], torch.from_numpy(want[i, :count[i]]).to(typ).double().numpy())
+                assert not got[i, count[i]:].any()
+    zeros = [0] * n
+    before = [host(t) for t in c.read(i32(slots.tolist()), i32(zeros), cap, dtype=torch.float32)]
+    for i in range(n):                                  # rows that no call named are as they were
+        for x in before:
+            assert not x[i, :start[i]].any() and not x[i, start[i] + count[i]:].any()
+    bad = a.float()
+    bad[2::5, ::7, :, 9], bad[3::5, ::5, :, d - 1] = float("nan"), float("-inf")
+    if dtype != "f16":                                  # (the largest number is not one of fp16's)
+        c.append(bad.to(a.dtype), bad.to(a.dtype), i32(slots.tolist()), i32(start.tolist()))
+        rk, rv = c.read(i32(slots.tolist()), i32(start.tolist()), m, dtype=torch.float32)
+        want = ref.values(host(bad.to(a.dtype)))
+        np.testing.assert_array_equal(host(rk), want)
+        np.testing.assert_array_equal(host(rv), want)
+        from accelerator_decode_gb300 import g4
+        assert c.device_error() == (g4.G4_ERR_DEVICE_CHECK, g4.G4_DEV_BAD_VALUE)
+    if page:
+        c._table[int(slots[0]), 0] = -1
+        rk, rv = c.read(i32(slots.tolist()), i32(zeros), cap)
+        assert not host(rk[0, :page]).any() and not host(rv[0, :page]).any()
+        from accelerator_decode_gb300 import g4
+        assert c.device_error() == (g4.G4_ERR_DEVICE_CHECK, g4.G4_DEV_BAD_POSITION)
+
+
 def test_append_borders(rt):
     """Rounding ties, numbers one step beside a border, zero groups, the smallest and largest scales."""
     d, m = 128, 64
