@@ -181,47 +181,46 @@ __device__ __forceinline__ void kv4_store16(const Kv4Dense& x, long off, const f
 __device__ __forceinline__ __nv_bfloat16 kv4_scale(float amax) {
   return __float2bfloat16_rn(fminf(__fmul_rn(amax, 1.f / 7.f), 4.8301e37f));
 }
-// Codes under scale s: round-half-even(x / s) clipped to +-7, exactly.  x (1 / s) is off by less
-// than 2^-20, so adding 1.5 2^23 rounds it right unless it lies that near a border (c + 1/2) s.
-// There the remainder x - c s decides: c s has 11 significant bits and the remainder at most 24,
-// so one fma gives it exactly, and s / 2 is exact.  (bf16 inputs meet a border exactly about once
-// in 2,000 numbers.)  A scale that is subnormal or that was bounded goes the long way round.
+// Codes under scale s: round-half-even(x / s) clipped to +-7, exactly and without a branch.
+// q = x (1 / s) is within 1.5 units in the last place of x / s, the remainder x - q s has a few
+// significant bits only (s has eight) and comes out of one fma exactly, and a second fma adds
+// what it is worth.  The sum meets a border c + 1/2 just where x / s does: beside a border x / s
+// is at least ulp(x) / s > 0.501 units of q away from it (24 bits of x, eight of s).  Adding
+// 1.5 2^23 then rounds half to even, and leaves the code in the sum's low bits, whose others are
+// zero below bit 16: codes are shifted and added as they are.  (A test for nearness to a border
+// with a slow path behind it was taken by 1 in 16 warps on bf16 numbers, for their ties.)
+// A scale that is tiny or was bounded takes the division (never clipped otherwise: x <= 7.03 s).
 struct Kv4Coder {
   float s, inv;
   bool odd;
   __device__ __forceinline__ explicit Kv4Coder(__nv_bfloat16 sb) {
     s = bf16f(sb);
-    odd = s > 0.f && !(s >= 0x1p-120f && s < 4.8e37f);
+    odd = s > 0.f && !(s >= 0x1p-90f && s < 4.8e37f);
     inv = s > 0.f && !odd ? 1.f / s : 0.f;
   }
-  // Four numbers -> their codes + 8 as nibbles, the first in bits 0-3: the sum of 16^j (c_j + 8)
-  // is formed in fp32, where it is exact, and read off the mantissa.
+  // Four numbers -> their codes + 8 as nibbles, the first in bits 0-3.
   __device__ __forceinline__ uint32_t four(const float* x) const {
-    float c[4], q[4], far = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      q[e] = x[e] * inv;
-      c[e] = (q[e] + 12582912.f) - 12582912.f;
-      far = fmaxf(far, fabsf(q[e] - c[e]));
-    }
-    if (far > 0.4999f || odd) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = border(x[e], c[e]);
-    }
-    return __float_as_uint(fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0]))) + (8388608.f + 34952.f)) & 0xFFFFu;
-  }
-  __device__ __noinline__ float border(float x, float c) const {  // by value: no array goes to memory for it
+    uint32_t u[4];
     if (odd) {
-      const float a = fabsf(x);
-      float k = fminf(rintf(a / s), 7.f);  // at most one off
-      const float lo = (k - 0.5f) * s, hi = (k + 0.5f) * s;
-      const bool one = ((int)k) & 1;
-      if (a > hi || (a == hi && one)) k += 1.f;
-      else if (a < lo || (a == lo && one)) k -= 1.f;
-      return copysignf(fminf(fmaxf(k, 0.f), 7.f), x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = far(x[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float q = __fmul_rn(x[e], inv);
+        u[e] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, x[e]), inv, q), 12582912.f));
+      }
     }
-    const float r = fmaf(-c, s, x), h = 0.5f * s;
-    return fabsf(r) > h || (fabsf(r) == h && (((int)c) & 1)) ? c + copysignf(1.f, r) : c;
+    return (u[0] + (u[1] << 4) + (u[2] << 8) + (u[3] << 12) + 0x8888u) & 0xFFFFu;
+  }
+  __device__ __noinline__ uint32_t far(float x) const {
+    const float a = fabsf(x);
+    float k = fminf(rintf(a / s), 7.f);  // at most one off
+    const float lo = (k - 0.5f) * s, hi = (k + 0.5f) * s;
+    const bool one = ((int)k) & 1;
+    if (a > hi || (a == hi && one)) k += 1.f;
+    else if (a < lo || (a == lo && one)) k -= 1.f;
+    return (uint32_t)(int)copysignf(fminf(fmaxf(k, 0.f), 7.f), x);
   }
   // One number: its code + 8.
   __device__ __forceinline__ uint32_t one(float x) const {
