@@ -154,3 +154,13 @@ def test_reference_borders():
     assert ref.bf16_round(1 + 2.0 ** -8) == 1.0 and ref.bf16_round(1 + 3 * 2.0 ** -8) == 1 + 2.0 ** -6
     assert ref.bf16_round(2.0 ** -134) == 0.0 and ref.bf16_round(3 * 2.0 ** -134) == 2.0 ** -132
     assert ref.evict_source(np.array([0, 1, 2, 3]), np.array([1., 1., 0., 1.]), 2, 1).tolist() == [0, 3]
+
+
+def test_oracle_rows_are_the_formats():
+    """The decode oracle's 4-bit rows and the reference of the cache's operators, written apart."""
+    from oracle import kv_int4_values
+    g = np.random.default_rng(2)
+    x = (g.standard_normal((50, 128)) * np.exp(g.uniform(-20, 20, (50, 1)))).astype(np.float32)
+    x[3, 32:64] = 0
+    x[4, :32] = np.clip(np.arange(-16, 16) * 0.5, -7, 7)   # a scale of one: ties
+    np.testing.assert_array_equal(kv_int4_values(x, np.float64), ref.values(x))
