@@ -16,8 +16,8 @@
 // query rows), so eight query rows waste nothing and 4-bit codes go from a 16-byte load to the
 // operand registers through 1.25 ALU operations and one bf16 operation per pair.
 //
-// Bound: the dependent chain of a block (load, decode, scores, softmax, values), with 12 to 15
-// warps on an SM to hide it.  64 sequences of up to 8,192 rows, eight KV heads of 128, four query heads
+// Bound: the dependent chain of a block (load, decode, scores, softmax, values), with 8 to 12
+// consumer warps on an SM to hide it.  64 sequences of up to 8,192 rows, eight KV heads of 128, four query heads
 // each (456 MB, 68 us at the measured copy rate): 109 us, 4.2 TB/s; loading alone takes 88 us
 // and the arithmetic on resident tiles 107.  At 16 sequences the issue slots are 48% busy, the
 // tensor cores 26%, DRAM 37%.  512-wide rows, eight sequences of up to 8,639, with the account: 43

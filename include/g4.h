@@ -379,7 +379,8 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
 
 /* Give rows back as the values they stand for, the inverse addressing of g4_kv4_append (k or v
  * may be NULL, not both).  What there is no row for (at and beyond d_counts[i], on a missing
- * page, of a skipped sequence) is left as it was, or with zero_rest != 0 set to zero.
+ * page, of a skipped sequence) is left as it was, or with zero_rest != 0 set to zero.  A value
+ * beyond an fp16 tensor's range is an infinity there.
  * Errors: INVALID_ARG. */
 g4_status g4_kv4_read(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                       const int32_t* d_start, const int32_t* d_counts, int32_t n_rows,
@@ -397,16 +398,17 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * token t sits at row d_lens[i] - m + t and sees rows up to its own (and with window > 0 only
  * the newest `window` of those):
  *   s_j = scale * q . K_j        o = sum_j softmax(s)_j V_j        (scale 0: 1/sqrt(head_dim))
- * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type, sharing no element.  A token that sees no row gets
- * zeros; query rows t >= m of `out` are left as they were, or with zero_rest != 0 set to zero.  accumulate != 0 (track, window 0):
- * each row's account grows by the attention weights it received, summed over the sequence's
- * query tokens and the query heads of its KV head.  The same slot may be named twice only
- * without accumulate.  The sums run in a fixed order: equal calls give equal bits.
- * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0,
- * a scale that is negative or not finite, q and out of different types or at one address, malformed tensors), UNSUPPORTED
- * (accumulate without track; a window with a cache that tracks: after an eviction its rows are
- * no longer in position order; n_seq * num_kv_heads * ceil(q_len * heads per KV head / 8) *
- * ceil(capacity / 64) at 2^31 or more). */
+ * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type, sharing no element.  A token that
+ * sees no row gets zeros; query rows t >= m of `out` are left as they were, or with
+ * zero_rest != 0 set to zero.  accumulate != 0 (track, window 0): each row's account grows by the
+ * attention weights it received, summed over the sequence's query tokens and the query heads of
+ * its KV head.  The same slot may be named twice only without accumulate.  The sums run in a
+ * fixed order: equal calls give equal bits.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, q_len outside 1..max_q_len, window < 0, a scale
+ * that is negative or not finite, q and out of different types or at one address, malformed
+ * tensors), UNSUPPORTED (accumulate without track; a window with a cache that tracks: after an
+ * eviction its rows are no longer in position order; n_seq * num_kv_heads *
+ * ceil(q_len * heads per KV head / 8) * ceil(capacity / 64) at 2^31 or more). */
 g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                         const int32_t* d_lens, int32_t q_len, const int32_t* d_q_lens, float scale,
                         int32_t window, int32_t accumulate, int32_t zero_rest,

@@ -175,6 +175,20 @@ def test_append_borders(rt):
     fine(c)
 
 
+def test_read_beyond_a_types_range(rt):
+    """fp16 results hold infinities where a row's value is too large for them; the row keeps it."""
+    x = torch.zeros(1, 2, 1, 64, device="cuda")
+    x[0, 0, 0, 0], x[0, 0, 0, 40], x[0, 1, 0, 5] = 7e6, -7e5, 3.0
+    c = make(rt, 1, 4, 1, 1, 64)
+    c.append(x, -x, i32([0]), i32([0]))
+    want = torch.from_numpy(ref.values(host(x)))
+    for typ in TYPES.values():
+        rk, rv = c.read(i32([0]), i32([0]), 2, dtype=typ)
+        np.testing.assert_array_equal(host(rk), want.to(typ).double().numpy())
+        np.testing.assert_array_equal(host(rv), (-want).to(typ).double().numpy())
+    fine(c)
+
+
 def test_append_not_finite(rt):
     """NaN is stored as 0, an infinity as the largest number; both are reported, neighbours are fine."""
     d = 64
