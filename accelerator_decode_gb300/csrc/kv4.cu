@@ -164,7 +164,7 @@ void kv4_launch_attend(const Kv4Work& op, Kv4AttendArgs& a, cudaStream_t st) {
   const int ctas = op.sms * C::kMinCtas;
   // the ring takes what shared memory the CTAs of an SM leave each other (1 KB each is the system's)
   const int room = (op.smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
-  a.stages = std::max(2, std::min(4, room / C::kTile));
+  a.stages = kv4_ring_stages(room, C::kTile, C::kSets);
   const int items = a.n_seq * a.c.kvh * a.row_tiles;
   // With items enough, or few tiles, no item is shared by many CTAs, and the last one to finish
   // joins the parts (a launch less); else the parts of a few long items are joined by a second

@@ -114,7 +114,8 @@ struct Kv4Att {
   static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
   static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
-  static constexpr int kRegions = D >= 256 ? 4 : 2;    // warps whose sums fit in shared memory at a time
+  static constexpr int kRegions = D == 256 ? 4 : 2;    // warps whose sums fit in shared memory at a time; at
+                                                       // D = 512 two leave the ring four stages in every type
   static constexpr int kOBytes = kRegions * D * 32;    // [region][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {

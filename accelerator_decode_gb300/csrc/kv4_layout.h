@@ -58,6 +58,18 @@ G4_HD long kv4_block(const Kv4Cache& c, int slot, int head, int b) {
   return ((long)pg * c.kvh + head) * c.bpp + (b & (c.bpp - 1));
 }
 
+// Stages of the attention kernel's ring of key tiles: as many as fit in `room` bytes, two at least and
+// four at most, and a multiple of the sets of warps that take tiles in turn (1 or 2).  A warp waits
+// for a fill of a stage by the parity of its number, which tells it from the fill before only when
+// the warp knows that one to be over.  With a multiple, tile t and tile t - stages belong to the
+// same set, which has waited for both; with three stages and two sets the fill before was the
+// other set's, and a wait could pass while the copy was still under way.
+G4_HD int kv4_ring_stages(long room, int tile, int sets) {
+  const long n = room / tile;
+  const int stages = n > 4 ? 4 : n < 2 ? 2 : (int)n;
+  return stages / sets * sets;
+}
+
 // Byte offsets inside a block of D-wide rows.
 template <int D>
 struct Kv4Off {
