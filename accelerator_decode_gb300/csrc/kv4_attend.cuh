@@ -60,6 +60,14 @@ __device__ __forceinline__ int kv4_seq_error(const Kv4AttendArgs& a, int slot) {
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+// A whole warp's bounded wait, with one answer for all its lanes: each lane counts and looks at the
+// abort flag for itself, and lanes that went on with different answers would meet the votes and
+// shuffles behind the wait without each other.
+__device__ __forceinline__ bool kv4_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+  if (!ok) *abort_flag = 1;
+  return ok;
+}
 __device__ __forceinline__ float kv4_exp2(float x) {  // 2^x, relative error 2^-22; 0 for -inf
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -567,26 +575,21 @@ __device__ __forceinline__ int kv4_consume(const Kv4AttendArgs& a, const Kv4Shar
     for (int x = 0; x < r.tiles; ++x, ++it) {
       if (!C::kOwnProducer && warp == 0) {
         // stages that their warps have left are filled again; only the tile at hand is waited for
-        while (fill.more(g1) && !*sh.abort_flag) {
+        while (fill.more(g1) && !__any_sync(0xFFFFFFFFu, *sh.abort_flag)) {
           if (fill.it >= a.stages) {
             uint64_t* e = &sh.empty[fill.it % a.stages];
             const uint32_t parity = (fill.it / a.stages - 1) & 1;
-            bool free_now = __any_sync(0xFFFFFFFFu, mbar_try(e, parity));
-            if (!free_now && fill.it <= it) {
-              free_now = mbar_wait(e, parity, sh.abort_flag);
-              if (!__all_sync(0xFFFFFFFFu, free_now)) *sh.abort_flag = 1;
-              __syncwarp();
-              free_now = !*sh.abort_flag;
-            }
-            if (!__all_sync(0xFFFFFFFFu, free_now)) break;
+            bool free_now = __all_sync(0xFFFFFFFFu, mbar_try(e, parity));
+            if (!free_now && fill.it <= it) free_now = kv4_wait_warp(e, parity, sh.abort_flag);
+            if (!free_now) break;
           }
           fill.put(a, sh, g1);
         }
       }
       if (C::kSets > 1 && it % C::kSets != set) continue;
       const int s = it % a.stages;
-      if (!mbar_wait(&sh.full[s], (it / a.stages) & 1, sh.abort_flag)) *sh.abort_flag = 1;
-      const uint32_t have = *sh.abort_flag ? 0u : sh.held[s] >> (wq * C::kBpw) & ((1u << C::kBpw) - 1u);
+      const bool here = kv4_wait_warp(&sh.full[s], (it / a.stages) & 1, sh.abort_flag);
+      const uint32_t have = here ? sh.held[s] >> (wq * C::kBpw) & ((1u << C::kBpw) - 1u) : 0u;
       if (have) {
         // the warp's blocks of the tile are neighbours: 16 NB consecutive keys
         const uint8_t* blk = sh.ring + (size_t)s * C::kTile + wq * C::kBpw * O::kBlock;
@@ -835,12 +838,10 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   fill.start(g0);
   while (fill.more(g1)) {
     const int s = fill.it % a.stages;
-    if (fill.it >= a.stages && !mbar_wait(&sh.empty[s], (fill.it / a.stages - 1) & 1, sh.abort_flag)) {
+    if (fill.it >= a.stages && !kv4_wait_warp(&sh.empty[s], (fill.it / a.stages - 1) & 1, sh.abort_flag)) {
       if (lane == 0) set_err(a.c.err, G4_DEV_TIMEOUT);
-      *sh.abort_flag = 1;
       break;
     }
-    __syncwarp();
     fill.put(a, sh, g1);
   }
   fill.drain(a, sh);

@@ -79,3 +79,22 @@ def test_ring_rule_is_sound(tmp_path):
     with open(os.path.join(CSRC, "kv4.cu")) as f:
         launches = [x for x in f if "stages =" in x]
     assert len(launches) == 1 and "kv4_ring_stages(room, C::kTile, C::kSets)" in launches[0]
+
+
+def test_waits_answer_for_whole_warps():
+    """A wait whose result decides what a warp does is voted on: lanes that left it with different
+    answers (one at its limit, one on the abort flag) would miss each other at the next vote.  In the
+    block kernel only the single issuing lane goes by the answer."""
+    lines = open(os.path.join(CSRC, "kv4_attend.cuh")).read().splitlines()
+    for x in lines:
+        if "mbar_wait(" in x or "mbar_try(" in x:
+            assert "__all_sync(0xFFFFFFFFu, mbar_" in x, x
+    assert not any("!*sh.abort_flag" in x or "*sh.abort_flag ?" in x for x in lines)
+    for x in open(os.path.join(CSRC, "kv4_block.cuh")).read().splitlines():
+        if "kv4_wait(" in x and "__device__" not in x:
+            before = x.split("kv4_wait(")[0].strip()
+            assert before == "" or before.startswith("if (n >= ") or before.startswith("if (y >= ") or \
+                before.startswith("if (runs >= ") or before in ("ok =", "bool ok ="), x
+            if before.startswith("if"):
+                after = before[before.index(")") + 1:].strip()
+                assert after in ("", "ok ="), x
