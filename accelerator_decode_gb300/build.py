@@ -11,9 +11,10 @@ LIB = os.path.join(HERE, "libg4.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("g4.cu", "kv4.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in (
     "common.cuh", "gemv.cuh", "gemv_s.cuh", "attn.cuh", "attn_mqa.cuh", "misc.cuh", "gemm_tc.cuh", "mega.cuh",
-    "host.h", "mbar.cuh", "kv4_layout.h", "kv4.cuh", "kv4_attend.cuh", "kv4_block.cuh")]
+    "host.h", "mbar.cuh", "kv4_layout.h", "kv4_host.h", "kv4.cuh", "kv4_attend.cuh", "kv4_block.cuh")]
 HEADERS.append(os.path.join(os.path.dirname(HERE), "include", "g4.h"))
-DEPS = SOURCES + HEADERS
+# the flags are in this file: an object older than it may have been compiled with others
+DEPS = SOURCES + HEADERS + [os.path.abspath(__file__)]
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
               "-Xcompiler", "-fPIC"]
@@ -38,15 +39,15 @@ def up_to_date():
 
 
 def build(force=False, verbose=False):
-    """Compile the translation units in parallel, then link; an object newer than its source
-    and every header is kept."""
+    """Compile the translation units in parallel, then link; an object newer than its source,
+    every header and this file is kept."""
     if not force and up_to_date():
         return LIB
     jobs, objects = [], []
     for src in SOURCES:
         obj = os.path.join(HERE, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
-        if not force and _newer(obj, [src] + HEADERS):
+        if not force and _newer(obj, [src] + [d for d in DEPS if d not in SOURCES]):
             continue
         cmd = [_nvcc()] + NVCC_FLAGS + ["-c", "-o", obj + ".tmp", src]
         if verbose:
