@@ -68,7 +68,11 @@ __device__ __forceinline__ bool kv4_wait_warp(uint64_t* bar, uint32_t parity, vo
   if (!ok) *abort_flag = 1;
   return ok;
 }
-__device__ __forceinline__ float kv4_exp2(float x) {  // 2^x, relative error 2^-22; 0 for -inf
+// 2^x, relative error 2^-22; 0 for -inf.  Its argument is a score minus a reference (a maximum, or the
+// log2 of a sum) that was itself taken of rounded scores, so the score is rounded before the
+// subtraction (__fmul_rn).  A fused multiply-subtract gives back what the rounding took, up to 2^-24
+// of the score: a weight of 1 became 1.03 at scores of 2^19, and infinite from 2^31 on.
+__device__ __forceinline__ float kv4_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -603,7 +607,7 @@ __device__ __forceinline__ int kv4_consume(const Kv4AttendArgs& a, const Kv4Shar
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) c[b][j] *= score_scale;  // keys g (0, 1) and g + 8 (2, 3); rows 2t, 2t + 1
+          for (int j = 0; j < 4; ++j) c[b][j] = __fmul_rn(c[b][j], score_scale);  // keys g (0, 1) and g + 8 (2, 3); rows 2t, 2t + 1
           if (edge) {
             const int ja = j0 + 16 * b + g, jb = ja + 8;
             const bool gone = !((have >> b) & 1);  // no page, or wholly outside: whatever the ring holds there
@@ -870,10 +874,10 @@ __device__ __forceinline__ void kv4_gain_tile(const Kv4AttendArgs& a, const uint
   const float sc = WIDE ? a.scale : a.scale * kKv4Up, e0 = lse8[2 * t], e1 = lse8[2 * t + 1];
   const int ra = row0 + 2 * t, rb = ra + 1;
   const int last0 = ra < n_rows ? len - m + ra / a.group : -1, last1 = rb < n_rows ? len - m + rb / a.group : -1;
-  if (key <= last0) gain0 += kv4_exp2(c[0][0] * sc - e0);
-  if (key <= last1) gain0 += kv4_exp2(c[0][1] * sc - e1);
-  if (key + 8 <= last0) gain1 += kv4_exp2(c[0][2] * sc - e0);
-  if (key + 8 <= last1) gain1 += kv4_exp2(c[0][3] * sc - e1);
+  if (key <= last0) gain0 += kv4_exp2(__fmul_rn(c[0][0], sc) - e0);
+  if (key <= last1) gain0 += kv4_exp2(__fmul_rn(c[0][1], sc) - e1);
+  if (key + 8 <= last0) gain1 += kv4_exp2(__fmul_rn(c[0][2], sc) - e0);
+  if (key + 8 <= last1) gain1 += kv4_exp2(__fmul_rn(c[0][3], sc) - e1);
 }
 // A block's codes and scales of this lane, from global memory.
 template <int D>

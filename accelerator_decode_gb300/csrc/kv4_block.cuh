@@ -294,6 +294,25 @@ __device__ __forceinline__ void kv4_share_queries(const Kv4AttendArgs& a, const 
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
 
+// Products of a score and its scale go to exponentials relative to a reference (kv4_exp2), fused with
+// the subtraction: rounding the 64 scores of every tile first costs 4 us of the case above.
+//
+// In the attention all weights of a row share the reference, and what a fused product keeps, up to
+// 2^-25 of it, cancels in the division by their sum; it only has to stay in range.  From references
+// of 2^31 on the factor becomes the power of two below the scale, whose product with the largest
+// score is exact.  Scores that differ at all there differ by 64 or more, so their weights are nothing
+// under either factor.
+//
+// In the account the product's rest would stay in the weight.  Warps with a reference beyond 2^12
+// round their products first.
+constexpr float kKv4FarAttention = 0x1p31f, kKv4FarAccount = 4096.f;
+__device__ __forceinline__ float kv4_power_below(float x) { return __uint_as_float(__float_as_uint(x) & 0x7F800000u); }
+__device__ __forceinline__ void kv4_round_far(float (&f)[64], float sc, float fused) {
+  if (fused == sc) return;
+#pragma unroll
+  for (int k = 0; k < 64; ++k) f[k] = __fmul_rn(f[k], sc);
+}
+
 // The run of tiles at `at`: for the account, of at most kKv4RunTiles tiles (a.row_tiles 1), with
 // `blocks` blocks of 128 query rows to take past them.
 template <bool ACCOUNT>
@@ -537,6 +556,8 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
         const float lse = !ACCOUNT ? 0.f
                           : row < n_rows ? __ldcg(a.lse + ((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row) : INFINITY;
         float m = -INFINITY, l = 0.f;
+        float factor = sc, ref = 0.f;  // of the exponentials' arguments
+        const float fused = ACCOUNT && __any_sync(0xFFFFFFFFu, fabsf(lse) > kKv4FarAccount && fabsf(lse) != INFINITY) ? 1.f : sc;
         for (int x = 0; x < r.tiles; ++x, ++n) {
           const int y = pairs + (x >> 1), sb = y % C::kSBufs;
           kv4_wait(&s->sfull[sb], (y / C::kSBufs) & 1, s);
@@ -559,8 +580,9 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
               if (j0 + k > last || j0 + k <= low || !((have >> (k >> 4)) & 1)) f[k] = -INFINITY;
           }
           if constexpr (ACCOUNT) {
+            kv4_round_far(f, sc, fused);
 #pragma unroll
-            for (int k = 0; k < 64; ++k) f[k] = kv4_exp2(fmaf(f[k], sc, -lse));
+            for (int k = 0; k < 64; ++k) f[k] = kv4_exp2(fmaf(f[k], fused, -lse));
             // each step a lane keeps half of its columns and adds its partner's half of them
 #pragma unroll
             for (int o = 16, w = 32; o > 0; o >>= 1, w >>= 1) {
@@ -578,12 +600,18 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
             float mx = f[0];
 #pragma unroll
             for (int k = 1; k < 64; ++k) mx = fmaxf(mx, f[k]);
-            mx *= sc;
+            const float raw = mx;
+            mx = __fmul_rn(mx, sc);
             const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
             if (__any_sync(0xFFFFFFFFu, raise)) {  // a row's numbers do not depend on its neighbours'
               const float nm = raise ? mx : m, fac = raise ? kv4_exp2(m - nm) : 1.f;
               m = nm;
               l *= fac;
+              if (raise) {
+                const bool far = fabsf(m) >= kKv4FarAttention && fabsf(m) != INFINITY;
+                factor = far ? kv4_power_below(sc) : sc;
+                ref = far ? __fmul_rn(raw, factor) : m;
+              }
               if (x > 0) {  // the output so far follows: the previous tile's product has to be in
                 kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
                 kv4_fence_after();
@@ -599,11 +627,10 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
                 kv4_tst_wait();
               }
             }
-            const float z = m == -INFINITY ? 0.f : m;
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float p0 = kv4_exp2(fmaf(f[2 * k], sc, -z)), p1 = kv4_exp2(fmaf(f[2 * k + 1], sc, -z));
+              const float p0 = kv4_exp2(fmaf(f[2 * k], factor, -ref)), p1 = kv4_exp2(fmaf(f[2 * k + 1], factor, -ref));
               s0 += p0;
               s1 += p1;
               v[k] = as_u32(__floats2bfloat162_rn(p0, p1));
