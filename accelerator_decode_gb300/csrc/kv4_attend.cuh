@@ -126,8 +126,10 @@ struct Kv4Att {
   static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
   static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
-  static constexpr int kRegions = D == 256 ? 4 : 2;    // warps whose sums fit in shared memory at a time; at
-                                                       // D = 512 two leave the ring four stages in every type
+  // Warps whose sums fit in shared memory at a time.  At D = 512 two regions leave the ring of fp16 and
+  // fp32 queries four stages (three would not be sound, kv4_ring_stages); bf16 ones have them beside
+  // four regions, which take a round of sums less (eight sequences of 8,639 rows: 43.3 us, with two 45.3).
+  static constexpr int kRegions = D == 256 || (D == 512 && DT == G4_DT_BF16) ? 4 : 2;
   static constexpr int kOBytes = kRegions * D * 32;    // [region][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
