@@ -126,10 +126,13 @@ struct Kv4Att {
   static constexpr int kMinCtas = D == 512 ? 1 : D == 256 ? 2 : 3;  // CTAs of an SM
   static_assert(kMinCtas <= kKv4MaxCtas, "the partial sums' buffers hold two items of so many CTAs per SM");
   static constexpr int kQBytes = kQP * D * 16;         // [part][D / 32][lane] 16-byte pieces
-  // Warps whose sums fit in shared memory at a time.  At D = 512 two regions leave the ring of fp16 and
-  // fp32 queries four stages (three would not be sound, kv4_ring_stages); bf16 ones have them beside
-  // four regions, which take a round of sums less (eight sequences of 8,639 rows: 43.3 us, with two 45.3).
-  static constexpr int kRegions = D == 256 || (D == 512 && DT == G4_DT_BF16) ? 4 : 2;
+  // Warps whose sums fit in shared memory at a time.  At D = 512 four regions leave the ring four
+  // stages with bf16 queries, and with fp16 ones up to 114 sequences (three are not sound,
+  // kv4_ring_stages: then two); fp32 queries have four stages beside two regions only, whose sums take
+  // one more round at an item's end.  Four / two regions, microseconds: bf16, eight sequences of 8,639
+  // rows 43.1 / 45.0; fp16, eight of those without the account 39.3 / 40.9, 64 of 640 rows 27.4 /
+  // 28.7, 128 of them 55.5 / 49.2.
+  static constexpr int kRegions = D == 256 || (D == 512 && DT != G4_DT_F32) ? 4 : 2;
   static constexpr int kOBytes = kRegions * D * 32;    // [region][D / 32][2][lane] float4
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
