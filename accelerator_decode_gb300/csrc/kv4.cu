@@ -1,6 +1,7 @@
 // C entry points of the 4-bit KV cache (include/g4.h, g4_kv4_*): argument checks, the handle
 // with its cache and workspace, and the launches of kv4.cuh and kv4_attend.cuh.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -150,6 +151,14 @@ void kv4_launch_block(const Kv4Work& op, Kv4AttendArgs a, cudaStream_t st) {
   launch(kv4_block_kernel<D, true>, dim3(op.sms), dim3(kKv4BlockThreads), Kv4Blk<D, true>::smem(a.n_seq), st, a);
 }
 
+// The softmax scale in the base-2 exponentials' units.  Narrow codes stand for 2^-64 of their values
+// (Kv4Scale), which the kernels make up for by 2^64 times the scale; where that passes fp32's range
+// the codes are decoded the plain way.
+void kv4_set_scale(Kv4AttendArgs& a, double scale) {
+  a.scale = (float)std::min(scale * 1.4426950408889634, (double)FLT_MAX);
+  a.plain = !std::isfinite(a.scale * kKv4Up);
+}
+
 void kv4_use(const Kv4Work& w, Kv4AttendArgs& a) {
   a.lse = w.lse;
   a.lse_rows = a.row_tiles * 8;
@@ -282,7 +291,7 @@ void kv4_step_attend(const Kv4Cache& c, const Kv4Work& w, int n, const int* slot
   a.q_len = 1;
   a.heads = a.group = nq;
   a.row_tiles = cdiv(nq, 8);
-  a.scale = (float)((double)scale * 1.4426950408889634);
+  kv4_set_scale(a, scale);
   a.window = window;
   a.q = Kv4Dense{q, (long)nq * c.d, (long)nq * c.d, c.d, G4_DT_F32, 2};
   a.out = Kv4Dense{out, out_stride, out_stride, c.d, G4_DT_F32, out_stride % 8 == 0 ? 2 : 0};
@@ -435,7 +444,7 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.heads = op->cfg.num_q_heads;
   a.group = a.heads / op->c.kvh;
   a.row_tiles = kv4_row_tiles(op, q_len);
-  a.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)op->c.d)) * 1.4426950408889634);
+  kv4_set_scale(a, scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)op->c.d));
   a.window = window < op->cfg.capacity ? window : 0;  // one that reaches every row is none
   a.accumulate = accumulate != 0;
   a.zero_rest = zero_rest != 0;

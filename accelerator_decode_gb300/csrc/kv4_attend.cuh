@@ -34,6 +34,7 @@ struct Kv4AttendArgs {
   int n_seq, q_len, heads, group;    // group: query heads per KV head
   int row_tiles;                     // items of a (sequence, KV head): ceil(q_len * group / 8)
   float scale;                       // times log2(e)
+  int plain;                         // codes are decoded as in a cache with wide scales: scale * 2^64 is infinite
   int window, accumulate, zero_rest;
   int join_inside;                   // the CTA that finishes a shared item last joins its parts
   int stages;
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   }
   pdl_wait();
   pdl_trigger();
-  const int wide = __ldcg(a.c.wide);
+  const int wide = __ldcg(a.c.wide) | a.plain;
   kv4_plan<C::kKeys>(a, sh.first, sh.seqs, blockIdx.x == 0);
   const int total = sh.first[a.n_seq];
   const int span = kv4_span(a, sh.first, gridDim.x);
@@ -921,7 +922,7 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const __g
   const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
   const bool join = (int)blockIdx.y < join_ctas;
   // What the first launch reads as well can be read before it has ended.
-  const int wide = __ldcg(a.c.wide);
+  const int wide = __ldcg(a.c.wide) | a.plain;
   kv4_plan<C::kKeys>(a, first, seqs, false);
   const int slot = seqs[i].x, len = seqs[i].y, m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
   if (!join && n > 0) kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
@@ -986,7 +987,7 @@ __global__ void __launch_bounds__(32 * kKv4GainWarps) kv4_gain_kernel(const __gr
   int slot, len, m;
   if (!kv4_seq(a, i, &slot, &len, &m) || m == 0) return;
   if (kv4_repeated(a.slots, i, slot)) return;
-  const int wide = __ldcg(a.c.wide);
+  const int wide = __ldcg(a.c.wide) | a.plain;
   const int n_rows = m * a.group;
   const int nb = (len + kKv4Block - 1) / kKv4Block;
   for (int b0 = blockIdx.x * kKv4GainWarps; b0 < nb; b0 += gridDim.x * kKv4GainWarps) {

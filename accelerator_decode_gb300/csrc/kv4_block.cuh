@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
   kv4_fence_before();
   pdl_wait();
   pdl_trigger();
-  const int wide = __ldcg(a.c.wide);
+  const int wide = __ldcg(a.c.wide) | a.plain;
   kv4_plan<kKv4N>(a, first, seqs, !ACCOUNT && blockIdx.x == 0);
   kv4_fence_after();
   const uint32_t tmem = s->tmem;

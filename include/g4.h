@@ -398,6 +398,8 @@ g4_status g4_kv4_account(g4_kv4* op, g4_stream stream, int32_t n_seq, const int3
  * token t sits at row d_lens[i] - m + t and sees rows up to its own (and with window > 0 only
  * the newest `window` of those):
  *   s_j = scale * q . K_j        o = sum_j softmax(s)_j V_j        (scale 0: 1/sqrt(head_dim))
+ * Scores are held in fp32 (times log2 e): scores of 2^s tell differences down to 2^(s - 24), and a
+ * row with one beyond the range is not finite.
  * q, out: [n_seq][q_len][num_q_heads][head_dim], of one type, sharing no element.  A token that
  * sees no row gets zeros; query rows t >= m of `out` are left as they were, or with
  * zero_rest != 0 set to zero.  accumulate != 0 (track, window 0): each row's account grows by the

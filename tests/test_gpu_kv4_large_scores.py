@@ -59,11 +59,17 @@ def check_one_hot(rt, dtype, d, q_len, scale, grow, kvh=2, group=4, page=0):
         assert gained[i].isfinite().all() and (sums <= q_len * group * (1 + 1e-6)).all()
 
 
-@pytest.mark.parametrize("scale", [1e15, 1.1e19])
+@pytest.mark.parametrize("scale", [1e15, 1.1e19, 1e20, 1e30])
 @pytest.mark.parametrize("dtype,d,q_len", [("f32", 64, 1), ("bf16", 128, 1), ("f16", 256, 1), ("f32", 512, 1), ("f16", 64, 9),
                                            ("bf16", 64, 20), ("bf16", 128, 64), ("bf16", 256, 33)])
 def test_large_scales(rt, dtype, d, q_len, scale):
     check_one_hot(rt, dtype, d, q_len, scale, 1.0)
+
+
+def test_largest_scale(rt):
+    """The largest finite fp32 number, on rows so small that the scores stay in range."""
+    check_one_hot(rt, "f32", 64, 1, 3.4028234e38, 2.0 ** -4)
+    check_one_hot(rt, "bf16", 128, 20, 3.4028234e38, 2.0 ** -4)
 
 
 @pytest.mark.parametrize("grow", [2.0 ** 9, 2.0 ** 15, 2.0 ** 20])
