@@ -243,6 +243,7 @@ g4_status kv4_create_impl(g4_kv4* op, const int32_t* d_page_table, cudaStream_t 
   if (f.track) {
     TRY(kv4_alloc(op, &c.pos, blocks * kKv4Block, st));
     TRY(kv4_alloc(op, &c.weight, blocks * kKv4Block, st));
+    TRY(kv4_alloc(op, &c.base, (size_t)f.n_slots * c.kvh, st));
     // at most half of a slot's rows move: a move takes an evicted row below the budget and a
     // kept one beyond it
     TRY(kv4_alloc(op, &op->holes, (size_t)f.n_slots * c.kvh * kv4_most_moves(op), st));
@@ -362,10 +363,13 @@ g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
   a.positions = d_positions;
   a.weights = d_weights;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (kv4_by_blocks(op, n_seq, n_rows, 3)) {
-    KV4_DISPATCH(op->c.d, launch(kv4_append_blocks_kernel<D>, kv4_block_grid(op, n_seq, n_rows), dim3(32 * kKv4BlockWarps), 0, st, a));
+  const bool blocks = kv4_by_blocks(op, n_seq, n_rows, 3);
+  dim3 grid = blocks ? kv4_block_grid(op, n_seq, n_rows) : kv4_row_grid(op, n_seq, n_rows);
+  grid.x += op->cfg.track;  // kv4_set_bases
+  if (blocks) {
+    KV4_DISPATCH(op->c.d, launch(kv4_append_blocks_kernel<D>, grid, dim3(32 * kKv4BlockWarps), 0, st, a));
   } else {
-    KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, kv4_row_grid(op, n_seq, n_rows), dim3(kKv4RowThreads), 0, st, a));
+    KV4_DISPATCH(op->c.d, launch(kv4_append_kernel<D>, grid, dim3(kKv4RowThreads), 0, st, a));
   }
   CK(cudaGetLastError());
   return G4_OK;

@@ -287,7 +287,7 @@ struct Kv4RowArgs {
   const int *slots, *start, *counts;  // counts may be NULL: n_rows each
   int n_rows;
   Kv4Dense k, v;                      // p may be NULL (read)
-  const int* positions;               // append: [n_seq][kvh][n_rows] or NULL (row index)
+  const int* positions;               // append: [n_seq][kvh][n_rows] or NULL (on from the newest)
   const float* weights;               // append: same layout, or NULL (0)
   int* positions_out;                 // account
   float* weights_out;
@@ -306,6 +306,42 @@ __device__ __forceinline__ bool kv4_rows_of(const Kv4RowArgs& a, int i, bool wri
   if (writes && kv4_repeated(a.slots, i, *slot)) bad |= G4_DEV_BAD_SLOT;
   if (bad && threadIdx.x == 0) set_err(a.c.err, bad);
   return bad == 0;
+}
+
+// Positions that append gives by itself: the row's index plus a base per (slot, head), which an
+// append at row 0 starts anew and an eviction sets so that the row behind the kept ones follows the
+// newest position there was.
+__device__ __forceinline__ int kv4_next_position(const Kv4RowArgs& a, int slot, int h, int row0, int row) {
+  const long base = row0 ? __ldcg(a.c.base + (size_t)slot * a.c.kvh + h) : 0;
+  return (int)min(base + row, (long)INT_MAX);
+}
+// The bases after an append of `count` rows from row0 on: given positions lift a base to where the row
+// behind them would follow the newest of them.  A tracked cache's append has one CTA more per
+// sequence for it, so that a long array of positions is read beside the rows (2 x 1,988 positions
+// ahead of a CTA's rows made a call 7 us longer).  Nothing else of the call reads a base that this
+// changes: the others need one only where no positions are given and row0 > 0.
+__device__ __forceinline__ void kv4_set_bases(const Kv4RowArgs& a, int i, int slot, int row0, int count) {
+  if (count == 0 || (!a.positions && row0)) return;
+  int* base = a.c.base + (size_t)slot * a.c.kvh;
+  if (!a.positions) {
+    for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) base[h] = 0;
+    return;
+  }
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int share = max(1, warps / a.c.kvh);  // warps of a head; those of one head are neighbours
+  __shared__ int most[64];
+  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) most[h] = row0 ? __ldcg(base + h) : INT_MIN;
+  __syncthreads();
+  for (int h = (threadIdx.x >> 5) / share; h < a.c.kvh; h += warps / share) {
+    const int* p = a.positions + ((size_t)i * a.c.kvh + h) * a.n_rows;
+    int m = INT_MIN;
+#pragma unroll 4
+    for (int t = (threadIdx.x >> 5) % share * 32 + lane; t < count; t += 32 * share) m = max(m, max(__ldcg(p + t), INT_MIN + (2 << 20)) - (row0 + t));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0) atomicMax(&most[h], m);
+  }
+  __syncthreads();
+  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) base[h] = most[h];
 }
 
 // ------------------------------------------------------------------------------ append
@@ -327,6 +363,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
   pdl_trigger();
   int slot, row0, count;
   if (!kv4_rows_of(a, i, true, &slot, &row0, &count)) return;
+  if (a.c.base && blockIdx.x == gridDim.x - 1) return kv4_set_bases(a, i, slot, row0, count);
   const long unit = ((long)blockIdx.x * kKv4RowThreads + threadIdx.x) / NO;
   const int o = threadIdx.x % NO, h = (int)(unit % a.c.kvh);
   const long t_ = unit / a.c.kvh;
@@ -372,7 +409,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
   if (wide) *a.c.wide = 1;
   if (o == 0 && a.c.pos && b >= 0) {
     const size_t at = ((size_t)i * a.c.kvh + h) * a.n_rows + t;
-    a.c.pos[b * kKv4Block + r] = a.positions ? __ldcg(a.positions + at) : row;
+    a.c.pos[b * kKv4Block + r] = a.positions ? __ldcg(a.positions + at) : kv4_next_position(a, slot, h, row0, row);
     a.c.weight[b * kKv4Block + r] = a.weights ? __ldcg(a.weights + at) : 0.f;
   }
 }
@@ -550,6 +587,7 @@ __global__ void __launch_bounds__(32) kv4_step_kernel(const Kv4Cache c, const Kv
 // r of the block is the call's and its index in the call is below `count`.
 constexpr int kKv4BlockWarps = 4;
 struct Kv4BlockUnit {
+  int slot, row0;       // the sequence's
   int head, row, base;  // first row of the block; the call's index of it (may be negative)
   long at;              // pool index, -1: no page
   unsigned live, rest;  // rows with data; rows of the call without (zero_rest)
@@ -560,6 +598,12 @@ __device__ __forceinline__ bool kv4_block_unit(const Kv4RowArgs& a, int i, bool 
     if (!a.zero_rest) return false;
     count = row0 = 0;
   }
+  if (writes && a.c.base && blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.z == 0) kv4_set_bases(a, i, slot, row0, count);
+    return false;
+  }
+  x->slot = slot;
+  x->row0 = row0;
   const int limit = a.zero_rest ? a.n_rows : count;
   const long u = (long)blockIdx.x * kKv4BlockWarps + (threadIdx.x >> 5);
   x->head = (int)(u % a.c.kvh);
@@ -694,7 +738,7 @@ __global__ void __launch_bounds__(32 * kKv4BlockWarps) kv4_append_blocks_kernel(
   if (odd.wide) *a.c.wide = 1;
   if (blockIdx.z == 0 && a.c.pos && lane < kKv4Block && ((x.live >> lane) & 1)) {
     const size_t at = ((size_t)i * a.c.kvh + x.head) * a.n_rows + x.base + lane;
-    a.c.pos[x.at * kKv4Block + lane] = a.positions ? __ldcg(a.positions + at) : x.row + lane;
+    a.c.pos[x.at * kKv4Block + lane] = a.positions ? __ldcg(a.positions + at) : kv4_next_position(a, x.slot, x.head, x.row0, x.row + lane);
     a.c.weight[x.at * kKv4Block + lane] = a.weights ? __ldcg(a.weights + at) : 0.f;
   }
 }
@@ -843,6 +887,7 @@ __device__ __forceinline__ void kv4_select(const Kv4EvictArgs& a, int i, int h, 
   if (lane == 0) atomicMax(&sh_newest, newest);
   __syncthreads();
   const long oldest_safe = (long)sh_newest - a.recent;  // safe: position > this
+  if (tid == 0) a.c.base[(size_t)slot * a.c.kvh + h] = (int)max((long)sh_newest + 1 - a.budget, (long)INT_MIN);
   auto make = [&](int p, float w) { return (long)p > oldest_safe ? 0xFFFFFFFFu : kv4_rank_bits(w); };
   auto rank = [&](int r) { return RANKS ? ranks[r] : make(__ldcg(a.c.pos + at(r)), __ldcg(a.c.weight + at(r))); };
   // the budget-th largest rank: `prefix` after the passes, of which the first `want` rows stay

@@ -36,6 +36,7 @@ struct Kv4Cache {
   uint8_t* data;      // blocks
   int* pos;           // tracked caches: logical position of every row, [page or slot][head][rows]
   float* weight;      // and its accumulated attention weight
+  int* base;          // tracked caches: what is added to a row's index for its position, [slot][head]
   const int* table;   // paged: [n_slots][max_pages]; NULL: static
   int log_bpp;        // paged: log2(blocks per page)
   int bpp;            // blocks per page (static: per slot)

@@ -321,7 +321,8 @@ class KV4Cache:
 
     # -- calls -------------------------------------------------------------------------------
     def append(self, k, v, slots, start, counts=None, positions=None, weights=None, stream=None):
-        """Code rows k, v [n, rows, num_kv_heads, head_dim] into rows start[i].. of slots[i]."""
+        """Code rows k, v [n, rows, num_kv_heads, head_dim] into rows start[i].. of slots[i].  With track,
+        positions not given are counted on from the newest that the slot holds (from 0 at row 0)."""
         n, rows = slots.numel(), k.shape[1] if k.dim() == 4 else -1
         shape = (n, rows, self.num_kv_heads, self.head_dim)
         self._dense("k", k, shape, self._ta)

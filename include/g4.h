@@ -368,8 +368,10 @@ g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_p
  * [n_seq][n_rows][num_kv_heads][head_dim] become rows d_start[i] + t of slot d_slots[i], in
  * place of what was there.  A number that is not finite sets G4_DEV_BAD_VALUE and is stored as
  * 0 (NaN) or as the largest finite number of its sign.  With track, the rows' positions and
- * accumulated weights become d_positions and d_weights [n_seq][num_kv_heads][n_rows] (NULL: the
- * row index, and 0); without it both must be NULL.
+ * accumulated weights become d_positions and d_weights [n_seq][num_kv_heads][n_rows]; without it
+ * both must be NULL.  d_weights NULL: 0.  d_positions NULL: the rows' tokens are counted on, also past
+ * evictions: an append at row 0 begins a slot anew at position 0, and rows behind the ones that a slot
+ * holds follow its newest position (of each KV head by itself, and up to 2^31 - 1).
  * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows outside 1..capacity, NULL or malformed
  * tensors), UNSUPPORTED (positions or weights without track). */
 g4_status g4_kv4_append(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
