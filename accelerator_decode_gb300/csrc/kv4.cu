@@ -22,6 +22,7 @@ struct g4_kv4 {
   Kv4Cache c{};
   std::vector<void*> allocs;
   size_t bytes = 0;
+  int fail_at = 0, n_allocs = 0;  // allocation-failure injection (G4_FAIL_ALLOC_AT), as in g4_create
   Kv4Work work;
   int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
   int* n_moves = nullptr;                     // [n_slots][kvh]
@@ -33,6 +34,7 @@ template <class T>
 g4_status kv4_alloc(g4_kv4* op, T** p, size_t count, cudaStream_t st) {
   void* q = nullptr;
   const size_t n = std::max<size_t>(count, 1) * sizeof(T);
+  if (op->fail_at > 0 && ++op->n_allocs == op->fail_at) return G4_ERR_OOM;  // injected
   const cudaError_t e = cudaMalloc(&q, n);
   if (e != cudaSuccess) {
     cuda_ok(e, "cudaMalloc");
@@ -325,6 +327,7 @@ g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_p
   if (!op) return G4_ERR_OOM;
   op->cfg = f;
   op->device = device;
+  if (const char* fa = getenv("G4_FAIL_ALLOC_AT")) op->fail_at = atoi(fa);
   g4_status s = G4_ERR_CUDA;
   cudaStream_t st = nullptr;
   if (cuda_ok(cudaDeviceGetAttribute(&op->work.sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
