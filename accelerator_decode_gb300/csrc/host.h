@@ -17,7 +17,11 @@ inline bool cuda_ok(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return true;
   char buf[512];
   snprintf(buf, sizeof buf, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-  g_last_cuda = buf;
+  try {
+    g_last_cuda = buf;
+  } catch (...) {  // no memory for the text: no exception may leave a C entry
+    g_last_cuda.clear();
+  }
   return false;
 }
 #define CK(call)                                           \

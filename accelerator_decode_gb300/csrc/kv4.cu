@@ -333,8 +333,13 @@ g4_status g4_kv4_create(int device, const g4_kv4_config* cfg, const int32_t* d_p
   if (cuda_ok(cudaDeviceGetAttribute(&op->work.sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaDeviceGetAttribute(&op->work.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
-    kv4_init(device, op->work.smem_optin);
-    s = kv4_create_impl(op, d_page_table, st);
+    try {
+      op->allocs.reserve(32);  // so that no allocation is lost for want of a place to note it
+      kv4_init(device, op->work.smem_optin);
+      s = kv4_create_impl(op, d_page_table, st);
+    } catch (...) {
+      s = G4_ERR_OOM;
+    }
     if (!cuda_ok(cudaStreamSynchronize(st), "cudaStreamSynchronize") && s == G4_OK) s = G4_ERR_CUDA;
     cudaStreamDestroy(st);
   }
