@@ -1,6 +1,7 @@
 """Device-side plumbing around libg4: upload host weights with PyTorch, hold the borrowed
 tensors alive, and marshal calls.  No decoder arithmetic happens here."""
 import ctypes
+import operator
 
 import numpy as np
 import torch
@@ -222,6 +223,14 @@ def argmax_rows_static(logits, stream=None):
 _KV4_TYPES = {torch.float32: _g4.G4_DT_F32, torch.bfloat16: _g4.G4_DT_BF16, torch.float16: _g4.G4_DT_F16}
 
 
+def _kv4_int(name, v):
+    """A whole number that C's int32 holds (ctypes would pass its low 32 bits without a word)."""
+    v = operator.index(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} is {v}: 32 bits do not hold it")
+    return v
+
+
 def _kv4_array(name, t, shape, dtype, index):
     """Checks a contiguous array on device `index`; its address (None: NULL)."""
     if t is None:
@@ -251,6 +260,10 @@ class KV4Cache:
                  page_table=None, n_pages=None, track=False, device=None):
         self.index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
         self.device = torch.device("cuda", self.index)
+        n_slots, capacity, num_q_heads, num_kv_heads, head_dim, max_q_len, page_size = (
+            _kv4_int(name, v) for name, v in (
+                ("n_slots", n_slots), ("capacity", capacity), ("num_q_heads", num_q_heads),
+                ("num_kv_heads", num_kv_heads), ("head_dim", head_dim), ("max_q_len", max_q_len), ("page_size", page_size)))
         if page_size:
             if page_table is None or page_size < 0:
                 raise ValueError("a paged cache needs its page_table")
@@ -261,7 +274,8 @@ class KV4Cache:
         self.num_q_heads, self.num_kv_heads, self.head_dim = num_q_heads, num_kv_heads, head_dim
         self._table = page_table
         c = _g4.g4_kv4_config(n_slots, capacity, num_q_heads, num_kv_heads, head_dim, max_q_len, page_size,
-                              (page_table.numel() if n_pages is None else n_pages) if page_size else 0, int(track))
+                              _kv4_int("n_pages", page_table.numel() if n_pages is None else n_pages) if page_size else 0,
+                              int(track))
         h = ctypes.c_void_p()
         _g4.check(_g4.lib.g4_kv4_create(self.index, ctypes.byref(c), _ptr(page_table), ctypes.byref(h)),
                   "g4_kv4_create")
@@ -338,7 +352,7 @@ class KV4Cache:
     def read(self, slots, start, n_rows, counts=None, dtype=torch.bfloat16, stream=None):
         """(k, v) of rows start[i].. of slots[i], [n, n_rows, num_kv_heads, head_dim]; zeros where
         there is no row (at and beyond counts[i], on a missing page)."""
-        n = slots.numel()
+        n, n_rows = slots.numel(), _kv4_int("n_rows", n_rows)
         shape = (n, n_rows, self.num_kv_heads, self.head_dim)
         if dtype not in _KV4_TYPES:
             raise TypeError(f"rows cannot be given as {dtype}")
@@ -353,7 +367,7 @@ class KV4Cache:
     def account(self, slots, start, n_rows, counts=None, stream=None):
         """(positions, accumulated weights) of rows, [n, num_kv_heads, n_rows]; zeros where there is
         no row."""
-        n = slots.numel()
+        n, n_rows = slots.numel(), _kv4_int("n_rows", n_rows)
         shape = (n, self.num_kv_heads, n_rows)
         args = (self._seq("slots", slots, n), self._seq("start", start, n), self._seq("counts", counts, n))
         pos, weight = self._empty(shape, torch.int32, stream), self._empty(shape, torch.float32, stream)
@@ -369,6 +383,7 @@ class KV4Cache:
         n, q_len = slots.numel(), q.shape[1] if q.dim() == 4 else -1
         shape = (n, q_len, self.num_q_heads, self.head_dim)
         self._dense("q", q, shape, self._ta)
+        window = _kv4_int("window", window)
         args = (self._seq("slots", slots, n), self._seq("lens", lens, n), q_len, self._seq("q_lens", q_lens, n))
         given = out is not None
         if given:
@@ -383,7 +398,7 @@ class KV4Cache:
 
     def evict(self, slots, lens, budget, recent=0, stream=None):
         """Keep `budget` rows of every slot (see g4_kv4_evict); returns the new lens."""
-        n = slots.numel()
+        n, budget, recent = slots.numel(), _kv4_int("budget", budget), _kv4_int("recent", recent)
         args = (self._seq("slots", slots, n), self._seq("lens", lens, n))
         new = self._empty((n,), torch.int32, stream)
         status = _g4.lib.g4_kv4_evict(self.h, self._stream(stream), n, *args, budget, recent, new.data_ptr())
