@@ -6,7 +6,8 @@ an output row of d numbers is then a sum of many small terms, and independent er
 add up as their squares do.  Errors are taken per output row (token, head), as |error| / |row|:
 
 * rounding the result: each number is off by at most u = eps / 2 of itself, by u / sqrt(3) in the
-  root mean square; 0.65 u leaves room for rows of 64 numbers;
+  root mean square; 0.65 u leaves room for rows of 64 numbers.  However few numbers make up a row, it
+  is off by at most u: sum (u x_i)^2 = u^2 |x|^2 (`few`);
 * scores: a score is the sum of d products in d / 16 steps per query part (bf16 one, fp16 two, fp32
   three), each step off by at most 2^-23 of numbers that stay below 4 after the softmax scale.  An
   error ds of the scores changes the weights by the factor 1 + ds, and a row by about ds (twice
@@ -28,11 +29,11 @@ def score_error(dtype, d):
     return PARTS[dtype] * d / 16 * 4 * 2.0 ** -23
 
 
-def row_limit(dtype, d, keys):
+def row_limit(dtype, d, keys, few=False):
     u = torch.finfo(TYPES[dtype]).eps / 2
     weight = 2.0 ** -22 + (2.0 ** -24 if dtype == "f32" else 2.0 ** -17)
     steps = (keys / 64 + 16) * 3 * 2.0 ** -23
-    return 0.65 * u + 2 * score_error(dtype, d) + weight + steps
+    return (1.0 if few else 0.65) * u + 2 * score_error(dtype, d) + weight + steps
 
 
 def gain_limit(dtype, d):
@@ -73,8 +74,8 @@ def row_errors(out, want):
     return torch.where(size > 0, err / torch.where(size > 0, size, 1.0), torch.where(err > 0, math.inf, 0.0))
 
 
-def right(out, want, dtype, keys):
-    return bool((row_errors(out, want) <= row_limit(dtype, want.shape[-1], keys)).all())
+def right(out, want, dtype, keys, few=False):
+    return bool((row_errors(out, want) <= row_limit(dtype, want.shape[-1], keys, few)).all())
 
 
 def gains_right(gained, want, dtype, d):
