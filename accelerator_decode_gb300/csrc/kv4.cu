@@ -139,6 +139,8 @@ int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.nu
 bool kv4_block_path(const g4_kv4* op, int q_len, int dtype) {
   return dtype == G4_DT_BF16 && op->cfg.head_dim <= 256 && q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads) > kKv4BlockRows;
 }
+// Shared memory of kv4_plan in a kernel that has no other use for the table's.
+size_t kv4_plan_smem(const Kv4AttendArgs& a) { return (size_t)a.n_seq * 20 + 16 + (a.accumulate ? (size_t)a.c.n_slots * 4 : 0); }
 template <int D>
 void kv4_launch_block(const Kv4Work& op, Kv4AttendArgs a, cudaStream_t st) {
   const int rows = a.q_len * a.group;
@@ -146,7 +148,7 @@ void kv4_launch_block(const Kv4Work& op, Kv4AttendArgs a, cudaStream_t st) {
   a.lse_rows = a.row_tiles * kKv4M;
   a.join_inside = 0;
   launch(kv4_block_kernel<D, false>, dim3(op.sms), dim3(kKv4BlockThreads), Kv4Blk<D, false>::smem(a.n_seq), st, a);
-  launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, D / 16), dim3(kKv4M), (size_t)a.n_seq * 20 + 16,
+  launch(kv4_block_join_kernel<D>, dim3(a.n_seq * a.c.kvh * a.row_tiles, D / 16), dim3(kKv4M), kv4_plan_smem(a),
          st, a, op.sms);
   if (!a.accumulate) return;
   a.row_tiles = 1;  // the account cuts the keys alone into spans
@@ -187,7 +189,7 @@ void kv4_launch_attend(const Kv4Work& op, Kv4AttendArgs& a, cudaStream_t st) {
   const int gain_ctas = one && a.accumulate ? std::max(1, std::min(cdiv(a.c.capacity, 4 * kKv4Block), cdiv(8 * op.sms, items))) : 0;
   if (join_ctas + gain_ctas)
     launch(kv4_finish_kernel<D, DT>, dim3(items, join_ctas + gain_ctas), dim3(kKv4FinishThreads),
-           (size_t)a.n_seq * 20 + 16 + C::kQBytes, st, a, ctas, join_ctas);
+           kv4_plan_smem(a) + C::kQBytes, st, a, ctas, join_ctas);
   if (a.accumulate && !one)
     launch(kv4_gain_kernel<D, DT>, dim3(std::max(1, std::min(cdiv(a.c.capacity, 64), 8 * op.sms / a.n_seq)), a.n_seq, a.c.kvh),
            dim3(32 * kKv4GainWarps), C::kQBytes, st, a);

@@ -135,6 +135,7 @@ struct Kv4Att {
   // 28.7, 128 of them 55.5 / 49.2.
   static constexpr int kRegions = D == 256 || (D == 512 && DT != G4_DT_F32) ? 4 : 2;
   static constexpr int kOBytes = kRegions * D * 32;    // [region][D / 32][2][lane] float4
+  static_assert(kOBytes >= kKv4MaxSlots * 4, "the plan's table of slots lies where the sums will");
   static constexpr int kFixed = kQBytes + kOBytes + kWarps * 64 + 256;  // + running (max, sum) of every warp, barriers
   static __host__ __device__ size_t smem(int stages, int n_seq) {
     return (size_t)stages * kTile + kFixed + (size_t)n_seq * 20 + 16;
@@ -150,18 +151,27 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttendArgs& a, int len, int m,
   *tile0 = lo / KEYS;
   return m > 0 && len > 0 ? (len + KEYS - 1) / KEYS - *tile0 : 0;
 }
+// owner: shared scratch of one int per slot, for a call that accumulates: the first sequence that
+// names it.  (Each sequence looking through the ones before it, in every CTA, took 38 ms with 1,024
+// sequences.)
 template <int KEYS>
-__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, int* first, int4* seqs, bool report) {
+__device__ __forceinline__ void kv4_plan(const Kv4AttendArgs& a, int* first, int4* seqs, int* owner, bool report) {
+  if (a.accumulate) {
+    for (int s = threadIdx.x; s < a.c.n_slots; s += blockDim.x) owner[s] = a.n_seq;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
+      const int slot = __ldcg(a.slots + i);
+      if (slot >= 0 && slot < a.c.n_slots) atomicMin(owner + slot, i);
+    }
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
     int slot, len, m, t0;
     bool ok = kv4_seq(a, i, &slot, &len, &m);
     if (!ok && report) set_err(a.c.err, kv4_seq_error(a, slot));
-    if (a.accumulate && ok) {  // a slot that an earlier sequence names is skipped
-      int same = 0;
-#pragma unroll 4
-      for (int j = 0; j < i; ++j) same |= __ldcg(a.slots + j) == slot;
-      if (same && report) set_err(a.c.err, G4_DEV_BAD_SLOT);
-      if (same) len = 0;
+    if (a.accumulate && ok && owner[slot] != i) {  // a slot that an earlier sequence names is skipped
+      if (report) set_err(a.c.err, G4_DEV_BAD_SLOT);
+      len = 0;
     }
     if (!ok) {  // all its query rows get zeros
       len = 0;
@@ -831,7 +841,7 @@ __global__ void __launch_bounds__(Kv4Att<D, DT>::kThreads, Kv4Att<D, DT>::kMinCt
   pdl_wait();
   pdl_trigger();
   const int wide = __ldcg(a.c.wide) | a.plain;
-  kv4_plan<C::kKeys>(a, sh.first, sh.seqs, blockIdx.x == 0);
+  kv4_plan<C::kKeys>(a, sh.first, sh.seqs, reinterpret_cast<int*>(sh.os), blockIdx.x == 0);
   const int total = sh.first[a.n_seq];
   const int span = kv4_span(a, sh.first, gridDim.x);
   const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
@@ -923,7 +933,7 @@ __global__ void __launch_bounds__(kKv4FinishThreads) kv4_finish_kernel(const __g
   const bool join = (int)blockIdx.y < join_ctas;
   // What the first launch reads as well can be read before it has ended.
   const int wide = __ldcg(a.c.wide) | a.plain;
-  kv4_plan<C::kKeys>(a, first, seqs, false);
+  kv4_plan<C::kKeys>(a, first, seqs, first + a.n_seq + 2, false);
   const int slot = seqs[i].x, len = seqs[i].y, m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
   if (!join && n > 0) kv4_stage_q<D, DT>(a, qs, i, head, 0, n_rows, tid, kKv4FinishThreads);
   const int span = kv4_span(a, first, ctas);

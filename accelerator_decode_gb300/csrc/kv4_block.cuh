@@ -44,6 +44,7 @@ struct Kv4Blk {
   static constexpr int kTile = 4 * kHalf;                   // and of a tile: a ring stage
   static constexpr int kKRing = ACCOUNT ? 3 : 2, kVRing = ACCOUNT ? 0 : 1;  // stages: what fits beside the operands
   static constexpr int kOperand = kKv4N * D * 2;            // decoded keys or values of a tile
+  static_assert(2 * kOperand >= kKv4MaxSlots * 4, "the plan's table of slots lies where the keys will");
   static constexpr int kKBufs = ACCOUNT ? 2 : 1;            // pairs of decoded key tiles
   static constexpr int kSBufs = kKBufs;
   static constexpr int kCols = 512;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
   pdl_wait();
   pdl_trigger();
   const int wide = __ldcg(a.c.wide) | a.plain;
-  kv4_plan<kKv4N>(a, first, seqs, !ACCOUNT && blockIdx.x == 0);
+  kv4_plan<kKv4N>(a, first, seqs, reinterpret_cast<int*>(kop), !ACCOUNT && blockIdx.x == 0);
   kv4_fence_after();
   const uint32_t tmem = s->tmem;
   const int total = first[a.n_seq], span = kv4_span(a, first, gridDim.x);
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(128) kv4_block_join_kernel(const __grid_consta
   int* first = reinterpret_cast<int*>(seqs + a.n_seq);
   const int item = blockIdx.x, per_seq = a.c.kvh * a.row_tiles, tid = threadIdx.x;
   const int i = item / per_seq, x = item % per_seq, head = x / a.row_tiles, rt = x % a.row_tiles;
-  kv4_plan<kKv4N>(a, first, seqs, false);  // inputs of the first launch too: read before it ends
+  kv4_plan<kKv4N>(a, first, seqs, first + a.n_seq + 2, false);  // inputs of the first launch too: read before it ends
   const int m = seqs[i].z, n = seqs[i].w, n_rows = m * a.group;
   const int span = kv4_span(a, first, ctas), t0 = first[i] + n * x;
   const int c0 = (unsigned)t0 / (unsigned)span, c1 = n ? (int)((unsigned)(t0 + n - 1) / (unsigned)span) : c0 - 1;
