@@ -137,7 +137,7 @@ int kv4_row_tiles(const g4_kv4* op, int q_len) { return cdiv(q_len * (op->cfg.nu
 
 // Blocks of query tokens on the 5th-generation tensor cores (kv4_block.cuh).
 bool kv4_block_path(const g4_kv4* op, int q_len, int dtype) {
-  return dtype == G4_DT_BF16 && op->cfg.head_dim <= 256 && q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads) > kKv4BlockRows;
+  return dtype == G4_DT_BF16 && op->cfg.head_dim <= 256 && q_len * (op->cfg.num_q_heads / op->cfg.num_kv_heads) > kv4_block_rows(op->cfg.head_dim);
 }
 // Shared memory of kv4_plan in a kernel that has no other use for the table's.
 size_t kv4_plan_smem(const Kv4AttendArgs& a) { return (size_t)a.n_seq * 20 + 16 + (a.accumulate ? (size_t)a.c.n_slots * 4 : 0); }

@@ -1,5 +1,5 @@
 // Attention of blocks of query tokens over the 4-bit cache on the 5th-generation tensor cores,
-// for bf16 queries with more than kKv4BlockRows query rows (tokens x heads) per KV head and head
+// for bf16 queries with more than kv4_block_rows query rows (tokens x heads) per KV head and head
 // dims up to 256; and the account of the weights the rows received.
 //
 // An item is 128 query rows of one KV head.  Four warps decode tiles of 64 keys, and four of values,
@@ -32,7 +32,20 @@
 
 namespace g4 {
 
-constexpr int kKv4BlockRows = 32;   // more query rows than this per KV head take these kernels
+// More query rows than this per KV head take these kernels.  Their cost hardly depends on the rows up
+// to 128 an item; the other path decodes the keys once per eight rows.  Measured (bf16, eight query
+// heads on one KV head; microseconds here / on the other path; with the account, without it):
+//                 eight sequences of 8,000 rows      of 2,000                     one of 200
+//   D = 64,  96:    50.7 / 47.0,   32.8 / 24.6    36.2 / 36.5,  24.0 / 16.5    20.1 / 24.5
+//           128:    53.8 / 55.9,   36.8 / 28.7    37.5 / 41.2,  25.4 / 16.5    20.4 / 28.6
+//   D = 128, 64:    52.2 / 54.6,   34.9 / 28.7    36.7 / 32.9,  24.7 / 18.3    22.6 / 22.7
+//            80:    52.8 / 61.4,   35.6 / 29.5    37.4 / 36.9,  24.7 / 18.6    23.3 / 25.1
+//   D = 256, 48:    63.9 / 67.0,   43.0 / 34.9    41.6 / 38.8,  28.3 / 22.4    26.6 / 24.8
+//            64:    64.0 / 79.1,   43.7 / 40.5    41.1 / 43.2,  28.6 / 22.8    26.7 / 28.4
+//           512:   108.8 / 444,    63.2 / 209     62.5 / 186,   37.9 / 69.8    34.8 / 113
+// The border is where the account's calls break even: those without it would still gain a few
+// microseconds beyond, but a call's numbers do not depend on whether it accumulates.
+__host__ __device__ constexpr int kv4_block_rows(int d) { return d == 64 ? 96 : d == 128 ? 64 : 48; }
 constexpr int kKv4M = 128;          // query rows of an item
 constexpr int kKv4N = 64;           // keys of a tile
 constexpr int kKv4RunTiles = 16;    // account: tiles of a run at the most

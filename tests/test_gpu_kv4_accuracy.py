@@ -208,3 +208,47 @@ def test_blocks_of_strided_tokens(rt, d, track):
 def c_attend(fresh, q, order, lens):
     c, _, _, _ = fresh()
     return c.attend(q, order, i32(lens))
+
+
+@pytest.mark.parametrize("d,rows", [(64, 96), (64, 98), (128, 64), (128, 66), (256, 48), (256, 50)])
+@pytest.mark.parametrize("tokens", [True, False])
+def test_both_sides_of_the_block_kernels_border(rt, d, rows, tokens):
+    """The most query rows per KV head that the single-token path takes, and two more: as tokens of one
+    head, and as heads of as few tokens as there can be."""
+    q_len = rows if tokens else -(-rows // 64)
+    while rows % q_len or q_len > 64:
+        q_len = q_len - 1 if tokens else q_len + 1
+    group = rows // q_len
+    lens = [q_len, 700, 65, 2051]
+    c, q, order, kv = filled(rt, lens, 2, group, q_len, d, "bf16", 64, True, rows)
+    compare(c, q, order, kv, lens, "bf16", d, track=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_strided_blocks_of_128_rows(rt, d):
+    """Odd and 8-byte places once more, with rows enough for the block kernels at every width."""
+    n, t, m, heads, lens, order = 2, 150, 32, 4, [150, 77], i32([0, 1])
+    fresh = lambda: filled(rt, lens, 1, heads, m, d, "bf16", 16, True, 4)
+    c, q, _, _ = fresh()
+    want = c.attend(q, order, i32(lens), accumulate=True)
+    gained = c.account(order, i32([0, 0]), t)[1]
+    for shift, pad in ((8, 8), (4, 4), (1, 5)):
+        c, _, _, _ = fresh()
+        src = torch.full((n, heads, m, d + pad + shift), 9.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)[..., shift:shift + d]
+        src.copy_(q)
+        buf = torch.full((n, m, heads, d + pad + shift), 7.0, dtype=torch.bfloat16, device="cuda")
+        c.attend(src, order, i32(lens), accumulate=True, out=buf[..., shift:shift + d])
+        assert torch.equal(buf[..., shift:shift + d], want)
+        assert (buf[..., :shift] == 7).all() and (buf[..., shift + d:] == 7).all()
+        assert torch.equal(c.account(order, i32([0, 0]), t)[1], gained)
+
+
+def test_not_finite_query_stays_in_its_row_of_a_block(rt):
+    d, t, m = 128, 100, 16
+    c, q, order, _ = filled(rt, [t], 1, 8, m, d, "bf16", 0, False, 5)
+    clean = c.attend(q, order, i32([t]))
+    q[0, 1, 3, 5], q[0, 0, 6, 0], q[0, 15, 7, 9] = float("nan"), float("inf"), float("-inf")
+    out = c.attend(q, order, i32([t]))
+    bad = torch.zeros(m, 8, dtype=torch.bool, device="cuda")
+    bad[1, 3] = bad[0, 6] = bad[15, 7] = True
+    assert out[0][bad].isnan().all() and torch.equal(out[0][~bad], clean[0][~bad])
