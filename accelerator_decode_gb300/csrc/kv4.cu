@@ -179,10 +179,14 @@ void kv4_launch_attend(const Kv4Work& op, Kv4AttendArgs& a, cudaStream_t st) {
   const int room = (op.smem_optin + 1024) / C::kMinCtas - 1024 - (int)C::smem(0, a.n_seq);
   a.stages = kv4_ring_stages(room, C::kTile, C::kSets);
   const int items = a.n_seq * a.c.kvh * a.row_tiles;
-  // With items enough, or few tiles, no item is shared by many CTAs, and the last one to finish
-  // joins the parts (a launch less); else the parts of a few long items are joined by a second
-  // launch with CTAs enough for them.
-  a.join_inside = (long)items * kKv4Join >= ctas || cdiv(a.c.capacity, C::kKeys) <= kKv4Join;
+  // Parts of shared items are joined by the last CTA to finish one (a launch less), or by a second
+  // launch with CTAs enough for the parts of long items.  Inside: with more items than CTAs, where the
+  // second launch would have a CTA or more for each, and with few tiles a slot.  Measured, microseconds
+  // inside / second launch.  One sequence of 200 rows, D = 256: 11.0 / 11.6, D = 512 and 450 rows: 16.5 /
+  // 19.3; 512 sequences of 640, 256: 53.5 / 57.4, 1,024: 88.2 / 115.5; 1,024 of 300 rows, eight heads of
+  // 64: 116 / 167.  64 sequences of 640, 256: 20.5 / 16.6; 64 of 3,000, 64: 18.5 / 14.4; eight of 8,000,
+  // eight heads of 128: 30.7 / 26.8; 64 of those (512 items, 456 CTAs): 109.2 / 108.6.
+  a.join_inside = items > ctas || cdiv(a.c.capacity, C::kKeys) <= kKv4Join;
   launch(kv4_attend_kernel<D, DT>, dim3(ctas), dim3(C::kThreads), C::smem(a.stages, a.n_seq), st, a);
   const int join_ctas = a.join_inside ? 0 : std::max(1, D * 2 / kKv4FinishThreads);
   const bool one = a.row_tiles == 1;  // the account of a single row tile rides along with the join

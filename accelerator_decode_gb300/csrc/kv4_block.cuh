@@ -48,7 +48,8 @@ namespace g4 {
 __host__ __device__ constexpr int kv4_block_rows(int d) { return d == 64 ? 96 : d == 128 ? 64 : 48; }
 constexpr int kKv4M = 128;          // query rows of an item
 constexpr int kKv4N = 64;           // keys of a tile
-constexpr int kKv4RunTiles = 16;    // account: tiles of a run at the most
+constexpr int kKv4RunTiles = 16;    // account: tiles of a run at the most (8 and 32 take the same time: their
+                                    // gains lie in shared memory, and few CTAs have longer runs)
 constexpr int kKv4BlockThreads = 512;
 
 template <int D, bool ACCOUNT>
