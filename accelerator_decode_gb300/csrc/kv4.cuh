@@ -315,8 +315,10 @@ __device__ __forceinline__ int kv4_next_position(const Kv4RowArgs& a, int slot, 
   const long base = row0 ? __ldcg(a.c.base + (size_t)slot * a.c.kvh + h) : 0;
   return (int)min(base + row, (long)INT_MAX);
 }
-// The bases after an append of `count` rows from row0 on: given positions lift a base to where the row
-// behind them would follow the newest of them.  A tracked cache's append has one CTA more per
+// The base that gives row `rows`, the first behind the held ones, the position `next`.
+__device__ __forceinline__ int kv4_base(long next, int rows) { return (int)max(next - rows, (long)INT_MIN); }
+// The bases after an append of `count` rows from row0 on: the row behind given positions follows the
+// newest of them, or what row0 would have had.  A tracked cache's append has one CTA more per
 // sequence for it, so that a long array of positions is read beside the rows (2 x 1,988 positions
 // ahead of a CTA's rows made a call 7 us longer).  Nothing else of the call reads a base that this
 // changes: the others need one only where no positions are given and row0 > 0.
@@ -330,18 +332,21 @@ __device__ __forceinline__ void kv4_set_bases(const Kv4RowArgs& a, int i, int sl
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   const int share = max(1, warps / a.c.kvh);  // warps of a head; those of one head are neighbours
   __shared__ int most[64];
-  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) most[h] = row0 ? __ldcg(base + h) : INT_MIN;
+  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) most[h] = INT_MIN;
   __syncthreads();
   for (int h = (threadIdx.x >> 5) / share; h < a.c.kvh; h += warps / share) {
     const int* p = a.positions + ((size_t)i * a.c.kvh + h) * a.n_rows;
     int m = INT_MIN;
 #pragma unroll 4
-    for (int t = (threadIdx.x >> 5) % share * 32 + lane; t < count; t += 32 * share) m = max(m, max(__ldcg(p + t), INT_MIN + (2 << 20)) - (row0 + t));
+    for (int t = (threadIdx.x >> 5) % share * 32 + lane; t < count; t += 32 * share) m = max(m, __ldcg(p + t));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if (lane == 0) atomicMax(&most[h], m);
   }
   __syncthreads();
-  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) base[h] = most[h];
+  for (int h = threadIdx.x; h < a.c.kvh; h += blockDim.x) {
+    const long next = max((long)most[h] + 1, row0 ? (long)__ldcg(base + h) + row0 : LONG_MIN);
+    base[h] = kv4_base(next, row0 + count);
+  }
 }
 
 // ------------------------------------------------------------------------------ append
@@ -869,11 +874,14 @@ template <bool RANKS>
 __device__ __forceinline__ void kv4_select(const Kv4EvictArgs& a, int i, int h, int slot, int len, uint32_t* ranks) {
   __shared__ int hist[256];
   __shared__ int counts[3][kKv4EvictWarps];
-  __shared__ int sh_newest, sh_digit, sh_want, sh_all;
+  __shared__ int sh_newest, sh_base, sh_digit, sh_want, sh_all;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto at = [&](int r) { return kv4_block(a.c, slot, h, r / kKv4Block) * kKv4Block + r % kKv4Block; };
   // newest position; the positions wait where the ranks will be
-  if (tid == 0) sh_newest = INT_MIN;
+  if (tid == 0) {
+    sh_newest = INT_MIN;
+    sh_base = __ldcg(a.c.base + (size_t)slot * a.c.kvh + h);
+  }
   if (tid < 256) hist[tid] = 0;
   __syncthreads();
   int newest = INT_MIN;
@@ -887,7 +895,6 @@ __device__ __forceinline__ void kv4_select(const Kv4EvictArgs& a, int i, int h, 
   if (lane == 0) atomicMax(&sh_newest, newest);
   __syncthreads();
   const long oldest_safe = (long)sh_newest - a.recent;  // safe: position > this
-  if (tid == 0) a.c.base[(size_t)slot * a.c.kvh + h] = (int)max((long)sh_newest + 1 - a.budget, (long)INT_MIN);
   auto make = [&](int p, float w) { return (long)p > oldest_safe ? 0xFFFFFFFFu : kv4_rank_bits(w); };
   auto rank = [&](int r) { return RANKS ? ranks[r] : make(__ldcg(a.c.pos + at(r)), __ldcg(a.c.weight + at(r))); };
   // the budget-th largest rank: `prefix` after the passes, of which the first `want` rows stay
@@ -984,10 +991,14 @@ __device__ __forceinline__ void kv4_select(const Kv4EvictArgs& a, int i, int h, 
     hole0 += __popc(hole);
     mover0 += __popc(mover);
   });
-  if (tid == 0) a.n_moves[(size_t)i * a.c.kvh + h] = total;
+  if (tid == 0) {
+    a.n_moves[(size_t)i * a.c.kvh + h] = total;
+    // the next row still follows every position there was, the evicted ones too
+    a.c.base[(size_t)slot * a.c.kvh + h] = kv4_base(max((long)sh_newest + 1, (long)sh_base + len), a.budget);
+  }
 }
 
-__global__ void __launch_bounds__(kKv4EvictThreads) kv4_select_kernel(const Kv4EvictArgs a) {
+__global__ void __launch_bounds__(kKv4EvictThreads, 1) kv4_select_kernel(const Kv4EvictArgs a) {
   extern __shared__ uint32_t kv4_ranks[];
   const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   pdl_wait();

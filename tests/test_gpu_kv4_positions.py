@@ -118,3 +118,35 @@ def test_positions_in_a_graph(rt):
         assert set(range(budget + 3, budget + 9)) <= set(p.tolist()) and p.max() == budget + 8
         assert len(set(p.tolist())) == budget
     assert c.device_error() == (0, 0)
+
+
+def test_recent_rows_stay_recent(rt):
+    """A slot put back out of order goes on with the next position, not a later one, so that the rows
+    that were recent still are; evictions one after the other do not step back."""
+    d, kvh = 64, 2
+    c = rt.KV4Cache(2, 64, kvh, kvh, d, track=True)
+    k = rows(1, 40, kvh, d, 1)
+    order = torch.stack([torch.randperm(30, generator=torch.Generator().manual_seed(h)) for h in range(kvh)])
+    at = int((order[0] == 29).nonzero())
+    order[0, at], order[0, 0] = int(order[0, 0]), 29                # the newest at row 0
+    pos = order.to(torch.int32).cuda()[None].contiguous()
+    for cuts in ((0, 30), (0, 11, 30), (0, 1, 2, 30)):                                   # in one call, in several
+        for a, b in zip(cuts, cuts[1:]):
+            c.append(k[:, a:b], k[:, a:b], i32([1]), i32([a]), positions=pos[:, :, a:b].contiguous())
+        c.append(k[:, :1], k[:, :1], i32([1]), i32([30]))
+        assert held(c, 1, 31)[:, 30].tolist() == [30, 30], cuts
+    assert c.evict(i32([1]), i32([31]), 12, 12).tolist() == [12]
+    assert np.sort(held(c, 1, 12), 1).tolist() == [list(range(19, 31))] * kvh
+    # the newest rows go by weight (recent 0): their positions are not given again
+    w = torch.ones(1, kvh, 20, device="cuda")
+    w[..., 15:] = 0
+    c.append(k[:, :20], k[:, :20], i32([0]), i32([0]), weights=w)
+    assert c.evict(i32([0]), i32([20]), 15, 0).tolist() == [15]
+    assert c.evict(i32([0]), i32([15]), 10, 0).tolist() == [10]
+    c.append(k[:, :2], k[:, :2], i32([0]), i32([10]))
+    assert held(c, 0, 12).tolist() == [list(range(10)) + [20, 21]] * kvh
+    # rows that the caller takes back (refused drafts) give their positions back
+    c.append(k[:, :5], k[:, :5], i32([0]), i32([12]))
+    c.append(k[:, :1], k[:, :1], i32([0]), i32([13]))
+    assert held(c, 0, 14)[:, 12:].tolist() == [[22, 23]] * kvh
+    assert c.device_error() == (0, 0)
