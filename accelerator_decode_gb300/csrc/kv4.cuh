@@ -354,9 +354,10 @@ __device__ __forceinline__ void kv4_set_bases(const Kv4RowArgs& a, int i, int sl
 // the four lanes of a group sharing their largest magnitude: short chains, small scattered
 // stores.  In large ones a warp codes a whole block of 16 rows in the layout's own order, so that
 // codes leave in 8-byte pieces and most groups lie in one lane (kv4_by_blocks has the rule).
-// Bound by latency in small calls (one row of eight sequences: 4 us), by issue in large ones:
-// 16 x 2,100 tokens, four heads of 128 in bf16 (78 MB, 12 us at the measured copy rate) take 27
-// us, 2.9 TB/s; a number costs about eight instructions.
+// Bound by latency in small calls (one row of eight sequences: 4 us).  Large ones: 16 x 2,100 tokens,
+// four heads of 128 in bf16, ragged (67.5 MB, 10 us at the measured copy rate) take 26 us, 2.6 TB/s.
+// A number costs 17 instructions, which fill half of the issue slots; the other half waits for loads,
+// with 38% of the warps that an SM could hold (72 registers a thread).
 constexpr int kKv4RowThreads = 256;
 
 template <int D>
@@ -420,9 +421,11 @@ __global__ void __launch_bounds__(kKv4RowThreads) kv4_append_kernel(const Kv4Row
 }
 
 // -------------------------------------------------------------------------------- read
-// The inverse, in the same two forms.  Bound by latency in small calls (639 rows of 256: 3.6 us),
-// in large ones by the stores (eight contexts of up to 8,639 rows of 512 to fp16, 142 MB: 41 us,
-// 3.4 TB/s; 32 x 2,048 rows, four heads of 128, 153 MB: 30 us, 5.1 TB/s).
+// The inverse, in the same two forms.  Bound by latency in small calls (639 rows of 256: 3.6 us).  Large
+// ones: 32 x 2,048 rows, four heads of 128 to fp16 (172 MB) take 31 us, 5.6 TB/s, issue slots 62% busy.
+// Eight contexts of up to 8,639 rows of 512 to fp16 (173 MB with the zeros behind the shorter ones)
+// take 42 us, 4.2 TB/s: two fifths of the stalls are loads and over a quarter instruction fetches of
+// the body unrolled over 512 numbers, with 28% of the warps that an SM could hold (84 registers a thread).
 template <int D>
 __global__ void __launch_bounds__(kKv4RowThreads) kv4_read_kernel(const Kv4RowArgs a) {
   using O = Kv4Off<D>;

@@ -13,15 +13,22 @@
 // shared-memory ring with bulk copies; each consumer warp takes whole blocks of 16 keys through scores, running softmax and output with
 // no synchronisation with the other warps until the item ends.  Both products run on the tensor
 // cores with the cache as the M operand (m16n8k16: 16 keys, or 16 numbers of the value, by 8
-// query rows), so eight query rows waste nothing and 4-bit codes go from a 16-byte load to the
-// operand registers through 1.25 ALU operations and one bf16 operation per pair.
+// query rows), so eight query rows of a KV head fill the N operand (four leave half of it empty), and
+// 4-bit codes go from a 16-byte load to the operand registers through 1.25 ALU operations and one
+// bf16 operation per pair.
 //
 // Bound: the dependent chain of a block (load, decode, scores, softmax, values), with 8 to 12
-// consumer warps on an SM to hide it.  64 sequences of up to 8,192 rows, eight KV heads of 128, four query heads
-// each (456 MB, 68 us at the measured copy rate): 109 us, 4.2 TB/s; loading alone takes 88 us
-// and the arithmetic on resident tiles 107.  At 16 sequences the issue slots are 48% busy, the
-// tensor cores 26%, DRAM 37%.  512-wide rows, eight sequences of up to 8,639, with the account: 43
-// us.  One sequence of 200 rows: 11 us, mostly one launch's start, ring and join.
+// consumer warps on an SM to hide it.  64 sequences of up to 8,192 rows, eight KV heads of 128, four
+// query heads each (456 MB, 68 us at the measured copy rate): 109 us, 4.2 TB/s; loading alone takes 88
+// us and the arithmetic on resident tiles 107.  At 16 sequences the issue slots are 48% busy, the
+// tensor cores 26%, DRAM 37%.  512-wide rows, eight sequences of up to 8,639: bf16 33 us (17% of the
+// issue slots, 9% of the tensor cores, DRAM 11%), fp32 40; of the 11 cycles between a warp's
+// instructions 3.5 wait for instruction fetches and 2.5 at barriers, three tiles a warp.  64 windows of
+// 512 rows of 256, fp32: 13 us and 7 for the join, two tiles a CTA.  One sequence of 200 rows: 11 us; of a
+// cold launch half are instruction fetches and a fifth barriers.
+//
+// The output's sums fill the registers.  Compiled, the 128-wide kernels spill 160 (fp32) and 24 (fp16)
+// bytes of their 128 registers a thread, the 64-wide fp32 one 20, the others none.
 #pragma once
 #include "kv4.cuh"
 #include "mbar.cuh"

@@ -24,9 +24,10 @@
 // buffers, and so have the decoded keys.
 //
 // Eight sequences of up to 8,000 rows, 512 query rows each (64 tokens, eight heads of 256): attention 54
-// us (17.5 GFLOP, 0.32 PFLOP/s), join 13, account 42 (8.7 GFLOP).  The tensor cores are busy 40% of
-// the first; what bounds it is the chain scores -> exponentials -> product of each pair of tiles
-// on 128 softmax threads, with the decoding behind it.
+// us (26.1 GFLOP, 0.48 PFLOP/s; 39.1 and 0.72 with the weights' second part), join 13, account 43 (13.0
+// GFLOP).  The tensor cores are busy 40% of the first; what bounds it is the chain scores ->
+// exponentials -> product of each pair of tiles on 128 softmax threads, with the decoding behind it.
+// Compiled, the attention spills 8 to 20 bytes of its 128 registers a thread.
 #pragma once
 #include "kv4_attend.cuh"
 
