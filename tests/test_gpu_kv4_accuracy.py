@@ -252,3 +252,10 @@ def test_not_finite_query_stays_in_its_row_of_a_block(rt):
     bad = torch.zeros(m, 8, dtype=torch.bool, device="cuda")
     bad[1, 3] = bad[0, 6] = bad[15, 7] = True
     assert out[0][bad].isnan().all() and torch.equal(out[0][~bad], clean[0][~bad])
+
+
+def test_more_sequences_than_the_block_kernels_hold(rt):
+    """Token blocks of 400 sequences: their spans do not fit beside a block kernel's operands."""
+    lens = [13 + (i * 37) % 60 for i in range(400)]
+    c, q, order, rows = filled(rt, lens, 1, 8, 13, 64, "bf16", 16, True, 9)
+    compare(c, q, order, rows, lens, "bf16", 64, track=True)

@@ -20,10 +20,12 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def check_one_hot(rt, dtype, d, q_len, scale, grow, kvh=2, group=4, page=0):
-    """Rows times `grow`; the largest score of every output row is far above the next."""
+def check_one_hot(rt, dtype, d, q_len, scale, grow, kvh=2, group=4, page=0, rising=0.0):
+    """Rows times `grow`; the largest score of every output row is far above the next.  rising: keys
+    grow by this power of two from row to row as well."""
     n, lens = 2, [150, 67]
     q, k, v = acc.inputs(n, 150, kvh, group, q_len, d, dtype, d + q_len)
+    k = k * (2.0 ** (rising * torch.arange(150.0)))[:, None, None].to(k.dtype)
     kw = {}
     if page:
         kw["page_table"] = torch.randperm(20, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(2, 10).cuda()
@@ -76,3 +78,11 @@ def test_largest_scale(rt):
 @pytest.mark.parametrize("dtype,d,q_len", [("f32", 64, 1), ("bf16", 512, 1), ("bf16", 64, 20), ("bf16", 128, 64), ("bf16", 256, 33)])
 def test_large_rows(rt, dtype, d, q_len, grow):
     check_one_hot(rt, dtype, d, q_len, 0.0, grow, page=16)
+
+
+@pytest.mark.parametrize("rising", [0.1, 0.25, -0.25])
+@pytest.mark.parametrize("dtype,d,q_len", [("f32", 256, 1), ("bf16", 512, 1), ("f32", 64, 7), ("bf16", 64, 30), ("bf16", 128, 64),
+                                           ("bf16", 256, 33)])
+def test_scores_that_grow_and_shrink(rt, dtype, d, q_len, rising):
+    """Keys from small to huge, and from huge to small: references are raised past every border."""
+    check_one_hot(rt, dtype, d, q_len, 0.0, 2.0 ** 13 if rising > 0 else 2.0 ** 24, page=16, rising=rising)
