@@ -1,5 +1,5 @@
 // C entry points of the 4-bit KV cache (include/g4.h, g4_kv4_*): argument checks, the handle
-// with its cache and workspace, and the launches of kv4.cuh and kv4_attend.cuh.
+// with its cache and workspace, and the launches of kv4.cuh, kv4_attend.cuh and kv4_block.cuh.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -24,7 +24,7 @@ struct g4_kv4 {
   size_t bytes = 0;
   int fail_at = 0, n_allocs = 0;  // allocation-failure injection (G4_FAIL_ALLOC_AT), as in g4_create
   Kv4Work work;
-  int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity]
+  int *holes = nullptr, *movers = nullptr;    // evict: [n_slots][kvh][capacity / 2]
   int* n_moves = nullptr;                     // [n_slots][kvh]
 };
 

@@ -419,8 +419,9 @@ g4_status g4_kv4_attend(g4_kv4* op, g4_stream stream, int32_t n_seq, const int32
                         const g4_kv4_tensor* q, const g4_kv4_tensor* out);
 
 /* Cut slots back to `budget` rows per KV head (track): of rows 0 .. d_lens[i] - 1 the ones at the
- * newest `recent` positions (position > newest - recent) are kept first, then those with the
- * largest accumulated weight (a NaN ranks last), equal ones by the lowest row.  Kept rows below
+ * newest `recent` positions (position > newest - recent) are kept first (the lowest ones, should
+ * more than `budget` share them), then those with the largest accumulated weight (a NaN ranks
+ * last), equal ones by the lowest row.  Kept rows below
  * the budget stay where they are; the kept rows from beyond it move, in row order, into the
  * places of the evicted rows below it, in row order, each with its position and account.
  * d_new_lens[i] = min(d_lens[i], budget); it must not be d_lens.  KV heads choose for themselves.

@@ -150,3 +150,22 @@ def test_recent_rows_stay_recent(rt):
     c.append(k[:, :1], k[:, :1], i32([0]), i32([13]))
     assert held(c, 0, 14)[:, 12:].tolist() == [[22, 23]] * kvh
     assert c.device_error() == (0, 0)
+
+
+def test_more_rows_at_recent_positions_than_the_budget(rt):
+    """Positions that rows share: the lowest rows stay, whatever their weights."""
+    d = 64
+    c = rt.KV4Cache(1, 40, 1, 1, d, track=True)
+    k = rows(1, 40, 1, d, 1)
+    pos = torch.zeros(1, 1, 40, dtype=torch.int32, device="cuda")
+    pos[..., 5:] = 9
+    pos[..., 38:] = 8
+    w = torch.rand(1, 1, 40, generator=torch.Generator().manual_seed(1)).cuda()
+    c.append(k, k, i32([0]), i32([0]), positions=pos, weights=w)
+    before = c.read(i32([0]), i32([0]), 40, dtype=torch.float32)[0]
+    assert c.evict(i32([0]), i32([40]), 7, 2).tolist() == [7]
+    p, gw = c.account(i32([0]), i32([0]), 7)
+    kept = [7, 8, 9, 10, 11, 5, 6]               # rows 5 and 6 stay in place, 7 .. 11 fill rows 0 .. 4
+    assert (p == 9).all() and torch.equal(gw[0, 0], w[0, 0, kept])
+    assert torch.equal(c.read(i32([0]), i32([0]), 7, dtype=torch.float32)[0][0], before[0, kept])
+    assert c.device_error() == (0, 0)
