@@ -8,10 +8,11 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libg4.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("g4.cu", "kv4.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("g4.cu", "kv4.cu", "pages.cu", "attn16.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in (
     "common.cuh", "gemv.cuh", "gemv_s.cuh", "attn.cuh", "attn_mqa.cuh", "misc.cuh", "gemm_tc.cuh", "mega.cuh",
-    "host.h", "mbar.cuh", "kv4_layout.h", "kv4_host.h", "kv4.cuh", "kv4_attend.cuh", "kv4_block.cuh")]
+    "host.h", "mbar.cuh", "kv4_layout.h", "kv4_host.h", "kv4.cuh", "kv4_attend.cuh", "kv4_block.cuh",
+    "tc05.cuh", "pages_layout.h", "pages.cuh", "paged_host.h", "attn16.cuh", "attn16_decode.cuh")]
 HEADERS.append(os.path.join(os.path.dirname(HERE), "include", "g4.h"))
 # the flags are in this file: an object older than it may have been compiled with others
 DEPS = SOURCES + HEADERS + [os.path.abspath(__file__)]

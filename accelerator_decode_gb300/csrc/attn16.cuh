@@ -1,0 +1,742 @@
+// Attention over 16-bit keys and values on the 5th-generation tensor cores: whole prompts (causal,
+// packed sequences, optionally a sliding window), and the part of a batch's tokens over a prefix that
+// all its sequences share.
+//
+//   s_j = scale * q . K_j     p_j = 2^(s_j log2 e - m)     o = sum p_j V_j / sum p_j
+//
+// The query rows of a KV head are its tokens' heads, token after token (row t * G + g), so that any
+// number of heads per KV head fills the 128 rows of a product.  A CTA takes items of NQ blocks of 128
+// such rows past tiles of 128 keys:
+//   one warp copies tiles of keys and values by TMA into a ring of 128-byte-swizzled stages,
+//   two warps copy an item's queries,
+//   one thread issues S = Q K^T (both operands shared, fp32 in tensor memory) and O += P V (P in
+//   tensor memory, in the columns of the S that it was made of),
+//   four warps for each block of rows take a row per thread: maximum, exponentials, sum.
+// With heads up to 128 two blocks of rows share each tile (NQ 2): while one's weights are made, the
+// other's products run.  Wider heads leave room for one block's output (256 columns of the 512); its
+// scores then have two buffers, and the next tile's product runs while a tile's weights are made.
+// 512-wide heads take two items per block of rows, each with half of the values' columns and scores of
+// its own: half as many products again, where the whole output would leave no column for scores.
+//
+// A row's reference m is raised, and its output so far rescaled, only when a score exceeds it by 2^8:
+// weights up to 256 lose nothing in fp32, nor in P.  P is rounded to the values' 16-bit type (the
+// operands of a product have one type): each weight is off by at most 2^-8 of itself (bf16; fp16:
+// 2^-11, and weights below 2^-14 by up to 2^-25), independently of the others, while the sum that
+// divides them is of the unrounded ones.
+#pragma once
+#include <cuda.h>
+
+#include "tc05.cuh"
+
+namespace g4 {
+
+constexpr int kAttM = 128;  // query rows of a block
+constexpr int kAttN = 128;  // keys of a tile
+
+template <int D>
+struct Att16 {
+  static constexpr int NQ = D <= 128 ? 2 : 1;
+  static constexpr int DV = D == 512 ? 256 : D;           // values' columns of an item
+  static constexpr int HV = D / DV;                       // items of a block of rows
+  static constexpr int kSlab = kAttN * 128;               // 128 rows of 64 numbers
+  static constexpr int kStage = D == 64 ? kSlab : 2 * kSlab;
+  static constexpr int KS = D * 2 * kAttN / kStage;       // stages of a tile of keys, by their columns
+  static constexpr int VS = DV * 2 * kAttN / kStage;      // and of values, by their rows
+  static constexpr int kVRows = kAttN / VS;               // rows of a stage of values
+  static constexpr int kStages = D == 64 ? 8 : D == 512 ? 3 : 5;
+  static constexpr int kQ = NQ * kAttM * D * 2;
+  static constexpr int kSoftWarps = 4 * NQ;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr int kColS = NQ * DV;                   // tensor memory: outputs, then two buffers of scores
+  static constexpr size_t kSmem = 1024 + kQ + (size_t)kStages * kStage + 512;
+};
+
+struct Att16Item {
+  int row0;       // first packed row of the sequence
+  int r0, rows;   // first query row of the item; query rows of the sequence
+  int head, half;
+  int lo, hi;     // keys lo .. hi - 1 of the sequence
+  int part;       // prefix: slot of its partial result
+};
+
+struct Att16Bars {
+  uint64_t full[8], empty[8], sfull[2], pfull[2], pvdone[2], qfull, qdone, ifull[2], iempty[2], vneed, vtail, drained;
+  Att16Item item[2];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Att16Bars) <= 512, "barriers");
+
+struct Att16Args {
+  const uint16_t* q;
+  uint16_t* out;
+  const uint16_t* v;  // prompt: for rows whose unseen keys carry values that are not finite
+  const uint16_t* k;
+  long q_row, q_head, o_row, o_head, k_row, k_head, v_row, v_head;  // strides in elements
+  int q_vec, o_vec;   // 16-byte accesses
+  int group, kvh;
+  float scale;        // times log2 e
+  int* err;
+  // prompt
+  const int* offsets;  // [n_seq + 1]
+  int n_seq, n_rows, window;
+  int zero_rest;       // rows in front of the first sequence and behind the last become zeros
+  unsigned* ticket;    // [2]: the next item, CTAs that are done
+  // prefix
+  const int *table, *slots, *lens;
+  int n_slots, n_pages, log_page, max_pages;
+  int keys, splits, tiles_per;  // keys of the prefix; parts of a block of rows, of tiles_per tiles each
+  float* part_o;       // [part][NQ * 128 rows][D]
+  float2* part_ml;     // [part][NQ * 128 rows]
+};
+
+__device__ __forceinline__ float att_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two numbers rounded to the 16-bit type (BF: bf16, else fp16), the first in the low half.
+template <bool BF>
+__device__ __forceinline__ uint32_t att_pack(float lo, float hi) {
+  uint32_t r;
+  if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ float att_float(uint16_t u) {
+  if (BF) return __uint_as_float((uint32_t)u << 16);
+  float f;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(u));
+  return f;
+}
+__device__ __forceinline__ bool att_finite(float x) { return fabsf(x) < INFINITY; }
+
+// kind::f16: operands of the type, fp32 result, M 128.
+template <bool BF>
+__device__ __forceinline__ constexpr uint32_t att_idesc(int n, bool b_leading) {
+  return (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (b_leading ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kAttM >> 4) << 24);
+}
+__device__ __forceinline__ void att_tma3(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(su32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void att_tma2(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(su32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(su32(bar))
+      : "memory");
+}
+// Waits for at most two seconds (a row that att_repair takes anew keeps its CTA for some tenths of one);
+// false when the time is up, or was for another thread of the CTA.
+__device__ __forceinline__ bool att_wait(uint64_t* b, uint32_t parity, Att16Bars* s) {
+  if (mbar_try(b, parity)) return true;
+  volatile int* const abort = reinterpret_cast<volatile int*>(&s->abort);
+  uint64_t now, end = 0;
+  while (!*abort) {
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try(b, parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+    if (end == 0) end = now + 2000000000ull;
+    else if (now > end) *abort = 1;
+  }
+  return false;
+}
+
+// The item that a role works on next (row0 < 0: none is left).  Every thread of the role calls it.
+struct Att16Items {
+  Att16Bars* s;
+  int n = 0;
+  __device__ __forceinline__ bool next(Att16Item& it) {
+    const int b = n & 1;
+    const bool ok = att_wait(&s->ifull[b], (n >> 1) & 1, s);
+    it = s->item[b];
+    mbar_arrive(&s->iempty[b]);
+    ++n;
+    return ok && it.row0 >= 0;
+  }
+};
+// Tiles of an item, and those that its second block of rows (y 1) or its first (y 0) sees any key of.
+template <int NQ>
+struct Att16Tiles {
+  int n, a1, b0;  // tiles; block 0: 0 .. a1 - 1, block 1: b0 .. n - 1 (b0 = n: it has no rows)
+  __device__ __forceinline__ Att16Tiles(const Att16Item& it, int group, int window, bool causal) {
+    n = (it.hi - it.lo + kAttN - 1) / kAttN;
+    a1 = n;
+    b0 = n;
+    if (NQ == 2 && it.r0 + kAttM < it.rows) {
+      b0 = 0;
+      if (causal) {
+        const int last = (it.r0 + kAttM - 1) / group, first = (it.r0 + kAttM) / group;
+        a1 = (last + 1 - it.lo + kAttN - 1) / kAttN;
+        if (window > 0) b0 = max(0, first - window + 1 - it.lo) / kAttN;
+      }
+    }
+  }
+  __device__ __forceinline__ bool sees(int y, int j) const { return y ? j >= b0 : j < a1; }
+};
+
+// The slot that the shared pages' names are read from: the first of the batch that holds their `keys` rows (-1: none does).
+// A warp's threads call it together.
+__device__ __forceinline__ int att_shared_slot(const int* slots, const int* lens, int n_seq, int n_slots, int keys) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < n_seq; i0 += 32) {
+    const int slot = i0 + lane < n_seq ? __ldcg(slots + i0 + lane) : -1;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, slot >= 0 && slot < n_slots && __ldcg(lens + max(slot, 0)) >= keys);
+    if (who) return __shfl_sync(0xFFFFFFFFu, slot, __ffs(who) - 1);
+  }
+  return -1;
+}
+
+// Finite values hidden from a row do not reach it: their weights are zero.  Hidden infinities and NaNs
+// would (0 * inf).  So a row whose weights add up to a finite sum and whose output is not finite looks
+// at the values that it sees, column by column, and where those are all finite takes its sum anew.
+// Rare and slow; row, q and out are the row's own.
+template <int D, bool BF>
+__device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, uint16_t* out, int row0, int head, int col0,
+                                        int cols, int first, int last, float m, float l) {
+  const uint16_t* k = a.k + (long)row0 * a.k_row + (long)head * a.k_head;
+  const uint16_t* v = a.v + (long)row0 * a.v_row + (long)head * a.v_head;
+  for (int c = col0; c < col0 + cols; c += 16) {
+    uint32_t bad = 0;
+    for (int e = 0; e < 16; ++e) bad |= (uint32_t)!att_finite(att_float<BF>(out[c + e])) << e;
+    if (!bad) continue;
+    for (int j = first; j <= last && bad; ++j)
+      for (int e = 0; e < 16; ++e)
+        if (!att_finite(att_float<BF>(v[(long)j * a.v_row + c + e]))) bad &= ~(1u << e);
+    if (!bad) continue;
+    float sum[16];
+    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+    for (int j = first; j <= last; ++j) {
+      float dot = 0.f;
+      for (int e = 0; e < D; ++e) dot = fmaf(att_float<BF>(q[e]), att_float<BF>(k[(long)j * a.k_row + e]), dot);
+      const float p = att_exp2(fmaf(dot, a.scale, -m));
+      for (int e = 0; e < 16; ++e)
+        if ((bad >> e) & 1) sum[e] = fmaf(p, att_float<BF>(v[(long)j * a.v_row + c + e]), sum[e]);
+    }
+    for (int e = 0; e < 16; ++e)
+      if ((bad >> e) & 1) out[c + e] = (uint16_t)att_pack<BF>(sum[e] / l, 0.f);
+  }
+}
+
+template <int D, bool BF, bool PREFIX>
+__global__ void __launch_bounds__(Att16<D>::kThreads, 1)
+    att16_kernel(const Att16Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = Att16<D>;
+  constexpr int NQ = C::NQ, DV = C::DV;
+  extern __shared__ __align__(16) uint8_t att_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(att_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qop = base;
+  uint8_t* ring = base + C::kQ;
+  Att16Bars* s = reinterpret_cast<Att16Bars*>(ring + C::kStages * C::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s->sfull[i], 1);
+      mbar_init(&s->pfull[i], 4);
+      mbar_init(&s->pvdone[i], 1);
+      mbar_init(&s->ifull[i], 1);
+      mbar_init(&s->iempty[i], 32 * C::kSoftWarps + 1 + 64);
+    }
+    mbar_init(&s->qfull, 64);
+    mbar_init(&s->qdone, 1);
+    mbar_init(&s->vneed, 1);
+    mbar_init(&s->vtail, 64);
+    mbar_init(&s->drained, 1);
+    s->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == C::kSoftWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&s->tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_fence_before();
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+
+  if (warp == C::kSoftWarps + 1) {
+    // ------------------------------------------------ items, and their tiles by TMA
+    int st = 0, lap = 0;
+    const int total = PREFIX ? C::HV * a.kvh * a.splits * ((a.n_seq * a.group + NQ * kAttM - 1) / (NQ * kAttM)) : 0;
+    const int from_slot = PREFIX ? max(0, att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys)) : 0;
+    int seq = 0, before = 0;          // prompt: blocks of rows of the sequences ahead of `seq` (a multiple of 32)
+    int index = blockIdx.x;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      Att16Item it;
+      it.row0 = -1;
+      if (PREFIX) {
+        if (index < total) {
+          int x = index;
+          it.part = x / C::HV;
+          it.half = x % C::HV;
+          x /= C::HV;
+          const int split = x % a.splits;
+          x /= a.splits;
+          it.head = x % a.kvh;
+          it.r0 = x / a.kvh * (NQ * kAttM);
+          it.row0 = 0;
+          it.rows = a.n_seq * a.group;
+          it.lo = split * a.tiles_per * kAttN;
+          it.hi = min(a.keys, it.lo + a.tiles_per * kAttN);
+        }
+        index += gridDim.x;
+      } else {
+        const int blk = index / (a.kvh * C::HV), x = index % (a.kvh * C::HV);
+        it.head = x / C::HV;
+        it.half = x % C::HV;
+        while (seq < a.n_seq) {  // 32 sequences at a time
+          const int i = seq + lane;
+          int from = 0, len = 0, blocks = 0;
+          if (i < a.n_seq) {
+            from = __ldg(a.offsets + i);
+            const int to = __ldg(a.offsets + i + 1);
+            if (from < 0 || to < from || to > a.n_rows) {
+              if (blockIdx.x == 0 && n == 0) set_err(a.err, G4_DEV_BAD_POSITION);
+            } else {
+              len = to - from;
+              blocks = (int)(((long)len * a.group + NQ * kAttM - 1) / (NQ * kAttM));
+            }
+          }
+          int upto = blocks;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+          if (blk < before + all) {
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, blk < before + upto);
+            const int w = __ffs(who) - 1;
+            it.row0 = __shfl_sync(0xFFFFFFFFu, from, w);
+            len = __shfl_sync(0xFFFFFFFFu, len, w);
+            // the last rows, with the most keys, come first
+            it.r0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * kAttM);
+            it.rows = len * a.group;
+            const int first = it.r0 / a.group, last = (min(it.r0 + NQ * kAttM, it.rows) - 1) / a.group;
+            it.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+            it.hi = last + 1;
+            break;
+          }
+          before += all;
+          seq += 32;
+        }
+        int next = 0;
+        if (lane == 0 && it.row0 >= 0) next = gridDim.x + atomicAdd(a.ticket, 1u);
+        index = __shfl_sync(0xFFFFFFFFu, next, 0);
+      }
+      if (n >= 2) ok = att_wait(&s->iempty[n & 1], ((n - 2) >> 1) & 1, s);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (lane == 0) {
+        if (!ok) it.row0 = -1;
+        s->item[n & 1] = it;
+        mbar_arrive(&s->ifull[n & 1]);
+      }
+      __syncwarp();
+      if (!ok || it.row0 < 0) break;
+      const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN;
+      // keys 0, [keys 1 if scores run a tile ahead], values 0, keys ...
+      for (int x = 0; x < 2 * tiles && ok; ++x) {
+        int j;
+        bool values;
+        if (NQ == 2) {
+          j = x >> 1;
+          values = x & 1;
+        } else {
+          values = x == 2 * tiles - 1 || (x >= 2 && !(x & 1));
+          j = values ? (x == 2 * tiles - 1 ? tiles - 1 : x / 2 - 1) : (x + 1) / 2;
+        }
+        const int key = it.lo + j * kAttN;
+        const int parts = values ? C::VS : C::KS;
+        for (int y = 0; y < parts && ok; ++y) {
+          if (lap) ok = att_wait(&s->empty[st], (lap - 1) & 1, s);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          uint8_t* to = ring + st * C::kStage;
+          const int rows = values ? C::kVRows : kAttN, from = key + (values ? y * C::kVRows : 0);
+          const int slabs = C::kStage / (rows * 128), col = values ? it.half * DV : y * slabs * 64;
+          const CUtensorMap* map = values ? &vmap : &kmap;
+          if (!PREFIX) {
+            if (lane == 0) {
+              mbar_expect_tx(&s->full[st], C::kStage);
+#pragma unroll 4
+              for (int z = 0; z < slabs; ++z)
+                att_tma3(to + z * rows * 128, map, col + 64 * z, it.head, it.row0 + from, &s->full[st]);
+            }
+          } else {
+            // boxes of up to a page; a page that is missing (the join's business) reads page 0
+            const int box = min(rows, 1 << a.log_page), boxes = rows / box;
+            const int live = min(boxes, max(0, (a.keys - from + box - 1) / box));
+            if (lane == 0) mbar_expect_tx(&s->full[st], live * slabs * box * 128);
+            __syncwarp();
+            if (lane < live * slabs) {
+              const int z = lane / live, b = lane % live, at = from + b * box;
+              int page = __ldcg(a.table + (long)from_slot * a.max_pages + (at >> a.log_page));
+              if (page < 0 || page >= a.n_pages) page = 0;
+              att_tma2(to + z * rows * 128 + b * box * 128, map, col + 64 * z,
+                       ((page * a.kvh + it.head) << a.log_page) + (at & ((1 << a.log_page) - 1)), &s->full[st]);
+            }
+            __syncwarp();
+          }
+          if (++st == C::kStages) st = 0, ++lap;
+        }
+      }
+    }
+    // every copy that was asked for arrives before the CTA ends
+    const int asked = lap * C::kStages + st;
+    for (int k = max(0, asked - C::kStages); k < asked; ++k) mbar_wait_drain(&s->full[k % C::kStages], (k / C::kStages) & 1);
+  } else if (warp == C::kSoftWarps) {
+    // ------------------------------------------------ matrix instructions
+    if (lane == 0) {
+      Att16Items items{s};
+      Att16Item it;
+      int st = 0, lap = 0, n_p[2] = {0, 0}, tiles_done = 0, tails = 0;
+      bool ok = true;
+      auto stage = [&]() {  // the next stage, filled
+        ok = att_wait(&s->full[st], lap & 1, s) && ok;
+        tc_fence_after();
+        return su32(ring + st * C::kStage);
+      };
+      auto done = [&]() {
+        tc_commit(&s->empty[st]);
+        if (++st == C::kStages) st = 0, ++lap;
+      };
+      auto scores_part = [&](int y, int buf, uint32_t kaddr, int part) {
+        if (!ok) return;
+        const uint32_t qaddr = su32(qop) + y * (kAttM * D * 2) + part * (C::kStage / C::kSlab) * (kAttM * 128);
+#pragma unroll
+        for (int k = 0; k < C::kStage / C::kSlab * 4; ++k) {
+          const uint32_t off = (k >> 2) * C::kSlab + (k & 3) * 32;
+          tc_mma_ss(tmem + C::kColS + buf * kAttN, tc_desc(qaddr + off, 0), tc_desc(kaddr + off, 0), att_idesc<BF>(kAttN, false), part > 0 || k > 0);
+        }
+      };
+      auto weights_part = [&](int y, int buf, uint32_t vaddr, int part, bool first) {
+        if (!ok) return;
+#pragma unroll
+        for (int k = 0; k < C::kVRows / 16; ++k)
+          tc_mma_ts(tmem + y * DV, tmem + C::kColS + buf * kAttN + (part * (C::kVRows / 16) + k) * 8, tc_desc(vaddr + k * 2048, C::kVRows * 128),
+                    att_idesc<BF>(DV, true), !first || part > 0 || k > 0);
+      };
+      auto clear_tail = [&]() {  // has the rows of values behind the last key cleared, once they are there
+        for (int y = 0; y < C::VS; ++y) {
+          const int x = st + y < C::kStages ? st + y : st + y - C::kStages;
+          ok = att_wait(&s->full[x], (st + y < C::kStages ? lap : lap + 1) & 1, s) && ok;
+        }
+        mbar_arrive(&s->vneed);
+        ok = att_wait(&s->vtail, tails & 1, s) && ok;
+        ++tails;
+        tc_fence_after();
+      };
+      while (items.next(it)) {
+        const Att16Tiles<NQ> t(it, a.group, a.window, !PREFIX);
+        const bool tail = (PREFIX || it.hi * a.group >= it.rows) && (it.hi - it.lo) % kAttN != 0;
+        ok = att_wait(&s->qfull, (items.n - 1) & 1, s) && ok;
+        tc_fence_after();
+        if (NQ == 2) {
+          uint32_t k0 = stage();
+          for (int y = 0; y < 2; ++y)
+            if (t.sees(y, 0)) {
+              scores_part(y, y, k0, 0);
+              tc_commit(&s->sfull[y]);
+            }
+          done();
+          if (t.n == 1) tc_commit(&s->qdone);
+          for (int j = 0; j < t.n; ++j) {
+            const uint32_t v0 = stage();
+            if (tail && j == t.n - 1) clear_tail();
+            const int vst = st, vlap = lap;
+            uint32_t k1 = 0;
+            bool have = false;
+            for (int y = 0; y < 2; ++y) {
+              if (t.sees(y, j)) {
+                ok = att_wait(&s->pfull[y], n_p[y] & 1, s) && ok;
+                ++n_p[y];
+                tc_fence_after();
+                weights_part(y, y, v0, 0, y ? j == t.b0 : j == 0);
+                tc_commit(&s->pvdone[y]);
+              }
+              if (y == 1) tc_commit(&s->empty[vst]);
+              if (j + 1 < t.n && t.sees(y, j + 1)) {
+                if (!have) {
+                  const int kst = vst + 1 == C::kStages ? 0 : vst + 1, klap = vst + 1 == C::kStages ? vlap + 1 : vlap;
+                  ok = att_wait(&s->full[kst], klap & 1, s) && ok;
+                  tc_fence_after();
+                  k1 = su32(ring + kst * C::kStage);
+                  have = true;
+                }
+                scores_part(y, y, k1, 0);
+                tc_commit(&s->sfull[y]);
+              }
+            }
+            if (++st == C::kStages) st = 0, ++lap;
+            if (j + 1 < t.n) {
+              done();
+              if (j + 2 == t.n) tc_commit(&s->qdone);
+            }
+          }
+        } else {
+          auto scores = [&](int j) {
+            const int b = (tiles_done + j) & 1;
+            for (int y = 0; y < C::KS; ++y) {
+              scores_part(0, b, stage(), y);
+              done();
+            }
+            tc_commit(&s->sfull[b]);
+            if (j == t.n - 1) tc_commit(&s->qdone);
+          };
+          scores(0);
+          for (int j = 0; j < t.n; ++j) {
+            const int b = (tiles_done + j) & 1;
+            if (j + 1 < t.n) scores(j + 1);
+            for (int y = 0; y < C::VS; ++y) {
+              const uint32_t v0 = stage();
+              if (y == 0) {
+                if (tail && j == t.n - 1) clear_tail();
+                ok = att_wait(&s->pfull[b], n_p[b] & 1, s) && ok;
+                ++n_p[b];
+                tc_fence_after();
+              }
+              weights_part(0, b, v0, y, j == 0);
+              done();
+            }
+            tc_commit(&s->pvdone[0]);
+          }
+          tiles_done += t.n;
+        }
+      }
+      tc_commit(&s->drained);
+      mbar_wait_drain(&s->drained, 0);
+    }
+  } else if (warp > C::kSoftWarps + 1) {
+    // ------------------------------------------------ queries; values behind the last key
+    const int me = threadIdx.x - 32 * (C::kSoftWarps + 2);
+    constexpr int CH = D / 8;  // 16-byte pieces of a row
+    Att16Items items{s};
+    Att16Item it;
+    int st = 0, tails = 0;  // stages and cleared tiles of the items so far
+    while (items.next(it)) {
+      if (items.n > 1) att_wait(&s->qdone, (items.n - 2) & 1, s);
+#pragma unroll 8
+      for (int e = me; e < NQ * kAttM * CH; e += 64) {
+        const int R = e / CH, c = e % CH, r = it.r0 + R;
+        const bool on = r < it.rows;
+        const int tok = on ? r / a.group : 0, g = on ? r % a.group : 0;
+        const uint16_t* src = a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + g) * a.q_head + 8 * c;
+        const int in = R & (kAttM - 1);
+        uint8_t* dst = qop + (R / kAttM) * (kAttM * D * 2) + (c >> 3) * (kAttM * 128) + in * 128 + (((c & 7) ^ (in & 7)) << 4);
+        if (a.q_vec) {
+          cp_async16(dst, src, on);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] = on ? (uint32_t)__ldcg(src + 2 * x) | ((uint32_t)__ldcg(src + 2 * x + 1) << 16) : 0u;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      cp_async_wait_all();
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      mbar_arrive(&s->qfull);
+      const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN, live = it.hi - it.lo - (tiles - 1) * kAttN;
+      st += tiles * (C::KS + C::VS);
+      if ((PREFIX || it.hi * a.group >= it.rows) && live != kAttN) {
+        // the last tile reaches past the sequence: what lies there may be anything
+        att_wait(&s->vneed, tails++ & 1, s);
+        for (int y = 0; y < C::VS; ++y) {
+          const int x = st - C::VS + y;
+          uint8_t* v = ring + (x % C::kStages) * C::kStage;
+          const int first = min(max(live - y * C::kVRows, 0), C::kVRows), pieces = (C::kVRows - first) * 8;
+          for (int z = 0; z < DV / 64; ++z)
+            for (int e = me; e < pieces; e += 64)
+              *reinterpret_cast<uint4*>(v + z * (C::kVRows * 128) + first * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        mbar_arrive(&s->vtail);
+      }
+    }
+    if (!PREFIX && a.zero_rest) {
+      const int front = min(max(__ldg(a.offsets), 0), a.n_rows), end = min(max(__ldg(a.offsets + a.n_seq), front), a.n_rows);
+      const int rest = front + a.n_rows - end, heads = a.kvh * a.group;
+      for (long e = blockIdx.x * 64 + me; e < (long)rest * heads * CH; e += gridDim.x * 64) {
+        const int c = (int)(e % CH), x = (int)(e / CH % heads), r = (int)(e / CH / heads);
+        uint16_t* o = a.out + (long)(r < front ? r : end + r - front) * a.o_row + (long)x * a.o_head + 8 * c;
+        if (a.o_vec) {
+          *reinterpret_cast<uint4*>(o) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          for (int y = 0; y < 8; ++y) o[y] = 0;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax: a query row per thread
+    const int y = warp >> 2, row_in = threadIdx.x & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ocol = lane_base + y * DV;
+    Att16Items items{s};
+    Att16Item it;
+    int n = 0;  // tiles of this block of rows so far
+    while (items.next(it)) {
+      const Att16Tiles<NQ> t(it, a.group, a.window, !PREFIX);
+      const int block0 = it.r0 + y * kAttM, row = block0 + row_in;
+      const bool on = row < it.rows;
+      const int j0 = y ? t.b0 : 0, j1 = y ? t.n : t.a1;
+      if (j0 >= j1) continue;
+      const int tok = (on ? row : it.rows - 1) / a.group;
+      // keys that the row sees: first .. last; every row of the block sees all_first .. all_last
+      int first = it.lo, last = it.hi - 1, all_first = it.lo, all_last = it.hi - 1;
+      if (!PREFIX) {
+        last = tok;
+        all_last = block0 / a.group;
+        if (a.window > 0) {
+          first = max(0, tok - a.window + 1);
+          all_first = max(0, (min(block0 + kAttM, it.rows) - 1) / a.group - a.window + 1);
+        }
+      }
+      float m = -INFINITY, ref = 0.f, l = 0.f;
+      for (int j = j0; j < j1; ++j, ++n) {
+        const int b = NQ == 2 ? y : n & 1;
+        att_wait(&s->sfull[b], (NQ == 2 ? n : n >> 1) & 1, s);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t cols = lane_base + C::kColS + b * kAttN;
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_tld32(cols + 32 * c, v + 32 * c);
+        tc_tld_wait();
+        const int key = it.lo + j * kAttN;
+        if (key + kAttN - 1 > all_last || key < all_first) {
+          const int most = last - key, least = first - key;
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k > most || k < least) v[k] = 0xFF800000u;
+        }
+        float mx = __uint_as_float(v[0]);
+#pragma unroll
+        for (int k = 1; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+        mx *= a.scale;
+        const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float nm = raise ? mx : m, fac = raise ? att_exp2(m - nm) : 1.f;
+          m = nm;
+          ref = m == -INFINITY ? 0.f : m;
+          l *= fac;
+          if (j > j0) {  // the output so far follows, when the previous tile's product is in
+            att_wait(&s->pvdone[NQ == 2 ? y : 0], (n - 1) & 1, s);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 32) {
+              uint32_t u[32];
+              tc_tld32(ocol + c, u);
+              tc_tld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * fac);
+              tc_tst32(ocol + c, u);
+            }
+            tc_tst_wait();
+          }
+        }
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float p0 = att_exp2(fmaf(__uint_as_float(v[2 * k]), a.scale, -ref));
+          const float p1 = att_exp2(fmaf(__uint_as_float(v[2 * k + 1]), a.scale, -ref));
+          s0 += p0;
+          s1 += p1;
+          v[k] = att_pack<BF>(p0, p1);
+        }
+        l += s0 + s1;
+        tc_tst32(cols, v);
+        tc_tst32(cols + 32, v + 32);
+        tc_tst_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->pfull[b]);
+      }
+      // ---- the row's output.  (A barrier's parity tells a phase from the one before it alone: with NQ 1 the
+      // last tile's scores say that the product before the previous one is in, no more.)
+      if (NQ == 1 && n >= 2) att_wait(&s->pvdone[0], n & 1, s);
+      att_wait(&s->pvdone[NQ == 2 ? y : 0], (n - 1) & 1, s);
+      __syncwarp();
+      tc_fence_after();
+      if (PREFIX) {
+        const long at = (long)it.part * (NQ * kAttM) + y * kAttM + row_in;
+        float* part = a.part_o + at * D + it.half * DV;
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 32) {
+          uint32_t u[32];
+          tc_tld32(ocol + c, u);
+          tc_tld_wait();
+          if (on) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(part + c)[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+          }
+          __syncwarp();
+        }
+        if (on && it.half == 0) a.part_ml[at] = make_float2(m, l);
+      } else {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        uint16_t* out = a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + row % a.group) * a.o_head;
+        bool odd = false;
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 32) {
+          uint32_t u[32], w[16];
+          tc_tld32(ocol + c, u);
+          tc_tld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float f0 = __uint_as_float(u[2 * k]) * inv, f1 = __uint_as_float(u[2 * k + 1]) * inv;
+            odd |= !att_finite(f0) || !att_finite(f1);
+            w[k] = att_pack<BF>(f0, f1);
+          }
+          uint16_t* o = out + it.half * DV + c;
+          if (!on) {
+          } else if (a.o_vec) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(o)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              o[2 * k] = (uint16_t)w[k];
+              o[2 * k + 1] = (uint16_t)(w[k] >> 16);
+            }
+          }
+          __syncwarp();
+        }
+        if (on && odd && att_finite(l))
+          att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + row % a.group) * a.q_head, out,
+                            it.row0, it.head, it.half * DV, DV, first, last, ref, l);
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (s->abort) set_err(a.err, G4_DEV_TIMEOUT);
+    if (!PREFIX) {  // the last CTA puts the counters back
+      __threadfence();
+      if (atomicAdd(a.ticket + 1, 1u) == gridDim.x - 1) {
+        a.ticket[0] = 0;
+        a.ticket[1] = 0;
+      }
+    }
+  }
+  if (warp == C::kSoftWarps) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+}  // namespace g4

@@ -30,6 +30,7 @@
 // Compiled, the attention spills 8 to 20 bytes of its 128 registers a thread.
 #pragma once
 #include "kv4_attend.cuh"
+#include "tc05.cuh"
 
 namespace g4 {
 
@@ -86,54 +87,6 @@ __device__ __forceinline__ bool kv4_wait(uint64_t* b, uint32_t parity, Kv4BlockB
   if (mbar_wait(b, parity, reinterpret_cast<volatile int*>(&s->abort))) return true;
   *reinterpret_cast<volatile int*>(&s->abort) = 1;
   return false;
-}
-__device__ __forceinline__ void kv4_commit(uint64_t* b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ void kv4_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-      : "memory");
-}
-__device__ __forceinline__ void kv4_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-      : "memory");
-}
-__device__ __forceinline__ void kv4_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void kv4_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-// 32 columns of the calling thread's lane, no wait.
-__device__ __forceinline__ void kv4_tld32(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void kv4_tst32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void kv4_tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void kv4_tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
-// Shared-memory operand descriptor, 128-byte swizzle, rows of 128 bytes in groups of eight 1,024
-// bytes apart.  Keys: the head dim runs along the rows (`lead` unused).  Values: the head dim is
-// the operand's leading dimension and `lead` the distance between its 64-wide slabs.
-__device__ __forceinline__ uint64_t kv4_desc(uint32_t saddr, uint32_t lead) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead ? lead >> 4 : 1) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // kind::f16: bf16 operands, fp32 result, M 128.
 __device__ __forceinline__ constexpr uint32_t kv4_idesc(int n, bool b_leading) {
@@ -275,9 +228,9 @@ __device__ __forceinline__ void kv4_load_queries(const Kv4AttendArgs& a, const K
       }
     }
 #pragma unroll
-    for (int c = 0; c < N / 64; ++c) kv4_tst32(addr + c0 / 2 + c * 32, u + 32 * c);
+    for (int c = 0; c < N / 64; ++c) tc_tst32(addr + c0 / 2 + c * 32, u + 32 * c);
   }
-  kv4_tst_wait();
+  tc_tst_wait();
 }
 
 // The queries of an item's 128 rows into a swizzled operand, by four warps of 32 rows each: a
@@ -378,12 +331,12 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&s->tmem)), "r"(C::kCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  kv4_fence_before();
+  tc_fence_before();
   pdl_wait();
   pdl_trigger();
   const int wide = __ldcg(a.c.wide) | a.plain;
   kv4_plan<kKv4N>(a, first, seqs, reinterpret_cast<int*>(kop), !ACCOUNT && blockIdx.x == 0);
-  kv4_fence_after();
+  tc_fence_after();
   const uint32_t tmem = s->tmem;
   const int total = first[a.n_seq], span = kv4_span(a, first, gridDim.x);
   const int g0 = (int)min((unsigned)total, blockIdx.x * (unsigned)span), g1 = (int)min((unsigned)total, (unsigned)g0 + span);
@@ -434,37 +387,37 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
               const int y = pairs + q, kb = y % C::kKBufs, sb = y % C::kSBufs;
               ok = kv4_wait(&s->kfull[kb], (y / C::kKBufs) & 1, s) && ok;
               if (y >= C::kSBufs) ok = kv4_wait(&s->sread[sb], (y / C::kSBufs - 1) & 1, s) && ok;
-              kv4_fence_after();
+              tc_fence_after();
               if (ok) {
                 const uint32_t kaddr = su32(kop + kb * 2 * C::kOperand), qaddr = su32(qop);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                   const uint32_t off = (k >> 2) * (kKv4M * 128) + (k & 3) * 32;
-                  const uint64_t kd = kv4_desc(kaddr + off, 0);
-                  if (ACCOUNT) kv4_mma_ts(tmem + C::kColS + sb * 128, tmem + C::kColQ + qb * (D / 2) + k * 8, kd, kv4_idesc(128, false), k > 0);
-                  else kv4_mma_ss(tmem + C::kColS, kv4_desc(qaddr + off, 0), kd, kv4_idesc(128, false), k > 0);
+                  const uint64_t kd = tc_desc(kaddr + off, 0);
+                  if (ACCOUNT) tc_mma_ts(tmem + C::kColS + sb * 128, tmem + C::kColQ + qb * (D / 2) + k * 8, kd, kv4_idesc(128, false), k > 0);
+                  else tc_mma_ss(tmem + C::kColS, tc_desc(qaddr + off, 0), kd, kv4_idesc(128, false), k > 0);
                 }
               }
-              kv4_commit(&s->sfull[sb]);
-              kv4_commit(&s->kempty[kb]);
-              if (ACCOUNT && q + 1 == np) kv4_commit(&s->qdone[qb]);
+              tc_commit(&s->sfull[sb]);
+              tc_commit(&s->kempty[kb]);
+              if (ACCOUNT && q + 1 == np) tc_commit(&s->qdone[qb]);
             }
             if (!ACCOUNT && q > 0) {  // outputs of pair q - 1
               for (int x = 2 * q - 2; x < min(2 * q, r.tiles); ++x) {
                 const int y = n + x, b = y & 1;
                 ok = kv4_wait(&s->vfull[b], (y >> 1) & 1, s) && ok;
                 ok = kv4_wait(&s->pfull[b], (y >> 1) & 1, s) && ok;
-                kv4_fence_after();
+                tc_fence_after();
                 if (ok) {
                   const uint32_t vaddr = su32(vop + b * C::kOperand);
 #pragma unroll
                   for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < kKv4N / 16; ++k)
-                      kv4_mma_ts(tmem, tmem + C::kColP + b * 64 + part * 32 + k * 8, kv4_desc(vaddr + k * 2048, kKv4N * 128),
+                      tc_mma_ts(tmem, tmem + C::kColP + b * 64 + part * 32 + k * 8, tc_desc(vaddr + k * 2048, kKv4N * 128),
                                  kv4_idesc(D, true), x > 0 || part > 0 || k > 0);
                 }
-                kv4_commit(&s->pvdone[b]);
+                tc_commit(&s->pvdone[b]);
               }
             }
           }
@@ -473,7 +426,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
         }
         at += r.tiles;
       }
-      kv4_commit(&s->drained);
+      tc_commit(&s->drained);
       mbar_wait_drain(&s->drained, 0);
     }
   } else if (ACCOUNT && warp >= 12) {
@@ -485,10 +438,10 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
       for (int rb = 0; rb < blocks; ++rb, ++runs) {
         const int qb = runs & 1;
         if (runs >= 2) kv4_wait(&s->qdone[qb], ((runs - 2) >> 1) & 1, s);
-        kv4_fence_after();
+        tc_fence_after();
         kv4_load_queries<D>(a, r, rb * kKv4M + (int)threadIdx.x - 384,
                             tmem + ((uint32_t)((warp - 12) * 32) << 16) + C::kColQ + qb * (D / 2));
-        kv4_fence_before();
+        tc_fence_before();
         mbar_arrive(&s->qfull[qb]);
       }
       at += r.tiles;
@@ -577,15 +530,15 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
         for (int x = 0; x < r.tiles; ++x, ++n) {
           const int y = pairs + (x >> 1), sb = y % C::kSBufs;
           kv4_wait(&s->sfull[sb], (y / C::kSBufs) & 1, s);
-          kv4_fence_after();
+          tc_fence_after();
           uint32_t v[64];
           const uint32_t cols = lane_base + C::kColS + sb * 128 + (x & 1) * kKv4N;
-          kv4_tld32(cols, v);
-          kv4_tld32(cols + 32, v + 32);
-          kv4_tld_wait();
+          tc_tld32(cols, v);
+          tc_tld32(cols + 32, v + 32);
+          tc_tld_wait();
           const int j0 = (r.tile + x) * kKv4N;
           const uint32_t have = s->held[0][n & 15];
-          kv4_fence_before();
+          tc_fence_before();
           if ((x & 1) || x + 1 == r.tiles) mbar_arrive(&s->sread[sb]);  // the pair's scores are in registers
           float f[64];
 #pragma unroll
@@ -630,17 +583,17 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
               }
               if (x > 0) {  // the output so far follows: the previous tile's product has to be in
                 kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
-                kv4_fence_after();
+                tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                   uint32_t u[32];
-                  kv4_tld32(lane_base + c, u);
-                  kv4_tld_wait();
+                  tc_tld32(lane_base + c, u);
+                  tc_tld_wait();
 #pragma unroll
                   for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * fac);
-                  kv4_tst32(lane_base + c, u);
+                  tc_tst32(lane_base + c, u);
                 }
-                kv4_tst_wait();
+                tc_tst_wait();
               }
             }
             float s0 = 0.f, s1 = 0.f;
@@ -656,12 +609,12 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
             const int pb = n & 1;
             if (n >= 2) {  // the weights before the previous tile's have been used
               kv4_wait(&s->pvdone[pb], ((n - 2) >> 1) & 1, s);
-              kv4_fence_after();
+              tc_fence_after();
             }
-            kv4_tst32(lane_base + C::kColP + pb * 64, v);
-            kv4_tst32(lane_base + C::kColP + pb * 64 + 32, v + 32);
-            kv4_tst_wait();
-            kv4_fence_before();
+            tc_tst32(lane_base + C::kColP + pb * 64, v);
+            tc_tst32(lane_base + C::kColP + pb * 64 + 32, v + 32);
+            tc_tst_wait();
+            tc_fence_before();
             mbar_arrive(&s->pfull[pb]);
           }
         }
@@ -669,7 +622,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
         if constexpr (!ACCOUNT) {
           // ---- the run's output row
           kv4_wait(&s->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, s);
-          kv4_fence_after();
+          tc_fence_after();
           const bool whole = r.whole;
           const float inv = (whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f) * up;
           const long slot_p = (long)blockIdx.x * 2 + (piece ? 1 : 0);
@@ -678,9 +631,9 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
 #pragma unroll 1
           for (int c = 0; c < D; c += 64) {
             uint32_t u[64];
-            kv4_tld32(lane_base + c, u);
-            kv4_tld32(lane_base + c + 32, u + 32);
-            kv4_tld_wait();
+            tc_tld32(lane_base + c, u);
+            tc_tld32(lane_base + c + 32, u + 32);
+            tc_tld_wait();
             float f[64];
 #pragma unroll
             for (int k = 0; k < 64; ++k) f[k] = __uint_as_float(u[k]) * inv;
@@ -694,7 +647,7 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
           }
           if (!whole) a.part_ml[slot_p * kKv4M + row_in] = make_float2(m, l);
           else a.lse[((long)r.seq * a.c.kvh + r.head) * a.lse_rows + row] = kv4_lse(make_float2(m, l));
-          kv4_fence_before();
+          tc_fence_before();
         }
       }
       if constexpr (ACCOUNT) {
@@ -712,11 +665,11 @@ __global__ void __launch_bounds__(kKv4BlockThreads, 1) kv4_block_kernel(const __
       at += r.tiles;
     }
   }
-  kv4_fence_before();
+  tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && s->abort) set_err(a.c.err, G4_DEV_TIMEOUT);
   if (warp == 1) {
-    kv4_fence_after();
+    tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
 }

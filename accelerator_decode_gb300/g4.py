@@ -29,6 +29,7 @@ G4_DEV_BAD_POSITION = 2
 G4_DEV_TIMEOUT = 4
 G4_DEV_BAD_SLOT = 8
 G4_DEV_BAD_VALUE = 16
+G4_DEV_NO_PAGES = 32
 G4_DT_F32 = 0
 G4_DT_BF16 = 1
 G4_DT_F16 = 2
@@ -74,6 +75,14 @@ class g4_phase_stat(ctypes.Structure):
 class g4_kv4_config(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("n_slots", "capacity", "num_q_heads", "num_kv_heads", "head_dim",
                                        "max_q_len", "page_size", "n_pages", "track")]
+
+
+class g4_pages_config(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("n_slots", "n_pages", "page_size", "max_pages")]
+
+
+class g4_attn_config(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "dtype", "max_seqs")]
 
 
 class g4_kv4_tensor(ctypes.Structure):
@@ -132,6 +141,22 @@ def _load():
         "g4_kv4_get_device_error": (c_int, [P, P, POINTER(c_int32)]),
         "g4_kv4_bytes": (c_int64, [P]),
         "g4_kv4_free": (None, [P]),
+        "g4_pages_create": (c_int, [c_int, POINTER(g4_pages_config), P, P, POINTER(P)]),
+        "g4_pages_extend": (c_int, [P, P, c_int32, P, P, c_int32, P, P, P]),
+        "g4_pages_share": (c_int, [P, P, c_int32, P, c_int32, c_int32]),
+        "g4_pages_truncate": (c_int, [P, P, c_int32, P, P]),
+        "g4_pages_store": (c_int, [P, P, c_int32, P, c_int32, c_int32, POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor), P, P]),
+        "g4_pages_get_device_error": (c_int, [P, P, POINTER(c_int32)]),
+        "g4_pages_bytes": (c_int64, [P]),
+        "g4_pages_free": (None, [P]),
+        "g4_attn_create": (c_int, [c_int, POINTER(g4_attn_config), POINTER(P)]),
+        "g4_attn_prompt": (c_int, [P, P, c_int32, P, c_int32, c_float, c_int32, c_int32, POINTER(g4_kv4_tensor),
+                                   POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor), POINTER(g4_kv4_tensor)]),
+        "g4_attn_shared": (c_int, [P, P, P, c_int32, P, c_int32, c_float, P, P, POINTER(g4_kv4_tensor),
+                                   POINTER(g4_kv4_tensor)]),
+        "g4_attn_get_device_error": (c_int, [P, P, POINTER(c_int32)]),
+        "g4_attn_bytes": (c_int64, [P]),
+        "g4_attn_free": (None, [P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -423,3 +423,202 @@ class KV4Cache:
             self.close()
         except Exception:
             pass
+
+
+_16BIT = {torch.bfloat16: _g4.G4_DT_BF16, torch.float16: _g4.G4_DT_F16}
+
+
+class _PagedOp:
+    """What PageTable and Attention share: a handle on device `index`, its arguments and results."""
+
+    def __init__(self, device):
+        self.index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
+        self.device = torch.device("cuda", self.index)
+
+    def _made(self, status, h):
+        _g4.check(status, f"{self._name}_create")
+        self.h = h
+
+    def _rows16(self, name, t, shape, dtype):
+        """Checks a [rows, heads, head_dim] argument of 16-bit numbers; its description for C."""
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+        s = t.stride()
+        if s[2] != 1:
+            raise ValueError(f"{name}: the last dimension has to be contiguous")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, the handle on {self.device}")
+        return ctypes.byref(_g4.g4_kv4_tensor(t.data_ptr(), _16BIT[dtype], 0, s[0], s[1]))
+
+    def _pool(self, name, t, table, kv_heads, head_dim, dtype):
+        shape = (table.n_pages, kv_heads, table.page_size, head_dim)
+        return _kv4_array(name, t, shape, dtype, self.index)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
+        return stream.cuda_stream
+
+    def _empty(self, shape, dtype, stream):
+        """A result, made on the stream that fills it."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _done(self, status, name, stream, used):
+        """Raises for an error; the caching allocator learns of the tensors used on a given stream."""
+        if status:
+            raise _g4.G4Error(status, name)
+        if stream is not None:
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def device_error(self, stream=None):
+        """(status, word) of the sticky device error word, cleared."""
+        w = ctypes.c_int32(0)
+        return getattr(_g4.lib, f"{self._name}_get_device_error")(self.h, self._stream(stream), ctypes.byref(w)), w.value
+
+    def device_bytes(self):
+        return getattr(_g4.lib, f"{self._name}_bytes")(self.h)
+
+    def close(self):
+        if getattr(self, "h", None) is not None:
+            getattr(_g4.lib, f"{self._name}_free")(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PageTable(_PagedOp):
+    """Pages of a paged cache's pools, given out on the device (g4_pages_* in include/g4.h).
+
+    table: int32 [n_slots, max_pages], the pages of each slot (-1: none); lens: int32 [n_slots], its
+    rows.  The calls keep both up to date; they are read, not written, by the caller.  slots, counts and
+    lens are int32 device tensors with one entry per sequence.  Calls run on `stream` (default: the
+    current one), where their results are valid; calls on one table have to be ordered, and come from
+    one host thread at a time."""
+
+    _name = "g4_pages"
+
+    def __init__(self, n_slots, n_pages, page_size, max_pages, device=None):
+        super().__init__(device)
+        c = _g4.g4_pages_config(*(_kv4_int(name, v) for name, v in (
+            ("n_slots", n_slots), ("n_pages", n_pages), ("page_size", page_size), ("max_pages", max_pages))))
+        if c.n_slots < 1 or c.max_pages < 1 or c.n_slots > 1024 or c.max_pages > 1 << 20:
+            raise ValueError("n_slots has to be 1..1024 and max_pages 1..2**20")
+        self.n_slots, self.n_pages, self.page_size, self.max_pages = c.n_slots, c.n_pages, c.page_size, c.max_pages
+        self.table = torch.empty(c.n_slots, c.max_pages, dtype=torch.int32, device=self.device)
+        self.lens = torch.empty(c.n_slots, dtype=torch.int32, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()     # what the memory held before is done with
+        h = ctypes.c_void_p()
+        self._made(_g4.lib.g4_pages_create(self.index, ctypes.byref(c), _ptr(self.table), _ptr(self.lens), ctypes.byref(h)), h)
+
+    def _seq(self, name, t, n):
+        return _kv4_array(name, t, (n,), torch.int32, self.index)
+
+    def extend(self, slots, counts, n_rows, stream=None):
+        """Plan counts[i] further rows of slots[i], n_rows in all.  Returns (rows [n_rows]: the pool row of
+        each new row, sequence after sequence, -1 where there is none; offsets [n + 1]: where each
+        sequence's rows begin among them; lens [n]: the slots' new lengths)."""
+        n, n_rows = slots.numel(), _kv4_int("n_rows", n_rows)
+        args = (self._seq("slots", slots, n), self._seq("counts", counts, n))
+        if n_rows < 0:
+            raise ValueError(f"n_rows is {n_rows}")
+        rows, offsets, lens = (self._empty((m,), torch.int32, stream) for m in (n_rows, n + 1, n))
+        status = _g4.lib.g4_pages_extend(self.h, self._stream(stream), n, *args, n_rows, rows.data_ptr(), offsets.data_ptr(),
+                                         lens.data_ptr())
+        self._done(status, "g4_pages_extend", stream, (slots, counts))
+        return rows, offsets, lens
+
+    def share(self, slots, source, n_pages, stream=None):
+        """Empty slots begin with the first n_pages pages (all full) of slot `source`."""
+        n = slots.numel()
+        status = _g4.lib.g4_pages_share(self.h, self._stream(stream), n, self._seq("slots", slots, n),
+                                        _kv4_int("source", source), _kv4_int("n_pages", n_pages))
+        self._done(status, "g4_pages_share", stream, (slots,))
+
+    def truncate(self, slots, lens=None, stream=None):
+        """Cut slots back to their first lens[i] rows (default: to none, which gives all pages back)."""
+        n = slots.numel()
+        status = _g4.lib.g4_pages_truncate(self.h, self._stream(stream), n, self._seq("slots", slots, n),
+                                           self._seq("lens", lens, n))
+        self._done(status, "g4_pages_truncate", stream, (slots, lens))
+
+    def store(self, k, v, rows, k_pool, v_pool, stream=None):
+        """k, v [n, kv_heads, head_dim] into pool rows rows[t] (-1: left out) of k_pool and v_pool
+        [n_pages, kv_heads, page_size, head_dim], bfloat16 or float16 all."""
+        if k.dim() != 3 or k.dtype not in _16BIT:
+            raise TypeError(f"k is {k.dtype} with {k.dim()} dimensions: [rows, heads, head_dim] of bfloat16 or float16 is wanted")
+        n, heads, d = k.shape
+        status = _g4.lib.g4_pages_store(
+            self.h, self._stream(stream), n, self._seq("rows", rows, n), heads, d, self._rows16("k", k, k.shape, k.dtype),
+            self._rows16("v", v, k.shape, k.dtype), self._pool("k_pool", k_pool, self, heads, d, k.dtype),
+            self._pool("v_pool", v_pool, self, heads, d, k.dtype))
+        self._done(status, "g4_pages_store", stream, (k, v, rows, k_pool, v_pool))
+
+
+class Attention(_PagedOp):
+    """Softmax attention over 16-bit keys and values (g4_attn_* in include/g4.h): whole prompts, and
+    tokens of a batch whose slots share their first pages.
+
+    Calls run on `stream` (default: the current one), where their results are valid; calls on one
+    object have to be ordered, and come from one host thread at a time."""
+
+    _name = "g4_attn"
+
+    def __init__(self, num_q_heads, num_kv_heads, head_dim, dtype=torch.bfloat16, max_seqs=256, device=None):
+        super().__init__(device)
+        if dtype not in _16BIT:
+            raise TypeError(f"attention of {dtype}: bfloat16 or float16 is wanted")
+        c = _g4.g4_attn_config(*(_kv4_int(name, v) for name, v in (
+            ("num_q_heads", num_q_heads), ("num_kv_heads", num_kv_heads), ("head_dim", head_dim))), _16BIT[dtype],
+            _kv4_int("max_seqs", max_seqs))
+        self.num_q_heads, self.num_kv_heads, self.head_dim, self.dtype = c.num_q_heads, c.num_kv_heads, c.head_dim, dtype
+        h = ctypes.c_void_p()
+        self._made(_g4.lib.g4_attn_create(self.index, ctypes.byref(c), ctypes.byref(h)), h)
+
+    def prompt(self, q, k, v, offsets, scale=0.0, window=0, out=None, stream=None):
+        """Causal attention of packed sequences: rows offsets[i] .. offsets[i + 1] - 1 of q [rows, num_q_heads,
+        head_dim] and k, v [rows, num_kv_heads, head_dim] are sequence i.  Returns out: the given tensor, whose
+        rows in front of the first sequence and behind the last stay as they were, or a new one, where
+        they are zeros."""
+        n, rows = offsets.numel() - 1, q.shape[0] if q.dim() == 3 else -1
+        mine, theirs = (rows, self.num_q_heads, self.head_dim), (rows, self.num_kv_heads, self.head_dim)
+        args = [self._rows16("q", q, mine, self.dtype), self._rows16("k", k, theirs, self.dtype),
+                self._rows16("v", v, theirs, self.dtype)]
+        where, window = _kv4_array("offsets", offsets, (n + 1,), torch.int32, self.index), _kv4_int("window", window)
+        given = out is not None
+        if not given:
+            out = self._empty(mine, self.dtype, stream)
+        status = _g4.lib.g4_attn_prompt(self.h, self._stream(stream), n, where, rows, scale, window, not given, *args,
+                                        self._rows16("out", out, mine, self.dtype))
+        self._done(status, "g4_attn_prompt", stream, (q, k, v, offsets, out))
+        return out
+
+    def shared(self, q, k_pool, v_pool, pages, slots, shared_pages, scale=0.0, out=None, stream=None):
+        """Attention of one token of each slot, q [n, num_q_heads, head_dim], over all rows that `pages` (a
+        PageTable) holds for it in the pools [n_pages, num_kv_heads, page_size, head_dim].  The first
+        shared_pages pages of all slots are the same ones (0: none need be)."""
+        n = slots.numel()
+        shape = (n, self.num_q_heads, self.head_dim)
+        arg = self._rows16("q", q, shape, self.dtype)
+        if out is None:
+            out = self._empty(shape, self.dtype, stream)
+        status = _g4.lib.g4_attn_shared(
+            self.h, self._stream(stream), pages.h, n, _kv4_array("slots", slots, (n,), torch.int32, self.index),
+            _kv4_int("shared_pages", shared_pages), scale,
+            self._pool("k_pool", k_pool, pages, self.num_kv_heads, self.head_dim, self.dtype),
+            self._pool("v_pool", v_pool, pages, self.num_kv_heads, self.head_dim, self.dtype), arg,
+            self._rows16("out", out, shape, self.dtype))
+        self._done(status, "g4_attn_shared", stream, (q, k_pool, v_pool, slots, out))
+        return out

@@ -63,7 +63,8 @@ enum {
   G4_DEV_BAD_POSITION = 2,
   G4_DEV_TIMEOUT = 4,
   G4_DEV_BAD_SLOT = 8,
-  G4_DEV_BAD_VALUE = 16 /* a key or value that is not finite (g4_kv4_append) */
+  G4_DEV_BAD_VALUE = 16, /* a key or value that is not finite (g4_kv4_append) */
+  G4_DEV_NO_PAGES = 32   /* the pool is short of pages (g4_pages_extend) */
 };
 
 /* Model shape and the numeric constants the pages leave open (every one is a field).
@@ -438,6 +439,150 @@ int64_t g4_kv4_bytes(const g4_kv4* op);
 
 /* Release everything the op owns (after synchronising its device).  NULL is a no-op. */
 void g4_kv4_free(g4_kv4* op);
+
+/* ----------------------------------------------------------------------------------------
+ * A page table kept on the device: pages given to new rows, shared between slots and taken back
+ * by kernels, from lengths that the host need not know; and the store of rows into the pages.
+ *
+ * A pool is [n_pages][num_kv_heads][page_size][head_dim]; pools of any number of layers, keys and
+ * values, go by one table.  Row r of slot s is row r % page_size of page table[s][r / page_size];
+ * its pool row is that page * page_size + r % page_size.  A page is held by the slots whose tables
+ * name it and goes back to the pool with the last of them.  Pages that nobody holds lie on a
+ * stack: a new pool's first page is 0, then 1 and so on, and what is taken back last is given first.
+ * Equal calls on equal states give equal results.
+ *
+ * Errors of one sequence that only the device can see set the op's device error word, and that
+ * sequence is passed over: its slot stays as it was.  G4_DEV_BAD_SLOT: a slot out of range, or named
+ * by an earlier sequence of the call.  Other bits stand with the calls.
+ *
+ * Calls on one g4_pages (captured graphs that hold such calls included) must be ordered by the
+ * caller, on one stream or by events.  No call after g4_pages_create allocates or synchronises,
+ * except g4_pages_get_device_error and g4_pages_free.
+ * --------------------------------------------------------------------------------------*/
+
+typedef struct g4_pages g4_pages;
+
+typedef struct g4_pages_config {
+  int32_t n_slots;   /* 1..1024 */
+  int32_t n_pages;   /* pages of the pool */
+  int32_t page_size; /* rows, a power of two >= 16; n_pages * page_size below 2^31 */
+  int32_t max_pages; /* pages of a slot; max_pages * page_size at most 2^20 */
+} g4_pages_config;
+
+/* Make an empty table on `device`.  d_table int32 [n_slots][max_pages] and d_lens int32 [n_slots]
+ * (rows of each slot) are BORROWED and kept up to date by the calls: they may be read, and become -1
+ * (no page) and 0 here.  Errors: INVALID_ARG, UNSUPPORTED (sizes outside the bounds above), OOM, CUDA. */
+g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_table, int32_t* d_lens,
+                          g4_pages** out);
+
+/* Plan d_counts[i] further rows for slot d_slots[i]: pages are taken for them, in the order of the
+ * sequences and their rows, and the slots' lengths grow.  The new rows of all sequences, one after the
+ * other, get d_rows [n_rows]: the pool row of each, -1 for the rows of a sequence that is passed
+ * over and behind the last; d_offsets [n_seq + 1]: the place of each sequence's first row among them
+ * (the last entry: their number; rows at and beyond n_rows are planned but not told); d_new_lens
+ * [n_seq]: the slots' lengths, 0 for one out of range.
+ * G4_DEV_BAD_POSITION: a count below 0, rows past max_pages (a count outside 0 .. max_pages *
+ * page_size takes no places in d_rows), or rows that would go into a page which another slot holds.
+ * G4_DEV_NO_PAGES: the pages of a sequence and of those before it, passed over or not, are more than
+ * the pool has left.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows < 0, NULL; d_rows may be NULL with n_rows 0). */
+g4_status g4_pages_extend(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                          const int32_t* d_counts, int32_t n_rows, int32_t* d_rows, int32_t* d_offsets,
+                          int32_t* d_new_lens);
+
+/* Empty slots begin with the first n_pages pages of slot `source` and hold their rows from then on.
+ * G4_DEV_BAD_POSITION: a slot that is not empty or the source itself, a source with fewer than n_pages
+ * full pages.  Errors: INVALID_ARG (n_seq outside 1..n_slots, source out of range, n_pages outside
+ * 0..max_pages, NULL). */
+g4_status g4_pages_share(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                         int32_t source, int32_t n_pages);
+
+/* Cut slots back to their first d_lens[i] rows (NULL: to none; a slot that has no more stays as it
+ * is).  Pages that no slot holds any more go back in the reverse order of the sequences and their
+ * rows, so that the same rows planned again get the same pages.  Table entries without a page are -1.
+ * G4_DEV_BAD_POSITION: a length below 0.  Errors: INVALID_ARG (n_seq outside 1..n_slots, NULL). */
+g4_status g4_pages_truncate(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
+                            const int32_t* d_lens);
+
+/* Keys and values into the pools: row t of k and v [n_rows][num_kv_heads][head_dim] (G4_DT_BF16 or
+ * G4_DT_F16, both the same; seq_stride unused) becomes pool row d_rows[t] of k_pool and v_pool, -1: left out.  head_dim is 64,
+ * 128, 256 or 512; the pools are contiguous, 16-byte aligned and of the rows' type.  Rows are distinct.
+ * G4_DEV_BAD_POSITION: a pool row below -1 or outside the pool; that row is left out.
+ * Errors: INVALID_ARG (NULL or malformed tensors, n_rows < 0), UNSUPPORTED (another type or
+ * head_dim, n_rows * num_kv_heads at 2^31 or more). */
+g4_status g4_pages_store(g4_pages* op, g4_stream stream, int32_t n_rows, const int32_t* d_rows,
+                         int32_t num_kv_heads, int32_t head_dim, const g4_kv4_tensor* k,
+                         const g4_kv4_tensor* v, void* k_pool, void* v_pool);
+
+/* Synchronise `stream`, read and clear the op's device error word (as g4_get_device_error). */
+g4_status g4_pages_get_device_error(g4_pages* op, g4_stream stream, int32_t* word_out);
+/* Bytes of device memory the op owns. */
+int64_t g4_pages_bytes(const g4_pages* op);
+/* Release everything the op owns (after synchronising its device).  NULL is a no-op. */
+void g4_pages_free(g4_pages* op);
+
+/* ----------------------------------------------------------------------------------------
+ * Softmax attention over 16-bit keys and values: whole prompts, and single tokens of a batch whose
+ * sequences share a prefix.  o = sum_j softmax(s)_j V_j with s_j = scale * q . K_j (scale 0:
+ * 1/sqrt(head_dim)); scores, sums and outputs in fp32 and rounded once, except that the weights go
+ * into the products as 16-bit numbers (g4_attn_prompt and the shared rows: one of the tensors' type,
+ * other rows: two bf16 or one fp16).  scale * |q . K_j| beyond 2^25 may give rows that are not
+ * finite.  Sums run in a fixed order: equal calls give equal bits.
+ *
+ * The handle holds one workspace: calls on one g4_attn (captured graphs that hold such calls
+ * included) must be ordered by the caller, on one stream or by events.  No call after g4_attn_create
+ * allocates or synchronises, except g4_attn_get_device_error and g4_attn_free.
+ * --------------------------------------------------------------------------------------*/
+
+typedef struct g4_attn g4_attn;
+
+typedef struct g4_attn_config {
+  int32_t num_q_heads;  /* a multiple of num_kv_heads, at most 64 per KV head */
+  int32_t num_kv_heads; /* 1..64; query heads h * G .. h * G + G - 1 read KV head h */
+  int32_t head_dim;     /* 64, 128, 256 or 512 */
+  int32_t dtype;        /* G4_DT_BF16 or G4_DT_F16: queries, keys, values and outputs */
+  int32_t max_seqs;     /* sequences of a call, 1..1024 */
+} g4_attn_config;
+
+/* Errors: INVALID_ARG, UNSUPPORTED (sizes outside the bounds above), OOM, CUDA. */
+g4_status g4_attn_create(int device, const g4_attn_config* cfg, g4_attn** out);
+
+/* Causal attention of n_seq packed sequences: rows d_offsets[i] .. d_offsets[i + 1] - 1 (int32, on the
+ * device) of q and out [n_rows][num_q_heads][head_dim] and of k and v [n_rows][num_kv_heads][head_dim] are
+ * sequence i's tokens, each of which sees itself and the ones before it, with window > 0 only the newest
+ * `window` of those (itself included).  Rows of no sequence are not seen; those in front of the first
+ * sequence and behind the last are left as they were, or with zero_rest != 0 set to zero.  Tensors
+ * are of the handle's type (seq_stride unused), k and v 16-byte aligned with positive strides that are
+ * multiples of 8 elements, and out shares no element with the others.
+ * A number that is not finite reaches only the rows that see it.
+ * G4_DEV_BAD_POSITION: offsets that fall, or lie outside 0..n_rows; that sequence is passed over.
+ * Errors: INVALID_ARG (n_seq outside 1..max_seqs, n_rows < 0, window < 0, a scale that is negative or not
+ * finite, NULL or malformed tensors), UNSUPPORTED (another type, k or v that are not aligned,
+ * n_rows * heads per KV head at 2^31 or more). */
+g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int32_t* d_offsets, int32_t n_rows,
+                         float scale, int32_t window, int32_t zero_rest, const g4_kv4_tensor* q,
+                         const g4_kv4_tensor* k, const g4_kv4_tensor* v, const g4_kv4_tensor* out);
+
+/* Attention of one token of each of n_seq slots over all rows of its slot, in pools that `pages` has the
+ * table of (g4_pages).  The first shared_pages pages of all slots are the same ones: their rows are read once for
+ * all.  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), sharing no
+ * element.  A slot may be named more than once.  An empty slot gets zeros.
+ * G4_DEV_BAD_SLOT: a slot out of range.  G4_DEV_BAD_POSITION: a slot with fewer rows than the shared
+ * pages hold, with other first pages than the first slot that has so many rows, or with a missing page.  Those sequences get zeros.
+ * Errors: INVALID_ARG (n_seq outside 1..max_seqs, shared_pages outside 0..max_pages, a scale that is negative
+ * or not finite, NULL or malformed tensors, pools that are not 16-byte aligned, `pages` on another device),
+ * UNSUPPORTED (another type; n_pages * num_kv_heads * page_size, or n_seq * num_kv_heads * ceil(heads per KV
+ * head / 8) * ceil(rows of a slot / 16), at 2^31 or more). */
+g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, int32_t n_seq,
+                         const int32_t* d_slots, int32_t shared_pages, float scale, const void* k_pool,
+                         const void* v_pool, const g4_kv4_tensor* q, const g4_kv4_tensor* out);
+
+/* Synchronise `stream`, read and clear the op's device error word (as g4_get_device_error). */
+g4_status g4_attn_get_device_error(g4_attn* op, g4_stream stream, int32_t* word_out);
+/* Bytes of device memory the op owns. */
+int64_t g4_attn_bytes(const g4_attn* op);
+/* Release everything the op owns (after synchronising its device).  NULL is a no-op. */
+void g4_attn_free(g4_attn* op);
 
 #ifdef __cplusplus
 }
