@@ -68,7 +68,8 @@ g4_status attn_init(int device, int optin) {
 }
 
 int attn_workers(const g4_attn* op) { return op->sms * (op->cfg.head_dim <= 128 ? AttTail<128>::kCtas : AttTail<512>::kCtas) * kAttWarps; }
-int attn_pre_rows(const g4_attn* op) { return op->cfg.head_dim <= 128 ? 2 * kAttM : kAttM; }  // query rows of an item
+int attn_group(const g4_attn* op) { return op->cfg.num_q_heads / op->cfg.num_kv_heads; }
+int attn_tokens(const g4_attn* op) { return (op->cfg.head_dim <= 128 ? 2 : 1) * (kAttM / attn_group(op)); }  // of an item
 int attn_half(const g4_attn* op) { return op->cfg.head_dim == 512 ? 2 : 1; }
 // Parts that each block of rows past `tiles` tiles of shared keys is cut into: one item per SM.
 int attn_splits(const g4_attn* op, int blocks, int tiles) {
@@ -77,9 +78,9 @@ int attn_splits(const g4_attn* op, int blocks, int tiles) {
 
 g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
   const g4_attn_config& f = op->cfg;
-  const size_t group = f.num_q_heads / f.num_kv_heads, rows = attn_pre_rows(op), d = f.head_dim;
-  const size_t blocks = (f.max_seqs * group + rows - 1) / rows * f.num_kv_heads;
-  const size_t parts = std::max<size_t>(blocks, op->sms) * rows;
+  const size_t group = attn_group(op), d = f.head_dim, rows = d <= 128 ? 2 * kAttM : kAttM;
+  const size_t items = (size_t)cdiv(f.max_seqs, attn_tokens(op)) * f.num_kv_heads;
+  const size_t parts = std::max<size_t>(items, op->sms) * rows;
   const size_t tails = (2 * (size_t)attn_workers(op) + (size_t)f.max_seqs * f.num_kv_heads * ((group + 7) / 8)) * 8;
   TRY(paged_alloc(&op->mem, &op->err, 1, 0, st));
   TRY(paged_alloc(&op->mem, &op->ticket, 2, 0, st));
@@ -102,6 +103,21 @@ bool attn_map_packed(const g4_attn* op, CUtensorMap* m, const Paged16& t, long r
   const cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box}, step[3] = {1, 1, 1};
   return g_encode(m, attn_type(op), 3, t.p, dim, stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Tokens of the queries: 64 numbers of all heads of a KV head, and as many tokens as a block has.
+bool attn_map_queries(const g4_attn* op, CUtensorMap* m, const Paged16& t, long rows) {
+  const int group = op->cfg.num_q_heads / op->cfg.num_kv_heads;
+  const cuuint64_t dim[3] = {(cuuint64_t)op->cfg.head_dim, (cuuint64_t)op->cfg.num_q_heads, (cuuint64_t)rows};
+  const long whole = (long)op->cfg.head_dim;
+  const cuuint64_t stride[2] = {(cuuint64_t)(dim[1] > 1 ? t.head : whole) * 2, (cuuint64_t)(rows > 1 ? t.row : whole) * 2};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)group, (cuuint32_t)(kAttM / group)}, step[3] = {1, 1, 1};
+  return g_encode(m, attn_type(op), 3, t.p, dim, stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Whether the TMA can copy a tensor's rows.
+bool attn_tma(const Paged16& t, long rows, long heads) {
+  return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && (rows == 1 || (t.row % 8 == 0 && t.row > 0 && t.row < (1L << 38))) &&
+         (heads == 1 || (t.head % 8 == 0 && t.head > 0 && t.head < (1L << 38)));
 }
 // Rows of a pool, all pages and heads one after the other.
 bool attn_map_pool(const g4_attn* op, CUtensorMap* m, const void* pool, long rows, int box) {
@@ -179,10 +195,8 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
     return G4_ERR_INVALID_ARG;
   if ((long)n_rows * group >= (1L << 31)) return G4_ERR_UNSUPPORTED;
   if (!n_rows) return G4_OK;
-  for (const Paged16* t : {&pk, &pv})
-    if (reinterpret_cast<uintptr_t>(t->p) % 16 || (n_rows > 1 && (t->row % 8 || t->row == 0)) ||
-        (f.num_kv_heads > 1 && (t->head % 8 || t->head == 0)) || t->row >= (1L << 39) || t->head >= (1L << 39))
-      return G4_ERR_UNSUPPORTED;
+  if (!attn_tma(pq, n_rows, f.num_q_heads) || !attn_tma(pk, n_rows, f.num_kv_heads) || !attn_tma(pv, n_rows, f.num_kv_heads))
+    return G4_ERR_UNSUPPORTED;
   DEVICE_GUARD(op->device);
   a.q = pq.p;
   a.out = po.p;
@@ -196,10 +210,10 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
   a.k_head = pk.head;
   a.v_row = pv.row;
   a.v_head = pv.head;
-  a.q_vec = pq.vec;
   a.o_vec = po.vec;
   a.group = group;
   a.kvh = f.num_kv_heads;
+  a.tb = kAttM / group;
   a.err = op->err;
   a.offsets = d_offsets;
   a.n_seq = n_seq;
@@ -207,16 +221,17 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
   a.window = window < n_rows ? window : 0;  // one that reaches every row is none
   a.ticket = op->ticket;
   a.zero_rest = zero_rest != 0;
-  // every sequence's last block of rows may be one that is not full
-  const long rows = attn_pre_rows(op), blocks = ((long)n_rows * group + rows - 1) / rows + n_seq;
+  // every sequence's last item may be one that is not full
+  const long blocks = n_rows / attn_tokens(op) + n_seq;
   const int ctas = (int)std::min<long>(op->sms, blocks * f.num_kv_heads * attn_half(op));
   bool ok = true;
   ATT_DISPATCH(d, f.dtype == G4_DT_BF16, {
+    CUtensorMap qm;
     CUtensorMap km;
     CUtensorMap vm;
-    ok = attn_map_packed(op, &km, pk, n_rows, kAttN) && attn_map_packed(op, &vm, pv, n_rows, Att16<D>::kVRows);
+    ok = attn_map_queries(op, &qm, pq, n_rows) && attn_map_packed(op, &km, pk, n_rows, kAttN) && attn_map_packed(op, &vm, pv, n_rows, Att16<D>::kVRows);
     if (ok)
-      launch(att16_kernel<D, BF, false>, dim3(ctas), dim3(Att16<D>::kThreads), Att16<D>::kSmem, reinterpret_cast<cudaStream_t>(stream), a, km, vm);
+      launch(att16_kernel<D, BF, false>, dim3(ctas), dim3(Att16<D>::kThreads), Att16<D>::kSmem, reinterpret_cast<cudaStream_t>(stream), a, qm, km, vm);
   });
   if (!ok) return G4_ERR_UNSUPPORTED;
   CK(cudaGetLastError());
@@ -239,6 +254,7 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
   Paged16 pq, po;
   if (!paged_tensor(q, n_seq, f.num_q_heads, d, false, &pq) || !paged_tensor(out, n_seq, f.num_q_heads, d, true, &po) || po.p == pq.p)
     return G4_ERR_INVALID_ARG;
+  if (!attn_tma(pq, n_seq, f.num_q_heads)) return G4_ERR_UNSUPPORTED;
   t.row_tiles = cdiv(group, 8);
   t.keys = shared_pages * pf.page_size;
   const long pool_rows = (long)pf.n_pages * f.num_kv_heads * pf.page_size;
@@ -247,14 +263,13 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
     return G4_ERR_UNSUPPORTED;
   DEVICE_GUARD(op->device);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int rows = attn_pre_rows(op), blocks = cdiv(n_seq * group, rows), tiles = cdiv(t.keys, kAttN);
+  const int blocks = cdiv(n_seq, attn_tokens(op)), tiles = cdiv(t.keys, kAttN);
   int splits = tiles ? attn_splits(op, blocks, tiles) : 0;
   const int tiles_per = splits ? cdiv(tiles, splits) : 0;
   if (splits) splits = cdiv(tiles, tiles_per);
   t.q = pq.p;
   t.q_row = pq.row;
   t.q_head = pq.head;
-  t.q_vec = pq.vec;
   t.kp = static_cast<const uint16_t*>(k_pool);
   t.vp = static_cast<const uint16_t*>(v_pool);
   t.out = po.p;
@@ -278,7 +293,8 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
   t.pre_o = op->pre_o;
   t.pre_ml = op->pre_ml;
   t.splits = splits;
-  t.pre_rows = rows;
+  t.tb = kAttM / group;
+  t.blocks = d <= 128 ? 2 : 1;
   t.err = op->err;
   bool ok = true;
   ATT_DISPATCH(d, f.dtype == G4_DT_BF16, {
@@ -287,9 +303,9 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
       a.q = pq.p;
       a.q_row = pq.row;
       a.q_head = pq.head;
-      a.q_vec = pq.vec;
-      a.group = group;
+          a.group = group;
       a.kvh = f.num_kv_heads;
+      a.tb = kAttM / group;
       a.scale = t.scale;
       a.err = op->err;
       a.n_seq = n_seq;
@@ -305,13 +321,14 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
       a.tiles_per = tiles_per;
       a.part_o = op->pre_o;
       a.part_ml = op->pre_ml;
+      CUtensorMap qm;
       CUtensorMap km;
       CUtensorMap vm;
-      ok = attn_map_pool(op, &km, k_pool, pool_rows, std::min(kAttN, pf.page_size)) &&
+      ok = attn_map_queries(op, &qm, pq, n_seq) && attn_map_pool(op, &km, k_pool, pool_rows, std::min(kAttN, pf.page_size)) &&
            attn_map_pool(op, &vm, v_pool, pool_rows, std::min(Att16<D>::kVRows, pf.page_size));
       const int items = blocks * f.num_kv_heads * splits * Att16<D>::HV;
       if (ok)
-        launch(att16_kernel<D, BF, true>, dim3(std::min(items, op->sms)), dim3(Att16<D>::kThreads), Att16<D>::kSmem, st, a, km, vm);
+        launch(att16_kernel<D, BF, true>, dim3(std::min(items, op->sms)), dim3(Att16<D>::kThreads), Att16<D>::kSmem, st, a, qm, km, vm);
     }
     if (ok) {
       launch(att_tail_kernel<D, BF>, dim3(op->sms * AttTail<D>::kCtas), dim3(32 * kAttWarps), AttTail<D>::smem(n_seq), st, t);

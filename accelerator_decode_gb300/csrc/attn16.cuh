@@ -4,11 +4,11 @@
 //
 //   s_j = scale * q . K_j     p_j = 2^(s_j log2 e - m)     o = sum p_j V_j / sum p_j
 //
-// The query rows of a KV head are its tokens' heads, token after token (row t * G + g), so that any
-// number of heads per KV head fills the 128 rows of a product.  A CTA takes items of NQ blocks of 128
-// such rows past tiles of 128 keys:
-//   one warp copies tiles of keys and values by TMA into a ring of 128-byte-swizzled stages,
-//   two warps copy an item's queries,
+// The query rows of a KV head are its tokens' heads, token after token (row t * G + g): a block is as
+// many whole tokens as the 128 rows of a product hold.  A CTA takes items of NQ blocks past tiles of
+// 128 keys:
+//   one warp copies an item's queries, and tiles of keys and values into a ring of 128-byte-swizzled
+//   stages, by TMA,
 //   one thread issues S = Q K^T (both operands shared, fp32 in tensor memory) and O += P V (P in
 //   tensor memory, in the columns of the S that it was made of),
 //   four warps for each block of rows take a row per thread: maximum, exponentials, sum.
@@ -53,7 +53,7 @@ struct Att16 {
 
 struct Att16Item {
   int row0;       // first packed row of the sequence
-  int r0, rows;   // first query row of the item; query rows of the sequence
+  int t0, len;    // first token of the item; tokens of the sequence
   int head, half;
   int lo, hi;     // keys lo .. hi - 1 of the sequence
   int part;       // prefix: slot of its partial result
@@ -73,8 +73,9 @@ struct Att16Args {
   const uint16_t* v;  // prompt: for rows whose unseen keys carry values that are not finite
   const uint16_t* k;
   long q_row, q_head, o_row, o_head, k_row, k_head, v_row, v_head;  // strides in elements
-  int q_vec, o_vec;   // 16-byte accesses
+  int o_vec;          // 16-byte accesses
   int group, kvh;
+  int tb;             // tokens of a block: kAttM / group
   float scale;        // times log2 e
   int* err;
   // prompt
@@ -163,16 +164,15 @@ struct Att16Items {
 template <int NQ>
 struct Att16Tiles {
   int n, a1, b0;  // tiles; block 0: 0 .. a1 - 1, block 1: b0 .. n - 1 (b0 = n: it has no rows)
-  __device__ __forceinline__ Att16Tiles(const Att16Item& it, int group, int window, bool causal) {
+  __device__ __forceinline__ Att16Tiles(const Att16Item& it, int tb, int window, bool causal) {
     n = (it.hi - it.lo + kAttN - 1) / kAttN;
     a1 = n;
     b0 = n;
-    if (NQ == 2 && it.r0 + kAttM < it.rows) {
+    if (NQ == 2 && it.t0 + tb < it.len) {
       b0 = 0;
       if (causal) {
-        const int last = (it.r0 + kAttM - 1) / group, first = (it.r0 + kAttM) / group;
-        a1 = (last + 1 - it.lo + kAttN - 1) / kAttN;
-        if (window > 0) b0 = max(0, first - window + 1 - it.lo) / kAttN;
+        a1 = (it.t0 + tb - it.lo + kAttN - 1) / kAttN;
+        if (window > 0) b0 = max(0, it.t0 + tb - window + 1 - it.lo) / kAttN;
       }
     }
   }
@@ -224,7 +224,8 @@ __device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, u
 
 template <int D, bool BF, bool PREFIX>
 __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
-    att16_kernel(const Att16Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    att16_kernel(const Att16Args a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
   using C = Att16<D>;
   constexpr int NQ = C::NQ, DV = C::DV;
   extern __shared__ __align__(16) uint8_t att_raw[];
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       mbar_init(&s->ifull[i], 1);
       mbar_init(&s->iempty[i], 32 * C::kSoftWarps + 1 + 64);
     }
-    mbar_init(&s->qfull, 64);
+    mbar_init(&s->qfull, 1);
     mbar_init(&s->qdone, 1);
     mbar_init(&s->vneed, 1);
     mbar_init(&s->vtail, 64);
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
 
   if (warp == C::kSoftWarps + 1) {
     // ------------------------------------------------ items, and their tiles by TMA
-    int st = 0, lap = 0;
-    const int total = PREFIX ? C::HV * a.kvh * a.splits * ((a.n_seq * a.group + NQ * kAttM - 1) / (NQ * kAttM)) : 0;
+    int st = 0, lap = 0, copied = 0;  // the ring's stage and lap; items whose queries were asked for
+    const int total = PREFIX ? C::HV * a.kvh * a.splits * ((a.n_seq + NQ * a.tb - 1) / (NQ * a.tb)) : 0;
     const int from_slot = PREFIX ? max(0, att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys)) : 0;
     int seq = 0, before = 0;          // prompt: blocks of rows of the sequences ahead of `seq` (a multiple of 32)
     int index = blockIdx.x;
@@ -285,9 +286,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           const int split = x % a.splits;
           x /= a.splits;
           it.head = x % a.kvh;
-          it.r0 = x / a.kvh * (NQ * kAttM);
+          it.t0 = x / a.kvh * (NQ * a.tb);
           it.row0 = 0;
-          it.rows = a.n_seq * a.group;
+          it.len = a.n_seq;
           it.lo = split * a.tiles_per * kAttN;
           it.hi = min(a.keys, it.lo + a.tiles_per * kAttN);
         }
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
               if (blockIdx.x == 0 && n == 0) set_err(a.err, G4_DEV_BAD_POSITION);
             } else {
               len = to - from;
-              blocks = (int)(((long)len * a.group + NQ * kAttM - 1) / (NQ * kAttM));
+              blocks = (len + NQ * a.tb - 1) / (NQ * a.tb);
             }
           }
           int upto = blocks;
@@ -320,13 +321,11 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
             const unsigned who = __ballot_sync(0xFFFFFFFFu, blk < before + upto);
             const int w = __ffs(who) - 1;
             it.row0 = __shfl_sync(0xFFFFFFFFu, from, w);
-            len = __shfl_sync(0xFFFFFFFFu, len, w);
-            // the last rows, with the most keys, come first
-            it.r0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * kAttM);
-            it.rows = len * a.group;
-            const int first = it.r0 / a.group, last = (min(it.r0 + NQ * kAttM, it.rows) - 1) / a.group;
-            it.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
-            it.hi = last + 1;
+            it.len = __shfl_sync(0xFFFFFFFFu, len, w);
+            // the last tokens, with the most keys, come first
+            it.t0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * a.tb);
+            it.lo = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
+            it.hi = min(it.t0 + NQ * a.tb, it.len);
             break;
           }
           before += all;
@@ -346,8 +345,22 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       __syncwarp();
       if (!ok || it.row0 < 0) break;
       const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN;
-      // keys 0, [keys 1 if scores run a tile ahead], values 0, keys ...
+      // keys 0, the queries, [keys 1 if scores run a tile ahead], values 0, keys ...
       for (int x = 0; x < 2 * tiles && ok; ++x) {
+        if (x == (C::KS < C::kStages ? 1 : 0)) {  // (a tile of keys that fills the ring waits for its products)
+          if (n) ok = att_wait(&s->qdone, (n - 1) & 1, s);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const int blocks = NQ == 2 && it.t0 + a.tb < it.len ? 2 : 1, bytes = a.tb * a.group * 128;
+          if (lane == 0) mbar_expect_tx(&s->qfull, blocks * (D / 64) * bytes);
+          __syncwarp();
+          if (lane < blocks * (D / 64)) {
+            const int y = lane / (D / 64), z = lane % (D / 64);
+            att_tma3(qop + y * (kAttM * D * 2) + z * (kAttM * 128), &qmap, 64 * z, it.head * a.group, it.row0 + it.t0 + y * a.tb, &s->qfull);
+          }
+          ++copied;
+          __syncwarp();
+        }
         int j;
         bool values;
         if (NQ == 2) {
@@ -394,6 +407,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       }
     }
     // every copy that was asked for arrives before the CTA ends
+    if (copied) mbar_wait_drain(&s->qfull, (copied - 1) & 1);
     const int asked = lap * C::kStages + st;
     for (int k = max(0, asked - C::kStages); k < asked; ++k) mbar_wait_drain(&s->full[k % C::kStages], (k / C::kStages) & 1);
   } else if (warp == C::kSoftWarps) {
@@ -439,8 +453,8 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         tc_fence_after();
       };
       while (items.next(it)) {
-        const Att16Tiles<NQ> t(it, a.group, a.window, !PREFIX);
-        const bool tail = (PREFIX || it.hi * a.group >= it.rows) && (it.hi - it.lo) % kAttN != 0;
+        const Att16Tiles<NQ> t(it, a.tb, a.window, !PREFIX);
+        const bool tail = (PREFIX || it.hi >= it.len) && (it.hi - it.lo) % kAttN != 0;
         ok = att_wait(&s->qfull, (items.n - 1) & 1, s) && ok;
         tc_fence_after();
         if (NQ == 2) {
@@ -519,37 +533,16 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       mbar_wait_drain(&s->drained, 0);
     }
   } else if (warp > C::kSoftWarps + 1) {
-    // ------------------------------------------------ queries; values behind the last key
+    // ------------------------------------------------ values behind the last key; rows of no sequence
     const int me = threadIdx.x - 32 * (C::kSoftWarps + 2);
     constexpr int CH = D / 8;  // 16-byte pieces of a row
     Att16Items items{s};
     Att16Item it;
     int st = 0, tails = 0;  // stages and cleared tiles of the items so far
     while (items.next(it)) {
-      if (items.n > 1) att_wait(&s->qdone, (items.n - 2) & 1, s);
-#pragma unroll 8
-      for (int e = me; e < NQ * kAttM * CH; e += 64) {
-        const int R = e / CH, c = e % CH, r = it.r0 + R;
-        const bool on = r < it.rows;
-        const int tok = on ? r / a.group : 0, g = on ? r % a.group : 0;
-        const uint16_t* src = a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + g) * a.q_head + 8 * c;
-        const int in = R & (kAttM - 1);
-        uint8_t* dst = qop + (R / kAttM) * (kAttM * D * 2) + (c >> 3) * (kAttM * 128) + in * 128 + (((c & 7) ^ (in & 7)) << 4);
-        if (a.q_vec) {
-          cp_async16(dst, src, on);
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = on ? (uint32_t)__ldcg(src + 2 * x) | ((uint32_t)__ldcg(src + 2 * x + 1) << 16) : 0u;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      cp_async_wait_all();
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(&s->qfull);
       const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN, live = it.hi - it.lo - (tiles - 1) * kAttN;
       st += tiles * (C::KS + C::VS);
-      if ((PREFIX || it.hi * a.group >= it.rows) && live != kAttN) {
+      if ((PREFIX || it.hi >= it.len) && live != kAttN) {
         // the last tile reaches past the sequence: what lies there may be anything
         att_wait(&s->vneed, tails++ & 1, s);
         for (int y = 0; y < C::VS; ++y) {
@@ -579,27 +572,27 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------ softmax: a query row per thread
-    const int y = warp >> 2, row_in = threadIdx.x & 127;
+    const int y = warp >> 2, row_in = threadIdx.x & 127, tok_in = row_in / a.group, hq = row_in % a.group;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ocol = lane_base + y * DV;
     Att16Items items{s};
     Att16Item it;
     int n = 0;  // tiles of this block of rows so far
     while (items.next(it)) {
-      const Att16Tiles<NQ> t(it, a.group, a.window, !PREFIX);
-      const int block0 = it.r0 + y * kAttM, row = block0 + row_in;
-      const bool on = row < it.rows;
+      const Att16Tiles<NQ> t(it, a.tb, a.window, !PREFIX);
+      const int block0 = it.t0 + y * a.tb;  // the block's first token
+      const bool on = tok_in < a.tb && block0 + tok_in < it.len;
       const int j0 = y ? t.b0 : 0, j1 = y ? t.n : t.a1;
       if (j0 >= j1) continue;
-      const int tok = (on ? row : it.rows - 1) / a.group;
+      const int tok = min(block0 + min(tok_in, a.tb - 1), it.len - 1);
       // keys that the row sees: first .. last; every row of the block sees all_first .. all_last
       int first = it.lo, last = it.hi - 1, all_first = it.lo, all_last = it.hi - 1;
       if (!PREFIX) {
         last = tok;
-        all_last = block0 / a.group;
+        all_last = block0;
         if (a.window > 0) {
           first = max(0, tok - a.window + 1);
-          all_first = max(0, (min(block0 + kAttM, it.rows) - 1) / a.group - a.window + 1);
+          all_first = max(0, min(block0 + a.tb, it.len) - a.window);
         }
       }
       float m = -INFINITY, ref = 0.f, l = 0.f;
@@ -686,7 +679,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         if (on && it.half == 0) a.part_ml[at] = make_float2(m, l);
       } else {
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        uint16_t* out = a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + row % a.group) * a.o_head;
+        uint16_t* out = a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + hq) * a.o_head;
         bool odd = false;
 #pragma unroll 1
         for (int c = 0; c < DV; c += 32) {
@@ -714,7 +707,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           __syncwarp();
         }
         if (on && odd && att_finite(l))
-          att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + row % a.group) * a.q_head, out,
+          att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out,
                             it.row0, it.head, it.half * DV, DV, first, last, ref, l);
         __syncwarp();
       }

@@ -31,7 +31,6 @@ struct AttTail {
 struct AttTailArgs {
   const uint16_t *q, *kp, *vp;
   long q_row, q_head;
-  int q_vec;
   uint16_t* out;
   long o_row, o_head;
   int o_vec;
@@ -47,7 +46,7 @@ struct AttTailArgs {
   // the prefix's parts
   const float* pre_o;
   const float2* pre_ml;
-  int splits, pre_rows;              // pre_rows: query rows of a part
+  int splits, tb, blocks;            // tokens of a block of 128 rows, blocks of a part
   int* err;
 };
 
@@ -138,8 +137,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, AttTail<D>::kCtas) att_tail_ke
       uint4 u = make_uint4(0u, 0u, 0u, 0u);
       if (row0 + r < a.group) {
         const uint16_t* p = a.q + (long)seq * a.q_row + (long)(head * a.group + row0 + r) * a.q_head + 8 * c;
-        if (a.q_vec) u = __ldcg(reinterpret_cast<const uint4*>(p));
-        else u = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+        u = __ldcg(reinterpret_cast<const uint4*>(p));
       }
       *reinterpret_cast<uint4*>(sq + r * C::kQRow + c * 16) = u;
     }
@@ -332,15 +330,15 @@ __global__ void __launch_bounds__(256) att_join_kernel(const AttTailArgs a) {
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   float inv = 0.f;
   if (!bad && len > 0) {
-    const int i = seq * a.group + gr;
-    const long pre = a.splits ? ((long)(i / a.pre_rows) * a.kvh + head) * a.splits * a.pre_rows + i % a.pre_rows : 0;
+    const int block = seq / a.tb, rows = a.blocks * kAttM;
+    const long pre = ((long)(block / a.blocks) * a.kvh + head) * a.splits * rows + block % a.blocks * kAttM + seq % a.tb * a.group + gr;
     const int x = head * a.row_tiles + gr / 8, b0 = __ldcg(a.plan + seq), span = __ldcg(a.plan + a.n_seq + 1);
     const int blocks = (len - a.keys + kAttBlock - 1) / kAttBlock, t0 = b0 + x * blocks;
     const int c0 = t0 / span, c1 = blocks ? (t0 + blocks - 1) / span : c0 - 1;
     const int own = c1 - c0 + 1, parts = a.splits + own;
     auto row_of = [&](int p, const float2** ml, const float** o) {
       if (p < a.splits) {
-        const long at = pre + (long)p * a.pre_rows;
+        const long at = pre + (long)p * rows;
         *ml = a.pre_ml + at;
         *o = a.pre_o + at * D;
       } else {

@@ -552,12 +552,12 @@ g4_status g4_attn_create(int device, const g4_attn_config* cfg, g4_attn** out);
  * sequence i's tokens, each of which sees itself and the ones before it, with window > 0 only the newest
  * `window` of those (itself included).  Rows of no sequence are not seen; those in front of the first
  * sequence and behind the last are left as they were, or with zero_rest != 0 set to zero.  Tensors
- * are of the handle's type (seq_stride unused), k and v 16-byte aligned with positive strides that are
+ * are of the handle's type (seq_stride unused), q, k and v 16-byte aligned with positive strides that are
  * multiples of 8 elements, and out shares no element with the others.
  * A number that is not finite reaches only the rows that see it.
  * G4_DEV_BAD_POSITION: offsets that fall, or lie outside 0..n_rows; that sequence is passed over.
  * Errors: INVALID_ARG (n_seq outside 1..max_seqs, n_rows < 0, window < 0, a scale that is negative or not
- * finite, NULL or malformed tensors), UNSUPPORTED (another type, k or v that are not aligned,
+ * finite, NULL or malformed tensors), UNSUPPORTED (another type, q, k or v that are not aligned,
  * n_rows * heads per KV head at 2^31 or more). */
 g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int32_t* d_offsets, int32_t n_rows,
                          float scale, int32_t window, int32_t zero_rest, const g4_kv4_tensor* q,
@@ -565,13 +565,13 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
 
 /* Attention of one token of each of n_seq slots over all rows of its slot, in pools that `pages` has the
  * table of (g4_pages).  The first shared_pages pages of all slots are the same ones: their rows are read once for
- * all.  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), sharing no
- * element.  A slot may be named more than once.  An empty slot gets zeros.
+ * all.  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), q aligned as
+ * in g4_attn_prompt, sharing no element.  A slot may be named more than once.  An empty slot gets zeros.
  * G4_DEV_BAD_SLOT: a slot out of range.  G4_DEV_BAD_POSITION: a slot with fewer rows than the shared
  * pages hold, with other first pages than the first slot that has so many rows, or with a missing page.  Those sequences get zeros.
  * Errors: INVALID_ARG (n_seq outside 1..max_seqs, shared_pages outside 0..max_pages, a scale that is negative
  * or not finite, NULL or malformed tensors, pools that are not 16-byte aligned, `pages` on another device),
- * UNSUPPORTED (another type; n_pages * num_kv_heads * page_size, or n_seq * num_kv_heads * ceil(heads per KV
+ * UNSUPPORTED (another type, a q that is not aligned; n_pages * num_kv_heads * page_size, or n_seq * num_kv_heads * ceil(heads per KV
  * head / 8) * ceil(rows of a slot / 16), at 2^31 or more). */
 g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, int32_t n_seq,
                          const int32_t* d_slots, int32_t shared_pages, float scale, const void* k_pool,
