@@ -210,7 +210,7 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
   a.k_head = pk.head;
   a.v_row = pv.row;
   a.v_head = pv.head;
-  a.o_vec = po.vec;
+  a.o_vec = po.vec && reinterpret_cast<uintptr_t>(po.p) % 32 == 0 && po.row % 16 == 0 && po.head % 16 == 0 ? 2 : po.vec;
   a.group = group;
   a.kvh = f.num_kv_heads;
   a.tb = kAttM / group;

@@ -9,7 +9,7 @@
 // 128 keys:
 //   one warp copies an item's queries, and tiles of keys and values into a ring of 128-byte-swizzled
 //   stages, by TMA,
-//   one thread issues S = Q K^T (both operands shared, fp32 in tensor memory) and O += P V (P in
+//   a warp issues S = Q K^T (both operands shared, fp32 in tensor memory) and O += P V (P in
 //   tensor memory, in the columns of the S that it was made of),
 //   four warps for each block of rows take a row per thread: maximum, exponentials, sum.
 // With heads up to 128 two blocks of rows share each tile (NQ 2): while one's weights are made, the
@@ -73,7 +73,7 @@ struct Att16Args {
   const uint16_t* v;  // prompt: for rows whose unseen keys carry values that are not finite
   const uint16_t* k;
   long q_row, q_head, o_row, o_head, k_row, k_head, v_row, v_head;  // strides in elements
-  int o_vec;          // 16-byte accesses
+  int o_vec;          // accesses of 16 bytes (1) or 32 (2)
   int group, kvh;
   int tb;             // tokens of a block: kAttM / group
   float scale;        // times log2 e
@@ -95,6 +95,34 @@ __device__ __forceinline__ float att_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float att_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 numbers at a time.
+__device__ __forceinline__ uint64_t att_two(float lo, float hi) {
+  uint64_t y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
+  return y;
+}
+__device__ __forceinline__ uint64_t att_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t att_add2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+__device__ __forceinline__ void att_split(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+// 32 bytes to a 32-byte-aligned address: a whole sector at a time.
+__device__ __forceinline__ void att_store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 // Two numbers rounded to the 16-bit type (BF: bf16, else fp16), the first in the low half.
 template <bool BF>
@@ -118,6 +146,30 @@ template <bool BF>
 __device__ __forceinline__ constexpr uint32_t att_idesc(int n, bool b_leading) {
   return (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (b_leading ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kAttM >> 4) << 24);
+}
+// A descriptor `bytes` further into shared memory (its address field does not carry into the next one).
+__device__ __forceinline__ uint64_t att_desc_at(uint64_t desc, uint32_t bytes) {
+  return (desc & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4));
+}
+// The warp that issues matrix instructions walks through its loops as one, so that what it computes is the
+// same in all lanes and descriptors come from uniform registers; the thread with `one` issues.  (Inside a
+// branch that one thread takes, each product cost some 80 cycles to issue, more than its 64 in the
+// pipe: 16,384 tokens took 1,630 us instead of 1,325.)
+__device__ __forceinline__ uint32_t att_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ void att_commit(uint32_t one, uint64_t* b) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(su32(b)), "r"(one) : "memory");
+}
+__device__ __forceinline__ void att_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void att_mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one) : "memory");
 }
 __device__ __forceinline__ void att_tma3(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -222,6 +274,10 @@ __device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, u
   }
 }
 
+// With NQ 2 the 12 warps begin with 168 registers a thread: 4 x 72 + 8 x 216 = 12 x 168.
+__device__ __forceinline__ void att_fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n"); }
+__device__ __forceinline__ void att_more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n"); }
+
 template <int D, bool BF, bool PREFIX>
 __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     att16_kernel(const Att16Args a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -245,7 +301,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       mbar_init(&s->pfull[i], 4);
       mbar_init(&s->pvdone[i], 1);
       mbar_init(&s->ifull[i], 1);
-      mbar_init(&s->iempty[i], 32 * C::kSoftWarps + 1 + 64);
+      mbar_init(&s->iempty[i], 32 * C::kSoftWarps + 32 + 64);
     }
     mbar_init(&s->qfull, 1);
     mbar_init(&s->qdone, 1);
@@ -268,10 +324,13 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
 
   if (warp == C::kSoftWarps + 1) {
     // ------------------------------------------------ items, and their tiles by TMA
+    if (NQ == 2) att_fewer_registers();
     int st = 0, lap = 0, copied = 0;  // the ring's stage and lap; items whose queries were asked for
     const int total = PREFIX ? C::HV * a.kvh * a.splits * ((a.n_seq + NQ * a.tb - 1) / (NQ * a.tb)) : 0;
     const int from_slot = PREFIX ? max(0, att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys)) : 0;
-    int seq = 0, before = 0;          // prompt: blocks of rows of the sequences ahead of `seq` (a multiple of 32)
+    // prompt: the lane's sequence of the 32 from `seq` on: its first row, length and last item (one too far);
+    // items of all 32, and of the sequences ahead of them
+    int seq = -32, from = 0, len = 0, upto = 0, all = 0, before = 0;
     int index = blockIdx.x;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -297,43 +356,37 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         const int blk = index / (a.kvh * C::HV), x = index % (a.kvh * C::HV);
         it.head = x / C::HV;
         it.half = x % C::HV;
-        while (seq < a.n_seq) {  // 32 sequences at a time
+        while (blk >= before + all && seq + 32 < a.n_seq) {
+          before += all;
+          seq += 32;
           const int i = seq + lane;
-          int from = 0, len = 0, blocks = 0;
+          from = len = upto = 0;
           if (i < a.n_seq) {
             from = __ldg(a.offsets + i);
             const int to = __ldg(a.offsets + i + 1);
             if (from < 0 || to < from || to > a.n_rows) {
-              if (blockIdx.x == 0 && n == 0) set_err(a.err, G4_DEV_BAD_POSITION);
+              if (blockIdx.x == 0) set_err(a.err, G4_DEV_BAD_POSITION);
             } else {
               len = to - from;
-              blocks = (len + NQ * a.tb - 1) / (NQ * a.tb);
+              upto = (len + NQ * a.tb - 1) / (NQ * a.tb);
             }
           }
-          int upto = blocks;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += y;
           }
-          const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-          if (blk < before + all) {
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, blk < before + upto);
-            const int w = __ffs(who) - 1;
-            it.row0 = __shfl_sync(0xFFFFFFFFu, from, w);
-            it.len = __shfl_sync(0xFFFFFFFFu, len, w);
-            // the last tokens, with the most keys, come first
-            it.t0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * a.tb);
-            it.lo = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
-            it.hi = min(it.t0 + NQ * a.tb, it.len);
-            break;
-          }
-          before += all;
-          seq += 32;
+          all = __shfl_sync(0xFFFFFFFFu, upto, 31);
         }
-        int next = 0;
-        if (lane == 0 && it.row0 >= 0) next = gridDim.x + atomicAdd(a.ticket, 1u);
-        index = __shfl_sync(0xFFFFFFFFu, next, 0);
+        if (blk < before + all) {
+          const int w = __ffs(__ballot_sync(0xFFFFFFFFu, blk < before + upto)) - 1;
+          it.row0 = __shfl_sync(0xFFFFFFFFu, from, w);
+          it.len = __shfl_sync(0xFFFFFFFFu, len, w);
+          // the last tokens, with the most keys, come first
+          it.t0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * a.tb);
+          it.lo = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
+          it.hi = min(it.t0 + NQ * a.tb, it.len);
+        }
       }
       if (n >= 2) ok = att_wait(&s->iempty[n & 1], ((n - 2) >> 1) & 1, s);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -405,14 +458,24 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           if (++st == C::kStages) st = 0, ++lap;
         }
       }
+      if (!PREFIX) {  // the next item, when this one's tiles are on their way: asked for earlier, the last items end unevenly
+        if (lane == 0) index = gridDim.x + atomicAdd(a.ticket, 1u);
+        index = __shfl_sync(0xFFFFFFFFu, index, 0);
+      }
     }
     // every copy that was asked for arrives before the CTA ends
     if (copied) mbar_wait_drain(&s->qfull, (copied - 1) & 1);
     const int asked = lap * C::kStages + st;
     for (int k = max(0, asked - C::kStages); k < asked; ++k) mbar_wait_drain(&s->full[k % C::kStages], (k / C::kStages) & 1);
+    // ... and so does every arrival of the matrix instructions that no other role waits for
+    if (copied) att_wait(&s->qdone, (copied - 1) & 1, s);
+    for (int k = max(0, asked - C::kStages); k < asked; ++k) att_wait(&s->empty[k % C::kStages], (k / C::kStages) & 1, s);
+    __syncwarp();
   } else if (warp == C::kSoftWarps) {
     // ------------------------------------------------ matrix instructions
-    if (lane == 0) {
+    if (NQ == 2) att_fewer_registers();
+    {
+      const uint32_t one = att_elect();
       Att16Items items{s};
       Att16Item it;
       int st = 0, lap = 0, n_p[2] = {0, 0}, tiles_done = 0, tails = 0;
@@ -423,31 +486,33 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         return su32(ring + st * C::kStage);
       };
       auto done = [&]() {
-        tc_commit(&s->empty[st]);
+        att_commit(one, &s->empty[st]);
         if (++st == C::kStages) st = 0, ++lap;
       };
       auto scores_part = [&](int y, int buf, uint32_t kaddr, int part) {
         if (!ok) return;
-        const uint32_t qaddr = su32(qop) + y * (kAttM * D * 2) + part * (C::kStage / C::kSlab) * (kAttM * 128);
+        const uint64_t qd = tc_desc(su32(qop) + y * (kAttM * D * 2) + part * (C::kStage / C::kSlab) * (kAttM * 128), 0), kd = tc_desc(kaddr, 0);
+        const uint32_t to = tmem + C::kColS + buf * kAttN;
 #pragma unroll
         for (int k = 0; k < C::kStage / C::kSlab * 4; ++k) {
           const uint32_t off = (k >> 2) * C::kSlab + (k & 3) * 32;
-          tc_mma_ss(tmem + C::kColS + buf * kAttN, tc_desc(qaddr + off, 0), tc_desc(kaddr + off, 0), att_idesc<BF>(kAttN, false), part > 0 || k > 0);
+          att_mma_ss(one, to, att_desc_at(qd, off), att_desc_at(kd, off), att_idesc<BF>(kAttN, false), part > 0 || k > 0);
         }
       };
       auto weights_part = [&](int y, int buf, uint32_t vaddr, int part, bool first) {
         if (!ok) return;
+        const uint64_t vd = tc_desc(vaddr, C::kVRows * 128);
+        const uint32_t to = tmem + y * DV, from = tmem + C::kColS + buf * kAttN + part * (C::kVRows / 16) * 8;
 #pragma unroll
         for (int k = 0; k < C::kVRows / 16; ++k)
-          tc_mma_ts(tmem + y * DV, tmem + C::kColS + buf * kAttN + (part * (C::kVRows / 16) + k) * 8, tc_desc(vaddr + k * 2048, C::kVRows * 128),
-                    att_idesc<BF>(DV, true), !first || part > 0 || k > 0);
+          att_mma_ts(one, to, from + k * 8, att_desc_at(vd, k * 2048), att_idesc<BF>(DV, true), !first || part > 0 || k > 0);
       };
       auto clear_tail = [&]() {  // has the rows of values behind the last key cleared, once they are there
         for (int y = 0; y < C::VS; ++y) {
           const int x = st + y < C::kStages ? st + y : st + y - C::kStages;
           ok = att_wait(&s->full[x], (st + y < C::kStages ? lap : lap + 1) & 1, s) && ok;
         }
-        mbar_arrive(&s->vneed);
+        if (one) mbar_arrive(&s->vneed);
         ok = att_wait(&s->vtail, tails & 1, s) && ok;
         ++tails;
         tc_fence_after();
@@ -462,10 +527,10 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           for (int y = 0; y < 2; ++y)
             if (t.sees(y, 0)) {
               scores_part(y, y, k0, 0);
-              tc_commit(&s->sfull[y]);
+              att_commit(one, &s->sfull[y]);
             }
           done();
-          if (t.n == 1) tc_commit(&s->qdone);
+          if (t.n == 1) att_commit(one, &s->qdone);
           for (int j = 0; j < t.n; ++j) {
             const uint32_t v0 = stage();
             if (tail && j == t.n - 1) clear_tail();
@@ -478,9 +543,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
                 ++n_p[y];
                 tc_fence_after();
                 weights_part(y, y, v0, 0, y ? j == t.b0 : j == 0);
-                tc_commit(&s->pvdone[y]);
+                if (!t.sees(y, j + 1) || j + 1 == t.n) att_commit(one, &s->pvdone[y]);  // (else the next scores tell it)
               }
-              if (y == 1) tc_commit(&s->empty[vst]);
+              if (y == 1) att_commit(one, &s->empty[vst]);
               if (j + 1 < t.n && t.sees(y, j + 1)) {
                 if (!have) {
                   const int kst = vst + 1 == C::kStages ? 0 : vst + 1, klap = vst + 1 == C::kStages ? vlap + 1 : vlap;
@@ -490,13 +555,13 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
                   have = true;
                 }
                 scores_part(y, y, k1, 0);
-                tc_commit(&s->sfull[y]);
+                att_commit(one, &s->sfull[y]);
               }
             }
             if (++st == C::kStages) st = 0, ++lap;
             if (j + 1 < t.n) {
               done();
-              if (j + 2 == t.n) tc_commit(&s->qdone);
+              if (j + 2 == t.n) att_commit(one, &s->qdone);
             }
           }
         } else {
@@ -506,8 +571,8 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
               scores_part(0, b, stage(), y);
               done();
             }
-            tc_commit(&s->sfull[b]);
-            if (j == t.n - 1) tc_commit(&s->qdone);
+            att_commit(one, &s->sfull[b]);
+            if (j == t.n - 1) att_commit(one, &s->qdone);
           };
           scores(0);
           for (int j = 0; j < t.n; ++j) {
@@ -524,16 +589,18 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
               weights_part(0, b, v0, y, j == 0);
               done();
             }
-            tc_commit(&s->pvdone[0]);
+            att_commit(one, &s->pvdone[0]);
           }
           tiles_done += t.n;
         }
       }
-      tc_commit(&s->drained);
+      att_commit(one, &s->drained);
       mbar_wait_drain(&s->drained, 0);
     }
+    __syncwarp();
   } else if (warp > C::kSoftWarps + 1) {
     // ------------------------------------------------ values behind the last key; rows of no sequence
+    if (NQ == 2) att_fewer_registers();
     const int me = threadIdx.x - 32 * (C::kSoftWarps + 2);
     constexpr int CH = D / 8;  // 16-byte pieces of a row
     Att16Items items{s};
@@ -572,12 +639,13 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------ softmax: a query row per thread
+    if (NQ == 2) att_more_registers();
     const int y = warp >> 2, row_in = threadIdx.x & 127, tok_in = row_in / a.group, hq = row_in % a.group;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ocol = lane_base + y * DV;
     Att16Items items{s};
     Att16Item it;
-    int n = 0;  // tiles of this block of rows so far
+    int n = 0, done = 0;  // tiles of this block of rows and items so far
     while (items.next(it)) {
       const Att16Tiles<NQ> t(it, a.tb, a.window, !PREFIX);
       const int block0 = it.t0 + y * a.tb;  // the block's first token
@@ -613,20 +681,26 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           for (int k = 0; k < 128; ++k)
             if (k > most || k < least) v[k] = 0xFF800000u;
         }
-        float mx = __uint_as_float(v[0]);
+        float top[4];
 #pragma unroll
-        for (int k = 1; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
-        mx *= a.scale;
+        for (int k = 0; k < 4; ++k) top[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
+#pragma unroll
+        for (int k = 8; k < 128; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = att_max3(top[e], __uint_as_float(v[k + e]), __uint_as_float(v[k + 4 + e]));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale;
         const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, raise)) {
           const float nm = raise ? mx : m, fac = raise ? att_exp2(m - nm) : 1.f;
           m = nm;
           ref = m == -INFINITY ? 0.f : m;
           l *= fac;
-          if (j > j0) {  // the output so far follows, when the previous tile's product is in
-            att_wait(&s->pvdone[NQ == 2 ? y : 0], (n - 1) & 1, s);
-            __syncwarp();
-            tc_fence_after();
+          if (j > j0) {  // the output so far follows, when the previous tile's product is in (NQ 2: it came before the scores)
+            if (NQ == 1) {
+              att_wait(&s->pvdone[0], (n - 1) & 1, s);
+              __syncwarp();
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
               uint32_t u[32];
@@ -639,27 +713,32 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
             tc_tst_wait();
           }
         }
-        float s0 = 0.f, s1 = 0.f;
+        const uint64_t sc = att_two(a.scale, a.scale), off = att_two(-ref, -ref);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int k = 0; k < 64; ++k) {
-          const float p0 = att_exp2(fmaf(__uint_as_float(v[2 * k]), a.scale, -ref));
-          const float p1 = att_exp2(fmaf(__uint_as_float(v[2 * k + 1]), a.scale, -ref));
-          s0 += p0;
-          s1 += p1;
+          const uint64_t x = att_fma2(att_two(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc, off);
+          float p0, p1;
+          att_split(x, p0, p1);
+          p0 = att_exp2(p0);
+          p1 = att_exp2(p1);
+          sum[k & 1] = att_add2(sum[k & 1], att_two(p0, p1));
           v[k] = att_pack<BF>(p0, p1);
         }
-        l += s0 + s1;
         tc_tst32(cols, v);
         tc_tst32(cols + 32, v + 32);
         tc_tst_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->pfull[b]);
+        float s0, s1;
+        att_split(att_add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       // ---- the row's output.  (A barrier's parity tells a phase from the one before it alone: with NQ 1 the
       // last tile's scores say that the product before the previous one is in, no more.)
       if (NQ == 1 && n >= 2) att_wait(&s->pvdone[0], n & 1, s);
-      att_wait(&s->pvdone[NQ == 2 ? y : 0], (n - 1) & 1, s);
+      att_wait(&s->pvdone[NQ == 2 ? y : 0], (NQ == 2 ? done++ : n - 1) & 1, s);
       __syncwarp();
       tc_fence_after();
       if (PREFIX) {
@@ -672,7 +751,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           tc_tld_wait();
           if (on) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(part + c)[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) att_store32(part + c + 8 * k, u + 8 * k);
           }
           __syncwarp();
         }
@@ -694,6 +773,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           }
           uint16_t* o = out + it.half * DV + c;
           if (!on) {
+          } else if (a.o_vec == 2) {
+            att_store32(o, w);
+            att_store32(o + 16, w + 8);
           } else if (a.o_vec) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(o)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
