@@ -16,7 +16,7 @@ struct g4_attn {
   unsigned* ticket = nullptr;
   float *pre_o = nullptr, *tail_o = nullptr;      // parts of the prefix, of the rows behind it
   float2 *pre_ml = nullptr, *tail_ml = nullptr;
-  int* plan = nullptr;
+  int4* plan = nullptr;
 };
 
 namespace {
@@ -67,13 +67,20 @@ g4_status attn_init(int device, int optin) {
   return G4_OK;
 }
 
-int attn_workers(const g4_attn* op) { return op->sms * (op->cfg.head_dim <= 128 ? AttTail<128>::kCtas : AttTail<512>::kCtas) * kAttWarps; }
+// Parts that the rows behind a prefix are cut into: two for each of the warps that take them.
+int attn_most(const g4_attn* op) {
+  const int d = op->cfg.head_dim;
+  return 2 * op->sms * (d <= 128 ? AttTail<128>::kWarps : d == 256 ? AttTail<256>::kWarps : AttTail<512>::kWarps);
+}
 int attn_group(const g4_attn* op) { return op->cfg.num_q_heads / op->cfg.num_kv_heads; }
 int attn_tokens(const g4_attn* op) { return (op->cfg.head_dim <= 128 ? 2 : 1) * (kAttM / attn_group(op)); }  // of an item
 int attn_half(const g4_attn* op) { return op->cfg.head_dim == 512 ? 2 : 1; }
-// Parts that each block of rows past `tiles` tiles of shared keys is cut into: one item per SM.
+// Parts that each item past `tiles` tiles of shared keys is cut into: one for each SM, or for every second where that leaves
+// an SM 32 tiles at the most; the others begin with the rows behind the prefix meanwhile.
 int attn_splits(const g4_attn* op, int blocks, int tiles) {
-  return std::max(1, std::min(tiles, op->sms / (blocks * op->cfg.num_kv_heads * attn_half(op))));
+  const int items = blocks * op->cfg.num_kv_heads * attn_half(op);
+  const int sms = (long)items * tiles > 32L * op->sms / 2 ? op->sms : op->sms / 2;
+  return std::max(1, std::min(tiles, sms / items));
 }
 
 g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
@@ -81,14 +88,14 @@ g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
   const size_t group = attn_group(op), d = f.head_dim, rows = d <= 128 ? 2 * kAttM : kAttM;
   const size_t items = (size_t)cdiv(f.max_seqs, attn_tokens(op)) * f.num_kv_heads;
   const size_t parts = std::max<size_t>(items, op->sms) * rows;
-  const size_t tails = (2 * (size_t)attn_workers(op) + (size_t)f.max_seqs * f.num_kv_heads * ((group + 7) / 8)) * 8;
+  const size_t tails = ((size_t)attn_most(op) + (size_t)f.max_seqs * f.num_kv_heads * ((group + 7) / 8)) * 8;
   TRY(paged_alloc(&op->mem, &op->err, 1, 0, st));
   TRY(paged_alloc(&op->mem, &op->ticket, 2, 0, st));
   TRY(paged_alloc(&op->mem, &op->pre_o, parts * d, 0, st));
   TRY(paged_alloc(&op->mem, &op->pre_ml, parts, 0, st));
   TRY(paged_alloc(&op->mem, &op->tail_o, tails * d, 0, st));
   TRY(paged_alloc(&op->mem, &op->tail_ml, tails, 0, st));
-  TRY(paged_alloc(&op->mem, &op->plan, (size_t)f.max_seqs + 2, 0, st));
+  TRY(paged_alloc(&op->mem, &op->plan, (size_t)f.max_seqs, 0, st));
   return G4_OK;
 }
 
@@ -289,7 +296,8 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
   t.part_o = op->tail_o;
   t.part_ml = op->tail_ml;
   t.plan = op->plan;
-  t.workers = attn_workers(op);
+  t.most = attn_most(op);
+  t.ticket = op->ticket;
   t.pre_o = op->pre_o;
   t.pre_ml = op->pre_ml;
   t.splits = splits;
@@ -331,8 +339,8 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
         launch(att16_kernel<D, BF, true>, dim3(std::min(items, op->sms)), dim3(Att16<D>::kThreads), Att16<D>::kSmem, st, a, qm, km, vm);
     }
     if (ok) {
-      launch(att_tail_kernel<D, BF>, dim3(op->sms * AttTail<D>::kCtas), dim3(32 * kAttWarps), AttTail<D>::smem(n_seq), st, t);
-      launch(att_join_kernel<D, BF>, dim3(cdiv(n_seq * f.num_q_heads, 8)), dim3(256), 0, st, t);
+      launch(att_tail_kernel<D, BF>, dim3(op->sms), dim3(32 * AttTail<D>::kWarps), AttTail<D>::smem(n_seq), st, t);
+      launch(att_join_kernel<D, BF>, dim3(n_seq * f.num_q_heads), dim3(32 * kAttJoinWarps), 0, st, t);
     }
   });
   if (!ok) return G4_ERR_UNSUPPORTED;

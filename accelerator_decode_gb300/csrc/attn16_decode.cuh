@@ -1,31 +1,33 @@
 // Attention of one token per sequence over a batch's rows behind their shared prefix, and the join of
 // those parts with the prefix's (attn16.cuh).
 //
-// HBM bounds it: every row is read once, by a warp that keeps it in registers.  A block is 16 rows of
-// one KV head, which lie in one page.  With the rows as the matrix instructions' 16-row operand and
-// up to eight query heads as their columns,
+// HBM bounds it: every row is read once.  A block is 16 rows of one KV head, which lie one after the
+// other in one page: a warp copies blocks into a ring of its own by two bulk copies each.  With the rows
+// as the matrix instructions' 16-row operand and up to eight query heads as their columns,
 //   S^T (16 keys x 8) = K Q^T     O^T (16 numbers x 8) += V^T P^T,
-// a lane's 16-byte loads are its operands as they come: a permutation of the head dim that keys and
+// 16-byte loads from the ring are the operands as they come: a permutation of the head dim that keys and
 // queries share, and pairs of values' rows interleaved by a byte permutation.  O^T takes D / 4
-// registers a lane.  All (sequence, KV head, block) triples are cut into equal spans, one per warp;
-// an item (sequence, KV head, eight query heads) that lies in several spans leaves a part in each, so
-// that few long rows use as many warps as many short ones.
+// registers a lane, the queries D / 8.
+// Every item (sequence, KV head, eight query heads) is cut into parts of equally many blocks, as many
+// as there are warps to take them, which they do one after the other as they come free: CTAs whose SM still
+// works on the prefix join in late.
 // Weights go into the products in two bf16 parts (p - bf16(p) as well), or as one fp16.
 #pragma once
 #include "attn16.cuh"
 
 namespace g4 {
 
-constexpr int kAttBlock = 16;     // rows of a block
-constexpr int kAttWarps = 4;      // warps of a CTA
+constexpr int kAttBlock = 16;      // rows of a block
+constexpr int kAttMinPart = 4;     // blocks of a part at the least
 constexpr int kAttMaxSeqs = 1024;
 
 template <int D>
 struct AttTail {
-  static constexpr int kCtas = D <= 128 ? 4 : 2;                         // CTAs of an SM
-  static constexpr int kQRow = D * 2 + 64;                               // bytes of a query row in shared memory
-  static constexpr size_t kSmemQ = (size_t)kAttWarps * 8 * kQRow;
-  static size_t smem(int n_seq) { return kSmemQ + (size_t)(2 * n_seq + 1) * 4; }
+  static constexpr int kRows = kAttBlock * D * 2;                        // bytes of a block's keys, or values
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kWarps = D <= 128 ? 12 : D == 256 ? 6 : 3;        // 192 KB of rings
+  static constexpr int kRing = kStages * 2 * kRows;
+  static size_t smem(int n_seq) { return (size_t)kWarps * (kRing + 8 * kStages) + 16 + (size_t)(2 * n_seq + 1) * 4; }
 };
 
 struct AttTailArgs {
@@ -39,10 +41,11 @@ struct AttTailArgs {
   const int *table, *slots, *lens;
   int n_slots, n_pages, log_page, max_pages;
   int keys;                          // rows of the prefix
-  float* part_o;                     // [2 * workers + items][8][D]
+  int most;                          // parts, but for one more of every item
+  float* part_o;                     // [most + items][8][D]
   float2* part_ml;
-  int* plan;                         // [n_seq + 1] blocks ahead of each sequence, then the span
-  int workers;
+  int4* plan;                        // of each sequence: its first part, parts of an item, error bits, rows
+  unsigned* ticket;                  // [2]: the next part, CTAs that are done
   // the prefix's parts
   const float* pre_o;
   const float2* pre_ml;
@@ -57,7 +60,26 @@ __device__ __forceinline__ int att_tail_len(const AttTailArgs& a, int i) {
   const int len = __ldcg(a.lens + slot);
   return len >= a.keys && len <= a.max_pages << a.log_page ? len - a.keys : 0;
 }
-__device__ __forceinline__ int att_part(int worker, int t0, int span) { return 2 * worker + (t0 > worker * span); }
+// What is wrong with sequence i (error bits), and its rows; a warp's threads call it together.
+__device__ __forceinline__ int att_check(const AttTailArgs& a, int i, int* rows) {
+  const int lane = threadIdx.x & 31, slot = __ldcg(a.slots + i);
+  *rows = 0;
+  if (slot < 0 || slot >= a.n_slots) return G4_DEV_BAD_SLOT;
+  const int len = __ldcg(a.lens + slot);
+  if (len == 0) return 0;
+  if (len < a.keys || len > a.max_pages << a.log_page) return G4_DEV_BAD_POSITION;
+  const int shared = a.keys >> a.log_page, pages = (len + (1 << a.log_page) - 1) >> a.log_page;
+  const int* table = a.table + (long)slot * a.max_pages;
+  const int* same = a.table + (long)att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys) * a.max_pages;  // (this slot at the latest)
+  int wrong = 0;
+#pragma unroll 4
+  for (int p = lane; p < pages; p += 32) {
+    const int id = __ldcg(table + p);
+    wrong |= id < 0 || id >= a.n_pages || (p < shared && id != __ldcg(same + p));
+  }
+  *rows = len;
+  return __any_sync(0xFFFFFFFFu, wrong) ? G4_DEV_BAD_POSITION : 0;
+}
 
 template <bool BF>
 __device__ __forceinline__ void att_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -75,115 +97,120 @@ __device__ __forceinline__ uint32_t att_transpose(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint4 att_stream(const uint16_t* p) {
-  uint4 u;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-  return u;
-}
 
 template <int D, bool BF>
-__global__ void __launch_bounds__(32 * kAttWarps, AttTail<D>::kCtas) att_tail_kernel(const AttTailArgs a) {
+__global__ void __launch_bounds__(32 * AttTail<D>::kWarps, 1) att_tail_kernel(const AttTailArgs a) {
   using C = AttTail<D>;
-  constexpr int KB = D / 32 < 8 ? D / 32 : 8, VB = D / 64 < 4 ? D / 64 : 4;  // pieces that a lane loads ahead
   extern __shared__ __align__(16) uint8_t att_raw[];
-  int* first = reinterpret_cast<int*>(att_raw + C::kSmemQ);  // [n_seq + 1] blocks ahead, all heads counted
-  int* lens = first + a.n_seq + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* sq = att_raw + warp * 8 * C::kQRow;
-  const int per_block = a.kvh * a.row_tiles;
+  uint8_t* ring = att_raw + warp * C::kRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(att_raw + C::kWarps * C::kRing) + warp * C::kStages;
+  int* shared = reinterpret_cast<int*>(att_raw + C::kWarps * (C::kRing + 8 * C::kStages));
+  int* first = shared + 4;               // [n_seq + 1] parts ahead of each sequence
+  int* lens = first + a.n_seq + 1;       // [n_seq]
+  const int per_seq = a.kvh * a.row_tiles;
+  if (lane < C::kStages) mbar_init(full + lane, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
 
   // The arguments are older than the prefix's launch, which waited for what made them: they may be
   // read, and the rows attended to, while it runs.
   if (a.splits == 0) pdl_wait();
   pdl_trigger();
+  for (int i = threadIdx.x; i < a.n_seq; i += 32 * C::kWarps) lens[i] = att_tail_len(a, i);
+  __syncthreads();
   if (warp == 0) {
+    int blocks = 0;
+    for (int i = lane; i < a.n_seq; i += 32) blocks += (lens[i] + kAttBlock - 1) / kAttBlock;
+    const int total = (int)__reduce_add_sync(0xFFFFFFFFu, blocks) * per_seq;
+    const int size = max(kAttMinPart, (total + a.most - 1) / a.most);  // blocks of a part
     int before = 0;
     for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
-      const int i = i0 + lane, len = i < a.n_seq ? att_tail_len(a, i) : 0;
-      int upto = (len + kAttBlock - 1) / kAttBlock * per_block;
+      const int i = i0 + lane;
+      int upto = i < a.n_seq ? ((lens[i] + kAttBlock - 1) / kAttBlock + size - 1) / size * per_seq : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
         if (lane >= o) upto += y;
       }
-      if (i < a.n_seq) {
-        first[i + 1] = before + upto;
-        lens[i] = len;
-      }
+      if (i < a.n_seq) first[i + 1] = before + upto;
       before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    if (lane == 0) first[0] = 0;
+    if (lane == 0) {
+      first[0] = 0;
+      shared[0] = size;
+    }
   }
   __syncthreads();
-  const int total = first[a.n_seq], span = max(1, (total + a.workers - 1) / a.workers);
-  const int me = blockIdx.x * kAttWarps + warp;
-  const int b0 = (int)min((long)total, (long)me * span), b1 = min(total, b0 + span);
-  for (int at = b0; at < b1;) {
+  const int total = first[a.n_seq], size = shared[0];
+  bool alive = true;
+  uint32_t used = 0;  // copies that were asked for: stage used % kStages
+  for (int part = warp * gridDim.x + blockIdx.x; part < total && alive;) {  // (neighbours on different SMs)
     int lo = 0, hi = a.n_seq;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (first[mid] <= at) lo = mid;
+      if (first[mid] <= part) lo = mid;
       else hi = mid;
     }
-    const int seq = lo, len = lens[seq], blocks = (len + kAttBlock - 1) / kAttBlock;
-    const int x = (at - first[seq]) / blocks, from = (at - first[seq]) % blocks, t0 = at - from;
-    const int head = x / a.row_tiles, row0 = x % a.row_tiles * 8;
-    const int upto = min(blocks, from + b1 - at);
+    const int seq = lo, len = lens[seq], blocks = (len + kAttBlock - 1) / kAttBlock, each = (blocks + size - 1) / size;
+    const int x = (part - first[seq]) / each, from = (part - first[seq]) % each * size;
+    const int head = x / a.row_tiles, row0 = x % a.row_tiles * 8, upto = min(blocks, from + size);
     const int* table = a.table + (long)__ldcg(a.slots + seq) * a.max_pages;
 
-    __syncwarp();
-    for (int e = lane; e < 8 * (D / 8); e += 32) {  // the item's queries
-      const int r = e / (D / 8), c = e % (D / 8);
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (row0 + r < a.group) {
-        const uint16_t* p = a.q + (long)seq * a.q_row + (long)(head * a.group + row0 + r) * a.q_head + 8 * c;
-        u = __ldcg(reinterpret_cast<const uint4*>(p));
+    // copy block b (a lane holds the page of block 32 k + lane of the part)
+    int page = 0, pages_at = from;
+    auto pages = [&](int at) {
+      const int b = at + lane;
+      page = b < upto ? __ldcg(table + ((a.keys + b * kAttBlock) >> a.log_page)) : 0;
+      if (page < 0 || page >= a.n_pages) page = 0;  // (the join gives such a sequence zeros)
+      pages_at = at;
+    };
+    auto copy = [&](int b) {
+      if (b - pages_at >= 32) pages(b);
+      const int pg = __shfl_sync(0xFFFFFFFFu, page, b - pages_at);
+      if (lane == 0) {
+        const int st = used % C::kStages, in = (a.keys + b * kAttBlock) & ((1 << a.log_page) - 1);
+        const long at = ((((long)pg * a.kvh + head) << a.log_page) + in) * D;
+        uint8_t* to = ring + st * 2 * C::kRows;
+        mbar_expect_tx(full + st, 2 * C::kRows);
+        bulk_g2s(to, a.kp + at, C::kRows, full + st);
+        bulk_g2s(to + C::kRows, a.vp + at, C::kRows, full + st);
       }
-      *reinterpret_cast<uint4*>(sq + r * C::kQRow + c * 16) = u;
-    }
-    __syncwarp();
+      ++used;
+    };
+    pages(from);
+    uint32_t next = used;  // the copy that is looked at next
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i)
+      if (from + i < upto) copy(from + i);
 
+    uint4 q[D / 32];  // row g, numbers 32 i + 8 t ..
+    {
+      const bool on = row0 + g < a.group;
+      const uint16_t* p = a.q + (long)seq * a.q_row + (long)(head * a.group + (on ? row0 + g : 0)) * a.q_head + 8 * t;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) q[i] = on ? __ldcg(reinterpret_cast<const uint4*>(p + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+    }
     float o[D / 16][4];  // [16 numbers][number 0: rows 2t, 2t + 1; number 1]
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    int page = __ldcg(table + ((a.keys + from * kAttBlock) >> a.log_page));
-    for (int b = from; b < upto; ++b) {
-      const int key = a.keys + b * kAttBlock, in = key & ((1 << a.log_page) - 1);
-      if (page < 0 || page >= a.n_pages) page = 0;  // (the join gives such a sequence zeros)
-      const long base = ((((long)page * a.kvh + head) << a.log_page) + in) * D;
-      if (b + 1 < upto) page = __ldcg(table + ((key + kAttBlock) >> a.log_page));
-      const uint16_t* kp = a.kp + base + g * D + t * 8;
-      const uint16_t* vp = a.vp + base + 2 * t * D + g * 8;
-      uint4 k[KB][2], v[VB][4];
-#pragma unroll
-      for (int i = 0; i < KB; ++i) {
-        k[i][0] = att_stream(kp + 32 * i);
-        k[i][1] = att_stream(kp + 8 * D + 32 * i);
+    for (int b = from; b < upto; ++b, ++next) {
+      const int st = next % C::kStages;
+      bool there = false;
+      for (uint32_t i = 0; i < kSpinLimit && !there; ++i) there = mbar_try(full + st, (next / C::kStages) & 1);
+      alive = __all_sync(0xFFFFFFFFu, there);
+      if (!alive) {
+        set_err(a.err, G4_DEV_TIMEOUT);
+        break;
       }
-#pragma unroll
-      for (int i = 0; i < VB; ++i) {
-        v[i][0] = att_stream(vp + 64 * i);
-        v[i][1] = att_stream(vp + D + 64 * i);
-        v[i][2] = att_stream(vp + 8 * D + 64 * i);
-        v[i][3] = att_stream(vp + 9 * D + 64 * i);
-      }
+      const uint8_t* kr = ring + st * 2 * C::kRows + g * (D * 2) + t * 16;
+      const uint8_t* vr = ring + st * 2 * C::kRows + C::kRows + 2 * t * (D * 2) + g * 16;
       float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i0 = 0; i0 < D / 32; i0 += KB) {
-#pragma unroll
-        for (int i = 0; i < KB; ++i) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sq + g * C::kQRow + (i0 + i) * 64 + t * 16);
-          att_mma<BF>(c, k[i][0].x, k[i][1].x, k[i][0].y, k[i][1].y, u.x, u.y);
-          att_mma<BF>(d, k[i][0].z, k[i][1].z, k[i][0].w, k[i][1].w, u.z, u.w);
-        }
-        if (i0 + KB < D / 32) {
-#pragma unroll
-          for (int i = 0; i < KB; ++i) {
-            k[i][0] = att_stream(kp + 32 * (i0 + KB + i));
-            k[i][1] = att_stream(kp + 8 * D + 32 * (i0 + KB + i));
-          }
-        }
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kr + 64 * i), k1 = *reinterpret_cast<const uint4*>(kr + 16 * D + 64 * i);
+        att_mma<BF>(c, k0.x, k1.x, k0.y, k1.y, q[i].x, q[i].y);
+        att_mma<BF>(d, k0.z, k1.z, k0.w, k1.w, q[i].z, q[i].w);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] = (c[i] + d[i]) * a.scale;
@@ -228,52 +255,42 @@ __global__ void __launch_bounds__(32 * kAttWarps, AttTail<D>::kCtas) att_tail_ke
         r1 = att_transpose(att_pack<BF>(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
       }
 #pragma unroll
-      for (int i0 = 0; i0 < D / 64; i0 += VB) {
+      for (int i = 0; i < D / 64; ++i) {
+        uint4 v[4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint4*>(vr + ((e & 1) + (e >> 1) * 8) * (D * 2) + 128 * i);
         if (live < kAttBlock) {  // what lies behind the last row may be anything
 #pragma unroll
-          for (int i = 0; i < VB; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (2 * t + (e & 1) + (e >> 1) * 8 >= live) v[i][e] = make_uint4(0u, 0u, 0u, 0u);
+          for (int e = 0; e < 4; ++e)
+            if (2 * t + (e & 1) + (e >> 1) * 8 >= live) v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
+        const uint32_t* y0 = reinterpret_cast<const uint32_t*>(&v[0]);
+        const uint32_t* y1 = reinterpret_cast<const uint32_t*>(&v[1]);
+        const uint32_t* y2 = reinterpret_cast<const uint32_t*>(&v[2]);
+        const uint32_t* y3 = reinterpret_cast<const uint32_t*>(&v[3]);
 #pragma unroll
-        for (int i = 0; i < VB; ++i) {
-          const uint32_t* y0 = reinterpret_cast<const uint32_t*>(&v[i][0]);
-          const uint32_t* y1 = reinterpret_cast<const uint32_t*>(&v[i][1]);
-          const uint32_t* y2 = reinterpret_cast<const uint32_t*>(&v[i][2]);
-          const uint32_t* y3 = reinterpret_cast<const uint32_t*>(&v[i][3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a0 = __byte_perm(y0[e], y1[e], 0x5410), a1 = __byte_perm(y0[e], y1[e], 0x7632);
-            const uint32_t a2 = __byte_perm(y2[e], y3[e], 0x5410), a3 = __byte_perm(y2[e], y3[e], 0x7632);
-            att_mma<BF>(o[(i0 + i) * 4 + e], a0, a1, a2, a3, w0, w1);
-            if (BF) att_mma<BF>(o[(i0 + i) * 4 + e], a0, a1, a2, a3, r0, r1);
-          }
-        }
-        if (i0 + VB < D / 64) {
-#pragma unroll
-          for (int i = 0; i < VB; ++i) {
-            const uint16_t* p = vp + 64 * (i0 + VB + i);
-            v[i][0] = att_stream(p);
-            v[i][1] = att_stream(p + D);
-            v[i][2] = att_stream(p + 8 * D);
-            v[i][3] = att_stream(p + 9 * D);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a0 = __byte_perm(y0[e], y1[e], 0x5410), a1 = __byte_perm(y0[e], y1[e], 0x7632);
+          const uint32_t a2 = __byte_perm(y2[e], y3[e], 0x5410), a3 = __byte_perm(y2[e], y3[e], 0x7632);
+          att_mma<BF>(o[i * 4 + e], a0, a1, a2, a3, w0, w1);
+          if (BF) att_mma<BF>(o[i * 4 + e], a0, a1, a2, a3, r0, r1);
         }
       }
+      __syncwarp();
+      if (b + C::kStages < upto) copy(b + C::kStages);
     }
+    unsigned mine = 0;
+    if (lane == 0) mine = atomicAdd(a.ticket, 1u);
 #pragma unroll
     for (int e = 4; e < 32; e <<= 1) {
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, e);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, e);
     }
-    const bool whole = from == 0 && upto == blocks;
-    const long part = whole ? 2L * a.workers + (long)seq * per_block + x : att_part(me, t0, span);
     if (lane < 4) {
-      a.part_ml[part * 8 + 2 * t] = make_float2(m0, l0);
-      a.part_ml[part * 8 + 2 * t + 1] = make_float2(m1, l1);
+      a.part_ml[(long)part * 8 + 2 * t] = make_float2(m0, l0);
+      a.part_ml[(long)part * 8 + 2 * t + 1] = make_float2(m1, l1);
     }
-    float* po = a.part_o + part * 8 * D + g * 8;
+    float* po = a.part_o + (long)part * 8 * D + g * 8;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       float4* even = reinterpret_cast<float4*>(po + (2 * t) * D + 64 * i);
@@ -283,119 +300,118 @@ __global__ void __launch_bounds__(32 * kAttWarps, AttTail<D>::kCtas) att_tail_ke
       odd[0] = make_float4(o[4 * i][1], o[4 * i][3], o[4 * i + 1][1], o[4 * i + 1][3]);
       odd[1] = make_float4(o[4 * i + 2][1], o[4 * i + 2][3], o[4 * i + 3][1], o[4 * i + 3][3]);
     }
-    at = t0 + upto;
+    part = gridDim.x * C::kWarps + (int)__shfl_sync(0xFFFFFFFFu, mine, 0);
   }
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i <= a.n_seq; i += 32 * kAttWarps) a.plan[i] = first[i];
-    if (threadIdx.x == 0) a.plan[a.n_seq + 1] = span;
+  if (!alive)  // what was asked for arrives before the CTA ends
+    for (uint32_t k = used < C::kStages ? 0 : used - C::kStages; k < used; ++k) mbar_wait_drain(full + k % C::kStages, (k / C::kStages) & 1);
+  // the sequences' checks and places, for the join
+  for (int i = warp * gridDim.x + blockIdx.x; i < a.n_seq; i += gridDim.x * C::kWarps) {
+    int rows;
+    const int bad = att_check(a, i, &rows);
+    if (lane == 0) {
+      if (bad) set_err(a.err, bad);
+      a.plan[i] = make_int4(first[i], (first[i + 1] - first[i]) / per_seq, bad, rows);
+    }
   }
   if (a.splits) pdl_wait();  // so that who waits for this launch has waited for the prefix's too
+  __syncthreads();
+  if (threadIdx.x == 0) {  // the last CTA puts the counters back
+    __threadfence();
+    if (atomicAdd(a.ticket + 1, 1u) == gridDim.x - 1) {
+      a.ticket[0] = 0;
+      a.ticket[1] = 0;
+    }
+  }
 }
 
-// The output of a query row from its parts: a warp per row, the prefix's parts before the rest's.  A
-// sequence whose slot, length or pages are not valid ones, or whose first pages are not the shared ones,
-// gets zeros, with the error word set (an empty one without).
+constexpr int kAttJoinWarps = 4;
+
+// The output of a query row from its parts: a CTA per row, its warps taking every fourth part (the prefix's
+// before the rest's), whose sums are added in a fixed order.  A sequence that has been found wrong (att_check)
+// gets zeros, and so does an empty one.
 template <int D, bool BF>
-__global__ void __launch_bounds__(256) att_join_kernel(const AttTailArgs a) {
-  const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(32 * kAttJoinWarps) att_join_kernel(const AttTailArgs a) {
+  constexpr int E = D / 32, R = E < 4 ? E : 4;  // numbers of a lane, in runs of 4 (2 at D = 64)
+  __shared__ float sums[kAttJoinWarps][D];
+  __shared__ float2 tops[kAttJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.kvh * a.group, seq = blockIdx.x / heads, hq = blockIdx.x % heads, head = hq / a.group, gr = hq % a.group;
+  const int block = seq / a.tb, rows = a.blocks * kAttM;
+  const long pre = ((long)(block / a.blocks) * a.kvh + head) * a.splits * rows + block % a.blocks * kAttM + seq % a.tb * a.group + gr;
   pdl_wait();
   pdl_trigger();
-  const int heads = a.kvh * a.group;
-  if (r >= a.n_seq * heads) return;
-  const int seq = r / heads, hq = r % heads, head = hq / a.group, gr = hq % a.group;
-  const int slot = __ldcg(a.slots + seq);
-  int bad = slot < 0 || slot >= a.n_slots ? G4_DEV_BAD_SLOT : 0, len = 0;
-  if (!bad) {
-    len = __ldcg(a.lens + slot);
-    if (len < 0 || len > a.max_pages << a.log_page || (len > 0 && len < a.keys)) bad = G4_DEV_BAD_POSITION;
-  }
-  if (!bad && len > 0) {
-    const int* table = a.table + (long)slot * a.max_pages;
-    const int shared = a.keys >> a.log_page, pages = (len + (1 << a.log_page) - 1) >> a.log_page;
-    const int* same = a.table + (long)att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys) * a.max_pages;  // (this slot at the latest)
-    int wrong = 0;
-#pragma unroll 4
-    for (int p = lane; p < pages; p += 32) {
-      const int id = __ldcg(table + p);
-      wrong |= id < 0 || id >= a.n_pages || (p < shared && id != __ldcg(same + p));
-    }
-    if (__any_sync(0xFFFFFFFFu, wrong)) bad = G4_DEV_BAD_POSITION;
-  }
-  if (bad && lane == 0 && gr == 0 && head == 0) set_err(a.err, bad);
-  uint16_t* out = a.out + (long)seq * a.o_row + (long)hq * a.o_head;
-  constexpr int E = D / 32;  // numbers of a lane, in runs of 4 (2 at D = 64)
-  constexpr int R = E < 4 ? E : 4;
-  float acc[E];
+  const int4 plan = __ldcg(a.plan + seq);
+  float acc[E], M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float inv = 0.f;
-  if (!bad && len > 0) {
-    const int block = seq / a.tb, rows = a.blocks * kAttM;
-    const long pre = ((long)(block / a.blocks) * a.kvh + head) * a.splits * rows + block % a.blocks * kAttM + seq % a.tb * a.group + gr;
-    const int x = head * a.row_tiles + gr / 8, b0 = __ldcg(a.plan + seq), span = __ldcg(a.plan + a.n_seq + 1);
-    const int blocks = (len - a.keys + kAttBlock - 1) / kAttBlock, t0 = b0 + x * blocks;
-    const int c0 = t0 / span, c1 = blocks ? (t0 + blocks - 1) / span : c0 - 1;
-    const int own = c1 - c0 + 1, parts = a.splits + own;
-    auto row_of = [&](int p, const float2** ml, const float** o) {
-      if (p < a.splits) {
-        const long at = pre + (long)p * rows;
-        *ml = a.pre_ml + at;
-        *o = a.pre_o + at * D;
-      } else {
-        const int c = c0 + p - a.splits;
-        const long at = (own == 1 ? 2L * a.workers + (long)seq * a.kvh * a.row_tiles + x : (long)att_part(c, t0, span)) * 8 + gr % 8;
-        *ml = a.part_ml + at;
-        *o = a.part_o + at * D;
-      }
-    };
-    const float2* ml;
-    const float* o;
-    float M = -INFINITY;
-    for (int p = lane; p < parts; p += 32) {
-      row_of(p, &ml, &o);
-      M = fmaxf(M, __ldcg(&ml->x));
-    }
-    M = warp_max(M);
-    if (M == -INFINITY) M = 0.f;
-    float L = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      row_of(p, &ml, &o);
-      const float2 w = __ldcg(ml);
-      const float f = att_exp2(w.x - M);
-      L = fmaf(w.y, f, L);
+  if (!plan.z && plan.w > 0) {
+    const int parts = a.splits + plan.y;
+    const long own = (long)plan.x + (long)(head * a.row_tiles + gr / 8) * plan.y;
+    // 32 of the warp's parts at a time: a lane looks at the maximum and sum of one
+    for (int p0 = warp; p0 < parts; p0 += 32 * kAttJoinWarps) {
+      const int p = p0 + lane * kAttJoinWarps;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (p < parts) ml = __ldcg(p < a.splits ? a.pre_ml + pre + (long)p * rows : a.part_ml + (own + p - a.splits) * 8 + gr % 8);
+      const float top = fmaxf(M, warp_max(ml.x)), Z = top == -INFINITY ? 0.f : top;
+      const float back = att_exp2(M - Z), mine = att_exp2(ml.x - Z);
+      L = L * back + warp_sum(ml.y * mine);
 #pragma unroll
-      for (int e = 0; e < E; e += R) {
-        if (R == 4) {
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(o + e * 32) + lane);
-          acc[e] = fmaf(u.x, f, acc[e]);
-          acc[e + 1] = fmaf(u.y, f, acc[e + 1]);
-          acc[e + 2 < E ? e + 2 : 0] = fmaf(u.z, f, acc[e + 2 < E ? e + 2 : 0]);
-          acc[e + 3 < E ? e + 3 : 0] = fmaf(u.w, f, acc[e + 3 < E ? e + 3 : 0]);
-        } else {
-          const float2 u = __ldcg(reinterpret_cast<const float2*>(o) + lane);
-          acc[e] = fmaf(u.x, f, acc[e]);
-          acc[e + 1] = fmaf(u.y, f, acc[e + 1]);
+      for (int e = 0; e < E; ++e) acc[e] *= back;
+      M = top;
+      const int count = min(32, (parts - p0 + kAttJoinWarps - 1) / kAttJoinWarps);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
+        const float f = __shfl_sync(0xFFFFFFFFu, mine, i);
+        const int r = p0 + i * kAttJoinWarps;
+        const float* o = r < a.splits ? a.pre_o + (pre + (long)r * rows) * D : a.part_o + ((own + r - a.splits) * 8 + gr % 8) * D;
+#pragma unroll
+        for (int e = 0; e < E; e += R) {
+          if constexpr (R == 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(o + e * 32) + lane);
+            acc[e] = fmaf(u.x, f, acc[e]);
+            acc[e + 1] = fmaf(u.y, f, acc[e + 1]);
+            acc[e + 2] = fmaf(u.z, f, acc[e + 2]);
+            acc[e + 3] = fmaf(u.w, f, acc[e + 3]);
+          } else {
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(o) + lane);
+            acc[e] = fmaf(u.x, f, acc[e]);
+            acc[e + 1] = fmaf(u.y, f, acc[e + 1]);
+          }
         }
       }
     }
-    inv = L != 0.f ? 1.f / L : 0.f;
   }
 #pragma unroll
-  for (int e = 0; e < E; e += R) {
-    uint32_t w[2];
+  for (int e = 0; e < E; e += R)
 #pragma unroll
-    for (int k = 0; k < R / 2; ++k) w[k] = att_pack<BF>(acc[e + 2 * k] * inv, acc[e + 2 * k + 1] * inv);
-    uint16_t* to = out + e * 32 + lane * R;
+    for (int k = 0; k < R; ++k) sums[warp][e * 32 + lane * R + k] = acc[e + k];
+  if (lane == 0) tops[warp] = make_float2(M, L);
+  __syncthreads();
+  float top = tops[0].x;
+#pragma unroll
+  for (int w = 1; w < kAttJoinWarps; ++w) top = fmaxf(top, tops[w].x);
+  if (top == -INFINITY) top = 0.f;
+  float f[kAttJoinWarps], total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kAttJoinWarps; ++w) {
+    f[w] = att_exp2(tops[w].x - top);
+    total = fmaf(tops[w].y, f[w], total);
+  }
+  const float inv = total != 0.f ? 1.f / total : 0.f;
+  uint16_t* out = a.out + (long)seq * a.o_row + (long)hq * a.o_head;
+  for (int c = 2 * threadIdx.x; c < D; c += 64 * kAttJoinWarps) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttJoinWarps; ++w) {
+      x = fmaf(sums[w][c], f[w], x);
+      y = fmaf(sums[w][c + 1], f[w], y);
+    }
+    const uint32_t u = att_pack<BF>(x * inv, y * inv);
     if (a.o_vec) {
-      if (R == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(to) = w[0];
+      *reinterpret_cast<uint32_t*>(out + c) = u;
     } else {
-#pragma unroll
-      for (int k = 0; k < R / 2; ++k) {
-        to[2 * k] = (uint16_t)w[k];
-        to[2 * k + 1] = (uint16_t)(w[k] >> 16);
-      }
+      out[c] = (uint16_t)u;
+      out[c + 1] = (uint16_t)(u >> 16);
     }
   }
 }
