@@ -245,18 +245,24 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
   };
   int* const twice = p.top + 1;   // whether a page was held twice (or badly)
   int* const counts = p.top + 2;  // [warps] pages that each warp puts back
-  bool odd = false;
-  for (int e = e0 + lane; e < e1; e += 32) {
-    const int page = __ldcg(entry(e));
-    if (page < 0 || page >= p.n_pages) {
-      odd = true;
-      set_err(p.err, G4_DEV_BAD_POSITION);
-      continue;
+  constexpr int kEach = 4;  // entries of a lane at a time: their loads, then their atomics, are in flight together
+  bool odd = false, bad = false;
+  for (int first = e0 + lane; first < e1; first += 32 * kEach) {
+    int page[kEach], r[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) page[k] = first + 32 * k < e1 ? __ldcg(entry(first + 32 * k)) : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const bool on = page[k] >= 0 && page[k] < p.n_pages;
+      r[k] = on ? atomicSub(p.refs + page[k], 1) : first + 32 * k < e1 ? 0 : 1;
     }
-    const int r = atomicSub(p.refs + page, 1);
-    if (r != 1) odd = true;
-    if (r < 1) set_err(p.err, G4_DEV_BAD_POSITION);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      odd |= r[k] != 1;
+      bad |= r[k] < 1;
+    }
   }
+  if (bad) set_err(p.err, G4_DEV_BAD_POSITION);
   if (odd) atomicOr(twice, 1);
   pages_cluster_sync();
   const bool some = __ldcg(twice) != 0;
@@ -282,19 +288,26 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     before = __reduce_add_sync(0xFFFFFFFFu, x);
     all = __reduce_add_sync(0xFFFFFFFFu, y);
   }
-  for (int e = e0; e < e1; e += 32) {
-    const bool on = e + lane < e1;
-    int* at = on ? entry(e + lane) : nullptr;
-    const int page = on ? __ldcg(at) : -1;
-    const bool back = on && (!some || let_go(e + lane, page));
-    const unsigned mask = __ballot_sync(0xFFFFFFFFu, back);
-    const int rank = some ? before + __popc(mask & ((1u << lane) - 1)) : e + lane;
-    if (back) {
-      const int to = top + all - 1 - rank;
-      if (to < p.n_pages) p.free[to] = page;
+  for (int first = e0; first < e1; first += 32 * kEach) {
+    int* at[kEach];
+    int page[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int e = first + 32 * k + lane;
+      at[k] = e < e1 ? entry(e) : nullptr;
+      page[k] = at[k] ? __ldcg(at[k]) : -1;
     }
-    if (on) *at = -1;
-    before += __popc(mask);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int e = first + 32 * k + lane;
+      const bool back = at[k] && (!some || let_go(e, page[k]));
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, back);
+      const int rank = some ? before + __popc(mask & ((1u << lane) - 1)) : e;
+      const int to = top + all - 1 - rank;
+      if (back && to < p.n_pages) p.free[to] = page[k];
+      if (at[k]) *at[k] = -1;
+      before += __popc(mask);
+    }
   }
   pages_cluster_sync();
   // (owners are looked up behind every entry's last reading of them)

@@ -438,9 +438,12 @@ class _PagedOp:
     def _made(self, status, h):
         _g4.check(status, f"{self._name}_create")
         self.h = h
+        # the tensor arguments of a call, filled in anew each time
+        self._t = [_g4.g4_kv4_tensor() for _ in range(4)]
+        self._p = [ctypes.byref(t) for t in self._t]
 
-    def _rows16(self, name, t, shape, dtype):
-        """Checks a [rows, heads, head_dim] argument of 16-bit numbers; its description for C."""
+    def _rows16(self, name, t, shape, dtype, at):
+        """Checks a [rows, heads, head_dim] argument of 16-bit numbers and describes it to C as argument `at`."""
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
         if t.dtype != dtype:
@@ -450,7 +453,9 @@ class _PagedOp:
             raise ValueError(f"{name}: the last dimension has to be contiguous")
         if t.get_device() != self.index:
             raise ValueError(f"{name} is on {t.device}, the handle on {self.device}")
-        return ctypes.byref(_g4.g4_kv4_tensor(t.data_ptr(), _16BIT[dtype], 0, s[0], s[1]))
+        into = self._t[at]
+        into.data, into.dtype, into.row_stride, into.head_stride = t.data_ptr(), _16BIT[dtype], s[0], s[1]
+        return self._p[at]
 
     def _pool(self, name, t, table, kv_heads, head_dim, dtype):
         shape = (table.n_pages, kv_heads, table.page_size, head_dim)
@@ -527,14 +532,15 @@ class PageTable(_PagedOp):
         return _kv4_array(name, t, (n,), torch.int32, self.index)
 
     def extend(self, slots, counts, n_rows, stream=None):
-        """Plan counts[i] further rows of slots[i], n_rows in all.  Returns (rows [n_rows]: the pool row of
+        """Plan counts[i] further rows of slots[i], n_rows in all.  Returns three tensors: rows [n_rows], the pool row of
         each new row, sequence after sequence, -1 where there is none; offsets [n + 1]: where each
         sequence's rows begin among them; lens [n]: the slots' new lengths)."""
         n, n_rows = slots.numel(), _kv4_int("n_rows", n_rows)
         args = (self._seq("slots", slots, n), self._seq("counts", counts, n))
         if n_rows < 0:
             raise ValueError(f"n_rows is {n_rows}")
-        rows, offsets, lens = (self._empty((m,), torch.int32, stream) for m in (n_rows, n + 1, n))
+        rows, offsets, lens = (self._empty(n_rows, torch.int32, stream), self._empty(n + 1, torch.int32, stream),
+                               self._empty(n, torch.int32, stream))
         status = _g4.lib.g4_pages_extend(self.h, self._stream(stream), n, *args, n_rows, rows.data_ptr(), offsets.data_ptr(),
                                          lens.data_ptr())
         self._done(status, "g4_pages_extend", stream, (slots, counts))
@@ -561,8 +567,8 @@ class PageTable(_PagedOp):
             raise TypeError(f"k is {k.dtype} with {k.dim()} dimensions: [rows, heads, head_dim] of bfloat16 or float16 is wanted")
         n, heads, d = k.shape
         status = _g4.lib.g4_pages_store(
-            self.h, self._stream(stream), n, self._seq("rows", rows, n), heads, d, self._rows16("k", k, k.shape, k.dtype),
-            self._rows16("v", v, k.shape, k.dtype), self._pool("k_pool", k_pool, self, heads, d, k.dtype),
+            self.h, self._stream(stream), n, self._seq("rows", rows, n), heads, d, self._rows16("k", k, k.shape, k.dtype, 0),
+            self._rows16("v", v, k.shape, k.dtype, 1), self._pool("k_pool", k_pool, self, heads, d, k.dtype),
             self._pool("v_pool", v_pool, self, heads, d, k.dtype))
         self._done(status, "g4_pages_store", stream, (k, v, rows, k_pool, v_pool))
 
@@ -594,14 +600,14 @@ class Attention(_PagedOp):
         they are zeros."""
         n, rows = offsets.numel() - 1, q.shape[0] if q.dim() == 3 else -1
         mine, theirs = (rows, self.num_q_heads, self.head_dim), (rows, self.num_kv_heads, self.head_dim)
-        args = [self._rows16("q", q, mine, self.dtype), self._rows16("k", k, theirs, self.dtype),
-                self._rows16("v", v, theirs, self.dtype)]
+        args = (self._rows16("q", q, mine, self.dtype, 0), self._rows16("k", k, theirs, self.dtype, 1),
+                self._rows16("v", v, theirs, self.dtype, 2))
         where, window = _kv4_array("offsets", offsets, (n + 1,), torch.int32, self.index), _kv4_int("window", window)
         given = out is not None
         if not given:
             out = self._empty(mine, self.dtype, stream)
         status = _g4.lib.g4_attn_prompt(self.h, self._stream(stream), n, where, rows, scale, window, not given, *args,
-                                        self._rows16("out", out, mine, self.dtype))
+                                        self._rows16("out", out, mine, self.dtype, 3))
         self._done(status, "g4_attn_prompt", stream, (q, k, v, offsets, out))
         return out
 
@@ -611,7 +617,7 @@ class Attention(_PagedOp):
         shared_pages pages of all slots are the same ones (0: none need be)."""
         n = slots.numel()
         shape = (n, self.num_q_heads, self.head_dim)
-        arg = self._rows16("q", q, shape, self.dtype)
+        arg = self._rows16("q", q, shape, self.dtype, 0)
         if out is None:
             out = self._empty(shape, self.dtype, stream)
         status = _g4.lib.g4_attn_shared(
@@ -619,6 +625,6 @@ class Attention(_PagedOp):
             _kv4_int("shared_pages", shared_pages), scale,
             self._pool("k_pool", k_pool, pages, self.num_kv_heads, self.head_dim, self.dtype),
             self._pool("v_pool", v_pool, pages, self.num_kv_heads, self.head_dim, self.dtype), arg,
-            self._rows16("out", out, shape, self.dtype))
+            self._rows16("out", out, shape, self.dtype, 1))
         self._done(status, "g4_attn_shared", stream, (q, k_pool, v_pool, slots, out))
         return out
