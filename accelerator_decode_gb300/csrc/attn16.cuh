@@ -112,6 +112,11 @@ __device__ __forceinline__ uint64_t att_fma2(uint64_t a, uint64_t b, uint64_t c)
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
   return y;
 }
+__device__ __forceinline__ uint64_t att_mul2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
 __device__ __forceinline__ uint64_t att_add2(uint64_t a, uint64_t b) {
   uint64_t y;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
@@ -663,24 +668,39 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           all_first = max(0, min(block0 + a.tb, it.len) - a.window);
         }
       }
+      const int warp_last = __reduce_max_sync(0xFFFFFFFFu, last), warp_first = __reduce_min_sync(0xFFFFFFFFu, first);
       float m = -INFINITY, ref = 0.f, l = 0.f;
-      for (int j = j0; j < j1; ++j, ++n) {
-        const int b = NQ == 2 ? y : n & 1;
-        att_wait(&s->sfull[b], (NQ == 2 ? n : n >> 1) & 1, s);
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t cols = lane_base + C::kColS + b * kAttN;
+      // The reference for a largest score mx of tile j; the sum and the output so far follow.
+      auto refer = [&](float mx, int j) {
+        const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
+        if (!__any_sync(0xFFFFFFFFu, raise)) return;
+        const float nm = raise ? mx : m, fac = raise ? att_exp2(m - nm) : 1.f;
+        m = nm;
+        ref = m == -INFINITY ? 0.f : m;
+        l *= fac;
+        if (j == j0) return;
+        if (NQ == 1) {  // when the previous tile's product is in (NQ 2: it came before the scores)
+          att_wait(&s->pvdone[0], (n - 1) & 1, s);
+          __syncwarp();
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 32) {
+          uint32_t u[32];
+          tc_tld32(ocol + c, u);
+          tc_tld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * fac);
+          tc_tst32(ocol + c, u);
+        }
+        tc_tst_wait();
+      };
+      // A tile of which every row of the block sees every key: the scores stay in registers.
+      auto whole_tile = [&](int j, uint32_t cols) {
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc_tld32(cols + 32 * c, v + 32 * c);
         tc_tld_wait();
-        const int key = it.lo + j * kAttN;
-        if (key + kAttN - 1 > all_last || key < all_first) {
-          const int most = last - key, least = first - key;
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k > most || k < least) v[k] = 0xFF800000u;
-        }
         float top[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) top[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
@@ -688,31 +708,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         for (int k = 8; k < 128; k += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[e] = att_max3(top[e], __uint_as_float(v[k + e]), __uint_as_float(v[k + 4 + e]));
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale;
-        const bool raise = mx > m + 8.f || (m == -INFINITY && mx > m);
-        if (__any_sync(0xFFFFFFFFu, raise)) {
-          const float nm = raise ? mx : m, fac = raise ? att_exp2(m - nm) : 1.f;
-          m = nm;
-          ref = m == -INFINITY ? 0.f : m;
-          l *= fac;
-          if (j > j0) {  // the output so far follows, when the previous tile's product is in (NQ 2: it came before the scores)
-            if (NQ == 1) {
-              att_wait(&s->pvdone[0], (n - 1) & 1, s);
-              __syncwarp();
-              tc_fence_after();
-            }
-#pragma unroll 1
-            for (int c = 0; c < DV; c += 32) {
-              uint32_t u[32];
-              tc_tld32(ocol + c, u);
-              tc_tld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * fac);
-              tc_tst32(ocol + c, u);
-            }
-            tc_tst_wait();
-          }
-        }
+        refer(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale, j);
         const uint64_t sc = att_two(a.scale, a.scale), off = att_two(-ref, -ref);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
@@ -727,13 +723,81 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         }
         tc_tst32(cols, v);
         tc_tst32(cols + 32, v + 32);
+        float s0, s1;
+        att_split(att_add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+      };
+      // Any other tile, 32 columns at a time: those of which no row of the warp sees a key are passed over.  (The
+      // weights of columns 32 c .. lie where the scores of columns 16 c .. did, which have been read by then.)
+      auto edge_tile = [&](int j, int key, uint32_t cols) {
+        auto scores = [&](int c, uint32_t (&u)[32]) {
+          const int most = last - key - c, least = first - key - c;
+          tc_tld32(cols + c, u);
+          tc_tld_wait();
+          if (key + c + 31 > all_last) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k > most) u[k] = 0xFF800000u;
+          }
+          if (key + c < all_first) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k < least) u[k] = 0xFF800000u;
+          }
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kAttN; c += 32) {
+          if (key + c > warp_last || key + c + 31 < warp_first) continue;
+          uint32_t u[32];
+          scores(c, u);
+          float top[2] = {mx, mx};
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = att_max3(top[e], __uint_as_float(u[k + e]), __uint_as_float(u[k + 2 + e]));
+          mx = fmaxf(top[0], top[1]);
+        }
+        refer(mx * a.scale, j);
+        const uint64_t sc = att_two(a.scale, a.scale), off = att_two(-ref, -ref);
+        uint64_t sum = 0ull;
+#pragma unroll 1
+        for (int c = 0; c < kAttN; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = 0u;
+          if (key + c <= warp_last && key + c + 31 >= warp_first) {
+            uint32_t u[32];
+            scores(c, u);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint64_t x = att_fma2(att_two(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), sc, off);
+              float p0, p1;
+              att_split(x, p0, p1);
+              p0 = att_exp2(p0);
+              p1 = att_exp2(p1);
+              sum = att_add2(sum, att_two(p0, p1));
+              w[k] = att_pack<BF>(p0, p1);
+            }
+          }
+          tc_tst16(cols + c / 2, w);
+        }
+        float s0, s1;
+        att_split(sum, s0, s1);
+        l += s0 + s1;
+      };
+      for (int j = j0; j < j1; ++j, ++n) {
+        const int b = NQ == 2 ? y : n & 1, key = it.lo + j * kAttN;
+        const uint32_t cols = lane_base + C::kColS + b * kAttN;
+        att_wait(&s->sfull[b], (NQ == 2 ? n : n >> 1) & 1, s);
+        __syncwarp();
+        tc_fence_after();
+        if (key + kAttN - 1 > all_last || key < all_first) edge_tile(j, key, cols);
+        else whole_tile(j, cols);
         tc_tst_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->pfull[b]);
-        float s0, s1;
-        att_split(att_add2(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
       }
       // ---- the row's output.  (A barrier's parity tells a phase from the one before it alone: with NQ 1 the
       // last tile's scores say that the product before the previous one is in, no more.)
@@ -744,14 +808,15 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       if (PREFIX) {
         const long at = (long)it.part * (NQ * kAttM) + y * kAttM + row_in;
         float* part = a.part_o + at * D + it.half * DV;
-#pragma unroll 1
+        uint32_t u[2][32];  // the next 32 numbers come while these are on their way out
+        tc_tld32(ocol, u[0]);
+#pragma unroll
         for (int c = 0; c < DV; c += 32) {
-          uint32_t u[32];
-          tc_tld32(ocol + c, u);
           tc_tld_wait();
+          if (c + 32 < DV) tc_tld32(ocol + c + 32, u[((c >> 5) + 1) & 1]);
           if (on) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) att_store32(part + c + 8 * k, u + 8 * k);
+            for (int k = 0; k < 4; ++k) att_store32(part + c + 8 * k, u[(c >> 5) & 1] + 8 * k);
           }
           __syncwarp();
         }
@@ -759,16 +824,22 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       } else {
         const float inv = l != 0.f ? 1.f / l : 0.f;
         uint16_t* out = a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + hq) * a.o_head;
-        bool odd = false;
-#pragma unroll 1
+        const uint64_t inv2 = att_two(inv, inv);
+        uint64_t odd = 0ull;  // becomes NaN with a number that is not finite
+        uint32_t u[2][32];    // the next 32 numbers come while these are on their way out
+        tc_tld32(ocol, u[0]);
+#pragma unroll
         for (int c = 0; c < DV; c += 32) {
-          uint32_t u[32], w[16];
-          tc_tld32(ocol + c, u);
+          uint32_t(&f)[32] = u[(c >> 5) & 1];
+          uint32_t w[16];
           tc_tld_wait();
+          if (c + 32 < DV) tc_tld32(ocol + c + 32, u[((c >> 5) + 1) & 1]);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float f0 = __uint_as_float(u[2 * k]) * inv, f1 = __uint_as_float(u[2 * k + 1]) * inv;
-            odd |= !att_finite(f0) || !att_finite(f1);
+            const uint64_t x = att_mul2(att_two(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])), inv2);
+            float f0, f1;
+            att_split(x, f0, f1);
+            odd = att_fma2(x, 0ull, odd);
             w[k] = att_pack<BF>(f0, f1);
           }
           uint16_t* o = out + it.half * DV + c;
@@ -788,7 +859,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (on && odd && att_finite(l))
+        float odd0, odd1;
+        att_split(odd, odd0, odd1);
+        if (on && !(odd0 + odd1 == 0.f) && att_finite(l))
           att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out,
                             it.row0, it.head, it.half * DV, DV, first, last, ref, l);
         __syncwarp();
