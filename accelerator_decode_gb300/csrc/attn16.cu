@@ -83,6 +83,17 @@ int attn_splits(const g4_attn* op, int blocks, int tiles) {
   return std::max(1, std::min(tiles, sms / items));
 }
 
+// Whether the shared rows are attended to once for all, on the tensor cores, or by each sequence with its own rows, out of
+// L2 after the first: a launch less, and short prefixes leave the tensor cores' kernel little but its start.  On their
+// own up to 20 MB of rows in all, or 40 MB with up to 1,024 rows each.  Measured, microseconds once / on their own (300 own
+// rows each): 8 x 2,048 rows, one head of 256 (17 MB) 14.8 / 15.1 and 3 fewer for the host; 8 x 512 13.3 / 12.1; 8 x 4,096
+// (34 MB) 15.7 / 18.5; 8 x 1,024, eight heads of 128 (34 MB) 16.4 / 14.5; 64 x 256, one of 512 (34 MB) 27.4 / 18.9; 64 x
+// 128 (34 MB) 20.2 / 12.6; 32 x 512 (67 MB) 20.1 / 23.3; 16 x 2,048 (134 MB) 19.1 / 29.5.
+bool attn_once(const g4_attn* op, int n_seq, int rows) {
+  const double bytes = 4.0 * n_seq * rows * op->cfg.num_kv_heads * op->cfg.head_dim;
+  return bytes > (rows <= 1024 ? 40e6 : 20e6);
+}
+
 g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
   const g4_attn_config& f = op->cfg;
   const size_t group = attn_group(op), d = f.head_dim, rows = d <= 128 ? 2 * kAttM : kAttM;
@@ -102,13 +113,13 @@ g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
 CUtensorMapDataType attn_type(const g4_attn* op) {
   return op->cfg.dtype == G4_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
-// Rows of a packed tensor, 64 numbers of `box` rows of one head at a time.
-bool attn_map_packed(const g4_attn* op, CUtensorMap* m, const Paged16& t, long rows, int box) {
-  const cuuint64_t dim[3] = {(cuuint64_t)op->cfg.head_dim, (cuuint64_t)op->cfg.num_kv_heads, (cuuint64_t)rows};
+// Rows of a packed tensor: `box` rows of one head and `slabs` times 64 numbers of them, 64 after 64.
+bool attn_map_packed(const g4_attn* op, CUtensorMap* m, const Paged16& t, long rows, int box, int slabs) {
+  const cuuint64_t dim[4] = {64, (cuuint64_t)op->cfg.num_kv_heads, (cuuint64_t)rows, (cuuint64_t)op->cfg.head_dim / 64};
   const long whole = (long)op->cfg.head_dim;  // (the stride of an axis of one is never taken)
-  const cuuint64_t stride[2] = {(cuuint64_t)(dim[1] > 1 ? t.head : whole) * 2, (cuuint64_t)(rows > 1 ? t.row : whole) * 2};
-  const cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box}, step[3] = {1, 1, 1};
-  return g_encode(m, attn_type(op), 3, t.p, dim, stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint64_t stride[3] = {(cuuint64_t)(dim[1] > 1 ? t.head : whole) * 2, (cuuint64_t)(rows > 1 ? t.row : whole) * 2, 128};
+  const cuuint32_t boxes[4] = {64, 1, (cuuint32_t)box, (cuuint32_t)slabs}, step[4] = {1, 1, 1, 1};
+  return g_encode(m, attn_type(op), 4, t.p, dim, stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // Tokens of the queries: 64 numbers of all heads of a KV head, and as many tokens as a block has.
@@ -236,7 +247,8 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
     CUtensorMap qm;
     CUtensorMap km;
     CUtensorMap vm;
-    ok = attn_map_queries(op, &qm, pq, n_rows) && attn_map_packed(op, &km, pk, n_rows, kAttN) && attn_map_packed(op, &vm, pv, n_rows, Att16<D>::kVRows);
+    ok = attn_map_queries(op, &qm, pq, n_rows) && attn_map_packed(op, &km, pk, n_rows, kAttN, Att16<D>::kStage / Att16<D>::kSlab) &&
+         attn_map_packed(op, &vm, pv, n_rows, Att16<D>::kVRows, Att16<D>::DV / 64);
     if (ok)
       launch(att16_kernel<D, BF, false>, dim3(ctas), dim3(Att16<D>::kThreads), Att16<D>::kSmem, reinterpret_cast<cudaStream_t>(stream), a, qm, km, vm);
   });
@@ -263,7 +275,8 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
     return G4_ERR_INVALID_ARG;
   if (!attn_tma(pq, n_seq, f.num_q_heads)) return G4_ERR_UNSUPPORTED;
   t.row_tiles = cdiv(group, 8);
-  t.keys = shared_pages * pf.page_size;
+  t.shared = shared_pages * pf.page_size;
+  t.keys = attn_once(op, n_seq, t.shared) ? t.shared : 0;
   const long pool_rows = (long)pf.n_pages * f.num_kv_heads * pf.page_size;
   if (pool_rows >= (1L << 31) ||
       (double)n_seq * f.num_kv_heads * t.row_tiles * ((double)((long)pf.max_pages * pf.page_size - t.keys) / kAttBlock + 1) >= 2147483647.0)

@@ -11,7 +11,8 @@
 //   stages, by TMA,
 //   a warp issues S = Q K^T (both operands shared, fp32 in tensor memory) and O += P V (P in
 //   tensor memory, in the columns of the S that it was made of),
-//   four warps for each block of rows take a row per thread: maximum, exponentials, sum.
+//   four warps for each block of rows take a row per thread: maximum, exponentials, sum; with NQ 1 four
+//   more give out an item's results while the next item's weights are made.
 // With heads up to 128 two blocks of rows share each tile (NQ 2): while one's weights are made, the
 // other's products run.  Wider heads leave room for one block's output (256 columns of the 512); its
 // scores then have two buffers, and the next tile's product runs while a tile's weights are made.
@@ -46,9 +47,9 @@ struct Att16 {
   static constexpr int kStages = D == 64 ? 8 : D == 512 ? 3 : 5;
   static constexpr int kQ = NQ * kAttM * D * 2;
   static constexpr int kSoftWarps = 4 * NQ;
-  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr int kThreads = 384;                    // softmax, four other warps, NQ 1: four that give out results
   static constexpr int kColS = NQ * DV;                   // tensor memory: outputs, then two buffers of scores
-  static constexpr size_t kSmem = 1024 + kQ + (size_t)kStages * kStage + 512;
+  static constexpr size_t kSmem = 1024 + kQ + (size_t)kStages * kStage + 512 + (NQ == 1 ? kAttM * 4 : 0);
 };
 
 struct Att16Item {
@@ -60,7 +61,7 @@ struct Att16Item {
 };
 
 struct Att16Bars {
-  uint64_t full[8], empty[8], sfull[2], pfull[2], pvdone[2], qfull, qdone, ifull[2], iempty[2], vneed, vtail, drained;
+  uint64_t full[8], empty[8], sfull[2], pfull[2], pvdone[2], qfull, qdone, ifull[2], iempty[2], vneed, vtail, lfull, odone, ofree, drained;
   Att16Item item[2];
   uint32_t tmem;
   int abort;
@@ -182,6 +183,14 @@ __device__ __forceinline__ void att_tma3(void* dst, const CUtensorMap* m, int x,
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
       : "memory");
 }
+// The same of rank 4, and the barrier's count of its bytes, by the thread with `one`.
+__device__ __forceinline__ void att_tma4(uint32_t one, void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %8, 0;\n @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%6], %7;\n"
+      " @q cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(su32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar)), "r"(bytes), "r"(one)
+      : "memory");
+}
 __device__ __forceinline__ void att_tma2(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(su32(dst)),
@@ -254,9 +263,16 @@ __device__ __forceinline__ int att_shared_slot(const int* slots, const int* lens
 // Rare and slow; row, q and out are the row's own.
 template <int D, bool BF>
 __device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, uint16_t* out, int row0, int head, int col0,
-                                        int cols, int first, int last, float m, float l) {
+                                        int cols, int first, int last) {
   const uint16_t* k = a.k + (long)row0 * a.k_row + (long)head * a.k_head;
   const uint16_t* v = a.v + (long)row0 * a.v_row + (long)head * a.v_head;
+  auto score = [&](int j) {
+    float dot = 0.f;
+    for (int e = 0; e < D; ++e) dot = fmaf(att_float<BF>(q[e]), att_float<BF>(k[(long)j * a.k_row + e]), dot);
+    return dot * a.scale;
+  };
+  float m = -INFINITY;
+  bool known = false;
   for (int c = col0; c < col0 + cols; c += 16) {
     uint32_t bad = 0;
     for (int e = 0; e < 16; ++e) bad |= (uint32_t)!att_finite(att_float<BF>(out[c + e])) << e;
@@ -265,12 +281,14 @@ __device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, u
       for (int e = 0; e < 16; ++e)
         if (!att_finite(att_float<BF>(v[(long)j * a.v_row + c + e]))) bad &= ~(1u << e);
     if (!bad) continue;
-    float sum[16];
+    if (!known)
+      for (int j = first; j <= last; ++j) m = fmaxf(m, score(j));
+    known = true;
+    float sum[16], l = 0.f;
     for (int e = 0; e < 16; ++e) sum[e] = 0.f;
     for (int j = first; j <= last; ++j) {
-      float dot = 0.f;
-      for (int e = 0; e < D; ++e) dot = fmaf(att_float<BF>(q[e]), att_float<BF>(k[(long)j * a.k_row + e]), dot);
-      const float p = att_exp2(fmaf(dot, a.scale, -m));
+      const float p = att_exp2(score(j) - m);
+      l += p;
       for (int e = 0; e < 16; ++e)
         if ((bad >> e) & 1) sum[e] = fmaf(p, att_float<BF>(v[(long)j * a.v_row + c + e]), sum[e]);
     }
@@ -279,7 +297,7 @@ __device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, u
   }
 }
 
-// With NQ 2 the 12 warps begin with 168 registers a thread: 4 x 72 + 8 x 216 = 12 x 168.
+// The 12 warps begin with 168 registers a thread; softmax warps need 200 or so: 4 x 72 + 8 x 216 = 12 x 168.
 __device__ __forceinline__ void att_fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n"); }
 __device__ __forceinline__ void att_more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n"); }
 
@@ -294,6 +312,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
   uint8_t* qop = base;
   uint8_t* ring = base + C::kQ;
   Att16Bars* s = reinterpret_cast<Att16Bars*>(ring + C::kStages * C::kStage);
+  float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(s) + 512);  // NQ 1: of an item's rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -306,12 +325,15 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       mbar_init(&s->pfull[i], 4);
       mbar_init(&s->pvdone[i], 1);
       mbar_init(&s->ifull[i], 1);
-      mbar_init(&s->iempty[i], 32 * C::kSoftWarps + 32 + 64);
+      mbar_init(&s->iempty[i], C::kThreads - 32);  // all but the warp that makes them
     }
     mbar_init(&s->qfull, 1);
     mbar_init(&s->qdone, 1);
     mbar_init(&s->vneed, 1);
     mbar_init(&s->vtail, 64);
+    mbar_init(&s->lfull, 4);
+    mbar_init(&s->odone, 1);
+    mbar_init(&s->ofree, 4);
     mbar_init(&s->drained, 1);
     s->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -327,9 +349,72 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s->tmem;
 
+  // The calling thread's output row of block y of an item, whose weights add up to l, from tensor memory.
+  auto give_out = [&](const Att16Item& it, int y, float l) {
+    const int row = (warp & 3) * 32 + lane, tok_in = row / a.group, hq = row % a.group, tok = it.t0 + y * a.tb + tok_in;
+    const bool on = tok_in < a.tb && tok < it.len;
+    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + y * DV;
+    const float factor = PREFIX ? 1.f : l != 0.f ? 1.f / l : 0.f;
+    const uint64_t inv = att_two(factor, factor);
+    float* part = PREFIX ? a.part_o + ((long)it.part * (NQ * kAttM) + y * kAttM + row) * D + it.half * DV : nullptr;
+    uint16_t* out = PREFIX || !on ? nullptr : a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + hq) * a.o_head;
+    uint64_t odd = 0ull;  // becomes NaN with a number that is not finite
+    uint32_t u[2][32];    // the next 32 numbers come while these are on their way out
+    tc_tld32(from, u[0]);
+#pragma unroll
+    for (int c = 0; c < DV; c += 32) {
+      uint32_t(&f)[32] = u[(c >> 5) & 1];
+      tc_tld_wait();
+      if (c + 32 < DV) tc_tld32(from + c + 32, u[((c >> 5) + 1) & 1]);
+      if (NQ == 1 && c + 32 >= DV) {  // all is in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->ofree);
+      }
+      if (PREFIX) {
+        if (on) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) att_store32(part + c + 8 * k, f + 8 * k);
+        }
+      } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint64_t x = att_mul2(att_two(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])), inv);
+          float f0, f1;
+          att_split(x, f0, f1);
+          odd = att_fma2(x, 0ull, odd);
+          w[k] = att_pack<BF>(f0, f1);
+        }
+        uint16_t* o = out + it.half * DV + c;
+        if (!on) {
+        } else if (a.o_vec == 2) {
+          att_store32(o, w);
+          att_store32(o + 16, w + 8);
+        } else if (a.o_vec) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(o)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            o[2 * k] = (uint16_t)w[k];
+            o[2 * k + 1] = (uint16_t)(w[k] >> 16);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    float odd0, odd1;
+    att_split(odd, odd0, odd1);
+    if (!PREFIX && on && !(odd0 + odd1 == 0.f) && att_finite(l))
+      att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out, it.row0, it.head,
+                        it.half * DV, DV, a.window > 0 ? max(0, tok - a.window + 1) : 0, tok);
+    __syncwarp();
+  };
   if (warp == C::kSoftWarps + 1) {
     // ------------------------------------------------ items, and their tiles by TMA
-    if (NQ == 2) att_fewer_registers();
+    att_fewer_registers();
+    const uint32_t one = att_elect();
     int st = 0, lap = 0, copied = 0;  // the ring's stage and lap; items whose queries were asked for
     const int total = PREFIX ? C::HV * a.kvh * a.splits * ((a.n_seq + NQ * a.tb - 1) / (NQ * a.tb)) : 0;
     const int from_slot = PREFIX ? max(0, att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys)) : 0;
@@ -403,9 +488,10 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       __syncwarp();
       if (!ok || it.row0 < 0) break;
       const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN;
-      // keys 0, the queries, [keys 1 if scores run a tile ahead], values 0, keys ...
+      int next = 0;
+      // NQ 2: keys 0, the queries, values 0, keys 1 ...; NQ 1, whose scores run a tile ahead: the queries, keys 0, keys 1, values 0, ...
       for (int x = 0; x < 2 * tiles && ok; ++x) {
-        if (x == (C::KS < C::kStages ? 1 : 0)) {  // (a tile of keys that fills the ring waits for its products)
+        if (x == (NQ == 2 ? 1 : 0)) {  // (NQ 1: a tile of keys may have to wait for products of this very item)
           if (n) ok = att_wait(&s->qdone, (n - 1) & 1, s);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
@@ -419,6 +505,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           ++copied;
           __syncwarp();
         }
+        // the next item, so that its number is there when this one's tiles are on their way (asked for earlier, the last
+        // items end unevenly)
+        if (!PREFIX && x == 2 * tiles - 2 && lane == 0) next = gridDim.x + atomicAdd(a.ticket, 1u);
         int j;
         bool values;
         if (NQ == 2) {
@@ -436,15 +525,11 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           if (!ok) break;
           uint8_t* to = ring + st * C::kStage;
           const int rows = values ? C::kVRows : kAttN, from = key + (values ? y * C::kVRows : 0);
-          const int slabs = C::kStage / (rows * 128), col = values ? it.half * DV : y * slabs * 64;
+          [[maybe_unused]] const int slabs = C::kStage / (rows * 128);
+          const int col = values ? it.half * DV : y * slabs * 64;
           const CUtensorMap* map = values ? &vmap : &kmap;
           if (!PREFIX) {
-            if (lane == 0) {
-              mbar_expect_tx(&s->full[st], C::kStage);
-#pragma unroll 4
-              for (int z = 0; z < slabs; ++z)
-                att_tma3(to + z * rows * 128, map, col + 64 * z, it.head, it.row0 + from, &s->full[st]);
-            }
+            att_tma4(one, to, map, 0, it.head, it.row0 + from, col / 64, &s->full[st], C::kStage);
           } else {
             // boxes of up to a page; a page that is missing (the join's business) reads page 0
             const int box = min(rows, 1 << a.log_page), boxes = rows / box;
@@ -463,10 +548,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           if (++st == C::kStages) st = 0, ++lap;
         }
       }
-      if (!PREFIX) {  // the next item, when this one's tiles are on their way: asked for earlier, the last items end unevenly
-        if (lane == 0) index = gridDim.x + atomicAdd(a.ticket, 1u);
-        index = __shfl_sync(0xFFFFFFFFu, index, 0);
-      }
+      if (!PREFIX) index = __shfl_sync(0xFFFFFFFFu, next, 0);
     }
     // every copy that was asked for arrives before the CTA ends
     if (copied) mbar_wait_drain(&s->qfull, (copied - 1) & 1);
@@ -478,7 +560,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     __syncwarp();
   } else if (warp == C::kSoftWarps) {
     // ------------------------------------------------ matrix instructions
-    if (NQ == 2) att_fewer_registers();
+    att_fewer_registers();
     {
       const uint32_t one = att_elect();
       Att16Items items{s};
@@ -587,6 +669,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
               const uint32_t v0 = stage();
               if (y == 0) {
                 if (tail && j == t.n - 1) clear_tail();
+                if (j == 0 && items.n > 1) ok = att_wait(&s->ofree, items.n & 1, s) && ok;  // the item before has been read
                 ok = att_wait(&s->pfull[b], n_p[b] & 1, s) && ok;
                 ++n_p[b];
                 tc_fence_after();
@@ -596,6 +679,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
             }
             att_commit(one, &s->pvdone[0]);
           }
+          att_commit(one, &s->odone);
           tiles_done += t.n;
         }
       }
@@ -603,9 +687,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       mbar_wait_drain(&s->drained, 0);
     }
     __syncwarp();
-  } else if (warp > C::kSoftWarps + 1) {
+  } else if (warp == C::kSoftWarps + 2 || warp == C::kSoftWarps + 3) {
     // ------------------------------------------------ values behind the last key; rows of no sequence
-    if (NQ == 2) att_fewer_registers();
+    att_fewer_registers();
     const int me = threadIdx.x - 32 * (C::kSoftWarps + 2);
     constexpr int CH = D / 8;  // 16-byte pieces of a row
     Att16Items items{s};
@@ -642,10 +726,22 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         }
       }
     }
+  } else if (NQ == 1 && warp >= C::kSoftWarps + 4) {
+    // ------------------------------------------------ outputs, while the next item's scores and weights are made
+    Att16Items items{s};
+    Att16Item it;
+    while (items.next(it)) {
+      att_wait(&s->lfull, (items.n - 1) & 1, s);
+      const float l = sums[(warp & 3) * 32 + lane];
+      att_wait(&s->odone, (items.n - 1) & 1, s);
+      __syncwarp();
+      tc_fence_after();
+      give_out(it, 0, l);
+    }
   } else {
     // ------------------------------------------------ softmax: a query row per thread
-    if (NQ == 2) att_more_registers();
-    const int y = warp >> 2, row_in = threadIdx.x & 127, tok_in = row_in / a.group, hq = row_in % a.group;
+    att_more_registers();
+    const int y = warp >> 2, row_in = threadIdx.x & 127, tok_in = row_in / a.group;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ocol = lane_base + y * DV;
     Att16Items items{s};
@@ -799,73 +895,18 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->pfull[b]);
       }
-      // ---- the row's output.  (A barrier's parity tells a phase from the one before it alone: with NQ 1 the
-      // last tile's scores say that the product before the previous one is in, no more.)
-      if (NQ == 1 && n >= 2) att_wait(&s->pvdone[0], n & 1, s);
-      att_wait(&s->pvdone[NQ == 2 ? y : 0], (NQ == 2 ? done++ : n - 1) & 1, s);
-      __syncwarp();
-      tc_fence_after();
-      if (PREFIX) {
-        const long at = (long)it.part * (NQ * kAttM) + y * kAttM + row_in;
-        float* part = a.part_o + at * D + it.half * DV;
-        uint32_t u[2][32];  // the next 32 numbers come while these are on their way out
-        tc_tld32(ocol, u[0]);
-#pragma unroll
-        for (int c = 0; c < DV; c += 32) {
-          tc_tld_wait();
-          if (c + 32 < DV) tc_tld32(ocol + c + 32, u[((c >> 5) + 1) & 1]);
-          if (on) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) att_store32(part + c + 8 * k, u[(c >> 5) & 1] + 8 * k);
-          }
-          __syncwarp();
-        }
-        if (on && it.half == 0) a.part_ml[at] = make_float2(m, l);
-      } else {
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        uint16_t* out = a.out + (long)(it.row0 + tok) * a.o_row + (long)(it.head * a.group + hq) * a.o_head;
-        const uint64_t inv2 = att_two(inv, inv);
-        uint64_t odd = 0ull;  // becomes NaN with a number that is not finite
-        uint32_t u[2][32];    // the next 32 numbers come while these are on their way out
-        tc_tld32(ocol, u[0]);
-#pragma unroll
-        for (int c = 0; c < DV; c += 32) {
-          uint32_t(&f)[32] = u[(c >> 5) & 1];
-          uint32_t w[16];
-          tc_tld_wait();
-          if (c + 32 < DV) tc_tld32(ocol + c + 32, u[((c >> 5) + 1) & 1]);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint64_t x = att_mul2(att_two(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])), inv2);
-            float f0, f1;
-            att_split(x, f0, f1);
-            odd = att_fma2(x, 0ull, odd);
-            w[k] = att_pack<BF>(f0, f1);
-          }
-          uint16_t* o = out + it.half * DV + c;
-          if (!on) {
-          } else if (a.o_vec == 2) {
-            att_store32(o, w);
-            att_store32(o + 16, w + 8);
-          } else if (a.o_vec) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(o)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              o[2 * k] = (uint16_t)w[k];
-              o[2 * k + 1] = (uint16_t)(w[k] >> 16);
-            }
-          }
-          __syncwarp();
-        }
-        float odd0, odd1;
-        att_split(odd, odd0, odd1);
-        if (on && !(odd0 + odd1 == 0.f) && att_finite(l))
-          att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out,
-                            it.row0, it.head, it.half * DV, DV, first, last, ref, l);
+      if (NQ == 2) {
+        att_wait(&s->pvdone[y], done++ & 1, s);
         __syncwarp();
+        tc_fence_after();
+        give_out(it, y, l);
+      } else {
+        if (items.n > 1) att_wait(&s->ofree, items.n & 1, s);  // the item before has been read, its sums too
+        sums[row_in] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->lfull);
       }
+      if (PREFIX && on && it.half == 0) a.part_ml[(long)it.part * (NQ * kAttM) + y * kAttM + row_in] = make_float2(m, l);
       tc_fence_before();
     }
   }

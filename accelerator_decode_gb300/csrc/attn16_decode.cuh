@@ -40,7 +40,8 @@ struct AttTailArgs {
   float scale;                       // times log2 e
   const int *table, *slots, *lens;
   int n_slots, n_pages, log_page, max_pages;
-  int keys;                          // rows of the prefix
+  int shared;                        // rows of the prefix that the slots share
+  int keys;                          // and of the one that another kernel attends to: all of those, or none
   int most;                          // parts, but for one more of every item
   float* part_o;                     // [most + items][8][D]
   float2* part_ml;
@@ -58,7 +59,7 @@ __device__ __forceinline__ int att_tail_len(const AttTailArgs& a, int i) {
   const int slot = __ldcg(a.slots + i);
   if (slot < 0 || slot >= a.n_slots) return 0;
   const int len = __ldcg(a.lens + slot);
-  return len >= a.keys && len <= a.max_pages << a.log_page ? len - a.keys : 0;
+  return len >= a.shared && len <= a.max_pages << a.log_page ? len - a.keys : 0;
 }
 // What is wrong with sequence i (error bits), and its rows; a warp's threads call it together.
 __device__ __forceinline__ int att_check(const AttTailArgs& a, int i, int* rows) {
@@ -67,10 +68,10 @@ __device__ __forceinline__ int att_check(const AttTailArgs& a, int i, int* rows)
   if (slot < 0 || slot >= a.n_slots) return G4_DEV_BAD_SLOT;
   const int len = __ldcg(a.lens + slot);
   if (len == 0) return 0;
-  if (len < a.keys || len > a.max_pages << a.log_page) return G4_DEV_BAD_POSITION;
-  const int shared = a.keys >> a.log_page, pages = (len + (1 << a.log_page) - 1) >> a.log_page;
+  if (len < a.shared || len > a.max_pages << a.log_page) return G4_DEV_BAD_POSITION;
+  const int shared = a.shared >> a.log_page, pages = (len + (1 << a.log_page) - 1) >> a.log_page;
   const int* table = a.table + (long)slot * a.max_pages;
-  const int* same = a.table + (long)att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.keys) * a.max_pages;  // (this slot at the latest)
+  const int* same = a.table + (long)att_shared_slot(a.slots, a.lens, a.n_seq, a.n_slots, a.shared) * a.max_pages;  // (this slot at the latest)
   int wrong = 0;
 #pragma unroll 4
   for (int p = lane; p < pages; p += 32) {
