@@ -206,13 +206,13 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
   Att16Args a{};
   if (!attn_scale(op, scale, &a.scale)) return G4_ERR_INVALID_ARG;
   if (q->dtype != f.dtype || k->dtype != f.dtype || v->dtype != f.dtype || out->dtype != f.dtype) return G4_ERR_UNSUPPORTED;
+  if (!n_rows) return G4_OK;
   Paged16 pq, pk, pv, po;
   if (!paged_tensor(q, n_rows, f.num_q_heads, d, false, &pq) || !paged_tensor(k, n_rows, f.num_kv_heads, d, false, &pk) ||
       !paged_tensor(v, n_rows, f.num_kv_heads, d, false, &pv) || !paged_tensor(out, n_rows, f.num_q_heads, d, true, &po) ||
       po.p == pq.p || po.p == pk.p || po.p == pv.p)
     return G4_ERR_INVALID_ARG;
   if ((long)n_rows * group >= (1L << 31)) return G4_ERR_UNSUPPORTED;
-  if (!n_rows) return G4_OK;
   if (!attn_tma(pq, n_rows, f.num_q_heads) || !attn_tma(pk, n_rows, f.num_kv_heads) || !attn_tma(pv, n_rows, f.num_kv_heads))
     return G4_ERR_UNSUPPORTED;
   DEVICE_GUARD(op->device);

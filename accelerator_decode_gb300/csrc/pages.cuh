@@ -140,25 +140,26 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
   // rows, four at a time
   const int total = s.at[a.n];
   const bool wide = (reinterpret_cast<uintptr_t>(a.rows) & 15) == 0;
-  for (int t0 = 4 * me; t0 < a.n_rows; t0 += 4 * threads) {
+  for (long t4 = 4L * me; t4 < a.n_rows; t4 += 4L * threads) {
+    const int t0 = (int)t4;
     int r[4] = {-1, -1, -1, -1};
     int q = t0 < total ? pages_find(s.at, a.n, t0) : a.n;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      if (t4 + k >= total) continue;
       const int t = t0 + k;
-      if (t >= total) continue;
       while (t >= s.at[q + 1]) ++q;
       if (s.slot[q] < 0) continue;
       const int row = s.held[q] + t - s.at[q], pg = row >> p.log_page;
       const int page = pg < s.from[q] ? __ldcg(p.table + (long)s.slot[q] * p.max_pages + pg) : __ldcg(p.free + top - 1 - (s.base[q] + pg - s.from[q]));
       r[k] = (page << p.log_page) + (row & (p.page() - 1));
     }
-    if (wide && t0 + 4 <= a.n_rows) {
+    if (wide && t4 + 4 <= a.n_rows) {
       *reinterpret_cast<int4*>(a.rows + t0) = make_int4(r[0], r[1], r[2], r[3]);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (t0 + k < a.n_rows) a.rows[t0 + k] = r[k];
+        if (t4 + k < a.n_rows) a.rows[t4 + k] = r[k];
     }
   }
 
