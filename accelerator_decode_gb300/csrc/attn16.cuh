@@ -22,7 +22,7 @@
 // A row's reference m is raised, and its output so far rescaled, only when a score exceeds it by 2^8:
 // weights up to 256 lose nothing in fp32, nor in P.  P is rounded to the values' 16-bit type (the
 // operands of a product have one type): each weight is off by at most 2^-8 of itself (bf16; fp16:
-// 2^-11, and weights below 2^-14 by up to 2^-25), independently of the others, while the sum that
+// 2^-11, and weights below 2^-20 by up to 2^-31), independently of the others, while the sum that
 // divides them is of the unrounded ones.
 #pragma once
 #include <cuda.h>
@@ -145,6 +145,9 @@ __device__ __forceinline__ float att_float(uint16_t u) {
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(u));
   return f;
 }
+// Weights go into products times 2^this: fp16 ones reach up to 2^8 . 2^6, and lose bits from 2^-20 down instead of 2^-14.
+template <bool BF>
+__device__ __forceinline__ constexpr float att_up() { return BF ? 0.f : 6.f; }
 __device__ __forceinline__ bool att_finite(float x) { return fabsf(x) < INFINITY; }
 
 // kind::f16: operands of the type, fp32 result, M 128.
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         if (!__any_sync(0xFFFFFFFFu, raise)) return;
         const float nm = raise ? mx : m, fac = raise ? att_exp2(m - nm) : 1.f;
         m = nm;
-        ref = m == -INFINITY ? 0.f : m;
+        ref = m == -INFINITY ? 0.f : m - att_up<BF>();
         l *= fac;
         if (j == j0) return;
         if (NQ == 1) {  // when the previous tile's product is in (NQ 2: it came before the scores)
@@ -906,7 +909,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->lfull);
       }
-      if (PREFIX && on && it.half == 0) a.part_ml[(long)it.part * (NQ * kAttM) + y * kAttM + row_in] = make_float2(m, l);
+      if (PREFIX && on && it.half == 0) a.part_ml[(long)it.part * (NQ * kAttM) + y * kAttM + row_in] = make_float2(m == -INFINITY ? m : ref, l);
       tc_fence_before();
     }
   }

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(32 * AttTail<D>::kWarps, 1) att_tail_kernel(co
           o[i][3] *= f1;
         }
       }
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      const float z0 = m0 == -INFINITY ? 0.f : m0 - att_up<BF>(), z1 = m1 == -INFINITY ? 0.f : m1 - att_up<BF>();
       const float p0 = att_exp2(c[0] - z0), p1 = att_exp2(c[1] - z1), p2 = att_exp2(c[2] - z0), p3 = att_exp2(c[3] - z1);
       l0 += p0 + p2;
       l1 += p1 + p3;
@@ -288,8 +288,8 @@ __global__ void __launch_bounds__(32 * AttTail<D>::kWarps, 1) att_tail_kernel(co
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, e);
     }
     if (lane < 4) {
-      a.part_ml[(long)part * 8 + 2 * t] = make_float2(m0, l0);
-      a.part_ml[(long)part * 8 + 2 * t + 1] = make_float2(m1, l1);
+      a.part_ml[(long)part * 8 + 2 * t] = make_float2(m0 - att_up<BF>(), l0);
+      a.part_ml[(long)part * 8 + 2 * t + 1] = make_float2(m1 - att_up<BF>(), l1);
     }
     float* po = a.part_o + (long)part * 8 * D + g * 8;
 #pragma unroll

@@ -6,7 +6,7 @@ independent errors).  With u = eps / 2 of the type, an output row is off by
 * its weights' rounding into the products: each weight is off by at most u of itself, independently
   of the others, which moves the row as its own rounding does: 0.65 u, or for a row of few keys at most
   u sum p |v| / |sum p v|, which for the random values here (angles near a right one) is below 1.5 u;
-  fp16 weights below 2^-14 are off by up to 2^-25 each, and n of them by 2^-25 sqrt(n) of a value;
+  fp16 weights below 2^-14 are off by up to 2^-25 each at the most, and n of them by 2^-25 sqrt(n) of a value;
 * scores: d / 16 steps, each off by at most 2^-23 of numbers below 4 after the scale; twice that;
 * the exponential's 2^-22 and 2^-23 for each of the (keys / 16 + 32) steps of the sums."""
 import math
