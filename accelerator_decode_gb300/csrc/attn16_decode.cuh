@@ -12,6 +12,11 @@
 // as there are warps to take them, which they do one after the other as they come free: CTAs whose SM still
 // works on the prefix join in late.
 // Weights go into the products in two bf16 parts (p - bf16(p) as well), or as one fp16.
+//
+// Measured: 64 sequences of 550 to 1,100 rows (217 MB) behind 16,384 (67 MB), 32 heads on 8 of 128: 70 us, 4.1 TB/s.  By
+// themselves the rows behind take 46 us (4.8 TB/s), the prefix 39 us on half of the SMs, the join 12 us of a cold
+// start: the first two run side by side, and the SMs of the prefix join in when it is done.  Small batches (8 sequences
+// of 167 to 333 rows behind 2,048) 14 us: two dependent launches.
 #pragma once
 #include "attn16.cuh"
 
