@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           const int i = seq + lane;
           from = len = upto = 0;
           if (i < a.n_seq) {
-            from = __ldg(a.offsets + i);
-            const int to = __ldg(a.offsets + i + 1);
+            from = __ldcg(a.offsets + i);
+            const int to = __ldcg(a.offsets + i + 1);
             if (from < 0 || to < from || to > a.n_rows) {
               if (blockIdx.x == 0) set_err(a.err, G4_DEV_BAD_POSITION);
             } else {
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       }
     }
     if (!PREFIX && a.zero_rest) {
-      const int front = min(max(__ldg(a.offsets), 0), a.n_rows), end = min(max(__ldg(a.offsets + a.n_seq), front), a.n_rows);
+      const int front = min(max(__ldcg(a.offsets), 0), a.n_rows), end = min(max(__ldcg(a.offsets + a.n_seq), front), a.n_rows);
       const int rest = front + a.n_rows - end, heads = a.kvh * a.group;
       for (long e = blockIdx.x * 64 + me; e < (long)rest * heads * CH; e += gridDim.x * 64) {
         const int c = (int)(e % CH), x = (int)(e / CH % heads), r = (int)(e / CH / heads);

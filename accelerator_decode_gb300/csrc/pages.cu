@@ -81,7 +81,8 @@ g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_tab
 
 g4_status g4_pages_extend(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_counts,
                           int32_t n_rows, int32_t* d_rows, int32_t* d_offsets, int32_t* d_new_lens) {
-  if (!op || !d_slots || !d_counts || !d_offsets || !d_new_lens || !pages_count(op, n_seq) || n_rows < 0 || (n_rows && !d_rows))
+  if (!op || !d_slots || !d_counts || !d_offsets || !d_new_lens || !pages_count(op, n_seq) || n_rows < 0 || (n_rows && !d_rows) ||
+      d_new_lens == op->p.lens)
     return G4_ERR_INVALID_ARG;
   DEVICE_GUARD(op->device);
   PagesExtend a{op->p, d_slots, d_counts, n_seq, n_rows, d_rows, d_offsets, d_new_lens};

@@ -485,7 +485,8 @@ g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_tab
  * page_size takes no places in d_rows), or rows that would go into a page which another slot holds.
  * G4_DEV_NO_PAGES: the pages of a sequence and of those before it, passed over or not, are more than
  * the pool has left.
- * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows < 0, NULL; d_rows may be NULL with n_rows 0). */
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows < 0, NULL, d_new_lens the table's own lengths; d_rows may
+ * be NULL with n_rows 0). */
 g4_status g4_pages_extend(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                           const int32_t* d_counts, int32_t n_rows, int32_t* d_rows, int32_t* d_offsets,
                           int32_t* d_new_lens);
@@ -505,8 +506,9 @@ g4_status g4_pages_truncate(g4_pages* op, g4_stream stream, int32_t n_seq, const
                             const int32_t* d_lens);
 
 /* Keys and values into the pools: row t of k and v [n_rows][num_kv_heads][head_dim] (G4_DT_BF16 or
- * G4_DT_F16, both the same; seq_stride unused) becomes pool row d_rows[t] of k_pool and v_pool, -1: left out.  head_dim is 64,
- * 128, 256 or 512; the pools are contiguous, 16-byte aligned and of the rows' type.  Rows are distinct.
+ * G4_DT_F16, both the same; seq_stride unused) becomes pool row d_rows[t] of k_pool and v_pool, -1:
+ * left out.  head_dim is 64, 128, 256 or 512; the pools are contiguous, 16-byte aligned and of the
+ * rows' type.  Rows are distinct.
  * G4_DEV_BAD_POSITION: a pool row below -1 or outside the pool; that row is left out.
  * Errors: INVALID_ARG (NULL or malformed tensors, n_rows < 0), UNSUPPORTED (another type or
  * head_dim, n_rows * num_kv_heads at 2^31 or more). */
@@ -568,11 +570,12 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
  * all.  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), q aligned as
  * in g4_attn_prompt, sharing no element.  A slot may be named more than once.  An empty slot gets zeros.
  * G4_DEV_BAD_SLOT: a slot out of range.  G4_DEV_BAD_POSITION: a slot with fewer rows than the shared
- * pages hold, with other first pages than the first slot that has so many rows, or with a missing page.  Those sequences get zeros.
+ * pages hold, with other first pages than the first slot that has so many rows, or with a missing
+ * page.  Those sequences get zeros.
  * Errors: INVALID_ARG (n_seq outside 1..max_seqs, shared_pages outside 0..max_pages, a scale that is negative
  * or not finite, NULL or malformed tensors, pools that are not 16-byte aligned, `pages` on another device),
- * UNSUPPORTED (another type, a q that is not aligned; n_pages * num_kv_heads * page_size, or n_seq * num_kv_heads * ceil(heads per KV
- * head / 8) * ceil(rows of a slot / 16), at 2^31 or more). */
+ * UNSUPPORTED (another type, a q that is not aligned; n_pages * num_kv_heads * page_size, or n_seq *
+ * num_kv_heads * ceil(heads per KV head / 8) * ceil(rows of a slot / 16), at 2^31 or more). */
 g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, int32_t n_seq,
                          const int32_t* d_slots, int32_t shared_pages, float scale, const void* k_pool,
                          const void* v_pool, const g4_kv4_tensor* q, const g4_kv4_tensor* out);
