@@ -102,14 +102,16 @@ g4_status attn_create_impl(g4_attn* op, cudaStream_t st) {
   const size_t items = (size_t)cdiv(f.max_seqs, attn_tokens(op)) * f.num_kv_heads;
   const size_t parts = std::max<size_t>(items, op->sms) * rows;
   const size_t tails = ((size_t)attn_most(op) + (size_t)f.max_seqs * f.num_kv_heads * ((group + 7) / 8)) * 8;
-  TRY(paged_alloc(&op->mem, &op->err, 1, 0, st));
-  TRY(paged_alloc(&op->mem, &op->ticket, 2, 0, st));
-  TRY(paged_alloc(&op->mem, &op->pre_o, parts * d, 0, st));
-  TRY(paged_alloc(&op->mem, &op->pre_ml, parts, 0, st));
-  TRY(paged_alloc(&op->mem, &op->tail_o, tails * d, 0, st));
-  TRY(paged_alloc(&op->mem, &op->tail_ml, tails, 0, st));
-  TRY(paged_alloc(&op->mem, &op->plan, (size_t)f.max_seqs, 0, st));
-  return G4_OK;
+  // (parts and the plan are written before they are read)
+  return paged_alloc(&op->mem, 512, st, [&](auto& take) {
+    take(&op->err, 1);
+    take(&op->ticket, 2);
+    take(&op->plan, (size_t)f.max_seqs);
+    take(&op->pre_o, parts * d);
+    take(&op->pre_ml, parts);
+    take(&op->tail_o, tails * d);
+    take(&op->tail_ml, tails);
+  });
 }
 
 CUtensorMapDataType attn_type(const g4_attn* op) {
@@ -173,14 +175,12 @@ g4_status g4_attn_create(int device, const g4_attn_config* cfg, g4_attn** out) {
   if (!op) return G4_ERR_OOM;
   op->cfg = f;
   op->device = device;
-  if (const char* fa = getenv("G4_FAIL_ALLOC_AT")) op->mem.fail_at = atoi(fa);
   g4_status s = G4_ERR_CUDA;
   cudaStream_t st = nullptr;
   if (cuda_ok(cudaDeviceGetAttribute(&op->sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaDeviceGetAttribute(&op->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
     try {
-      op->mem.allocs.reserve(16);
       s = attn_init(device, op->smem_optin);
       if (s == G4_OK) s = attn_create_impl(op, st);
     } catch (...) {
@@ -190,7 +190,7 @@ g4_status g4_attn_create(int device, const g4_attn_config* cfg, g4_attn** out) {
     cudaStreamDestroy(st);
   }
   if (s != G4_OK) {
-    for (void* q : op->mem.allocs) cudaFree(q);
+    cudaFree(op->mem.all);
     delete op;
     return s;
   }
@@ -374,7 +374,7 @@ void g4_attn_free(g4_attn* op) {
   if (!op) return;
   DeviceGuard dg(op->device);
   cudaDeviceSynchronize();
-  for (void* q : op->mem.allocs) cudaFree(q);
+  cudaFree(op->mem.all);
   delete op;
 }
 

@@ -2,16 +2,16 @@
 #pragma once
 #include <algorithm>
 #include <new>
-#include <vector>
+#include <type_traits>
 
 #include "host.h"
 #include "pages_layout.h"
 
-// Device memory of an op, with the allocation-failure injection of g4_create (G4_FAIL_ALLOC_AT).
+// Device memory of an op: one allocation, cut into arrays (with the allocation-failure injection of g4_create,
+// G4_FAIL_ALLOC_AT).
 struct g4_paged_memory {
-  std::vector<void*> allocs;
+  void* all = nullptr;
   size_t bytes = 0;
-  int fail_at = 0, n_allocs = 0;
 };
 
 struct g4_pages {
@@ -23,21 +23,31 @@ struct g4_pages {
 
 namespace g4 {
 
-template <class T>
-g4_status paged_alloc(g4_paged_memory* op, T** p, size_t count, int fill, cudaStream_t st) {
-  void* q = nullptr;
-  const size_t n = std::max<size_t>(count, 1) * sizeof(T);
-  if (op->fail_at > 0 && ++op->n_allocs == op->fail_at) return G4_ERR_OOM;  // injected
-  const cudaError_t e = cudaMalloc(&q, n);
+// The arrays that `visit` names as take(&pointer, count): a first pass adds their sizes up, a second hands them out.
+// The first `zeros` bytes, which hold the arrays named first, are cleared on `st`.
+template <class Visit>
+g4_status paged_alloc(g4_paged_memory* m, size_t zeros, cudaStream_t st, Visit visit) {
+  size_t at = 0;
+  char* base = nullptr;
+  auto take = [&](auto** p, size_t count) {
+    if (base) *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + at);
+    at += (std::max<size_t>(count, 1) * sizeof(**p) + 255) / 256 * 256;
+  };
+  visit(take);
+  const char* fail = getenv("G4_FAIL_ALLOC_AT");
+  if (fail && atoi(fail) == 1) return G4_ERR_OOM;  // injected
+  const cudaError_t e = cudaMalloc(&m->all, at);
   if (e != cudaSuccess) {
+    m->all = nullptr;
     cuda_ok(e, "cudaMalloc");
     cudaGetLastError();
     return e == cudaErrorMemoryAllocation ? G4_ERR_OOM : G4_ERR_CUDA;
   }
-  op->allocs.push_back(q);
-  op->bytes += n;
-  *p = static_cast<T*>(q);
-  CK(cudaMemsetAsync(q, fill, n, st));
+  m->bytes = at;
+  base = static_cast<char*>(m->all);
+  at = 0;
+  visit(take);
+  CK(cudaMemsetAsync(m->all, 0, std::min(zeros, m->bytes), st));
   return G4_OK;
 }
 

@@ -21,12 +21,14 @@ __global__ void pages_init_kernel(const Pages p) {
 
 g4_status pages_create_impl(g4_pages* op, cudaStream_t st) {
   Pages& p = op->p;
-  TRY(paged_alloc(&op->mem, &p.refs, p.n_pages, 0, st));
-  TRY(paged_alloc(&op->mem, &p.owner, p.n_pages, 0, st));
-  TRY(paged_alloc(&op->mem, &p.free, p.n_pages, 0, st));
-  TRY(paged_alloc(&op->mem, &p.top, 2 + kPagesCluster * kPagesThreads / 32, 0, st));
-  TRY(paged_alloc(&op->mem, &p.ticket, 1, 0, st));
-  TRY(paged_alloc(&op->mem, &p.err, 1, 0, st));
+  TRY(paged_alloc(&op->mem, ~(size_t)0, st, [&](auto& take) {
+    take(&p.top, 2 + kPagesCluster * kPagesThreads / 32);
+    take(&p.ticket, 1);
+    take(&p.err, 1);
+    take(&p.refs, p.n_pages);
+    take(&p.owner, p.n_pages);
+    take(&p.free, p.n_pages);
+  }));
   pages_init_kernel<<<op->sms, 256, 0, st>>>(p);
   CK(cudaGetLastError());
   return G4_OK;
@@ -56,22 +58,16 @@ g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_tab
   op->p.n_pages = f.n_pages;
   op->p.max_pages = f.max_pages;
   while ((1 << op->p.log_page) < f.page_size) ++op->p.log_page;
-  if (const char* fa = getenv("G4_FAIL_ALLOC_AT")) op->mem.fail_at = atoi(fa);
   g4_status s = G4_ERR_CUDA;
   cudaStream_t st = nullptr;
   if (cuda_ok(cudaDeviceGetAttribute(&op->sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute") &&
       cuda_ok(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking), "cudaStreamCreate")) {
-    try {
-      op->mem.allocs.reserve(16);
-      s = pages_create_impl(op, st);
-    } catch (...) {
-      s = G4_ERR_OOM;
-    }
+    s = pages_create_impl(op, st);
     if (!cuda_ok(cudaStreamSynchronize(st), "cudaStreamSynchronize") && s == G4_OK) s = G4_ERR_CUDA;
     cudaStreamDestroy(st);
   }
   if (s != G4_OK) {
-    for (void* q : op->mem.allocs) cudaFree(q);
+    cudaFree(op->mem.all);
     delete op;
     return s;
   }
@@ -158,7 +154,7 @@ void g4_pages_free(g4_pages* op) {
   if (!op) return;
   DeviceGuard dg(op->device);
   cudaDeviceSynchronize();
-  for (void* q : op->mem.allocs) cudaFree(q);
+  cudaFree(op->mem.all);
   delete op;
 }
 
