@@ -528,7 +528,7 @@ void g4_pages_free(g4_pages* op);
  * sequences share a prefix.  o = sum_j softmax(s)_j V_j with s_j = scale * q . K_j (scale 0:
  * 1/sqrt(head_dim)); scores, sums and outputs in fp32 and rounded once, except that the weights go
  * into the products as 16-bit numbers (g4_attn_prompt and the shared rows: one of the tensors' type,
- * other rows: two bf16 or one fp16).  scale * |q . K_j| beyond 2^25 may give rows that are not
+ * other rows: two bf16 or one fp16).  scale * |q . K_j| beyond 2^24 may give rows that are not
  * finite.  Sums run in a fixed order: equal calls give equal bits.
  *
  * The handle holds one workspace: calls on one g4_attn (captured graphs that hold such calls
