@@ -534,7 +534,7 @@ class PageTable(_PagedOp):
     def extend(self, slots, counts, n_rows, stream=None):
         """Plan counts[i] further rows of slots[i], n_rows in all.  Returns three tensors: rows [n_rows], the pool row of
         each new row, sequence after sequence, -1 where there is none; offsets [n + 1]: where each
-        sequence's rows begin among them; lens [n]: the slots' new lengths)."""
+        sequence's rows begin among them; lens [n]: the slots' new lengths."""
         n, n_rows = slots.numel(), _kv4_int("n_rows", n_rows)
         args = (self._seq("slots", slots, n), self._seq("counts", counts, n))
         if n_rows < 0:
@@ -597,7 +597,7 @@ class Attention(_PagedOp):
         """Causal attention of packed sequences: rows offsets[i] .. offsets[i + 1] - 1 of q [rows, num_q_heads,
         head_dim] and k, v [rows, num_kv_heads, head_dim] are sequence i.  Returns out: the given tensor, whose
         rows in front of the first sequence and behind the last stay as they were, or a new one, where
-        they are zeros."""
+        they are zeros (and the rows of a sequence that is passed over may be anything)."""
         n, rows = offsets.numel() - 1, q.shape[0] if q.dim() == 3 else -1
         mine, theirs = (rows, self.num_q_heads, self.head_dim), (rows, self.num_kv_heads, self.head_dim)
         args = (self._rows16("q", q, mine, self.dtype, 0), self._rows16("k", k, theirs, self.dtype, 1),

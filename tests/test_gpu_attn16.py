@@ -263,6 +263,31 @@ def test_strides_and_given_outputs(rt, d):
         assert (big[keep] == 7).all()
 
 
+@pytest.mark.parametrize("d", [64, 512])
+@pytest.mark.parametrize("n", [5, 60])
+def test_shared_strides_scale_and_given_outputs(rt, d, n):
+    """Queries out of a packed projection, outputs between others and not aligned, another scale; 60 sequences of
+    1,280 rows are attended to once, five on their own."""
+    heads, kvh, page, shared = 8, 2, 64, 20
+    lens = [shared * page + (13 * i) % 90 for i in range(n)]
+    t, pools, dense = pool_of(rt, lens, shared, kvh, d, "bf16", page, d + n)
+    a = rt.Attention(heads, kvh, d, max_seqs=n)
+    wide = torch.randn(n, heads + 4, d, generator=torch.Generator().manual_seed(n)).bfloat16().cuda()
+    q, slots = wide[:, 2:2 + heads], i32(list(range(n)))
+    plain = a.shared(q.contiguous(), *pools, t, slots, shared, scale=0.05)
+    for i, (k, v) in enumerate(dense):
+        right(plain[i:i + 1], acc.attend(q[i:i + 1], k, v, 0.05)[0], "bf16", len(k))
+    for pad in (0, 1, 8):
+        big = torch.full((n, heads + 1, d + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = big[:, 1:, pad // 2:pad // 2 + d]
+        if pad == 1:
+            out = big.flatten()[1:1 + n * heads * d].view(n, heads, d)
+        assert a.shared(q, *pools, t, slots, shared, scale=0.05, out=out) is out
+        assert torch.equal(out, plain)
+        if pad != 1:
+            assert (big[:, 0] == 7).all() and (pad == 0 or (big[:, 1:, pad // 2 + d:] == 7).all())
+
+
 def test_scale(rt):
     q, k, v, offsets = packed([140], 4, 2, 128, "bf16", 3)
     a = rt.Attention(4, 2, 128, max_seqs=1)
