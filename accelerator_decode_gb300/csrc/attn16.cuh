@@ -71,6 +71,14 @@ struct Att16Item {
   int part;       // prefix: slot of its partial result
 };
 
+// Whether an item's last tile reaches past the sequence (PREFIX: the prefix), where anything may lie: the next
+// sequence's rows, or what a program left behind the last.  So can the tile of an item that ends before its sequence does.
+template <bool PREFIX>
+__device__ __forceinline__ bool att_past_end(const Att16Item& it) {
+  const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN;
+  return it.lo + tiles * kAttN > (PREFIX ? it.hi : it.len);
+}
+
 struct Att16Bars {
   uint64_t full[8], empty[8], sfull[2], pfull[2], pvdone[2], qfull, qdone, ifull[2], iempty[2], vneed, vtail, lfull, odone, ofree, drained;
   Att16Item item[2];
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         for (int k = 0; k < C::kVRows / 16; ++k)
           att_mma_ts(one, to, from + k * 8, att_desc_at(vd, k * 2048), att_idesc<BF>(DV, true), !first || part > 0 || k > 0);
       };
-      auto clear_tail = [&]() {  // has the rows of values behind the last key cleared, once they are there
+      auto clear_tail = [&]() {  // has the rows of values behind the item's last key cleared, once they are there
         for (int y = 0; y < C::VS; ++y) {
           const int x = st + y < C::kStages ? st + y : st + y - C::kStages;
           ok = att_wait(&s->full[x], (st + y < C::kStages ? lap : lap + 1) & 1, s) && ok;
@@ -620,7 +628,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       };
       while (items.next(it)) {
         const Att16Tiles<NQ> t(it, a.tb, a.window, !PREFIX);
-        const bool tail = (PREFIX || it.hi >= it.len) && (it.hi - it.lo) % kAttN != 0;
+        const bool tail = att_past_end<PREFIX>(it);
         ok = att_wait(&s->qfull, (items.n - 1) & 1, s) && ok;
         tc_fence_after();
         if (NQ == 2) {
@@ -712,8 +720,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     while (items.next(it)) {
       const int tiles = (it.hi - it.lo + kAttN - 1) / kAttN, live = it.hi - it.lo - (tiles - 1) * kAttN;
       st += tiles * (C::KS + C::VS);
-      if ((PREFIX || it.hi >= it.len) && live != kAttN) {
-        // the last tile reaches past the sequence: what lies there may be anything
+      if (att_past_end<PREFIX>(it)) {  // from the item's last key on: no row of it sees more
         att_wait(&s->vneed, tails++ & 1, s);
         for (int y = 0; y < C::VS; ++y) {
           const int x = st - C::VS + y;
