@@ -84,6 +84,7 @@ struct Att16Bars {
   Att16Item item[2];
   uint32_t tmem;
   int abort;
+  int beat;  // steps of att_repair
 };
 static_assert(sizeof(Att16Bars) <= 512, "barriers");
 
@@ -157,9 +158,12 @@ __device__ __forceinline__ uint32_t att_pack(float lo, float hi) {
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Number x of eight.
 template <bool BF>
-__device__ __forceinline__ float att_float(uint16_t u) {
-  if (BF) return __uint_as_float((uint32_t)u << 16);
+__device__ __forceinline__ float att_one(const uint4& v, int x) {
+  const uint32_t w = x < 2 ? v.x : x < 4 ? v.y : x < 6 ? v.z : v.w;
+  if (BF) return __uint_as_float(x & 1 ? w & 0xFFFF0000u : w << 16);
+  const uint16_t u = (uint16_t)(x & 1 ? w >> 16 : w);
   float f;
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(u));
   return f;
@@ -219,18 +223,25 @@ __device__ __forceinline__ void att_tma2(void* dst, const CUtensorMap* m, int x,
       "l"(m), "r"(x), "r"(y), "r"(su32(bar))
       : "memory");
 }
-// Waits for at most two seconds (a row that att_repair takes anew keeps its CTA for some tenths of one);
-// false when the time is up, or was for another thread of the CTA.
+// Waits until nothing has gone on for two seconds: a CTA whose rows are made anew (att_repair) may take longer for an item, and
+// counts its steps.  False when the time is up, or was for another thread of the CTA.
 __device__ __forceinline__ bool att_wait(uint64_t* b, uint32_t parity, Att16Bars* s) {
   if (mbar_try(b, parity)) return true;
   volatile int* const abort = reinterpret_cast<volatile int*>(&s->abort);
+  volatile int* const beat = reinterpret_cast<volatile int*>(&s->beat);
   uint64_t now, end = 0;
+  int seen = 0;
   while (!*abort) {
     for (int i = 0; i < 256; ++i)
       if (mbar_try(b, parity)) return true;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-    if (end == 0) end = now + 2000000000ull;
-    else if (now > end) *abort = 1;
+    const int steps = *beat;
+    if (end == 0 || steps != seen) {
+      end = now + 2000000000ull;
+      seen = steps;
+    } else if (now > end) {
+      *abort = 1;
+    }
   }
   return false;
 }
@@ -279,43 +290,190 @@ __device__ __forceinline__ int att_shared_slot(const int* slots, const int* lens
   return -1;
 }
 
-// Finite values hidden from a row do not reach it: their weights are zero.  Hidden infinities and NaNs
-// would (0 * inf).  So a row whose weights add up to a finite sum and whose output is not finite looks
-// at the values that it sees, column by column, and where those are all finite takes its sum anew.
-// Rare and slow; row, q and out are the row's own.
+// Finite values hidden from a row do not reach it: their weights are zero.  Hidden infinities and NaNs would, as
+// NaN (0 * inf).  So where a row's weights add up to a finite sum and its output holds a NaN, the values that it sees
+// are looked at, and if they do not account for it, the row is taken anew, with weights in fp32.
+// A warp does this for its rows together (`on`: the lane's row is one of them).  L lanes share a key: each has eight
+// columns of the item's values, and of the head dim in one piece or two.  First the keys that all of the rows see are
+// searched for values that are not finite, then the few that only some see; rows that are still not accounted for are
+// made four at a time, in one pass with a running maximum.  Rare, and bound by the latency of each step's loads and sums: a prompt
+// of 4,000 tokens of 512 (8 heads on 1) with a row of NaNs 60 tokens from its end takes 13 ms, one of 16,384 tokens 57 (fp16 75).
+// The other roles wait longer than usual meanwhile: `beat` counts the steps (att_wait).
 template <int D, bool BF>
-__device__ __noinline__ void att_repair(const Att16Args& a, const uint16_t* q, uint16_t* out, int row0, int head, int col0,
-                                        int cols, int first, int last) {
-  const uint16_t* k = a.k + (long)row0 * a.k_row + (long)head * a.k_head;
-  const uint16_t* v = a.v + (long)row0 * a.v_row + (long)head * a.v_head;
-  auto score = [&](int j) {
-    float dot = 0.f;
-    for (int e = 0; e < D; ++e) dot = fmaf(att_float<BF>(q[e]), att_float<BF>(k[(long)j * a.k_row + e]), dot);
-    return dot * a.scale;
+__device__ __noinline__ void att_repair(const Att16Args& a, int* beat, bool on, const uint16_t* q, uint16_t* out, int row0, int head,
+                                        int half, int first, int last) {
+  constexpr int DV = Att16<D>::DV, L = DV / 8, KP = 32 / L, CK = D / DV, R = 4, U = 4, US = 8;
+  constexpr uint32_t kAll = 0xFFFFFFFFu, kExp = BF ? 0x7F80u : 0x7C00u;
+  const int lane = threadIdx.x & 31, sub = lane / L, col = lane % L * 8;
+  const uint16_t* k = a.k + (long)row0 * a.k_row + (long)head * a.k_head + col;
+  const uint16_t* v = a.v + (long)row0 * a.v_row + (long)head * a.v_head + half * DV + col;
+  auto row_out = [&](int r) {
+    return reinterpret_cast<uint16_t*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(out), r)) + half * DV + col;
   };
-  float m = -INFINITY;
-  bool known = false;
-  for (int c = col0; c < col0 + cols; c += 16) {
-    uint32_t bad = 0;
-    for (int e = 0; e < 16; ++e) bad |= (uint32_t)!att_finite(att_float<BF>(out[c + e])) << e;
-    if (!bad) continue;
-    for (int j = first; j <= last && bad; ++j)
-      for (int e = 0; e < 16; ++e)
-        if (!att_finite(att_float<BF>(v[(long)j * a.v_row + c + e]))) bad &= ~(1u << e);
-    if (!bad) continue;
-    if (!known)
-      for (int j = first; j <= last; ++j) m = fmaxf(m, score(j));
-    known = true;
-    float sum[16], l = 0.f;
-    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
-    for (int j = first; j <= last; ++j) {
-      const float p = att_exp2(score(j) - m);
-      l += p;
-      for (int e = 0; e < 16; ++e)
-        if ((bad >> e) & 1) sum[e] = fmaf(p, att_float<BF>(v[(long)j * a.v_row + c + e]), sum[e]);
+  auto nans = [&](const uint16_t* o) {  // which of the lane's columns hold a NaN
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m |= (uint32_t)((__ldcg(o + e) & 0x7FFFu) > kExp) << e;
+    return m;
+  };
+  auto odd = [&](const uint4& x) {  // which of eight numbers are not finite
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m |= (uint32_t)((w[e] & kExp) == kExp) << (2 * e) | (uint32_t)((w[e] >> 16 & kExp) == kExp) << (2 * e + 1);
+    return m;
+  };
+  // Those of the columns `want` in which a value of the keys from .. to is not finite; the search ends when all are found.
+  auto search = [&](int from, int to, uint32_t want) {
+    uint32_t found = 0;
+    for (int j0 = from; j0 <= to; j0 += KP * US) {
+      uint4 x[US];
+#pragma unroll
+      for (int u = 0; u < US; ++u) {
+        const int j = j0 + u * KP + sub;
+        x[u] = j <= to ? *reinterpret_cast<const uint4*>(v + (long)j * a.v_row) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < US; ++u) found |= odd(x[u]);
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) found |= __shfl_xor_sync(kAll, found, o);
+      if (lane == 0) atomicAdd(beat, 1);
+      if (!__any_sync(kAll, want & ~found)) break;
     }
-    for (int e = 0; e < 16; ++e)
-      if ((bad >> e) & 1) out[c + e] = (uint16_t)att_pack<BF>(sum[e] / l, 0.f);
+    return found & want;
+  };
+  uint32_t any = 0;
+  unsigned rows = 0;
+  for (unsigned m = __ballot_sync(kAll, on); m; m &= m - 1) {
+    const int r = __ffs(m) - 1;
+    const uint32_t bad = nans(row_out(r));
+    if (__any_sync(kAll, bad)) rows |= 1u << r;
+    any |= bad;
+  }
+  if (!rows) return;
+  on = rows >> lane & 1;
+  const int lo = __reduce_max_sync(kAll, on ? first : 0), hi = __reduce_min_sync(kAll, on ? last : 0x7FFFFFFF);
+  const uint32_t seen = search(lo, hi, any);
+  unsigned left = 0;
+  for (unsigned m = rows; m; m &= m - 1) {
+    const int r = __ffs(m) - 1, f = __shfl_sync(kAll, first, r), e = __shfl_sync(kAll, last, r);
+    uint32_t bad = nans(row_out(r)) & ~seen;
+    if (__any_sync(kAll, bad)) bad &= ~search(f, min(lo - 1, e), bad);
+    if (__any_sync(kAll, bad)) bad &= ~search(max(hi + 1, f), e, bad);
+    if (__any_sync(kAll, bad)) left |= 1u << r;
+  }
+  while (left) {
+    const uint16_t* qr[R];
+    uint16_t* o[R];
+    int f[R], e[R], n = 0, j_lo = 0x7FFFFFFF, j_hi = -1, r = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {  // (fewer than R are left: the last one again)
+      if (left) {
+        r = __ffs(left) - 1;
+        left &= left - 1;
+        n = i + 1;
+      }
+      qr[i] = reinterpret_cast<const uint16_t*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(q), r)) + col;
+      o[i] = row_out(r);
+      f[i] = __shfl_sync(kAll, first, r);
+      e[i] = __shfl_sync(kAll, last, r);
+      j_lo = min(j_lo, f[i]);
+      j_hi = max(j_hi, e[i]);
+    }
+    uint4 qv[R][CK];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int c = 0; c < CK; ++c) qv[i][c] = *reinterpret_cast<const uint4*>(qr[i] + c * DV);
+    float acc[R][8], top[R], sum[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      top[i] = -INFINITY;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[i][x] = 0.f;
+    }
+    for (int j0 = j_lo; j0 <= j_hi; j0 += KP * U) {
+      uint4 kx[U][CK], vx[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long j = min(j0 + u * KP + sub, j_hi);
+#pragma unroll
+        for (int c = 0; c < CK; ++c) kx[u][c] = *reinterpret_cast<const uint4*>(k + j * a.k_row + c * DV);
+        vx[u] = *reinterpret_cast<const uint4*>(v + j * a.v_row);
+      }
+      float s[R][U];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[i][u] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CK; ++c)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          float kf[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) kf[u] = att_one<BF>(kx[u][c], x);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float qf = att_one<BF>(qv[i][c], x);
+#pragma unroll
+            for (int u = 0; u < U; ++u) s[i][u] = fmaf(qf, kf[u], s[i][u]);
+          }
+        }
+#pragma unroll
+      for (int w = 1; w < L; w <<= 1)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int u = 0; u < U; ++u) s[i][u] += __shfl_xor_sync(kAll, s[i][u], w);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float most = top[i];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * KP + sub;
+          s[i][u] = j >= f[i] && j <= e[i] ? s[i][u] * a.scale : -INFINITY;
+          most = fmaxf(most, s[i][u]);
+        }
+        const float ref = most == -INFINITY ? 0.f : most, back = att_exp2(top[i] - ref);
+        top[i] = most;
+        sum[i] *= back;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[i][x] *= back;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * KP + sub;
+          const bool sees = j >= f[i] && j <= e[i];
+          const float p = att_exp2(s[i][u] - ref);
+          sum[i] += p;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) acc[i][x] = sees ? fmaf(p, att_one<BF>(vx[u], x), acc[i][x]) : acc[i][x];
+        }
+      }
+      if (lane == 0) atomicAdd(beat, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int w = L; w < 32; w <<= 1) {  // the lanes' keys together
+        const float most = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], w)), mine = most == -INFINITY ? 0.f : att_exp2(top[i] - most);
+        top[i] = most;
+        sum[i] *= mine;
+        sum[i] += __shfl_xor_sync(kAll, sum[i], w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          acc[i][x] *= mine;
+          acc[i][x] += __shfl_xor_sync(kAll, acc[i][x], w);
+        }
+      }
+      const uint32_t bad = i < n && sub == 0 ? nans(o[i]) : 0u;
+      const float inv = sum[i] != 0.f ? 1.f / sum[i] : 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (bad >> x & 1) o[i][x] = (uint16_t)att_pack<BF>(acc[i][x] * inv, 0.f);
+      __syncwarp();
+    }
   }
 }
 
@@ -325,7 +483,7 @@ __device__ __forceinline__ void att_more_registers() { asm volatile("setmaxnreg.
 
 template <int D, bool BF, bool PREFIX>
 __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
-    att16_kernel(const Att16Args a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+    att16_kernel(const __grid_constant__ Att16Args a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
   using C = Att16<D>;
   constexpr int NQ = C::NQ, DV = C::DV;
@@ -358,6 +516,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     mbar_init(&s->ofree, 4);
     mbar_init(&s->drained, 1);
     s->abort = 0;
+    s->beat = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == C::kSoftWarps) {
@@ -428,9 +587,11 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     }
     float odd0, odd1;
     att_split(odd, odd0, odd1);
-    if (!PREFIX && on && !(odd0 + odd1 == 0.f) && att_finite(l))
-      att_repair<D, BF>(a, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out, it.row0, it.head,
-                        it.half * DV, DV, a.window > 0 ? max(0, tok - a.window + 1) : 0, tok);
+    const bool spoilt = !PREFIX && on && !(odd0 + odd1 == 0.f) && att_finite(l) && !*reinterpret_cast<volatile int*>(&s->abort);
+    __syncwarp();
+    if (__any_sync(0xFFFFFFFFu, spoilt))
+      att_repair<D, BF>(a, &s->beat, spoilt, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out, it.row0,
+                        it.head, it.half, a.window > 0 ? max(0, tok - a.window + 1) : 0, tok);
     __syncwarp();
   };
   if (warp == C::kSoftWarps + 1) {
