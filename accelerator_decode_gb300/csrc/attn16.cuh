@@ -737,9 +737,6 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     if (copied) mbar_wait_drain(&s->qfull, (copied - 1) & 1);
     const int asked = lap * C::kStages + st;
     for (int k = max(0, asked - C::kStages); k < asked; ++k) mbar_wait_drain(&s->full[k % C::kStages], (k / C::kStages) & 1);
-    // ... and so does every arrival of the matrix instructions that no other role waits for
-    if (copied) att_wait(&s->qdone, (copied - 1) & 1, s);
-    for (int k = max(0, asked - C::kStages); k < asked; ++k) att_wait(&s->empty[k % C::kStages], (k / C::kStages) & 1, s);
     __syncwarp();
   } else if (warp == C::kSoftWarps) {
     // ------------------------------------------------ matrix instructions
@@ -748,7 +745,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       const uint32_t one = att_elect();
       Att16Items items{s};
       Att16Item it;
-      int st = 0, lap = 0, n_p[2] = {0, 0}, tiles_done = 0, tails = 0;
+      int st = 0, lap = 0, n_p[2] = {0, 0}, tiles_done = 0, tails = 0, second = 0;
       bool ok = true;
       auto stage = [&]() {  // the next stage, filled
         ok = att_wait(&s->full[st], lap & 1, s) && ok;
@@ -793,6 +790,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         ok = att_wait(&s->qfull, (items.n - 1) & 1, s) && ok;
         tc_fence_after();
         if (NQ == 2) {
+          second += t.b0 < t.n;
           uint32_t k0 = stage();
           for (int y = 0; y < 2; ++y)
             if (t.sees(y, 0)) {
@@ -868,6 +866,18 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       }
       att_commit(one, &s->drained);
       mbar_wait_drain(&s->drained, 0);
+      // Nothing says that commits arrive in the order in which they were made, so the last arrival at each barrier is waited for,
+      // also behind a wait that gave up; every earlier one has been waited for by the role that it is for.
+      const int whole = items.n - 1;
+      auto last = [&](uint64_t* b, int commits) {
+        if (commits > 0) mbar_wait_drain(b, (commits - 1) & 1);
+      };
+      for (int y = 0; y < 2; ++y) last(&s->sfull[y], n_p[y]);
+      last(&s->pvdone[0], NQ == 2 ? whole : tiles_done);
+      last(&s->pvdone[1], second);
+      last(&s->qdone, whole);
+      if (NQ == 1) last(&s->odone, whole);
+      for (int k = 0; k < C::kStages; ++k) last(&s->empty[k], lap + (k < st));
     }
     __syncwarp();
   } else if (warp == C::kSoftWarps + 2 || warp == C::kSoftWarps + 3) {
@@ -957,7 +967,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         ref = m == -INFINITY ? 0.f : m - att_up<BF>();
         l *= fac;
         if (j == j0) return;
-        if (NQ == 1) {  // when the previous tile's product is in (NQ 2: it came before the scores)
+        if (NQ == 1) {  // when the previous tile's product is in (NQ 2: it came before the scores); it is the newest that can be
           att_wait(&s->pvdone[0], (n - 1) & 1, s);
           __syncwarp();
           tc_fence_after();
@@ -1075,7 +1085,12 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         tc_tst_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s->pfull[b]);
+        if (lane == 0) {
+          // the previous tile's product, long in by now: no arrival at pvdone goes unseen, so that a phase stands for one tile
+          if (NQ == 1 && n > 0) att_wait(&s->pvdone[0], (n - 1) & 1, s);
+          mbar_arrive(&s->pfull[b]);
+        }
+        __syncwarp();
       }
       if (NQ == 2) {
         att_wait(&s->pvdone[y], done++ & 1, s);
