@@ -906,7 +906,17 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       }
     }
     if (!PREFIX && a.zero_rest) {
-      const int front = min(max(__ldcg(a.offsets), 0), a.n_rows), end = min(max(__ldcg(a.offsets + a.n_seq), front), a.n_rows);
+      // in front of and behind every sequence: where offsets fall, the first and the last need not be the outermost
+      int front = min(max(__ldcg(a.offsets), 0), a.n_rows), end = min(max(__ldcg(a.offsets + a.n_seq), front), a.n_rows);
+#pragma unroll 4
+      for (int i = lane; i < a.n_seq; i += 32) {
+        const int x = __ldcg(a.offsets + i), y = __ldcg(a.offsets + i + 1);
+        if (x < 0 || y <= x || y > a.n_rows) continue;
+        front = min(front, x);
+        end = max(end, y);
+      }
+      front = __reduce_min_sync(0xFFFFFFFFu, front);
+      end = __reduce_max_sync(0xFFFFFFFFu, end);
       const int rest = front + a.n_rows - end, heads = a.kvh * a.group;
       for (long e = blockIdx.x * 64 + me; e < (long)rest * heads * CH; e += gridDim.x * 64) {
         const int c = (int)(e % CH), x = (int)(e / CH % heads), r = (int)(e / CH / heads);

@@ -552,12 +552,13 @@ g4_status g4_attn_create(int device, const g4_attn_config* cfg, g4_attn** out);
 /* Causal attention of n_seq packed sequences: rows d_offsets[i] .. d_offsets[i + 1] - 1 (int32, on the
  * device) of q and out [n_rows][num_q_heads][head_dim] and of k and v [n_rows][num_kv_heads][head_dim] are
  * sequence i's tokens, each of which sees itself and the ones before it, with window > 0 only the newest
- * `window` of those (itself included).  Rows of no sequence are not seen; those in front of the first
- * sequence and behind the last are left as they were, or with zero_rest != 0 set to zero.  Tensors
+ * `window` of those (itself included).  Rows of no sequence are not seen; those in front of every
+ * sequence and behind every one are left as they were, or with zero_rest != 0 set to zero.  Tensors
  * are of the handle's type (seq_stride unused), q, k and v 16-byte aligned with positive strides that are
  * multiples of 8 elements, and out shares no element with the others.
  * A number that is not finite reaches only the rows that see it.
- * G4_DEV_BAD_POSITION: offsets that fall, or lie outside 0..n_rows; that sequence is passed over.
+ * G4_DEV_BAD_POSITION: offsets that fall, or lie outside 0..n_rows; that sequence is passed over (and rows that two of
+ * the others name get either's result).
  * Errors: INVALID_ARG (n_seq outside 1..max_seqs, n_rows < 0, window < 0, a scale that is negative or not
  * finite, NULL or malformed tensors), UNSUPPORTED (another type, q, k or v that are not aligned,
  * n_rows * heads per KV head at 2^31 or more). */

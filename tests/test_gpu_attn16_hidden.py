@@ -96,3 +96,26 @@ def test_values_hidden_inside_a_long_sequence(rt, d, heads, kvh, t, window, dtyp
     err = (diff.norm(dim=-1) / ref.norm(dim=-1))[whole]
     assert float(err.max()) <= lim, (float(err.max()), lim)
     assert torch.equal(out.nan_to_num(7.0), a.prompt(q, k, v, off, window=window).nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("many", [0, 100])
+def test_rows_of_no_sequence_where_offsets_fall(rt, d, many):
+    """A new result is zero in front of every sequence that is attended to and behind every one, and their own rows are
+    right, although the first offset is not the lowest or the last not the highest."""
+    n, heads, kvh = 400, 4, 2
+    q, k, v = rows(n, heads, d, "bf16", d), rows(n, kvh, d, "bf16", 1), rows(n, kvh, d, "bf16", 2)
+    a = rt.Attention(heads, kvh, d, max_seqs=4 + many)
+    for offsets, good in (([0, 300, 10], [(0, 300)]), ([300, 5, 350], [(5, 350)]), ([390, 20, 200, 100, 100], [(20, 200)]),
+                          ([0, 300, 300, 300, 7], [(0, 300)]), ([1000, 40, 60, 3], [(40, 60)])):
+        offsets = offsets[:-1] + [offsets[-2]] * many + offsets[-1:]
+        for _ in range(20):
+            out = a.prompt(q, k, v, i32(offsets))
+            assert a.device_error() == (-7, 2)
+            clamped = [min(max(x, 0), n) for x in (offsets[0], offsets[-1])]
+            front, end = min([clamped[0]] + [x for x, _ in good]), max([max(clamped)] + [y for _, y in good])
+            assert not out[:front].any() and not out[end:].any()
+            for x, y in good:
+                want, _ = acc.attend(q[x:y], k[x:y], v[x:y])
+                err = acc.row_errors(out[x:y], want).max()
+                assert err <= 2.5 * 2.0 ** -8 + d / 16 * 2.0 ** -21 + 2.0 ** -22 + 64 * 2.0 ** -23
