@@ -8,6 +8,12 @@ namespace {
 
 bool pages_count(const g4_pages* op, int n_seq) { return n_seq >= 1 && n_seq <= op->cfg.n_slots; }
 
+// Whether n and m int32 numbers share none.
+bool pages_apart(const int32_t* a, long n, const int32_t* b, long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return n <= 0 || m <= 0 || x + 4 * n <= y || y + 4 * m <= x;
+}
+
 __global__ void pages_init_kernel(const Pages p) {
   const long i = (long)blockIdx.x * blockDim.x + threadIdx.x, n = (long)gridDim.x * blockDim.x;
   for (long e = i; e < (long)p.n_slots * p.max_pages; e += n) p.table[e] = -1;
@@ -77,8 +83,16 @@ g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_tab
 
 g4_status g4_pages_extend(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots, const int32_t* d_counts,
                           int32_t n_rows, int32_t* d_rows, int32_t* d_offsets, int32_t* d_new_lens) {
-  if (!op || !d_slots || !d_counts || !d_offsets || !d_new_lens || !pages_count(op, n_seq) || n_rows < 0 || (n_rows && !d_rows) ||
-      d_new_lens == op->p.lens)
+  if (!op || !d_slots || !d_counts || !d_offsets || !d_new_lens || !pages_count(op, n_seq) || n_rows < 0 || (n_rows && !d_rows))
+    return G4_ERR_INVALID_ARG;
+  // what a thread still reads, and what the call keeps up to date, are no outputs
+  const long entries = (long)op->cfg.n_slots * op->cfg.max_pages;
+  const struct { const int32_t* p; long n; } outs[3] = {{d_rows, n_rows}, {d_offsets, n_seq + 1L}, {d_new_lens, n_seq}};
+  for (auto& o : outs)
+    if (!pages_apart(o.p, o.n, op->p.table, entries) || !pages_apart(o.p, o.n, op->p.lens, op->cfg.n_slots)) return G4_ERR_INVALID_ARG;
+  if (!pages_apart(d_rows, n_rows, d_offsets, n_seq + 1L) || !pages_apart(d_rows, n_rows, d_new_lens, n_seq) ||
+      !pages_apart(d_offsets, n_seq + 1L, d_new_lens, n_seq) || !pages_apart(d_rows, n_rows, d_slots, n_seq) ||
+      !pages_apart(d_rows, n_rows, d_counts, n_seq))
     return G4_ERR_INVALID_ARG;
   DEVICE_GUARD(op->device);
   PagesExtend a{op->p, d_slots, d_counts, n_seq, n_rows, d_rows, d_offsets, d_new_lens};

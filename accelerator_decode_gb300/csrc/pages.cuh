@@ -79,8 +79,8 @@ struct PagesExtend {
 
 // Every CTA works the whole plan out for itself (a sequence per thread, two sums over the block) and
 // writes its part of the rows and of the new pages' names; the last CTA to finish, when all have read
-// the old state, writes the new one.  Latency bounds it: three dependent loads and the sums.  With the
-// truncation before it: 64 sequences by 5 rows 10.3 us, 250 sequences by 896 to 1,790 rows (336,195 rows) 15.5 us.
+// the old state and the arguments, writes the new state, offsets and lengths.  Latency bounds it: three dependent
+// loads and the sums.  With the truncation before it: 64 sequences by 5 rows 10.3 us, 250 sequences by 896 to 1,790 rows (336,195 rows) 15.5 us.
 __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const PagesExtend a) {
   __shared__ PagesShared s;
   __shared__ int last;
@@ -122,11 +122,6 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
   s.at[i + 1] = sum;
   s.base[i + 1] = upto;
   if (i == 0) s.at[0] = s.base[0] = 0;
-  if (tell && i < a.n) {
-    a.offsets[i + 1] = sum;
-    a.lens[i] = slot >= 0 ? ok ? held + count : held : 0;
-    if (i == 0) a.offsets[0] = 0;
-  }
   __syncthreads();
 
   // new pages; those of sequences that were passed over for want of pages are all behind the others
@@ -175,7 +170,12 @@ __global__ void __launch_bounds__(kPagesThreads) pages_extend_kernel(const Pages
     if (!last) return;
     if (i == 0) *p.ticket = 0;
   }
-  __syncthreads();  // all have read
+  __syncthreads();  // all have read, the arguments too: offsets and new lengths may be written over them
+  if (i < a.n) {
+    a.offsets[i + 1] = sum;
+    a.lens[i] = slot >= 0 ? ok ? held + count : held : 0;
+    if (i == 0) a.offsets[0] = 0;
+  }
   if (ok) p.lens[slot] = held + count;
   int most = ok && need > 0 ? upto : 0;
 #pragma unroll

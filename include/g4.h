@@ -485,7 +485,9 @@ g4_status g4_pages_create(int device, const g4_pages_config* cfg, int32_t* d_tab
  * page_size takes no places in d_rows), or rows that would go into a page which another slot holds.
  * G4_DEV_NO_PAGES: the pages of a sequence and of those before it, passed over or not, are more than
  * the pool has left.
- * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows < 0, NULL, d_new_lens the table's own lengths; d_rows may
+ * d_offsets and d_new_lens may lie where d_slots and d_counts do; other than that an output shares no memory with
+ * another argument or with the table and its lengths.
+ * Errors: INVALID_ARG (n_seq outside 1..n_slots, n_rows < 0, NULL, outputs that share memory; d_rows may
  * be NULL with n_rows 0). */
 g4_status g4_pages_extend(g4_pages* op, g4_stream stream, int32_t n_seq, const int32_t* d_slots,
                           const int32_t* d_counts, int32_t n_rows, int32_t* d_rows, int32_t* d_offsets,
