@@ -38,6 +38,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <cstddef>
+
 #include "tc05.cuh"
 
 namespace g4 {
@@ -80,13 +82,16 @@ __device__ __forceinline__ bool att_past_end(const Att16Item& it) {
 }
 
 struct Att16Bars {
-  uint64_t full[8], empty[8], sfull[2], pfull[2], pvdone[2], qfull, qdone, ifull[2], iempty[2], vneed, vtail, lfull, odone, ofree, drained;
+  uint64_t full[8];
+  uint64_t empty[8], sfull[2], pvdone[2], qdone, odone;  // what commits arrive at, in this order (the end of the warp that issues)
+  uint64_t pfull[2], qfull, ifull[2], iempty[2], vneed, vtail, lfull, ofree, drained;
   Att16Item item[2];
   uint32_t tmem;
   int abort;
   int beat;  // steps of att_repair
 };
 static_assert(sizeof(Att16Bars) <= 512, "barriers");
+static_assert(offsetof(Att16Bars, sfull) == 8 * 16 && offsetof(Att16Bars, odone) == 8 * 21, "the order of the barriers");
 
 struct Att16Args {
   const uint16_t* q;
@@ -244,6 +249,21 @@ __device__ __forceinline__ bool att_wait(uint64_t* b, uint32_t parity, Att16Bars
     }
   }
   return false;
+}
+
+// The issuing warp's last wait.  Nothing says that commits arrive in the order in which they were made, so the last arrival at
+// each of their barriers is waited for, also behind a wait that gave up; every earlier one has been waited for by the role
+// that it is for.  A lane takes a barrier; the numbers are those of its commits (the ring's stages: `lap` each, one more for
+// the first `st`).  (A call: written out in its place it cost the long prompts 1% by where the rest came to lie.)
+__device__ __noinline__ void att_last(Att16Bars* s, int stages, int st, int lap, int sfull0, int sfull1, int pvdone0, int pvdone1, int qdone,
+                                      int odone) {
+  const int lane = threadIdx.x & 31;
+  int commits = lane < stages ? lap + (lane < st) : 0;
+  if (lane >= 8 && lane < 10) commits = lane & 1 ? sfull1 : sfull0;
+  if (lane >= 10 && lane < 12) commits = lane & 1 ? pvdone1 : pvdone0;
+  if (lane == 12) commits = qdone;
+  if (lane == 13) commits = odone;
+  if (commits > 0) mbar_wait_drain(reinterpret_cast<uint64_t*>(s) + 8 + lane, (commits - 1) & 1);
 }
 
 // The item that a role works on next (row0 < 0: none is left).  Every thread of the role calls it.
@@ -589,7 +609,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     att_split(odd, odd0, odd1);
     const bool spoilt = !PREFIX && on && !(odd0 + odd1 == 0.f) && att_finite(l) && !*reinterpret_cast<volatile int*>(&s->abort);
     __syncwarp();
-    if (__any_sync(0xFFFFFFFFu, spoilt))
+    if (!PREFIX && __any_sync(0xFFFFFFFFu, spoilt))
       att_repair<D, BF>(a, &s->beat, spoilt, a.q + (long)(it.row0 + tok) * a.q_row + (long)(it.head * a.group + hq) * a.q_head, out, it.row0,
                         it.head, it.half, a.window > 0 ? max(0, tok - a.window + 1) : 0, tok);
     __syncwarp();
@@ -866,18 +886,8 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
       }
       att_commit(one, &s->drained);
       mbar_wait_drain(&s->drained, 0);
-      // Nothing says that commits arrive in the order in which they were made, so the last arrival at each barrier is waited for,
-      // also behind a wait that gave up; every earlier one has been waited for by the role that it is for.
       const int whole = items.n - 1;
-      auto last = [&](uint64_t* b, int commits) {
-        if (commits > 0) mbar_wait_drain(b, (commits - 1) & 1);
-      };
-      for (int y = 0; y < 2; ++y) last(&s->sfull[y], n_p[y]);
-      last(&s->pvdone[0], NQ == 2 ? whole : tiles_done);
-      last(&s->pvdone[1], second);
-      last(&s->qdone, whole);
-      if (NQ == 1) last(&s->odone, whole);
-      for (int k = 0; k < C::kStages; ++k) last(&s->empty[k], lap + (k < st));
+      att_last(s, C::kStages, st, lap, n_p[0], n_p[1], NQ == 2 ? whole : tiles_done, second, whole, NQ == 1 ? whole : 0);
     }
     __syncwarp();
   } else if (warp == C::kSoftWarps + 2 || warp == C::kSoftWarps + 3) {
