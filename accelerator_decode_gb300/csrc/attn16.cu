@@ -90,7 +90,9 @@ int attn_splits(const g4_attn* op, int blocks, int tiles) {
 // own up to 20 MB of rows in all, or 40 MB with up to 1,024 rows each.  Measured, microseconds once / on their own (300 own
 // rows each): 8 x 2,048 rows, one head of 256 (17 MB) 14.8 / 15.1 and 3 fewer for the host; 8 x 512 13.3 / 12.1; 8 x 4,096
 // (34 MB) 15.7 / 18.5; 8 x 1,024, eight heads of 128 (34 MB) 16.4 / 14.5; 64 x 256, one of 512 (34 MB) 27.4 / 18.9; 64 x
-// 128 (34 MB) 20.2 / 12.6; 32 x 512 (67 MB) 20.1 / 23.3; 16 x 2,048 (134 MB) 19.1 / 29.5.
+// 128 (34 MB) 20.2 / 12.6; 32 x 512 (67 MB) 20.1 / 23.3; 16 x 2,048 (134 MB) 19.1 / 29.5.  All with groups of up to eight heads;
+// a wider group's rows are copied once for each eight of its heads, which is not counted.  (On their own, bf16 weights go into the
+// products in two parts, once for all in one: g4_attn_shared tells the border.)
 bool attn_once(const g4_attn* op, int n_seq, int rows) {
   const double bytes = 4.0 * n_seq * rows * op->cfg.num_kv_heads * op->cfg.head_dim;
   return bytes > (rows <= 1024 ? 40e6 : 20e6);
@@ -326,7 +328,7 @@ g4_status g4_attn_shared(g4_attn* op, g4_stream stream, const g4_pages* pages, i
       a.q = pq.p;
       a.q_row = pq.row;
       a.q_head = pq.head;
-          a.group = group;
+      a.group = group;
       a.kvh = f.num_kv_heads;
       a.tb = kAttM / group;
       a.scale = t.scale;

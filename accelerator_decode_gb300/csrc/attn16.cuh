@@ -26,15 +26,15 @@
 // divides them is of the unrounded ones.
 //
 // Measured (bf16 unless said; useful operations, the triangle's half of the tiles at its edge not counted):
-//   16,384 tokens, 32 heads on 8 of 128         1,350 us, 1.63 PFLOP/s; tensor pipe busy 73%: two chains of scores ->
+//   16,384 tokens, 32 heads on 8 of 128         1,360 us, 1.62 PFLOP/s; tensor pipe busy 73%: two chains of scores ->
 //     maximum, exponentials (1,250 cycles a tile) -> product share it, and the operands' bytes in shared memory
 //     take as long as the products (a tile of both blocks: 2,048 cycles of either, 2,480 measured)
-//   8 prompts of 2,250 to 4,000, 8 heads on 1 of 512   650 us, 1.02 PFLOP/s (1.53 with the scores made twice); busy 69%: a
+//   8 prompts of 2,250 to 4,000, 8 heads on 1 of 512   660 us, 1.00 PFLOP/s (1.50 with the scores made twice); busy 69%: a
 //     ring of three stages waits for L2 a sixth of the time
-//   the same of 256, window 512                 104 us, 0.92 PFLOP/s; busy 47%: items of five tiles, whose first scores
+//   the same of 256, window 512                 103 us, 0.93 PFLOP/s; busy 47%: items of five tiles, whose first scores
 //     and last product nothing else covers
 //   61 prompts of 168 to 333, 12 heads on 4 of 64 (fp16)   40 us; items of one to three tiles: latency of their chains
-//   one of 128 tokens, 8 heads on 1 of 256      9.5 us: latency of one tile's chain
+//   one of 128 tokens, 8 heads on 1 of 256      9.2 us: latency of one tile's chain
 #pragma once
 #include <cuda.h>
 

@@ -1,7 +1,8 @@
 // Attention of one token per sequence over a batch's rows behind their shared prefix, and the join of
 // those parts with the prefix's (attn16.cuh).
 //
-// HBM bounds it: every row is read once.  A block is 16 rows of one KV head, which lie one after the
+// HBM bounds it: with up to eight query heads per KV head every row is copied once, with more once for each eight of
+// them (out of L2 after the first, where they come at about the same time).  A block is 16 rows of one KV head, which lie one after the
 // other in one page: a warp copies blocks into a ring of its own by two bulk copies each.  With the rows
 // as the matrix instructions' 16-row operand and up to eight query heads as their columns,
 //   S^T (16 keys x 8) = K Q^T     O^T (16 numbers x 8) += V^T P^T,
@@ -16,7 +17,7 @@
 // Measured: 64 sequences of 550 to 1,100 rows (217 MB) behind 16,384 (67 MB), 32 heads on 8 of 128: 70 us, 4.1 TB/s.  By
 // themselves the rows behind take 46 us (4.8 TB/s), the prefix 39 us on half of the SMs, the join 12 us of a cold
 // start: the first two run side by side, and the SMs of the prefix join in when it is done.  Small batches (8 sequences
-// of 167 to 333 rows behind 2,048) 14 us: two dependent launches.
+// of 167 to 333 rows behind 2,048) 14.5 us: two dependent launches.
 #pragma once
 #include "attn16.cuh"
 

@@ -110,8 +110,12 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // at most two kernels of the step are resident at once (the one computing and the next one
 // loading its weights): triggered at the start, every following kernel became resident in a
 // cascade, SMs ran out of room, and the CTA scheduler put two CTAs of one kernel on one SM
-// (half speed) while other SMs had none.  Both are no-ops for a launch without the PDL
-// attribute.
+// (half speed) while other SMs had none.  One kernel writes and triggers before its wait,
+// att_tail_kernel behind a prefix (attn16_decode.cuh), so that three can be resident there: it is
+// launched directly behind the prefix's kernel, which triggers only after its own wait, so all
+// that came before that one is complete; it writes what neither that kernel nor anything still
+// running reads, and waits at its end, so that who waits for it has waited for both.  Both are
+// no-ops for a launch without the PDL attribute.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 

@@ -529,9 +529,10 @@ void g4_pages_free(g4_pages* op);
  * Softmax attention over 16-bit keys and values: whole prompts, and single tokens of a batch whose
  * sequences share a prefix.  o = sum_j softmax(s)_j V_j with s_j = scale * q . K_j (scale 0:
  * 1/sqrt(head_dim)); scores, sums and outputs in fp32 and rounded once, except that the weights go
- * into the products as 16-bit numbers (g4_attn_prompt and the shared rows: one of the tensors' type,
- * other rows: two bf16 or one fp16).  scale * |q . K_j| beyond 2^24 may give rows that are not
- * finite.  Sums run in a fixed order: equal calls give equal bits.
+ * into the products as 16-bit numbers (g4_attn_prompt, and rows that g4_attn_shared attends to once for all
+ * sequences: one of the tensors' type, which adds up to 0.4 of the outputs' own rounding error; other rows: two
+ * bf16 or one fp16).  scale * |q . K_j| beyond 2^24, bf16 values beyond 2^90 and fp16 values within 2^-10 of the
+ * type's largest may give outputs that are not finite.  Sums run in a fixed order: equal calls give equal bits.
  *
  * The handle holds one workspace: calls on one g4_attn (captured graphs that hold such calls
  * included) must be ordered by the caller, on one stream or by events.  No call after g4_attn_create
@@ -569,8 +570,9 @@ g4_status g4_attn_prompt(g4_attn* op, g4_stream stream, int32_t n_seq, const int
                          const g4_kv4_tensor* k, const g4_kv4_tensor* v, const g4_kv4_tensor* out);
 
 /* Attention of one token of each of n_seq slots over all rows of its slot, in pools that `pages` has the
- * table of (g4_pages).  The first shared_pages pages of all slots are the same ones: their rows are read once for
- * all.  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), q aligned as
+ * table of (g4_pages).  The first shared_pages pages of all slots are the same ones: their rows are attended to
+ * once for all where n_seq times their keys and values are more than 20 MB (40 MB for up to 1,024 rows), and else by each
+ * sequence with its other rows; so n_seq decides how the weights of the shared rows are rounded (above).  q, out: [n_seq][num_q_heads][head_dim] (row_stride: of the sequences; seq_stride unused), q aligned as
  * in g4_attn_prompt, sharing no element.  A slot may be named more than once.  An empty slot gets zeros.
  * G4_DEV_BAD_SLOT: a slot out of range.  G4_DEV_BAD_POSITION: a slot with fewer rows than the shared
  * pages hold, with other first pages than the first slot that has so many rows, or with a missing
