@@ -66,7 +66,7 @@ struct Att16 {
 };
 
 struct Att16Item {
-  int row0;       // first packed row of the sequence
+  int row0;       // first packed row of the sequence; below 0: no item is left, and lo .. hi - 1 are the rows that all span
   int t0, len;    // first token of the item; tokens of the sequence
   int head, half;
   int lo, hi;     // keys lo .. hi - 1 of the sequence
@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
     // prompt: the lane's sequence of the 32 from `seq` on: its first row, length and last item (one too far);
     // items of all 32, and of the sequences ahead of them
     int seq = -32, from = 0, len = 0, upto = 0, all = 0, before = 0;
+    int lowest = a.n_rows, highest = 0;  // of the rows of the lane's sequences
     int index = blockIdx.x;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -661,6 +662,10 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
               if (blockIdx.x == 0) set_err(a.err, G4_DEV_BAD_POSITION);
             } else {
               len = to - from;
+              if (len > 0) {
+                lowest = min(lowest, from);
+                highest = max(highest, to);
+              }
               upto = (len + NQ * a.tb - 1) / (NQ * a.tb);
             }
           }
@@ -679,6 +684,9 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
           it.t0 = (__shfl_sync(0xFFFFFFFFu, upto, w) - 1 - (blk - before)) * (NQ * a.tb);
           it.lo = a.window > 0 ? max(0, it.t0 - a.window + 1) : 0;
           it.hi = min(it.t0 + NQ * a.tb, it.len);
+        } else {  // all sequences have been looked at: the rows that they span
+          it.lo = __reduce_min_sync(0xFFFFFFFFu, lowest);
+          it.hi = __reduce_max_sync(0xFFFFFFFFu, highest);
         }
       }
       if (n >= 2) ok = att_wait(&s->iempty[n & 1], ((n - 2) >> 1) & 1, s);
@@ -915,18 +923,11 @@ __global__ void __launch_bounds__(Att16<D>::kThreads, 1)
         mbar_arrive(&s->vtail);
       }
     }
-    if (!PREFIX && a.zero_rest) {
+    if (!PREFIX && a.zero_rest && !*reinterpret_cast<volatile int*>(&s->abort)) {
       // in front of and behind every sequence: where offsets fall, the first and the last need not be the outermost
       int front = min(max(__ldcg(a.offsets), 0), a.n_rows), end = min(max(__ldcg(a.offsets + a.n_seq), front), a.n_rows);
-#pragma unroll 4
-      for (int i = lane; i < a.n_seq; i += 32) {
-        const int x = __ldcg(a.offsets + i), y = __ldcg(a.offsets + i + 1);
-        if (x < 0 || y <= x || y > a.n_rows) continue;
-        front = min(front, x);
-        end = max(end, y);
-      }
-      front = __reduce_min_sync(0xFFFFFFFFu, front);
-      end = __reduce_max_sync(0xFFFFFFFFu, end);
+      front = min(front, it.lo);
+      end = max(end, it.hi);
       const int rest = front + a.n_rows - end, heads = a.kvh * a.group;
       for (long e = blockIdx.x * 64 + me; e < (long)rest * heads * CH; e += gridDim.x * 64) {
         const int c = (int)(e % CH), x = (int)(e / CH % heads), r = (int)(e / CH / heads);
